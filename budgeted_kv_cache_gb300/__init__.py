@@ -20,12 +20,13 @@ LIB_PATH = os.path.join(_HERE, "libkvc.so")
 KVC_OK = 0
 STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "unsupported configuration",
                 3: "workspace missing or too small", 4: "CUDA error", 5: "no usable sm_103 device"}
-UNIT_OK, UNIT_OVER_BUDGET, UNIT_BAD_INDEX, UNIT_BAD_FLAGS, UNIT_TIMEOUT = 0, 1, 2, 3, 4
+UNIT_OK, UNIT_OVER_BUDGET, UNIT_BAD_INDEX, UNIT_BAD_FLAGS, UNIT_TIMEOUT, UNIT_FULL = 0, 1, 2, 3, 4, 5
 ACT_RELEASE, ACT_INT4, ACT_INT8, ACT_BF16 = 0, 1, 2, 3
 POOL_INT4, POOL_INT8, POOL_BF16, N_POOLS = 0, 1, 2, 3
 FLAG_PROTECT, FLAG_EXCLUDE = 1, 2
 QUANT_G32_BF16, QUANT_ROW_FP16 = 0, 1
 SCORE_ACCUMULATE = 1
+ATTN_ADD_MASS = 1
 
 
 class KvcError(RuntimeError):
@@ -71,6 +72,23 @@ class kvc_bf16_rows(ctypes.Structure):
                 ("count", ctypes.c_void_p), ("capacity", ctypes.c_int32)]
 
 
+class kvc_score_mods(ctypes.Structure):
+    """Score modifiers of kvc_prompt_attn and kvc_i4_attn (slopes, prefix_len: device pointers)."""
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("window", ctypes.c_int32),
+                ("prefix_len", ctypes.c_void_p)]
+
+
+class kvc_strides(ctypes.Structure):
+    """Element strides of a [B][L][H][n][d] tensor."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "layer", "head", "token")]
+
+
+class kvc_i4_rows(ctypes.Structure):
+    """A cache held in 4 bits (device pointers)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "pos", "mass", "count", "next_pos")] + \
+        [("capacity", ctypes.c_int32), ("quant_mode", ctypes.c_int32)]
+
+
 class kvc_effect_record(ctypes.Structure):
     """Window record of kvc_deletion_effect (device pointers: o, lse, s, u)."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("o", "lse", "s", "u")]
@@ -100,6 +118,7 @@ def _load():
         RS = ctypes.POINTER(kvc_ref_store)
         ER, CT = ctypes.POINTER(kvc_effect_record), ctypes.POINTER(kvc_commit_thresholds)
         BR = ctypes.POINTER(kvc_bf16_rows)
+        SM, ST, RW = ctypes.POINTER(kvc_score_mods), ctypes.POINTER(kvc_strides), ctypes.POINTER(kvc_i4_rows)
         sig = {
             "kvc_score_workspace_bytes": (SZ, [SH, I32]),
             "kvc_score": (ctypes.c_int, [SH, P, P, I32, F32, P, P, I32, U32, P, P, P, P, SZ, P]),
@@ -124,6 +143,14 @@ def _load():
                                                      P]),
             "kvc_protect_pending": (ctypes.c_int, [SH, I32, I32, P, P, P, I32, I32, P, P]),
             "kvc_commit_flags": (ctypes.c_int, [I32, I64, I32, P, P, P, P, P, P]),
+            "kvc_prompt_attn_workspace_bytes": (SZ, [SH, I32, I32]),
+            "kvc_prompt_attn": (ctypes.c_int, [SH, P, ST, I32, P, P, ST, P, P, P, SM, F32, P, ST, P, P, P, SZ, P]),
+            "kvc_i4_append": (ctypes.c_int, [SH, RW, P, P, ST, I32, P, P, P]),
+            "kvc_i4_read": (ctypes.c_int, [SH, RW, I32, P, P, ST, P]),
+            "kvc_i4_attn_workspace_bytes": (SZ, [SH, RW, I32, U32]),
+            "kvc_i4_attn": (ctypes.c_int, [SH, RW, P, ST, I32, P, SM, F32, U32, P, ST, P, P, SZ, P]),
+            "kvc_i4_evict_workspace_bytes": (SZ, [SH, RW, I32]),
+            "kvc_i4_evict": (ctypes.c_int, [SH, RW, I32, I32, I32, P, P, SZ, P]),
             "kvc_set_overrides": (ctypes.c_int, [ctypes.POINTER(kvc_overrides)]),
             "kvc_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         }
@@ -458,3 +485,182 @@ def kvc_engine_attn(shape, policy: Optional[Policy], q, n_q, q_pos, pools: Optio
         ctypes.byref(recent) if recent is not None else None,
         ctypes.byref(current) if current is not None else None, float(softmax_scale), _p(out),
         _p(workspace), wb, _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- prompt attention, 4-bit cache
+
+@dataclasses.dataclass
+class ScoreMods:
+    """Score modifiers of kvc_prompt_attn and kvc_i4_attn (see include/kvc.h): tanh cap, distance slopes
+    fp32 [H_q], sliding window, prefix lengths int32 [B]."""
+    softcap: float = 0.0
+    slopes: Optional[torch.Tensor] = None
+    window: int = 0
+    prefix_len: Optional[torch.Tensor] = None
+
+
+@dataclasses.dataclass
+class I4Rows:
+    """A growing cache held in 4 bits (torch tensors; see kvc_i4_rows in include/kvc.h)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    pos: torch.Tensor
+    count: torch.Tensor
+    next_pos: torch.Tensor
+    mass: Optional[torch.Tensor] = None
+    quant_mode: int = QUANT_G32_BF16
+
+    def __post_init__(self):
+        """Shapes and types that belong together: codes [U][capacity][d/2], the scales of the mode,
+        positions and mass [U][capacity], counters [U]; contiguous, on one device."""
+        if self.k.dim() != 3 or self.pos.dim() != 2 or tuple(self.pos.shape) != tuple(self.k.shape[:2]):
+            raise KvcError("I4Rows", 1)
+        U, cap, half = self.k.shape
+        g32 = self.quant_mode == QUANT_G32_BF16
+        ns, sdt = (half // 16, torch.bfloat16) if g32 else (1, torch.float16)
+        want = [(self.k, U * cap * half, torch.uint8), (self.v, U * cap * half, torch.uint8),
+                (self.k_scale, U * cap * ns, sdt), (self.v_scale, U * cap * ns, sdt), (self.pos, U * cap, torch.int32),
+                (self.mass, U * cap, torch.float32), (self.count, U, torch.int32), (self.next_pos, U, torch.int32)]
+        for t, n, dtype in want:
+            if t is not None and (t.numel() != n or t.dtype != dtype or not t.is_contiguous() or t.device != self.k.device):
+                raise KvcError("I4Rows", 1)
+
+    def c(self) -> kvc_i4_rows:
+        return kvc_i4_rows(_p(self.k), _p(self.v), _p(self.k_scale), _p(self.v_scale), _p(self.pos),
+                           _p(self.mass), _p(self.count), _p(self.next_pos), int(self.pos.shape[-1]),
+                           int(self.quant_mode))
+
+    @staticmethod
+    def allocate(shape: kvc_shape, capacity: int, quant_mode: int = QUANT_G32_BF16, device="cuda",
+                 mass: bool = True) -> "I4Rows":
+        """An empty cache: counts and next positions 0."""
+        U, d = shape.batch * shape.n_layers * shape.n_kv_heads, shape.head_dim
+        e = lambda *s, dt: torch.empty(s, dtype=dt, device=device)
+        ns, sdt = (d // 32, torch.bfloat16) if quant_mode == QUANT_G32_BF16 else (1, torch.float16)
+        return I4Rows(k=e(U, capacity, d // 2, dt=torch.uint8), v=e(U, capacity, d // 2, dt=torch.uint8),
+                      k_scale=e(U, capacity, ns, dt=sdt), v_scale=e(U, capacity, ns, dt=sdt),
+                      pos=e(U, capacity, dt=torch.int32),
+                      count=torch.zeros(U, dtype=torch.int32, device=device),
+                      next_pos=torch.zeros(U, dtype=torch.int32, device=device),
+                      mass=e(U, capacity, dt=torch.float32) if mass else None, quant_mode=quant_mode)
+
+    @staticmethod
+    def from_pools(pools: Pools, policy: Policy, kept_count: torch.Tensor, next_pos: torch.Tensor,
+                   mass: Optional[torch.Tensor] = None) -> "I4Rows":
+        """The int4 pool of a compaction pass as a growing cache (no copy): kept_count as written by
+        kvc_select, next_pos int32 [U]."""
+        return I4Rows(pools.k_i4, pools.v_i4, pools.k_i4_scale, pools.v_i4_scale,
+                      pools.pos_out[POOL_INT4], kept_count[POOL_INT4], next_pos, mass, policy.quant_mode)
+
+
+def _strides(fn: str, t: torch.Tensor, shape: kvc_shape, heads: int, n: int):
+    """Strides of a bf16 [B][L][H][n][d] tensor of the current device; n < 0 takes the tensor's."""
+    if t.dtype != torch.bfloat16 or t.dim() != 5 or not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise KvcError(fn, 1)
+    st = t.stride()
+    if tuple(t.shape) != (shape.batch, shape.n_layers, heads, t.shape[3] if n < 0 else n, shape.head_dim) or st[4] != 1:
+        raise KvcError(fn, 1)
+    return ctypes.byref(kvc_strides(*st[:4]))
+
+
+def _dense(fn: str, t: Optional[torch.Tensor], dtype, n: int) -> Optional[int]:
+    """Address of an optional contiguous device tensor of n elements."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != torch.cuda.current_device():
+        raise KvcError(fn, 1)
+    return t.data_ptr()
+
+
+def _mods(fn: str, mods: Optional[ScoreMods], shape: kvc_shape):
+    if mods is None:
+        return None
+    return ctypes.byref(kvc_score_mods(
+        float(mods.softcap), _dense(fn, mods.slopes, torch.float32, shape.n_q_heads), int(mods.window),
+        _dense(fn, mods.prefix_len, torch.int32, shape.batch)))
+
+
+def _units(shape: kvc_shape) -> int:
+    return shape.batch * shape.n_layers * shape.n_kv_heads
+
+
+def _bytes(workspace) -> int:
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def kvc_prompt_attn_workspace_bytes(shape, n_q: int, with_docs: bool = False) -> int:
+    return _load().kvc_prompt_attn_workspace_bytes(ctypes.byref(shape), int(n_q), int(with_docs))
+
+
+def kvc_prompt_attn(shape, q, k, v, out, q_len=None, kv_len=None, docs=None, mods: Optional[ScoreMods] = None,
+                    softmax_scale=0.0, row_lse=None, unit_status=None, workspace=None, stream=None):
+    """Attention of q [B][L][H_q][n_q][d] over k, v [B][L][H_kv][T][d] (any strides whose innermost is 1;
+    k and v alike) with score modifiers and documents (see include/kvc.h)."""
+    f, n_q = "kvc_prompt_attn", int(q.shape[3]) if q.dim() == 5 else 0
+    if v.stride() != k.stride() or v.shape != k.shape:
+        raise KvcError(f, 1)
+    _check(f, _load().kvc_prompt_attn(
+        ctypes.byref(shape), _p(q), _strides(f, q, shape, shape.n_q_heads, n_q), n_q, _p(k), _p(v),
+        _strides(f, k, shape, shape.n_kv_heads, shape.n_tokens),
+        _dense(f, q_len, torch.int32, shape.batch), _dense(f, kv_len, torch.int32, shape.batch),
+        _dense(f, docs, torch.int32, shape.batch * shape.n_tokens), _mods(f, mods, shape), float(softmax_scale),
+        _p(out), _strides(f, out, shape, shape.n_q_heads, n_q),
+        _dense(f, row_lse, torch.float32, shape.batch * shape.n_layers * shape.n_q_heads * n_q),
+        _dense(f, unit_status, torch.int32, _units(shape)), _p(workspace), _bytes(workspace), _stream(stream)))
+
+
+def kvc_i4_append(shape, rows: I4Rows, k, v, n_new=None, unit_status=None, stream=None):
+    """Quantise k, v [B][L][H_kv][n][d] into the rows behind those in use (see include/kvc.h)."""
+    f, r = "kvc_i4_append", rows.c()
+    if v.stride() != k.stride() or v.shape != k.shape:
+        raise KvcError(f, 1)
+    _check(f, _load().kvc_i4_append(
+        ctypes.byref(shape), ctypes.byref(r), _p(k), _p(v), _strides(f, k, shape, shape.n_kv_heads, -1),
+        int(k.shape[3]), _dense(f, n_new, torch.int32, shape.batch), _dense(f, unit_status, torch.int32, _units(shape)),
+        _stream(stream)))
+
+
+def kvc_i4_read(shape, rows: I4Rows, k_out, v_out, stream=None):
+    """Rows 0 .. n-1 of every unit as bf16 into k_out, v_out [B][L][H_kv][n][d] (see include/kvc.h)."""
+    f, r = "kvc_i4_read", rows.c()
+    if v_out.stride() != k_out.stride() or v_out.shape != k_out.shape:
+        raise KvcError(f, 1)
+    _check(f, _load().kvc_i4_read(
+        ctypes.byref(shape), ctypes.byref(r), int(k_out.shape[3]) if k_out.dim() == 5 else 0, _p(k_out),
+        _p(v_out), _strides(f, k_out, shape, shape.n_kv_heads, -1), _stream(stream)))
+
+
+def kvc_i4_attn_workspace_bytes(shape, rows: I4Rows, n_q: int, add_mass: bool = False) -> int:
+    r = rows.c()
+    return _load().kvc_i4_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(r), int(n_q),
+                                               ATTN_ADD_MASS if add_mass else 0)
+
+
+def kvc_i4_attn(shape, rows: I4Rows, q, out, q_pos=None, mods: Optional[ScoreMods] = None, softmax_scale=0.0,
+                add_mass: bool = False, row_lse=None, workspace=None, stream=None):
+    """Attention of q [B][L][H_q][n_q][d] over a 4-bit cache; add_mass adds the softmax weights to
+    rows.mass (see include/kvc.h)."""
+    f, r, n_q = "kvc_i4_attn", rows.c(), int(q.shape[3]) if q.dim() == 5 else 0
+    _check(f, _load().kvc_i4_attn(
+        ctypes.byref(shape), ctypes.byref(r), _p(q), _strides(f, q, shape, shape.n_q_heads, n_q), n_q,
+        _dense(f, q_pos, torch.int32, shape.batch * n_q), _mods(f, mods, shape), float(softmax_scale),
+        ATTN_ADD_MASS if add_mass else 0, _p(out), _strides(f, out, shape, shape.n_q_heads, n_q),
+        _dense(f, row_lse, torch.float32, shape.batch * shape.n_layers * shape.n_q_heads * n_q), _p(workspace),
+        _bytes(workspace), _stream(stream)))
+
+
+def kvc_i4_evict_workspace_bytes(shape, rows: I4Rows, budget: int) -> int:
+    r = rows.c()
+    return _load().kvc_i4_evict_workspace_bytes(ctypes.byref(shape), ctypes.byref(r), int(budget))
+
+
+def kvc_i4_evict(shape, rows: I4Rows, budget: int, n_sink: int, n_recent: int, unit_status=None, workspace=None,
+                 stream=None):
+    """Evict in place the rows of least mass above `budget` rows per unit (see include/kvc.h)."""
+    r = rows.c()
+    _check("kvc_i4_evict", _load().kvc_i4_evict(
+        ctypes.byref(shape), ctypes.byref(r), int(budget), int(n_sink), int(n_recent),
+        _dense("kvc_i4_evict", unit_status, torch.int32, _units(shape)), _p(workspace), _bytes(workspace),
+        _stream(stream)))

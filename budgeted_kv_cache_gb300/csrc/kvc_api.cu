@@ -325,6 +325,55 @@ kvc_status device_view(const void** p) {
   return KVC_ERR_INVALID_ARG;
 }
 
+// ---------------------------------------------------------------- prompt attention, 4-bit cache
+
+// Strides of a bf16 [B][L][H][n][d] tensor: the caller's, checked, or dense.
+kvc_status tensor_strides(const kvc_shape* s, int64_t heads, int64_t n, const kvc_strides* in, kvc_strides* out) {
+  if (!in) {
+    *out = {s->n_layers * heads * n * s->head_dim, heads * n * s->head_dim, n * s->head_dim, s->head_dim};
+    return KVC_OK;
+  }
+  const int64_t sizes[4] = {s->batch, s->n_layers, heads, n};
+  const int64_t given[4] = {in->batch, in->layer, in->head, in->token};
+  int64_t* to[4] = {&out->batch, &out->layer, &out->head, &out->token};
+  for (int i = 0; i < 4; ++i) {
+    *to[i] = given[i];
+    if (sizes[i] <= 1) *to[i] = 0;
+    else if (given[i] <= 0 || given[i] % 8 || given[i] > (1LL << 38)) return KVC_ERR_INVALID_ARG;
+  }
+  return KVC_OK;
+}
+
+kvc_status check_mods(const kvc_score_mods* m, Mods* out) {
+  *out = {};
+  if (!m) return KVC_OK;
+  if (!(m->softcap >= 0.f) || isinf(m->softcap) || m->window < 0) return KVC_ERR_INVALID_ARG;
+  *out = {m->softcap, m->slopes, m->window, m->prefix_len};
+  return KVC_OK;
+}
+
+kvc_status check_i4(const kvc_shape* s, const kvc_i4_rows* r) {
+  kvc_status st = check_shape(s);
+  if (st != KVC_OK) return st;
+  if (!r || !r->k || !r->v || !r->k_scale || !r->v_scale || !r->pos || !r->count || !r->next_pos)
+    return KVC_ERR_INVALID_ARG;
+  if (!aligned(r->k, 16) || !aligned(r->v, 16) || !aligned(r->k_scale, 16) || !aligned(r->v_scale, 16))
+    return KVC_ERR_INVALID_ARG;
+  if (r->capacity < 1) return KVC_ERR_INVALID_ARG;
+  if (r->quant_mode != KVC_QUANT_G32_BF16 && r->quant_mode != KVC_QUANT_ROW_FP16) return KVC_ERR_INVALID_ARG;
+  return KVC_OK;
+}
+
+// Queries of one call: at least one, the packed rows of a unit within 31 bits.
+kvc_status check_queries(const kvc_shape* s, int64_t n_q) {
+  if (n_q < 1) return KVC_ERR_INVALID_ARG;
+  return n_q * (s->n_q_heads / s->n_kv_heads) > (1 << 30) ? KVC_ERR_UNSUPPORTED : KVC_OK;
+}
+
+size_t i4_attn_lse_bytes(const kvc_shape* s, int64_t n_q) {
+  return static_cast<size_t>(s->batch) * s->n_layers * s->n_q_heads * n_q * sizeof(float);
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------- CommitKV plans
@@ -825,6 +874,171 @@ kvc_status kvc_engine_attn(const kvc_shape* shape, const kvc_policy* policy, con
   }
   if (launch_engine(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVC_ERR_CUDA;
   return KVC_OK;
+}
+
+size_t kvc_prompt_attn_workspace_bytes(const kvc_shape* shape, int32_t n_q, int32_t with_docs) {
+  (void)with_docs;
+  if (check_shape(shape) != KVC_OK || check_queries(shape, n_q) != KVC_OK) return 0;
+  return 0;
+}
+
+kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_strides* q_strides,
+                           int32_t n_q, const void* k, const void* v, const kvc_strides* kv_strides,
+                           const int32_t* q_len, const int32_t* kv_len, const int32_t* docs,
+                           const kvc_score_mods* mods, float softmax_scale, void* out,
+                           const kvc_strides* out_strides, float* row_lse, int32_t* unit_status,
+                           void* workspace, size_t workspace_bytes, kvc_stream stream) {
+  kvc_status st = check_shape(shape);
+  if (st != KVC_OK) return st;
+  if ((st = check_queries(shape, n_q)) != KVC_OK) return st;
+  if (!q || !k || !v || !out) return KVC_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16)) return KVC_ERR_INVALID_ARG;
+  PromptArgs a = {};
+  if ((st = tensor_strides(shape, shape->n_q_heads, n_q, q_strides, &a.qs)) != KVC_OK) return st;
+  if ((st = tensor_strides(shape, shape->n_kv_heads, shape->n_tokens, kv_strides, &a.kvs)) != KVC_OK) return st;
+  if ((st = tensor_strides(shape, shape->n_q_heads, n_q, out_strides, &a.os)) != KVC_OK) return st;
+  if ((st = check_mods(mods, &a.mods)) != KVC_OK) return st;
+  DevInfo info;
+  if ((st = check_device(&info)) != KVC_OK) return st;
+  const size_t need = kvc_prompt_attn_workspace_bytes(shape, n_q, docs != nullptr);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return KVC_ERR_WORKSPACE;
+  if (!(softmax_scale > 0.f)) softmax_scale = 1.0f / sqrtf(static_cast<float>(shape->head_dim));
+  a.U = static_cast<int32_t>(n_units(shape));
+  a.L = shape->n_layers;
+  a.Hkv = shape->n_kv_heads;
+  a.B = shape->batch;
+  a.G = shape->n_q_heads / shape->n_kv_heads;
+  a.d = shape->head_dim;
+  a.n_q = n_q;
+  a.T = shape->n_tokens;
+  a.scale = softmax_scale;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_len = q_len;
+  a.kv_len = kv_len;
+  a.docs = docs;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = row_lse;
+  a.unit_status = unit_status;
+  return launch_prompt(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+kvc_status kvc_i4_append(const kvc_shape* shape, const kvc_i4_rows* rows, const void* k,
+                         const void* v, const kvc_strides* strides, int32_t n, const int32_t* n_new,
+                         int32_t* unit_status, kvc_stream stream) {
+  kvc_status st = check_i4(shape, rows);
+  if (st != KVC_OK) return st;
+  if (n < 0) return KVC_ERR_INVALID_ARG;
+  if (n == 0) return KVC_OK;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return KVC_ERR_INVALID_ARG;
+  I4AppendArgs a = {};
+  if ((st = tensor_strides(shape, shape->n_kv_heads, n, strides, &a.st)) != KVC_OK) return st;
+  DevInfo info;
+  if ((st = check_device(&info)) != KVC_OK) return st;
+  a.U = static_cast<int32_t>(n_units(shape));
+  a.L = shape->n_layers;
+  a.Hkv = shape->n_kv_heads;
+  a.d = shape->head_dim;
+  a.n = n;
+  a.rows = *rows;
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.n_new = n_new;
+  a.unit_status = unit_status;
+  return launch_i4_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+kvc_status kvc_i4_read(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t n, void* k_out,
+                       void* v_out, const kvc_strides* strides, kvc_stream stream) {
+  kvc_status st = check_i4(shape, rows);
+  if (st != KVC_OK) return st;
+  if (n < 0 || n > rows->capacity) return KVC_ERR_INVALID_ARG;
+  if (n == 0) return KVC_OK;
+  if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16)) return KVC_ERR_INVALID_ARG;
+  I4ReadArgs a = {};
+  if ((st = tensor_strides(shape, shape->n_kv_heads, n, strides, &a.st)) != KVC_OK) return st;
+  DevInfo info;
+  if ((st = check_device(&info)) != KVC_OK) return st;
+  a.U = static_cast<int32_t>(n_units(shape));
+  a.L = shape->n_layers;
+  a.Hkv = shape->n_kv_heads;
+  a.d = shape->head_dim;
+  a.n = n;
+  a.rows = *rows;
+  a.k = static_cast<__nv_bfloat16*>(k_out);
+  a.v = static_cast<__nv_bfloat16*>(v_out);
+  return launch_i4_read(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+size_t kvc_i4_attn_workspace_bytes(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t n_q, uint32_t flags) {
+  if (check_i4(shape, rows) != KVC_OK || check_queries(shape, n_q) != KVC_OK) return 0;
+  return (flags & KVC_ATTN_ADD_MASS) ? i4_attn_lse_bytes(shape, n_q) : 0;
+}
+
+kvc_status kvc_i4_attn(const kvc_shape* shape, const kvc_i4_rows* rows, const void* q,
+                       const kvc_strides* q_strides, int32_t n_q, const int32_t* q_pos,
+                       const kvc_score_mods* mods, float softmax_scale, uint32_t flags, void* out,
+                       const kvc_strides* out_strides, float* row_lse, void* workspace,
+                       size_t workspace_bytes, kvc_stream stream) {
+  kvc_status st = check_i4(shape, rows);
+  if (st != KVC_OK) return st;
+  if ((st = check_queries(shape, n_q)) != KVC_OK) return st;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return KVC_ERR_INVALID_ARG;
+  if (flags & ~static_cast<uint32_t>(KVC_ATTN_ADD_MASS)) return KVC_ERR_INVALID_ARG;
+  if ((flags & KVC_ATTN_ADD_MASS) && !rows->mass) return KVC_ERR_INVALID_ARG;
+  I4AttnArgs a = {};
+  if ((st = tensor_strides(shape, shape->n_q_heads, n_q, q_strides, &a.qs)) != KVC_OK) return st;
+  if ((st = tensor_strides(shape, shape->n_q_heads, n_q, out_strides, &a.os)) != KVC_OK) return st;
+  if ((st = check_mods(mods, &a.mods)) != KVC_OK) return st;
+  DevInfo info;
+  if ((st = check_device(&info)) != KVC_OK) return st;
+  const size_t need = kvc_i4_attn_workspace_bytes(shape, rows, n_q, flags);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return KVC_ERR_WORKSPACE;
+  if (!(softmax_scale > 0.f)) softmax_scale = 1.0f / sqrtf(static_cast<float>(shape->head_dim));
+  a.U = static_cast<int32_t>(n_units(shape));
+  a.L = shape->n_layers;
+  a.Hkv = shape->n_kv_heads;
+  a.B = shape->batch;
+  a.G = shape->n_q_heads / shape->n_kv_heads;
+  a.d = shape->head_dim;
+  a.n_q = n_q;
+  a.scale = softmax_scale;
+  a.rows = *rows;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_pos = q_pos;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.add_mass = (flags & KVC_ATTN_ADD_MASS) != 0;
+  a.lse = row_lse ? row_lse : a.add_mass ? static_cast<float*>(workspace) : nullptr;
+  return launch_i4_attn(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+size_t kvc_i4_evict_workspace_bytes(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t budget) {
+  if (check_i4(shape, rows) != KVC_OK || budget < 1 || budget >= rows->capacity) return 0;
+  return static_cast<size_t>(n_units(shape)) * 2 * std::min(budget, rows->capacity - budget) * sizeof(int32_t);
+}
+
+kvc_status kvc_i4_evict(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t budget,
+                        int32_t n_sink, int32_t n_recent, int32_t* unit_status, void* workspace,
+                        size_t workspace_bytes, kvc_stream stream) {
+  kvc_status st = check_i4(shape, rows);
+  if (st != KVC_OK) return st;
+  if (budget < 1 || n_sink < 0 || n_recent < 0 || !rows->mass) return KVC_ERR_INVALID_ARG;
+  DevInfo info;
+  if ((st = check_device(&info)) != KVC_OK) return st;
+  const size_t need = kvc_i4_evict_workspace_bytes(shape, rows, budget);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return KVC_ERR_WORKSPACE;
+  I4EvictArgs a = {};
+  a.U = static_cast<int32_t>(n_units(shape));
+  a.d = shape->head_dim;
+  a.budget = budget;
+  a.n_sink = n_sink;
+  a.n_recent = n_recent;
+  a.max_moves = budget < rows->capacity ? std::min(budget, rows->capacity - budget) : 0;
+  a.rows = *rows;
+  a.lists = static_cast<int32_t*>(workspace);
+  a.unit_status = unit_status;
+  return launch_i4_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
 size_t kvc_deletion_effect_workspace_bytes(const kvc_shape* shape, int32_t window) {

@@ -200,6 +200,72 @@ struct FlagArgs {
   uint8_t* flags;              // [B][T]
 };
 
+// Score modifiers of the prompt attention and the 4-bit attention.
+struct Mods {
+  float softcap;               // 0 = off
+  const float* slopes;         // optional [H_q]
+  int32_t window;              // 0 = unlimited
+  const int32_t* prefix_len;   // optional [B]
+};
+
+struct PromptArgs {
+  int32_t U, L, Hkv, B, G, d, n_q;
+  int64_t T;
+  float scale;
+  kvc_strides qs, kvs, os;     // element strides
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const int32_t* q_len;        // optional [B]
+  const int32_t* kv_len;       // optional [B]
+  const int32_t* docs;         // optional [B][T]
+  Mods mods;
+  __nv_bfloat16* out;
+  float* lse;                  // optional [B][L][H_q][n_q]
+  int32_t* unit_status;        // optional [U]
+};
+
+struct I4AppendArgs {
+  int32_t U, L, Hkv, d, n;
+  int32_t rows_per_block;
+  kvc_i4_rows rows;
+  kvc_strides st;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const int32_t* n_new;        // optional [B]
+  int32_t* unit_status;        // optional [U]
+};
+
+struct I4ReadArgs {
+  int32_t U, L, Hkv, d, n;
+  int32_t rows_per_block;
+  kvc_i4_rows rows;
+  kvc_strides st;
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+};
+
+struct I4AttnArgs {
+  int32_t U, L, Hkv, B, G, d, n_q;
+  float scale;
+  kvc_i4_rows rows;
+  kvc_strides qs, os;
+  const __nv_bfloat16* q;
+  const int32_t* q_pos;        // optional [B][n_q]
+  Mods mods;
+  __nv_bfloat16* out;
+  float* lse;                  // [B][L][H_q][n_q]: the caller's or the workspace's
+  bool add_mass;
+};
+
+struct I4EvictArgs {
+  int32_t U, d, budget, n_sink, n_recent;
+  int32_t max_moves;           // entries of each list
+  kvc_i4_rows rows;
+  int32_t* lists;              // [U][2][max_moves]: holes, donors
+  int32_t* unit_status;        // optional [U]
+};
+
 // host launchers (each returns a cudaError_t from the launch)
 cudaError_t launch_bonus(const BonusArgs& a, cudaStream_t stream);
 cudaError_t launch_pool(const float* in, float* out, int64_t rows, int64_t n, int kernel, int mode,
@@ -221,6 +287,11 @@ cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_engine(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t stream);
+cudaError_t launch_i4_append(const I4AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_i4_read(const I4ReadArgs& a, cudaStream_t stream);
+cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_i4_evict(const I4EvictArgs& a, cudaStream_t stream);
 size_t effect_smem_bytes(int Rp, int n_stages);
 cudaError_t launch_effect(const EffectArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                           const CUtensorMap& tmap_q, int grid, size_t smem_bytes, cudaStream_t stream);

@@ -12,6 +12,15 @@
  *   kvc_compact_rerotate_quant_ref   the same through a key reference store
  *   kvc_decode_attn             one decode-attention step over the result
  *
+ * and, for the prompt and the tokens around it:
+ *
+ *   kvc_prompt_attn             attention of a prompt (or of single tokens)
+ *                               over a bf16 cache, with score modifiers
+ *   kvc_i4_append, kvc_i4_read  rows into and out of a growing 4-bit cache
+ *   kvc_i4_attn                 attention over the 4-bit cache, which may add
+ *                               the softmax weights to its rows' mass
+ *   kvc_i4_evict                in-place eviction of the rows of least mass
+ *
  * Sources, cited by page title and section:
  *   PASK     "Parser Transitions Already Reveal Structural Responsibility:
  *             KV Persistence for Structured Generation" (arXiv 2608.28276)
@@ -66,7 +75,8 @@ enum {
   KVC_UNIT_OVER_BUDGET = 1, /* forced rows alone exceed the token budget   */
   KVC_UNIT_BAD_INDEX = 2,   /* a kept index or position outside its range */
   KVC_UNIT_BAD_FLAGS = 3,   /* an item flagged both PROTECT and EXCLUDE    */
-  KVC_UNIT_TIMEOUT = 4      /* a bounded device wait gave up (no progress) */
+  KVC_UNIT_TIMEOUT = 4,     /* a bounded device wait gave up (no progress) */
+  KVC_UNIT_FULL = 5         /* appended rows do not fit the rows' capacity */
 };
 
 /* Storage actions of the (tag, layer-group) table: PASK's {R, L, H} with L
@@ -468,6 +478,181 @@ kvc_status kvc_engine_attn(const kvc_shape* shape, const kvc_policy* policy, con
                            const int32_t* kept_count, const kvc_bf16_rows* recent,
                            const kvc_bf16_rows* current, float softmax_scale, void* out,
                            void* workspace, size_t workspace_bytes, kvc_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Score modifiers of kvc_prompt_attn and kvc_i4_attn.  A query at position
+ * p_q of head h scores a key at position p_k
+ *
+ *   x = (q . k) * scale
+ *   x <- softcap tanh(x / softcap)                      if softcap > 0
+ *   x <- x - slopes[h] |p_q - p_k|                      if slopes
+ *
+ * and sees it iff  p_k < prefix_len[b]  or
+ *                  p_k <= p_q and (window == 0 or p_q - p_k < window).
+ *
+ * A NULL kvc_score_mods is all zeros: causal attention.  With prefix_len at
+ * the sequence's length every query sees every key.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  float softcap;             /* finite, >= 0; 0 = off                        */
+  const float* slopes;       /* optional fp32 [H_q]                          */
+  int32_t window;            /* >= 0; 0 = unlimited                          */
+  const int32_t* prefix_len; /* optional int32 [B]                           */
+} kvc_score_mods;
+
+/* Element strides of a bf16 [B][L][H][n][d] tensor whose innermost dimension
+ * is contiguous.  Every stride is a positive multiple of 8 elements (those of
+ * dimensions of size 1 are not looked at), the data 16-byte aligned.  NULL =
+ * dense. */
+typedef struct {
+  int64_t batch, layer, head, token;
+} kvc_strides;
+
+/* ------------------------------------------------------------------------
+ * kvc_prompt_attn -- attention of a prompt, a chunk of one, or single tokens
+ * over a bf16 cache (PASK Eq. 1 with the score modifiers above).
+ *
+ *   out[h][i] = sum_j softmax_j(x_hij) v_j,  row_lse[h][i] = ln sum_j exp(x_hij)
+ *
+ * over the keys j that query i sees.  Sequence b holds kv_len[b] keys, key j
+ * at position j; its q_len[b] queries are the last ones: query i sits at
+ * position kv_len[b] - q_len[b] + i.  fp32 scores, statistics and
+ * accumulation; the weights are rounded to bf16 for the value product; bf16
+ * output.  A query that sees no key outputs 0 and row_lse -inf.
+ *
+ * row_lse of the last `window` queries is what kvc_score takes as row_lse
+ * (without softcap, slopes, window, prefix and documents, which kvc_score
+ * does not apply).
+ *
+ * q        bf16 [B][L][H_q][n_q][d], out alike; k, v bf16 [B][L][H_kv][T][d],
+ *          T = shape->n_tokens; strides as in kvc_strides (k and v share
+ *          theirs).
+ * q_len    optional int32 [B], limited to [0, n_q] (NULL: n_q).  Rows of out
+ *          and row_lse at or past q_len[b] are left as they were.
+ * kv_len   optional int32 [B], limited to [0, T] (NULL: T).  A query whose
+ *          position is negative (q_len > kv_len) sees no key.
+ * docs     optional int32 [B][T]: document of each key; a query (whose
+ *          document is that of its position) sees only keys of the same
+ *          document.  Tokens of a negative document see and are seen by
+ *          nothing.
+ * Rows of k and v at or past kv_len[b] and of negative documents may hold
+ * any bits.  A row that some query sees is finite: a NaN or infinity in one
+ * may also reach queries that do not see it.
+ * row_lse  optional fp32 [B][L][H_q][n_q], dense.
+ * unit_status  optional int32 [U]; KVC_UNIT_TIMEOUT if a device wait gave up
+ *          (its rows are then undefined); untouched otherwise.
+ * workspace >= kvc_prompt_attn_workspace_bytes(shape, n_q, docs != NULL),
+ *          256-byte aligned, contents need not be initialised (may be 0
+ *          bytes: then NULL is accepted).
+ * ---------------------------------------------------------------------- */
+size_t kvc_prompt_attn_workspace_bytes(const kvc_shape* shape, int32_t n_q, int32_t with_docs);
+kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_strides* q_strides,
+                           int32_t n_q, const void* k, const void* v, const kvc_strides* kv_strides,
+                           const int32_t* q_len, const int32_t* kv_len, const int32_t* docs,
+                           const kvc_score_mods* mods, float softmax_scale, void* out,
+                           const kvc_strides* out_strides, float* row_lse, int32_t* unit_status,
+                           void* workspace, size_t workspace_bytes, kvc_stream stream);
+
+/* ------------------------------------------------------------------------
+ * A growing cache held in 4 bits.  Row storage is that of the int4 pool of
+ * kvc_pools (the same codes and scales, so a pool's arrays can be used as
+ * they are); every unit uses its first count[u] rows, in any order.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  void* k;            /* packed int4 [U][capacity][d/2], 16-byte aligned     */
+  void* v;
+  void* k_scale;      /* g32: bf16 [U][capacity][d/32]; row mode: fp16 [U][capacity] */
+  void* v_scale;      /* (scales 16-byte aligned)                            */
+  int32_t* pos;       /* int32 [U][capacity]: position of each row           */
+  float* mass;        /* optional fp32 [U][capacity]: softmax weight it got  */
+  int32_t* count;     /* int32 [U]: rows in use                              */
+  int32_t* next_pos;  /* int32 [U]: position of the next appended row        */
+  int32_t capacity;   /* rows per unit                                       */
+  int32_t quant_mode; /* KVC_QUANT_*                                         */
+} kvc_i4_rows;
+
+/* ------------------------------------------------------------------------
+ * kvc_i4_append -- quantises new rows (as the int4 pool of
+ * kvc_compact_rerotate_quant does) into slots count[u].. of every unit, at
+ * positions next_pos[u].., with mass 0, and advances count and next_pos.
+ *
+ * k, v       bf16 [B][L][H_kv][n][d] (keys rotated at their positions), with
+ *            strides as in kvc_strides.  Rows are finite.
+ * n_new      optional int32 [B], limited to [0, n]: rows of each sequence
+ *            (NULL: n).
+ * unit_status  optional int32 [U], only errors are written: KVC_UNIT_FULL if
+ *            the rows do not fit, KVC_UNIT_BAD_INDEX if count[u] is outside
+ *            [0, capacity]; such a unit is left as it was.
+ * shape->n_tokens is not read by the kvc_i4 calls.
+ * ---------------------------------------------------------------------- */
+kvc_status kvc_i4_append(const kvc_shape* shape, const kvc_i4_rows* rows, const void* k,
+                         const void* v, const kvc_strides* strides, int32_t n, const int32_t* n_new,
+                         int32_t* unit_status, kvc_stream stream);
+
+/* ------------------------------------------------------------------------
+ * kvc_i4_read -- rows 0 .. n-1 of every unit as bf16 (code * scale, rounded
+ * once), for calls that read a bf16 cache (kvc_score).  k_out, v_out bf16
+ * [B][L][H_kv][n][d] with strides as in kvc_strides; rows at or past count[u]
+ * are left as they were.  n <= capacity.
+ * ---------------------------------------------------------------------- */
+kvc_status kvc_i4_read(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t n, void* k_out,
+                       void* v_out, const kvc_strides* strides, kvc_stream stream);
+
+/* ------------------------------------------------------------------------
+ * kvc_i4_attn -- attention over the rows of a 4-bit cache, dequantised inside
+ * the kernel (x = code * scale), with the score modifiers above; for single
+ * tokens, several tokens at once or a chunk.
+ *
+ * q        bf16 [B][L][H_q][n_q][d], out alike; strides as in kvc_strides.
+ * q_pos    optional int32 [B][n_q] (NULL: the n_q tokens appended last, query
+ *          i of unit u at position next_pos[u] - n_q + i).
+ * mods     as above, with the rows' own positions; prefix_len [B].
+ * KVC_ATTN_ADD_MASS: mass[u][r] += the sum over the unit's G heads and n_q
+ *          queries of their softmax weight on row r, for every row in use
+ *          (PACE Sec. 2: H2O's cumulative score; rows->mass is required).
+ * row_lse  optional fp32 [B][L][H_q][n_q], dense: natural-log log-sum-exps.
+ * fp32 scores, statistics and accumulation; the weights (times the value
+ * scales) are rounded to bf16 for the value product, not for the mass; bf16
+ * output.  A query that sees no row outputs 0 and row_lse -inf.
+ * workspace >= kvc_i4_attn_workspace_bytes(...), 256-byte aligned, contents
+ *          need not be initialised (may be 0 bytes: then NULL is accepted).
+ * ---------------------------------------------------------------------- */
+enum { KVC_ATTN_ADD_MASS = 1 };
+
+size_t kvc_i4_attn_workspace_bytes(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t n_q,
+                                   uint32_t flags);
+kvc_status kvc_i4_attn(const kvc_shape* shape, const kvc_i4_rows* rows, const void* q,
+                       const kvc_strides* q_strides, int32_t n_q, const int32_t* q_pos,
+                       const kvc_score_mods* mods, float softmax_scale, uint32_t flags, void* out,
+                       const kvc_strides* out_strides, float* row_lse, void* workspace,
+                       size_t workspace_bytes, kvc_stream stream);
+
+/* ------------------------------------------------------------------------
+ * kvc_i4_evict -- evicts, in place, the count[u] - budget rows of least mass
+ * of every unit that holds more than `budget` rows (H2O retention, PACE
+ * Sec. 2, with the accumulated weight that kvc_i4_attn leaves).
+ *
+ * Rows with pos < n_sink or pos >= next_pos[u] - n_recent stay.  Of the
+ * others those leave first that have the least mass (NaN counts as -inf, -0
+ * as +0), of equal mass the later position (kvc_select's order: ties keep
+ * the lower index).  Nothing moves but what has to: the slots below `budget`
+ * that lost their row take, in ascending order, the remaining rows from
+ * slots at or past it, in ascending order, with their positions and mass;
+ * count[u] becomes budget.  Slots at or past the new count are left as they
+ * were.  Positions are unique within a unit (of rows that share one the
+ * lower slot leaves first).
+ *
+ * budget >= 1.  unit_status optional int32 [U], only errors are written:
+ * KVC_UNIT_OVER_BUDGET if the rows that have to stay exceed the budget,
+ * KVC_UNIT_BAD_INDEX if count[u] is outside [0, capacity]; such a unit is
+ * left as it was.
+ * workspace >= kvc_i4_evict_workspace_bytes(...), 256-byte aligned, contents
+ * need not be initialised (may be 0 bytes: then NULL is accepted).
+ * ---------------------------------------------------------------------- */
+size_t kvc_i4_evict_workspace_bytes(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t budget);
+kvc_status kvc_i4_evict(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t budget,
+                        int32_t n_sink, int32_t n_recent, int32_t* unit_status, void* workspace,
+                        size_t workspace_bytes, kvc_stream stream);
 
 /* ------------------------------------------------------------------------
  * CommitKV lifecycle-aware retirement ("CommitKV: Lifecycle-Aware KV Cache
