@@ -370,6 +370,60 @@ kvc_status check_queries(const kvc_shape* s, int64_t n_q) {
   return n_q * (s->n_q_heads / s->n_kv_heads) > (1 << 30) ? KVC_ERR_UNSUPPORTED : KVC_OK;
 }
 
+struct PromptPlan {
+  int32_t n_tiles = 0, block_rows = 0, n_blocks = 0, splits = 1;
+  size_t ws_docs = 0, ws_ml = 0, ws_total = 0;
+};
+
+kvc_status plan_prompt(const kvc_shape* s, int32_t n_q, bool with_docs, PromptPlan* p) {
+  kvc_status st = check_shape(s);
+  if (st != KVC_OK) return st;
+  if ((st = check_queries(s, n_q)) != KVC_OK) return st;
+  if (s->n_tokens > 0x7fffff00LL) return KVC_ERR_UNSUPPORTED;        // tile ends within 31 bits
+  DevInfo info;
+  if ((st = check_device(&info)) != KVC_OK) return st;
+  const int64_t U = n_units(s), rows = static_cast<int64_t>(n_q) * (s->n_q_heads / s->n_kv_heads);
+  p->n_tiles = static_cast<int32_t>((s->n_tokens + kTileTokens - 1) / kTileTokens);
+  // two row tiles per item share the key tiles; one row tile per item where
+  // that is all there is or where pairs would leave SMs idle
+  p->block_rows = rows > 128 && U * ((rows + 255) / 256) >= info.sms ? 256 : 128;
+  p->n_blocks = static_cast<int32_t>((rows + p->block_rows - 1) / p->block_rows);
+  const int64_t items = U * p->n_blocks;
+  if (items > (1 << 28)) return KVC_ERR_UNSUPPORTED;
+  if (items < 2LL * info.sms) {
+    // several CTAs per SM's worth of items, so that ragged lengths even out;
+    // a split keeps at least 8 key tiles
+    const int64_t want = std::min<int64_t>((4LL * info.sms + items - 1) / items, p->n_tiles / 8);
+    p->splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(want, 256)));
+  }
+  if (with_docs) p->ws_docs = (static_cast<size_t>(s->batch) * p->n_tiles * sizeof(int2) + 255) / 256 * 256;
+  p->ws_total = p->ws_docs;
+  if (p->splits > 1) {
+    const size_t parts = static_cast<size_t>(U) * rows * p->splits;
+    p->ws_ml = (parts * sizeof(float2) + 255) / 256 * 256;
+    p->ws_total += p->ws_ml + parts * s->head_dim * sizeof(float);
+  }
+  return KVC_OK;
+}
+
+// [B][L][H][n][d] bf16 tensor as (d, n, H, L, B) in boxes of 64 x 128 rows.
+kvc_status encode_rows(CUtensorMap* map, const void* ptr, const kvc_shape* s, int64_t heads, int64_t n,
+                       const kvc_strides& st) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return KVC_ERR_CUDA;
+  cuuint64_t dims[5] = {static_cast<cuuint64_t>(s->head_dim), static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(s->n_layers), static_cast<cuuint64_t>(s->batch)};
+  const int64_t given[4] = {st.token, st.head, st.layer, st.batch};
+  cuuint64_t strides[4];
+  for (int i = 0; i < 4; ++i) strides[i] = given[i] > 0 ? given[i] * 2 : s->head_dim * 2;   // 0: a dimension of size 1
+  cuuint32_t box[5] = {64, kTileTokens, 1, 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? KVC_OK : KVC_ERR_CUDA;
+}
+
 size_t i4_attn_lse_bytes(const kvc_shape* s, int64_t n_q) {
   return static_cast<size_t>(s->batch) * s->n_layers * s->n_q_heads * n_q * sizeof(float);
 }
@@ -877,9 +931,8 @@ kvc_status kvc_engine_attn(const kvc_shape* shape, const kvc_policy* policy, con
 }
 
 size_t kvc_prompt_attn_workspace_bytes(const kvc_shape* shape, int32_t n_q, int32_t with_docs) {
-  (void)with_docs;
-  if (check_shape(shape) != KVC_OK || check_queries(shape, n_q) != KVC_OK) return 0;
-  return 0;
+  PromptPlan p;
+  return plan_prompt(shape, n_q, with_docs != 0, &p) == KVC_OK ? p.ws_total : 0;
 }
 
 kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_strides* q_strides,
@@ -898,9 +951,9 @@ kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_stri
   if ((st = tensor_strides(shape, shape->n_kv_heads, shape->n_tokens, kv_strides, &a.kvs)) != KVC_OK) return st;
   if ((st = tensor_strides(shape, shape->n_q_heads, n_q, out_strides, &a.os)) != KVC_OK) return st;
   if ((st = check_mods(mods, &a.mods)) != KVC_OK) return st;
-  DevInfo info;
-  if ((st = check_device(&info)) != KVC_OK) return st;
-  const size_t need = kvc_prompt_attn_workspace_bytes(shape, n_q, docs != nullptr);
+  PromptPlan p;
+  if ((st = plan_prompt(shape, n_q, docs != nullptr, &p)) != KVC_OK) return st;
+  const size_t need = p.ws_total;
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return KVC_ERR_WORKSPACE;
   if (!(softmax_scale > 0.f)) softmax_scale = 1.0f / sqrtf(static_cast<float>(shape->head_dim));
   a.U = static_cast<int32_t>(n_units(shape));
@@ -921,7 +974,20 @@ kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_stri
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = row_lse;
   a.unit_status = unit_status;
-  return launch_prompt(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+  a.n_tiles = p.n_tiles;
+  a.block_rows = p.block_rows;
+  a.n_blocks = p.n_blocks;
+  a.splits = p.splits;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (docs) a.doc_tiles = reinterpret_cast<int2*>(ws);
+  if (p.splits > 1) {
+    a.part_ml = reinterpret_cast<float2*>(ws + p.ws_docs);
+    a.part_o = reinterpret_cast<float*>(ws + p.ws_docs + p.ws_ml);
+  }
+  CUtensorMap mk, mv;
+  if ((st = encode_rows(&mk, k, shape, shape->n_kv_heads, shape->n_tokens, a.kvs)) != KVC_OK) return st;
+  if ((st = encode_rows(&mv, v, shape, shape->n_kv_heads, shape->n_tokens, a.kvs)) != KVC_OK) return st;
+  return launch_prompt(a, mk, mv, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
 kvc_status kvc_i4_append(const kvc_shape* shape, const kvc_i4_rows* rows, const void* k,

@@ -223,6 +223,13 @@ struct PromptArgs {
   __nv_bfloat16* out;
   float* lse;                  // optional [B][L][H_q][n_q]
   int32_t* unit_status;        // optional [U]
+  int32_t n_tiles;             // key tiles of T
+  int32_t block_rows;          // packed rows per item: 128 or 256
+  int32_t n_blocks;            // items per unit
+  int32_t splits;              // CTAs that share an item's keys
+  float* part_o;               // splits > 1: [U][n_q G][splits][d] unnormalised outputs
+  float2* part_ml;             // [U][n_q G][splits] (log2-domain maximum, sum)
+  int2* doc_tiles;             // with docs: [B][n_tiles] (min, max) document
 };
 
 struct I4AppendArgs {
@@ -287,7 +294,8 @@ cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_engine(const DecodeArgs& a, cudaStream_t stream);
-cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t stream);
+size_t prompt_smem_bytes(int d);
+cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream);
 cudaError_t launch_i4_append(const I4AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_read(const I4ReadArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream);

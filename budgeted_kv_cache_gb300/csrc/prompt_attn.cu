@@ -1,67 +1,764 @@
 // Attention of a prompt, a chunk of one or single tokens over a bf16 cache
 // (PASK Eq. 1) with score modifiers, documents and a prefix.
-#include "attn_rows.cuh"
+//
+// Rows.  The G heads that share a KV head are packed: row r of a unit is
+// query r / G of head r % G, so one read of a key tile serves all of them and
+// a single token fills G rows of a tile instead of one.
+//
+// One CTA per SM works on one item: a block of 256 rows of a unit (two tiles
+// of 128 that share every key and value tile) or, where that leaves SMs idle
+// or the unit has no more, of 128 rows, whose two streams take the key tiles
+// in turn.  Either way two streams run against each other on the tensor core:
+// while the warps of one turn scores into weights, the other's products run.
+// Per step of a stream
+//   S = Q K^T      tcgen05, operands in shared memory, S in tensor memory
+//   softmax        128 threads, one row each: S to registers, running maximum
+//                  and sum (base 2), P = 2^(y - m) rounded to bf16 and stored
+//                  over S in tensor memory; the accumulator is rescaled only
+//                  when the maximum grew by more than 2^8 (P then stays below
+//                  2^8 and every sum in fp32), which a row does a few times
+//   O += P V       tcgen05, P from tensor memory, V read as an MN-major
+//                  operand straight from its TMA tile
+// Few rows: the keys of an item are split over CTAs and the partial (m, l, O)
+// joined by PASK Eq. 15 in a second kernel.
+//
+// Masks.  An item walks only key tiles that some of its rows see; a tile that
+// every row of a warp sees whole takes no mask.  Values of keys that no row of
+// the item sees are zeroed in shared memory (0 x NaN is NaN in a product).
+//
+// Warp roles (12 warps): 0-3 and 4-7 softmax of stream 0 and 1 (a row of 128
+// scores per thread in registers: their warpgroups take 208 registers a
+// thread, the third gives them up and keeps 88; 2 x 208 + 88 = 3 x 168, what
+// the block was launched with), 8 TMA producer, 9 TMEM owner and MMA issuer.  Every wait is bounded; one that
+// gives up raises a shared abort flag, the unit is marked KVC_UNIT_TIMEOUT
+// and the CTA drains its copies and MMAs before it frees tensor memory.
+#include <algorithm>
+
+#include "kvc_internal.cuh"
 
 namespace kvc {
 
 namespace {
 
-struct PromptSrc {
-  const PromptArgs& a;
-  int b, l, g;
-  int nq, first;              // queries, position of query 0
-  int64_t nk, prefix;
-  __device__ PromptSrc(const PromptArgs& a_, int u) : a(a_) {
-    b = u / (a.L * a.Hkv), l = u / a.Hkv % a.L, g = u % a.Hkv;
-    nk = a.kv_len ? max(0, min(static_cast<int>(a.T), a.kv_len[b])) : a.T;
-    nq = a.q_len ? clamp_count(a.q_len[b], a.n_q) : a.n_q;
-    first = static_cast<int>(nk) - nq;
-    prefix = a.mods.prefix_len ? a.mods.prefix_len[b] : 0;
+constexpr int kThreads = 384;                    // three warpgroups of 168 registers a thread at launch
+constexpr int kTileRows = 128;
+constexpr int kKeys = 128;                       // keys per tile
+constexpr int kChunkBytes = 128 * 128;           // 128 rows x 64 bf16, 128-byte swizzle
+constexpr uint32_t kTmemCols = 512;              // S0, S1, O0, O1 of 128 columns each
+constexpr uint32_t kOCol = 256;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.f;                     // log2 growth of the maximum that forces a rescale
+
+template <int D>
+struct Cfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kTile = kChunks * kChunkBytes;          // a Q, K or V tile
+  static constexpr int kNk = D == 128 ? 2 : 4, kNv = D == 128 ? 3 : 4;
+  static constexpr int kSmem = (2 + kNk + kNv) * kTile + 1024 /* alignment */ + 512;
+};
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A bf16, two elements of K per column.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// mbar_wait by a whole warp, with one answer for all lanes (what follows is
+// executed by the warp together).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
+// Bounded wait that goes on after an abort: for copies and products in flight.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return;
   }
-  __device__ int rows() const { return nq * a.G; }
-  __device__ int64_t keys() const { return nk; }
-  __device__ float query(int r, int c) const {
-    return __bfloat162float(a.q[b * a.qs.batch + l * a.qs.layer + (g * a.G + r % a.G) * a.qs.head +
-                                (r / a.G) * a.qs.token + c]);
+}
+
+// Descriptor of an MN-major operand in 128-byte swizzle: 64 elements along N
+// per 128-byte row, rows along K, 8 rows 1024 bytes, the next 64 elements
+// along N kChunkBytes further.
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(kChunkBytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Bits [lo, hi) of a 32-bit word, either end outside it allowed.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 32);
+  if (lo >= hi) return 0u;
+  return (0xffffffffu >> (32 - (hi - lo))) << lo;
+}
+
+// What an item covers.
+struct Item {
+  int u, b, l, g, split;
+  int row0, rows;              // first packed row, packed rows of the item (<= 256)
+  int nk, first, pre;          // keys, position of query 0, visible prefix
+  int lo, hi;                  // keys [lo, hi) are seen through the causal window by some row
+  int n, skip_at, skip;        // tiles to walk: index i is tile i, or i + skip from skip_at on
+  int i0, i1;                  // indices of this split
+};
+
+__device__ __forceinline__ Item make_item(const PromptArgs& a, int id) {
+  Item t;
+  t.split = id % a.splits;
+  id /= a.splits;
+  t.u = id % a.U;
+  const int qb = a.n_blocks - 1 - id / a.U;      // long rows first: the causal tail fills the gaps
+  t.b = t.u / (a.L * a.Hkv), t.l = t.u / a.Hkv % a.L, t.g = t.u % a.Hkv;
+  t.nk = a.kv_len ? max(0, min(static_cast<int>(a.T), a.kv_len[t.b])) : static_cast<int>(a.T);
+  const int nq = a.q_len ? clamp_count(a.q_len[t.b], a.n_q) : a.n_q;
+  t.first = t.nk - nq;
+  t.row0 = qb * a.block_rows;
+  t.rows = min(a.block_rows, nq * a.G - t.row0);
+  t.pre = a.mods.prefix_len ? max(0, min(t.nk, a.mods.prefix_len[t.b])) : 0;
+  if (t.rows <= 0) {
+    t.rows = t.lo = t.hi = t.n = t.skip = t.skip_at = t.i0 = t.i1 = 0;
+    return t;
   }
-  __device__ int64_t at(int64_t j) const { return b * a.kvs.batch + l * a.kvs.layer + g * a.kvs.head + j * a.kvs.token; }
-  __device__ bool dead(int64_t j) const { return a.docs && a.docs[b * a.T + j] < 0; }
-  __device__ float key(int64_t j, int c) const { return dead(j) ? 0.f : __bfloat162float(a.k[at(j) + c]); }
-  __device__ float value(int64_t j, int c) const { return dead(j) ? 0.f : __bfloat162float(a.v[at(j) + c]); }
-  __device__ float score(int r, int64_t j, float x) const {
-    const int64_t p = first + r / a.G;
-    if (p < 0 || !sees(p, j, a.mods.window, prefix)) return -INFINITY;
-    if (a.docs) {
-      const int32_t doc = a.docs[b * a.T + j];
-      if (doc < 0 || doc != a.docs[b * a.T + p]) return -INFINITY;
+  const int p_min = t.first + t.row0 / a.G, p_max = t.first + (t.row0 + t.rows - 1) / a.G;
+  t.hi = max(0, p_max + 1);
+  t.lo = a.mods.window && p_min >= a.mods.window ? p_min - a.mods.window + 1 : 0;
+  t.lo = min(t.lo, t.hi);
+  if (p_max < 0) t.pre = 0;
+  const int pre_tiles = (t.pre + kKeys - 1) / kKeys;
+  const int lo_tile = t.lo / kKeys, hi_tile = (t.hi + kKeys - 1) / kKeys;
+  t.skip_at = pre_tiles;
+  t.skip = max(0, lo_tile - pre_tiles);
+  t.n = max(pre_tiles, hi_tile) - t.skip;
+  if (hi_tile <= lo_tile) t.n = pre_tiles, t.skip = 0;
+  t.i0 = static_cast<int>(static_cast<int64_t>(t.n) * t.split / a.splits);
+  t.i1 = static_cast<int>(static_cast<int64_t>(t.n) * (t.split + 1) / a.splits);
+  return t;
+}
+
+// The tiles of an item that may be seen, in order; every lane of the warp
+// calls next() together.
+struct TileWalk {
+  const Item& t;
+  const int2* table;           // [tiles] (min, max) document of each key tile, or null
+  int q_min, q_max;            // documents of the item's queries
+  int at, base;
+  uint32_t mask;
+  __device__ TileWalk(const Item& t_, const int2* table_, int q_min_, int q_max_)
+      : t(t_), table(table_), q_min(q_min_), q_max(q_max_), at(t_.i0), base(0), mask(0) {}
+  __device__ __forceinline__ int tile(int i) const { return i + (i >= t.skip_at ? t.skip : 0); }
+  __device__ __forceinline__ int next() {
+    if (!table) return at < t.i1 ? tile(at++) : -1;
+#pragma unroll 1
+    while (mask == 0) {
+      if (at >= t.i1) return -1;
+      const int i = at + (threadIdx.x & 31);
+      bool ok = false;
+      if (i < t.i1) {
+        const int2 d = __ldg(table + tile(i));
+        ok = d.y >= q_min && d.x <= q_max;
+      }
+      mask = __ballot_sync(0xffffffffu, ok);
+      base = at;
+      at += 32;
     }
-    return mod_score(x * a.scale, a.mods.softcap, a.mods.slopes ? a.mods.slopes[g * a.G + r % a.G] : 0.f,
-                     static_cast<float>(p - j));
-  }
-  __device__ void store(int r, int c, float x) const {
-    a.out[b * a.os.batch + l * a.os.layer + (g * a.G + r % a.G) * a.os.head + (r / a.G) * a.os.token + c] =
-        __float2bfloat16_rn(x);
-  }
-  __device__ void store_lse(int r, float x) const {
-    if (a.lse) a.lse[((static_cast<int64_t>(b) * a.L + l) * (a.Hkv * a.G) + g * a.G + r % a.G) * a.n_q + r / a.G] = x;
+    const int i = base + __ffs(mask) - 1;
+    mask &= mask - 1;
+    return tile(i);
   }
 };
 
+struct Bars {
+  uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
+  uint64_t sfull[2], pfull[2], odone[2], qfull, done;
+  uint32_t tmem;
+  int abort_flag;
+  int q_min, q_max;
+};
+
+// D: head dimension.  MODS: a cap or slopes (the logits are transformed
+// before the softmax).
+template <int D, bool MODS>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sq = base;                                  // two Q tiles
+  uint8_t* sk = sq + 2 * C::kTile;
+  uint8_t* sv = sk + C::kNk * C::kTile;
+  Bars& s = *reinterpret_cast<Bars*>(sv + C::kNv * C::kTile);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &s.abort_flag;
+  const Item t = make_item(a, blockIdx.x);
+  if (t.rows == 0) return;                             // rows past the sequence's queries
+  const bool share = t.rows > kTileRows;               // two Q tiles, or two streams over one
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&s.kfull[i]), 1);
+      mbar_init(smem_u32(&s.kempty[i]), 1);
+      mbar_init(smem_u32(&s.vfull[i]), 1);
+      mbar_init(smem_u32(&s.vempty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.sfull[i]), 1);
+      mbar_init(smem_u32(&s.pfull[i]), 4);
+      mbar_init(smem_u32(&s.odone[i]), 1);
+    }
+    mbar_init(smem_u32(&s.qfull), 8);
+    mbar_init(smem_u32(&s.done), 1);
+    s.abort_flag = 0;
+    s.q_min = INT32_MAX;
+    s.q_max = -1;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&s.tmem), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem;
+  const int32_t* docs = a.docs ? a.docs + static_cast<int64_t>(t.b) * a.T : nullptr;
+  const int2* table = a.docs ? a.doc_tiles + static_cast<int64_t>(t.b) * a.n_tiles : nullptr;
+
+  // Q tiles (softmax warps, one row per thread) and the documents of their positions
+  if (warp < 8) {
+    const int tile = warp >> 2, r = threadIdx.x & 127;
+    const int row = tile * kTileRows + r;
+    if (tile == 0 || share) {
+      uint8_t* dst = sq + tile * C::kTile + r * 128;
+      const bool ok = row < t.rows;
+      const int pr = t.row0 + (ok ? row : 0);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + t.b * a.qs.batch + t.l * a.qs.layer + static_cast<int64_t>(t.g * a.G + pr % a.G) * a.qs.head +
+          static_cast<int64_t>(pr / a.G) * a.qs.token);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 w = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * kChunkBytes + (((c & 7) ^ (r & 7)) << 4)) = w;
+      }
+      if (docs && ok) {
+        const int p = t.first + pr / a.G;
+        const int doc = p >= 0 ? __ldg(docs + p) : -1;
+        if (doc >= 0) {
+          atomicMin(&s.q_min, doc);
+          atomicMax(&s.q_max, doc);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&s.qfull));
+  }
+  if (docs) __syncthreads();
+  const int q_min = docs ? s.q_min : 0, q_max = docs ? s.q_max : 0;
+
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == kLoadWarp) {
+    // -------------------------------------------------------------- TMA producer: K(i + 1) before V(i)
+    if (lane == 0) {
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+    }
+    TileWalk walk(t, table, q_min, q_max);
+    auto load = [&](const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty, uint32_t n, int i,
+                    int tile) -> bool {
+      const uint32_t st = i % n, ph = (i / n) & 1;
+      if (!warp_wait(smem_u32(&empty[st]), ph ^ 1, abort_flag)) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(smem_u32(&full[st]), C::kTile);
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_load_5d(smem_u32(ring + st * C::kTile + c * kChunkBytes), map, smem_u32(&full[st]), c * 64, tile * kKeys,
+                      t.g, t.l, t.b);
+      }
+      __syncwarp();
+      return true;
+    };
+    int nk = 0, nv = 0;
+    int cur = walk.next();
+    bool ok = cur < 0 || load(&map_k, sk, s.kfull, s.kempty, C::kNk, nk++, cur);
+    if (cur < 0 || !ok) nk = 0;
+    while (cur >= 0 && ok) {
+      const int nxt = walk.next();
+      if (nxt >= 0) {
+        if (!(ok = load(&map_k, sk, s.kfull, s.kempty, C::kNk, nk, nxt))) break;
+        ++nk;
+      }
+      if (!(ok = load(&map_v, sv, s.vfull, s.vempty, C::kNv, nv, cur))) break;
+      ++nv;
+      cur = nxt;
+    }
+    // every copy issued above lands before the CTA exits
+    for (int i = max(0, nk - C::kNk); i < nk; ++i)
+      drain(smem_u32(&s.kfull[i % C::kNk]), (i / C::kNk) & 1);
+    for (int i = max(0, nv - C::kNv); i < nv; ++i)
+      drain(smem_u32(&s.vfull[i % C::kNv]), (i / C::kNv) & 1);
+  } else if (warp == kMmaWarp) {
+    // -------------------------------------------------------------- MMA issuer
+    const uint32_t idesc_s = mma_idesc_bf16(128, kKeys);
+    const uint32_t idesc_o = mma_idesc_bf16(128, D) | (1u << 16);     // B (values) MN-major
+    TileWalk walk(t, table, q_min, q_max), walk_v(t, table, q_min, q_max);
+    bool ok = warp_wait(smem_u32(&s.qfull), 0, abort_flag);
+    int n_k = 0, n_v = 0;                // K and V tiles taken up
+    bool k_more = true;
+    // the scores of step x (stream x & 1); false when there is no such step
+    auto scores = [&](int x) -> bool {
+      const int h = x & 1;
+      const bool fresh = !share || h == 0;
+      if (fresh) {
+        if (!k_more || walk.next() < 0) return k_more = false;
+        const uint32_t st = n_k % C::kNk;
+        if (!warp_wait(smem_u32(&s.kfull[st]), (n_k / C::kNk) & 1, abort_flag)) return ok = false;
+        ++n_k;
+      } else if (!k_more) {
+        return false;
+      }
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t st = (n_k - 1) % C::kNk;
+        const uint64_t qd = sw128_desc(smem_u32(sq + (share ? h : 0) * C::kTile));
+        const uint64_t kd = sw128_desc(smem_u32(sk + st * C::kTile));
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * (kChunkBytes >> 4) + (ks & 3) * 2;
+          tc_mma_bf16(tmem + h * 128, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u);
+        }
+        tc_commit(smem_u32(&s.sfull[h]));
+        if (!share || h == 1) tc_commit(smem_u32(&s.kempty[st]));
+      }
+      __syncwarp();
+      return true;
+    };
+    auto values = [&](int x) -> bool {
+      const int h = x & 1;
+      if (!share || h == 0) {
+        const int j0 = walk_v.next() * kKeys;
+        const uint32_t st = n_v % C::kNv;
+        if (!warp_wait(smem_u32(&s.vfull[st]), (n_v / C::kNv) & 1, abort_flag)) return false;
+        ++n_v;
+        // values of keys that no row of the item sees become zeros
+        bool live = j0 + kKeys <= t.nk && (j0 + kKeys <= t.pre || (j0 >= t.lo && j0 + kKeys <= t.hi));
+        if (docs) live = live && __ldg(table + j0 / kKeys).x >= 0;
+        if (!live) {
+#pragma unroll 1
+          for (int c = lane; c < kKeys; c += 32) {
+            const int j = j0 + c;
+            const bool keep = j < t.nk && (j < t.pre || (j >= t.lo && j < t.hi)) && (!docs || __ldg(docs + j) >= 0);
+            if (!keep) {
+              uint4* row = reinterpret_cast<uint4*>(sv + st * C::kTile + c * 128);
+              for (int k = 0; k < C::kChunks; ++k)
+                for (int i = 0; i < 8; ++i) row[k * (kChunkBytes / 16) + i] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
+      if (!warp_wait(smem_u32(&s.pfull[h]), (x >> 1) & 1, abort_flag)) return false;
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t st = (n_v - 1) % C::kNv;
+        const uint64_t vd = v_desc(smem_u32(sv + st * C::kTile));
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks)
+          tc_mma_ts(tmem + kOCol + h * 128, tmem + h * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o,
+                    (x > 1 || ks > 0) ? 1u : 0u);
+        tc_commit(smem_u32(&s.odone[h]));
+        if (!share || h == 1) tc_commit(smem_u32(&s.vempty[st]));
+      }
+      __syncwarp();
+      return true;
+    };
+    if (ok) {
+      int issued = 0;
+      while (issued < 2 && scores(issued)) ++issued;
+      for (int x = 0; ok && x < issued; ++x) {
+        if (!(ok = values(x))) break;
+        if (issued == x + 2 && scores(issued)) ++issued;
+      }
+    }
+    // all MMAs issued above complete before tensor memory is freed
+    if (lane == 0) tc_commit(smem_u32(&s.done));
+    __syncwarp();
+    drain(smem_u32(&s.done), 0);
+  } else if (warp < 8) {
+    // -------------------------------------------------------------- softmax
+    const int h = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const int row = (share ? h * kTileRows : 0) + r;
+    const bool valid = row < t.rows;
+    const int pr = t.row0 + (valid ? row : 0);
+    const int p = t.first + pr / a.G;
+    const int head = t.g * a.G + pr % a.G;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_col = tmem + lanes + h * 128, o_col = tmem + lanes + kOCol + h * 128;
+    const bool warp_valid = __any_sync(0xffffffffu, valid);
+    // keys of this row: [row_lo, row_hi) and [0, row_pre)
+    int row_hi = min(p + 1, t.nk), row_lo = a.mods.window && p >= a.mods.window ? p - a.mods.window + 1 : 0;
+    int row_pre = t.pre;
+    int my_doc = 0;
+    if (docs) my_doc = p >= 0 && p < t.nk ? __ldg(docs + p) : -1;
+    if (p < 0 || my_doc < 0) row_hi = row_lo = row_pre = 0;
+    const float cs = MODS ? 1.f : a.scale * kLog2e;
+    const float cap = a.mods.softcap;
+    const float zs = MODS && cap > 0.f ? 2.f * kLog2e * a.scale / cap : 0.f;      // tanh argument x 2 log2 e
+    const float slope2 = MODS && a.mods.slopes ? a.mods.slopes[head] * kLog2e : 0.f;
+    float m = -INFINITY, l = 0.f;              // reference maximum (of y / cs) and sum of 2^(y - m cs)
+    TileWalk walk(t, table, q_min, q_max);
+    int n = 0;                                 // tiles of this stream
+    bool fail = false;
+    for (int i = 0;; ++i) {
+      const int tile = walk.next();
+      if (tile < 0) break;
+      if (!share && (i & 1) != h) continue;
+      if (!warp_wait(smem_u32(&s.sfull[h]), n & 1, abort_flag)) {
+        fail = true;
+        break;
+      }
+      ++n;
+      tc_fence_after();
+      if (!warp_valid) {                       // nothing of this warp is a row: the product's result is not read
+        tc_fence_before();
+        if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h]));
+        continue;
+      }
+      uint32_t sr[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32_issue(s_col + c * 32, sr[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
+      float (&y)[4][32] = reinterpret_cast<float (&)[4][32]>(sr);
+      const int j0 = tile * kKeys;
+      if constexpr (MODS) {
+        const float far = static_cast<float>(p - j0);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float x = y[c][e];
+            if (cap > 0.f) {
+              // cap tanh(z) = cap (1 - 2 / (1 + e^2z)): right at both infinities
+              const float ez = ex2_approx(x * zs);
+              x = fmaf(-2.f * cap, __frcp_rn(1.f + ez), cap) * kLog2e;
+            } else {
+              x *= a.scale * kLog2e;
+            }
+            y[c][e] = fmaf(-slope2, fabsf(far - static_cast<float>(c * 32 + e)), x);
+          }
+      }
+      // masks, unless every row of the warp sees the whole tile
+      bool whole = j0 + kKeys <= row_pre || (j0 >= row_lo && j0 + kKeys <= row_hi);
+      bool same = true;
+      if (docs) {
+        const int2 d = __ldg(table + tile);
+        same = d.x == d.y && d.x == my_doc;
+      }
+      if (!__all_sync(0xffffffffu, (whole && same) || !valid)) {
+        const bool by_doc = !__all_sync(0xffffffffu, same || !valid);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int jc = j0 + c * 32;
+          uint32_t bits = bit_range(row_lo - jc, row_hi - jc) | bit_range(0, row_pre - jc);
+          if (by_doc) {
+            uint32_t eq = 0;
+#pragma unroll 8
+            for (int e = 0; e < 32; ++e)
+              eq |= (jc + e < t.nk && __ldg(docs + jc + e) == my_doc ? 1u : 0u) << e;
+            bits &= eq;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(bits & (1u << e))) y[c][e] = -INFINITY;
+        }
+      }
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mx[c] = fmaxf(y[c][0], y[c][1]);
+#pragma unroll
+        for (int e = 2; e < 32; e += 2) mx[c] = fmaxf(mx[c], fmaxf(y[c][e], y[c][e + 1]));
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const bool grow = (top - m) * cs > kGrow;          // also from -inf
+      if (__any_sync(0xffffffffu, grow)) {
+        float f = 1.f;
+        if (grow) {
+          f = m == -INFINITY ? 0.f : ex2_approx((m - top) * cs);
+          m = top;
+          l *= f;
+        }
+        if (n > 1) {
+          if (!warp_wait(smem_u32(&s.odone[h]), n & 1, abort_flag)) {     // the product of tile n - 2
+            fail = true;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32_issue(o_col + c * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(o_col + c * 32, o);
+          }
+        }
+      }
+      const float sub = m == -INFINITY ? 0.f : m * cs;
+      float sum[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        sum[c] = 0.f;
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float p0 = ex2_approx(fmaf(y[c][e], cs, -sub)), p1 = ex2_approx(fmaf(y[c][e + 1], cs, -sub));
+          sum[c] += p0 + p1;
+          pk[e / 2] = pack_bf16x2(p0, p1);
+        }
+        tmem_st16(s_col + c * 16, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h]));
+    }
+    // the last product of this stream
+    if (!fail && n > 0 && !warp_wait(smem_u32(&s.odone[h]), (n - 1) & 1, abort_flag)) fail = true;
+    tc_fence_after();
+    float m2 = m == -INFINITY ? -INFINITY : m * cs;
+    if (!share) {
+      // two streams over one set of rows: stream 1 hands over through shared memory (the rings are empty by
+      // now: every tile was consumed by a product that has completed, of this stream or, below, the other)
+      float* box = reinterpret_cast<float*>(sk) + r * (D + 4);
+      if (named_bar_or(1, 256, fail)) fail = true;           // both streams' products are done
+      if (h == 1 && !fail && warp_valid) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32_issue(o_col + c * 32, o);
+            tmem_ld_wait(o);
+          }
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(box + 4 + c * 32 + e) =
+                  n > 0 ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0, 0, 0, 0);
+          }
+        }
+        box[0] = m2;
+        box[1] = l;
+      }
+      named_bar_sync(2, 256);
+    }
+    if (!fail && warp_valid && (share || h == 0)) {
+      float f0 = 1.f, f1 = 0.f;
+      const float* box = reinterpret_cast<const float*>(sk) + r * (D + 4);
+      if (!share && valid) {
+        const float mo = box[0], lo = box[1];
+        const float mm = fmaxf(m2, mo);
+        f0 = m2 == -INFINITY ? 0.f : ex2_approx(m2 - mm);
+        f1 = mo == -INFINITY ? 0.f : ex2_approx(mo - mm);
+        l = l * f0 + lo * f1;
+        m2 = mm;
+      }
+      const bool part = a.splits > 1;
+      if (!part) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        f0 *= inv;
+        f1 *= inv;
+      }
+      const int64_t prow = static_cast<int64_t>(t.u) * a.n_q * a.G + pr;
+      __nv_bfloat16* out = a.out + t.b * a.os.batch + t.l * a.os.layer + static_cast<int64_t>(head) * a.os.head +
+                           static_cast<int64_t>(pr / a.G) * a.os.token;
+      float* part_o = a.part_o + (prow * a.splits + t.split) * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32_issue(o_col + c * 32, o);
+          tmem_ld_wait(o);
+        }
+        if (!valid) continue;
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
+        if (!share) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(box + 4 + c * 32 + e);
+            x[e] = fmaf(w.x, f1, x[e]);
+            x[e + 1] = fmaf(w.y, f1, x[e + 1]);
+            x[e + 2] = fmaf(w.z, f1, x[e + 2]);
+            x[e + 3] = fmaf(w.w, f1, x[e + 3]);
+          }
+        }
+        if (part) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part_o + c * 32 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(out + c * 32 + e) =
+                make_uint4(pack_bf16x2(x[e], x[e + 1]), pack_bf16x2(x[e + 2], x[e + 3]),
+                           pack_bf16x2(x[e + 4], x[e + 5]), pack_bf16x2(x[e + 6], x[e + 7]));
+        }
+      }
+      if (valid && part) {
+        a.part_ml[prow * a.splits + t.split] = make_float2(m2, l);
+      } else if (valid && a.lse) {
+        a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n_q + pr / a.G] =
+            l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
+      }
+    }
+    if (fail && lane == 0 && a.unit_status) a.unit_status[t.u] = KVC_UNIT_TIMEOUT;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the splits of a row (PASK Eq. 15): one warp per row.
 template <int D>
-__global__ void __launch_bounds__(kPlainThreads) prompt_plain_kernel(const PromptArgs a) {
-  for (int u = blockIdx.y; u < a.U; u += gridDim.y) {
-    plain_attention<D>(PromptSrc(a, u), blockIdx.x * kPlainRows);
-    __syncthreads();
+__global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
+  const int64_t rows = static_cast<int64_t>(a.U) * a.n_q * a.G;
+  const int64_t prow = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (prow >= rows) return;
+  const int lane = threadIdx.x & 31;
+  const int u = static_cast<int>(prow / (static_cast<int64_t>(a.n_q) * a.G));
+  const int pr = static_cast<int>(prow % (static_cast<int64_t>(a.n_q) * a.G));
+  const int b = u / (a.L * a.Hkv), l = u / a.Hkv % a.L, g = u % a.Hkv;
+  if (a.q_len && pr / a.G >= clamp_count(a.q_len[b], a.n_q)) return;
+  const float2* ml = a.part_ml + prow * a.splits;
+  float top = -INFINITY;
+  for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, ml[i].x);
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float x[D / 32] = {}, sum = 0.f;
+  if (top > -INFINITY) {
+    for (int i = 0; i < a.splits; ++i) {
+      const float2 v = ml[i];
+      if (v.x == -INFINITY) continue;
+      const float f = ex2_approx(v.x - top);
+      sum += v.y * f;
+      const float* o = a.part_o + (prow * a.splits + i) * D + lane * (D / 32);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) x[c] = fmaf(o[c], f, x[c]);
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int head = g * a.G + pr % a.G;
+  __nv_bfloat16* out = a.out + b * a.os.batch + l * a.os.layer + static_cast<int64_t>(head) * a.os.head +
+                       static_cast<int64_t>(pr / a.G) * a.os.token + lane * (D / 32);
+#pragma unroll
+  for (int c = 0; c < D / 32; c += 2)
+    *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(x[c] * inv, x[c + 1] * inv);
+  if (lane == 0 && a.lse)
+    a.lse[((static_cast<int64_t>(b) * a.L + l) * (a.Hkv * a.G) + head) * a.n_q + pr / a.G] =
+        sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// Smallest and largest document of each key tile: one warp per tile.
+__global__ void __launch_bounds__(256) doc_tiles_kernel(const PromptArgs a) {
+  const int tile = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (tile >= a.n_tiles) return;
+  for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
+    int lo = INT32_MAX, hi = INT32_MIN;
+    for (int c = lane; c < kKeys; c += 32) {
+      const int64_t j = static_cast<int64_t>(tile) * kKeys + c;
+      if (j >= a.T) continue;
+      const int d = __ldg(a.docs + b * a.T + j);
+      lo = min(lo, d);
+      hi = max(hi, d);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) a.doc_tiles[static_cast<int64_t>(b) * a.n_tiles + tile] = make_int2(lo, hi);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(a.n_q) * a.G;
-  const dim3 grid(static_cast<unsigned>((rows + kPlainRows - 1) / kPlainRows), a.U < 65535 ? a.U : 65535);
-  if (a.d == 128) prompt_plain_kernel<128><<<grid, kPlainThreads, 0, stream>>>(a);
-  else prompt_plain_kernel<64><<<grid, kPlainThreads, 0, stream>>>(a);
+size_t prompt_smem_bytes(int d) { return d == 128 ? Cfg<128>::kSmem : Cfg<64>::kSmem; }
+
+cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream) {
+  if (a.docs)
+    doc_tiles_kernel<<<dim3((a.n_tiles + 7) / 8, std::min(a.B, 65535)), 256, 0, stream>>>(a);
+  const bool mods = a.mods.softcap > 0.f || a.mods.slopes;
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.n_blocks) * a.U * a.splits);
+  auto go = [&](auto kernel) -> cudaError_t {
+    const int bytes = static_cast<int>(prompt_smem_bytes(a.d));
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, bytes, stream>>>(map_k, map_v, a);
+    return cudaGetLastError();
+  };
+  cudaError_t e = a.d == 128 ? (mods ? go(prompt_kernel<128, true>) : go(prompt_kernel<128, false>))
+                             : (mods ? go(prompt_kernel<64, true>) : go(prompt_kernel<64, false>));
+  if (e != cudaSuccess || a.splits == 1) return e;
+  const int64_t rows = static_cast<int64_t>(a.U) * a.n_q * a.G;
+  const unsigned blocks = static_cast<unsigned>((rows + 7) / 8);
+  if (a.d == 128) prompt_merge_kernel<128><<<blocks, 256, 0, stream>>>(a);
+  else prompt_merge_kernel<64><<<blocks, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
