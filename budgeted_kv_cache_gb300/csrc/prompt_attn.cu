@@ -88,18 +88,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // mbar_wait by a whole warp, with one answer for all lanes (what follows is
@@ -133,6 +121,29 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__device__ __forceinline__ void unpair(uint64_t v, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Bits [lo, hi) of a 32-bit word, either end outside it allowed.
@@ -306,8 +317,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
   if (docs) __syncthreads();
   const int q_min = docs ? s.q_min : 0, q_max = docs ? s.q_max : 0;
 
-  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == kLoadWarp) {
     // -------------------------------------------------------------- TMA producer: K(i + 1) before V(i)
     if (lane == 0) {
@@ -435,8 +446,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     if (lane == 0) tc_commit(smem_u32(&s.done));
     __syncwarp();
     drain(smem_u32(&s.done), 0);
-  } else if (warp < 8) {
+  }
+  } else {
     // -------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int h = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const int row = (share ? h * kTileRows : 0) + r;
@@ -547,32 +560,36 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             break;
           }
           tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o_col + c * 16, o);
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32_issue(o_col + c * 32, o);
-            tmem_ld_wait(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(o_col + c * 32, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(o_col + c * 16, o);
           }
         }
       }
       const float sub = m == -INFINITY ? 0.f : m * cs;
-      float sum[4];
+      const uint64_t cs2 = pair(cs, cs), sub2 = pair(-sub, -sub);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        sum[c] = 0.f;
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float p0 = ex2_approx(fmaf(y[c][e], cs, -sub)), p1 = ex2_approx(fmaf(y[c][e + 1], cs, -sub));
-          sum[c] += p0 + p1;
+          float p0, p1;
+          unpair(fma2(pair(y[c][e], y[c][e + 1]), cs2, sub2), &p0, &p1);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(p0, p1));
           pk[e / 2] = pack_bf16x2(p0, p1);
         }
         tmem_st16(s_col + c * 16, pk);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float s0, s1;
+      unpair(add2(sum[0], sum[1]), &s0, &s1);
+      l += s0 + s1;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
