@@ -1,103 +1,541 @@
 // Attention over the rows of a 4-bit cache, with score modifiers; optionally
 // adds the softmax weights to the rows' mass.
-#include "attn_rows.cuh"
+//
+// HBM-bound by the codes and scales (144 bytes a row at d = 128) as long as a
+// row's 256 codes are turned into operands in about six SM cycles, so the
+// design counts instructions per code.
+//   * One warp works alone on tiles of 32 rows (keys): its own asynchronous
+//     copies, three tiles ahead, its own running maximum and sum, no barrier
+//     in the loop; the warps of a block and the blocks of a unit are joined
+//     at the end (PASK Eq. 15).
+//   * Both products put the codes in the 16-row operand and the packed query
+//     rows (row r = query r / G, head r % G of the unit) in the 8-column one:
+//     S^T = K Q^T and O^T = V^T P^T, so eight query rows cost one instruction.
+//     A pair of codes becomes a bf16 pair by one logical operation
+//     ((w & 0x000f000f) ^ 0x43084308 = 136 + code) and one subtraction, both
+//     exact; the scales never touch the codes:
+//   * the key scale of a group multiplies that group's partial sum in fp32;
+//     the value scale multiplies the weight, which is rounded to bf16 once
+//     after it, per group of 32 columns.
+//   * The order of d inside a product is free: a lane takes the eight codes of
+//     one 32-bit word as they lie, and the queries are laid out to match.  For
+//     the values a byte permutation pairs the words of two rows.
+//   * Shared rows are swizzled in 16-byte chunks so that both access patterns
+//     (8 rows x 4 words, and 4 row pairs x 4 words) meet every bank once.
+// With mass, the loop leaves each row's logits (base 2) in the workspace and a
+// second kernel adds 2^(y - lse) over the query rows, in order.
+#include <algorithm>
+#include <type_traits>
+
+#include "kvc_internal.cuh"
 
 namespace kvc {
 
 namespace {
 
-struct I4Src {
-  const I4AttnArgs& a;
-  int u, b, l, g;
-  int n, next;
-  int64_t prefix, base;
-  bool row_mode;
-  __device__ I4Src(const I4AttnArgs& a_, int u_) : a(a_), u(u_) {
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kTile = 32;                        // keys per warp tile
+constexpr int kStages = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.f;                     // log2 growth of the maximum that forces a rescale
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D (16 x 8) += A (16 x 16) B (16 x 8), bf16 in, fp32 out.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// The codes in bits 0..3 and 16..19 of w as a bf16 pair.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43084308, 0x6a;" : "=r"(r) : "r"(w));      // (w & mask) ^ magic
+  asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0x43084308u));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+struct Unit {
+  int u, b, l, g, n, R;
+  int64_t base;
+  __device__ __forceinline__ Unit(const I4AttnArgs& a, int u_) : u(u_) {
     b = u / (a.L * a.Hkv), l = u / a.Hkv % a.L, g = u % a.Hkv;
     n = clamp_count(a.rows.count[u], a.rows.capacity);
-    next = a.rows.next_pos[u];
-    prefix = a.mods.prefix_len ? a.mods.prefix_len[b] : INT64_MIN;
+    R = a.n_q * a.G;
     base = static_cast<int64_t>(u) * a.rows.capacity;
-    row_mode = a.rows.quant_mode == KVC_QUANT_ROW_FP16;
   }
-  __device__ int rows() const { return a.n_q * a.G; }
-  __device__ int64_t keys() const { return n; }
-  __device__ float query(int r, int c) const {
-    return __bfloat162float(a.q[b * a.qs.batch + l * a.qs.layer + (g * a.G + r % a.G) * a.qs.head +
-                                (r / a.G) * a.qs.token + c]);
+  __device__ __forceinline__ int64_t q_at(const I4AttnArgs& a, const kvc_strides& s, int r) const {
+    return b * s.batch + l * s.layer + static_cast<int64_t>(g * a.G + r % a.G) * s.head +
+           static_cast<int64_t>(r / a.G) * s.token;
   }
-  __device__ float element(const void* codes, const void* scales, int64_t j, int c) const {
-    const int d = a.d;
-    const uint8_t byte = static_cast<const uint8_t*>(codes)[(base + j) * (d / 2) + c / 2];
-    const int code = static_cast<int>((c & 1 ? byte >> 4 : byte & 15) ^ 8) - 8;
-    const uint16_t s = static_cast<const uint16_t*>(scales)[row_mode ? base + j : (base + j) * (d / 32) + c / 32];
-    return code * (row_mode ? __half2float(__ushort_as_half(s)) : bf16_bits_to_float(s));
-  }
-  __device__ float key(int64_t j, int c) const { return element(a.rows.k, a.rows.k_scale, j, c); }
-  __device__ float value(int64_t j, int c) const { return element(a.rows.v, a.rows.v_scale, j, c); }
-  __device__ float score(int r, int64_t j, float x) const {
-    const int i = r / a.G;
-    const int64_t p = a.q_pos ? a.q_pos[b * a.n_q + i] : static_cast<int64_t>(next) - a.n_q + i;
-    const int64_t pk = a.rows.pos[base + j];
-    if (!sees(p, pk, a.mods.window, prefix)) return -INFINITY;
-    return mod_score(x * a.scale, a.mods.softcap, a.mods.slopes ? a.mods.slopes[g * a.G + r % a.G] : 0.f,
-                     static_cast<float>(p - pk));
-  }
-  __device__ void store(int r, int c, float x) const {
-    a.out[b * a.os.batch + l * a.os.layer + (g * a.G + r % a.G) * a.os.head + (r / a.G) * a.os.token + c] =
-        __float2bfloat16_rn(x);
-  }
-  __device__ int64_t lse_at(int r) const {
+  __device__ __forceinline__ int64_t lse_at(const I4AttnArgs& a, int r) const {
     return ((static_cast<int64_t>(b) * a.L + l) * (a.Hkv * a.G) + g * a.G + r % a.G) * a.n_q + r / a.G;
-  }
-  __device__ void store_lse(int r, float x) const {
-    if (a.lse) a.lse[lse_at(r)] = x;
   }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kPlainThreads) i4_plain_kernel(const I4AttnArgs a) {
-  for (int u = blockIdx.y; u < a.U; u += gridDim.y) {
-    plain_attention<D>(I4Src(a, u), blockIdx.x * kPlainRows);
+// Keys [t0, t1) tiles of split `split` of a unit with n rows in use.
+__device__ __forceinline__ void split_range(const I4AttnArgs& a, int n, int split, int* t0, int* t1) {
+  const int tiles = (n + kTile - 1) / kTile;
+  *t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / a.splits);
+  *t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / a.splits);
+}
+
+// NT: query rows of a block / 8.  ROW: one scale per row.
+template <int D, int NT, bool ROW>
+struct Smem {
+  alignas(128) uint8_t codes[kWarps][kStages][2][kTile][D / 2];
+  alignas(16) uint16_t scale[kWarps][2][kTile][ROW ? 1 : D / 32];
+  int32_t pos[kWarps][kTile];
+  float m[kWarps][NT * 8], l[kWarps][NT * 8];
+  alignas(16) float o[NT * 8][D + 4];
+};
+
+template <int D, int NT, bool ROW>
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(const I4AttnArgs a) {
+  constexpr int NG = D / 32;                       // scale groups
+  constexpr int CH = D / 32;                       // 16-byte chunks per row
+  extern __shared__ __align__(128) uint8_t raw[];
+  using S = Smem<D, NT, ROW>;
+  S& s = *reinterpret_cast<S*>(raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if (static_cast<int>(blockIdx.y + blockIdx.z * 65535) >= a.U) return;
+  const Unit un(a, blockIdx.y + blockIdx.z * 65535);
+  const int split = blockIdx.x % a.splits, r0 = blockIdx.x / a.splits * (NT * 8);
+  int t0, t1;
+  split_range(a, un.n, split, &t0, &t1);
+
+  // one warp's copies of tile i: 16-byte chunks of key and value codes, rows past n filled with zeros
+  auto swz = [](int row, int chunk) { return D == 128 ? chunk ^ ((row >> 1) & 3) : chunk ^ ((row >> 2) & 1); };
+  auto copy_tile = [&](int i, int st) {
+    if (i < t1) {
+#pragma unroll
+      for (int c = lane; c < kTile * CH; c += 32) {
+        const int row = c / CH, chunk = c % CH, j = i * kTile + row;
+        const bool ok = j < un.n;
+        const int64_t at = (un.base + (ok ? j : 0)) * (D / 2) + chunk * 16;
+        cp_async16(smem_u32(&s.codes[warp][st][0][row][swz(row, chunk) * 16]), static_cast<const uint8_t*>(a.rows.k) + at, ok);
+        cp_async16(smem_u32(&s.codes[warp][st][1][row][swz(row, chunk) * 16]), static_cast<const uint8_t*>(a.rows.v) + at, ok);
+      }
+    }
+    cp_async_commit();
+  };
+  // scales and position of this lane's key of tile i
+  using Scales = typename std::conditional<ROW, uint16_t, typename std::conditional<D == 128, uint2, uint32_t>::type>::type;
+  Scales ks_next = {}, vs_next = {};
+  int32_t pos_next = 0;
+  auto fetch = [&](int i) {
+    const int j = i * kTile + lane;
+    if (i < t1 && j < un.n) {
+      ks_next = __ldg(static_cast<const Scales*>(a.rows.k_scale) + un.base + j);
+      vs_next = __ldg(static_cast<const Scales*>(a.rows.v_scale) + un.base + j);
+      pos_next = __ldg(a.rows.pos + un.base + j);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) copy_tile(t0 + warp + i * kWarps, i);
+  fetch(t0 + warp);
+
+  // query rows 2t, 2t + 1 of each column block: limits, slopes; and the query operand
+  int q_hi[NT][2], q_lo[NT][2];
+  float slope[NT][2];
+  const int prefix = a.mods.prefix_len ? a.mods.prefix_len[un.b] : INT32_MIN;
+  const int32_t next = a.rows.next_pos[un.u];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = min(r0 + nt * 8 + 2 * t + e, un.R - 1), i = r / a.G;
+      const int64_t p = a.q_pos ? a.q_pos[un.b * a.n_q + i] : static_cast<int64_t>(next) - a.n_q + i;
+      q_hi[nt][e] = static_cast<int>(max(p, static_cast<int64_t>(INT32_MIN)));
+      q_lo[nt][e] = a.mods.window ? static_cast<int>(max(p - a.mods.window + 1, static_cast<int64_t>(INT32_MIN))) : INT32_MIN;
+      slope[nt][e] = a.mods.slopes ? a.mods.slopes[un.g * a.G + r % a.G] * kLog2e : 0.f;
+    }
+  uint32_t qf[NT][NG][4];                          // operand of both products' k-steps of a group
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = r0 + nt * 8 + g;
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) + un.q_at(a, a.qs, min(r, un.R - 1)) + 8 * t;
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+      const uint4 w = r < un.R ? __ldg(reinterpret_cast<const uint4*>(q + 32 * gr)) : make_uint4(0, 0, 0, 0);
+      // elements (0,4), (1,5), (2,6), (3,7) of the lane's eight
+      qf[nt][gr][0] = __byte_perm(w.x, w.z, 0x5410);
+      qf[nt][gr][1] = __byte_perm(w.x, w.z, 0x7632);
+      qf[nt][gr][2] = __byte_perm(w.y, w.w, 0x5410);
+      qf[nt][gr][3] = __byte_perm(w.y, w.w, 0x7632);
+    }
+  }
+
+  const bool capped = a.mods.softcap > 0.f, biased = a.mods.slopes != nullptr;
+  const float cs = a.scale * kLog2e;
+  const uint32_t half_sel = (g >> 2) ? 0x7632u : 0x5410u;
+  float m[NT][2], l[NT][2], o[NG][2][NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[gr][k >> 2][nt][k & 3] = 0.f;
+  }
+
+  int st = 0;
+#pragma unroll 1
+  for (int i = t0 + warp; i < t1; i += kWarps) {
+    copy_tile(i + (kStages - 1) * kWarps, (st + kStages - 1) % kStages);
+    // scales and positions of this tile: one lane per key, then to all
+    *reinterpret_cast<Scales*>(&s.scale[warp][0][lane][0]) = ks_next;
+    *reinterpret_cast<Scales*>(&s.scale[warp][1][lane][0]) = vs_next;
+    s.pos[warp][lane] = pos_next;
+    fetch(i + kWarps);
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const uint8_t* kc = &s.codes[warp][st][0][0][0];
+    const uint8_t* vc = &s.codes[warp][st][1][0][0];
+    auto scale_f = [&](int which, int key, float (&f)[NG]) {
+      if constexpr (ROW) {
+        f[0] = __half2float(__ushort_as_half(s.scale[warp][which][key][0]));
+      } else {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&s.scale[warp][which][key][0]);
+#pragma unroll
+        for (int k = 0; k < NG / 2; ++k) {
+          f[2 * k] = __uint_as_float(w[k] << 16);
+          f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+      }
+    };
+
+    // ---- y = logits in base 2: y[sub][nt][c], key 16 sub + g (+ 8 for c >= 2), query row 2t + (c & 1)
+    float y[2][NT][4];
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[sub][nt][c] = 0.f;
+      const int k0 = sub * 16 + g, k1 = k0 + 8;
+      float f0[NG], f1[NG];
+      scale_f(0, k0, f0);
+      scale_f(0, k1, f1);
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(kc + k0 * (D / 2) + swz(k0, gr) * 16 + t * 4);
+        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(kc + k1 * (D / 2) + swz(k1, gr) * 16 + t * 4);
+        const uint32_t lo[4] = {code_pair(w0), code_pair(w1), code_pair(w0 >> 4), code_pair(w1 >> 4)};
+        const uint32_t hi[4] = {code_pair(w0 >> 8), code_pair(w1 >> 8), code_pair(w0 >> 12), code_pair(w1 >> 12)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (ROW) {
+            mma16816(y[sub][nt], lo, qf[nt][gr][0], qf[nt][gr][1]);
+            mma16816(y[sub][nt], hi, qf[nt][gr][2], qf[nt][gr][3]);
+          } else {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(acc, lo, qf[nt][gr][0], qf[nt][gr][1]);
+            mma16816(acc, hi, qf[nt][gr][2], qf[nt][gr][3]);
+            y[sub][nt][0] = fmaf(acc[0], f0[gr], y[sub][nt][0]);
+            y[sub][nt][1] = fmaf(acc[1], f0[gr], y[sub][nt][1]);
+            y[sub][nt][2] = fmaf(acc[2], f1[gr], y[sub][nt][2]);
+            y[sub][nt][3] = fmaf(acc[3], f1[gr], y[sub][nt][3]);
+          }
+        }
+      }
+      const int pk[2] = {s.pos[warp][k0], s.pos[warp][k1]};
+      const bool in_use[2] = {i * kTile + k0 < un.n, i * kTile + k1 < un.n};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int e = c & 1, k = c >> 1;
+          float x = y[sub][nt][c];
+          if constexpr (ROW) x *= k ? f1[0] : f0[0];
+          if (capped) x = a.mods.softcap * tanhf(x * a.scale / a.mods.softcap) * kLog2e;
+          else x *= cs;
+          if (biased) x = fmaf(-slope[nt][e], fabsf(static_cast<float>(q_hi[nt][e] - pk[k])), x);
+          const bool seen = in_use[k] && ((pk[k] <= q_hi[nt][e] && pk[k] >= q_lo[nt][e]) || pk[k] < prefix);
+          y[sub][nt][c] = seen ? x : -INFINITY;
+        }
+      if (a.logits) {
+        // [unit][key][R rounded up to even]
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (!in_use[k]) continue;
+          float* dst = a.logits + (un.base + i * kTile + (k ? k1 : k0)) * a.logit_stride + r0 + 2 * t;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            if (r0 + nt * 8 + 2 * t < a.logit_stride)
+              *reinterpret_cast<float2*>(dst + nt * 8) = make_float2(y[sub][nt][2 * k], y[sub][nt][2 * k + 1]);
+        }
+      }
+    }
+
+    // ---- running maximum per query row over the warp's keys
+    bool grow = false;
+    float top[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(fmaxf(y[0][nt][e], y[0][nt][e + 2]), fmaxf(y[1][nt][e], y[1][nt][e + 2]));
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, k));
+        top[nt][e] = x;
+        grow |= x - m[nt][e] > kGrow;
+      }
+    if (__any_sync(kFull, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (!(top[nt][e] > m[nt][e])) continue;
+          const float f = m[nt][e] == -INFINITY ? 0.f : ex2_approx(m[nt][e] - top[nt][e]);
+          m[nt][e] = top[nt][e];
+          l[nt][e] *= f;
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              o[gr][mt][nt][e] *= f;
+              o[gr][mt][nt][e + 2] *= f;
+            }
+        }
+    }
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float ref = m[nt][c & 1];
+          y[sub][nt][c] = ex2_approx(y[sub][nt][c] - (ref == -INFINITY ? 0.f : ref));
+          l[nt][c & 1] += y[sub][nt][c];
+        }
+
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      const int k0 = sub * 16 + g, k1 = k0 + 8;
+      float f0[NG], f1[NG];
+      scale_f(1, k0, f0);
+      scale_f(1, k1, f1);
+      const bool in0 = i * kTile + k0 < un.n, in1 = i * kTile + k1 < un.n;
+#pragma unroll
+      for (int gr = 0; gr < (ROW ? 1 : NG); ++gr) {
+        if (!in0) f0[gr] = 0.f;                    // scales behind the rows in use may be NaN
+        if (!in1) f1[gr] = 0.f;
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        if (!ROW || gr == 0) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            pb[nt][0] = transpose8x8(pack_bf16x2(y[sub][nt][0] * f0[gr], y[sub][nt][1] * f0[gr]));
+            pb[nt][1] = transpose8x8(pack_bf16x2(y[sub][nt][2] * f1[gr], y[sub][nt][3] * f1[gr]));
+          }
+        }
+        uint32_t w[4];                             // rows 2t, 2t + 1, 2t + 8, 2t + 9; word g & 3 of the chunk
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = sub * 16 + 2 * t + (k & 1) + (k >> 1) * 8;
+          w[k] = *reinterpret_cast<const uint32_t*>(vc + key * (D / 2) + swz(key, gr) * 16 + (g & 3) * 4);
+        }
+        const uint32_t x0 = __byte_perm(w[0], w[1], half_sel), x1 = __byte_perm(w[2], w[3], half_sel);
+        const uint32_t a0[4] = {code_pair(x0), code_pair(x0 >> 4), code_pair(x1), code_pair(x1 >> 4)};
+        const uint32_t a1[4] = {code_pair(x0 >> 8), code_pair(x0 >> 12), code_pair(x1 >> 8), code_pair(x1 >> 12)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816(o[gr][0][nt], a0, pb[nt][0], pb[nt][1]);
+          mma16816(o[gr][1][nt], a1, pb[nt][0], pb[nt][1]);
+        }
+      }
+    }
+    __syncwarp();
+    st = (st + 1) % kStages;
+  }
+  cp_async_wait<0>();
+
+  // ---- join the warps: sums over the lanes' keys, one reference maximum, sums in warp order
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], k);
+      if (g == 0) {
+        s.m[warp][nt * 8 + 2 * t + e] = m[nt][e];
+        s.l[warp][nt * 8 + 2 * t + e] = l[nt][e];
+      }
+    }
+  __syncthreads();
+  float f[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = nt * 8 + 2 * t + e;
+      const float mm = fmaxf(fmaxf(s.m[0][c], s.m[1][c]), fmaxf(s.m[2][c], s.m[3][c]));
+      f[nt][e] = m[nt][e] == -INFINITY ? 0.f : ex2_approx(m[nt][e] - mm);
+    }
+#pragma unroll 1
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            float4* dst = reinterpret_cast<float4*>(&s.o[nt * 8 + 2 * t + e][32 * gr + 8 * (g & 3) + 4 * (g >> 2)]);
+            float4 v = w ? *dst : make_float4(0.f, 0.f, 0.f, 0.f);
+            v.x = fmaf(o[gr][0][nt][e], f[nt][e], v.x);
+            v.y = fmaf(o[gr][0][nt][e + 2], f[nt][e], v.y);
+            v.z = fmaf(o[gr][1][nt][e], f[nt][e], v.z);
+            v.w = fmaf(o[gr][1][nt][e + 2], f[nt][e], v.w);
+            *dst = v;
+          }
+    }
     __syncthreads();
+  }
+  constexpr int LPR = D / 8;                       // lanes per output row
+  for (int c = threadIdx.x / LPR; c < NT * 8; c += kThreads / LPR) {
+    const int r = r0 + c, d0 = threadIdx.x % LPR * 8;
+    if (r >= un.R) break;
+    const float mm = fmaxf(fmaxf(s.m[0][c], s.m[1][c]), fmaxf(s.m[2][c], s.m[3][c]));
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      if (s.m[w][c] != -INFINITY) sum += s.l[w][c] * ex2_approx(s.m[w][c] - mm);
+    const float* x = &s.o[c][d0];
+    if (a.splits > 1) {
+      const int64_t part = (static_cast<int64_t>(un.u) * un.R + r) * a.splits + split;
+#pragma unroll
+      for (int k = 0; k < 8; k += 4)
+        *reinterpret_cast<float4*>(a.part_o + part * D + d0 + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+      if (d0 == 0) a.part_ml[part] = make_float2(mm, sum);
+    } else {
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      *reinterpret_cast<uint4*>(a.out + un.q_at(a, a.os, r) + d0) =
+          make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
+                     pack_bf16x2(x[4] * inv, x[5] * inv), pack_bf16x2(x[6] * inv, x[7] * inv));
+      if (d0 == 0) {
+        if (a.lse) a.lse[un.lse_at(a, r)] = sum > 0.f ? (mm + log2f(sum)) * kLn2 : -INFINITY;
+        if (a.part_ml) a.part_ml[static_cast<int64_t>(un.u) * un.R + r] = make_float2(mm, sum);
+      }
+    }
   }
 }
 
-// mass[j] += sum over the rows of exp(x_rj - lse_r), one warp per key.
+// Second kernel: blocks [0, a.merge_blocks) of a unit join the splits of its
+// rows, the others add the weights of their keys to the mass.
+constexpr int kFinThreads = 256;
+
 template <int D>
-__global__ void __launch_bounds__(kPlainThreads) i4_mass_kernel(const I4AttnArgs a) {
-  for (int u = blockIdx.y; u < a.U; u += gridDim.y) {
-    const I4Src src(a, u);
-    const int lane = threadIdx.x & 31;
-    for (int64_t j = blockIdx.x * (kPlainThreads / 32) + (threadIdx.x >> 5); j < src.n;
-         j += gridDim.x * (kPlainThreads / 32)) {
-      float k[D / 32], sum = 0.f;
-      for (int c = 0; c < D / 32; ++c) k[c] = src.key(j, c * 32 + lane);
-      for (int r = 0; r < src.rows(); ++r) {
-        float x = 0.f;
-        for (int c = 0; c < D / 32; ++c) x += src.query(r, c * 32 + lane) * k[c];
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        x = src.score(r, j, x);
-        if (x > -INFINITY) sum += expf(x - a.lse[src.lse_at(r)]);
-      }
-      if (lane == 0) a.rows.mass[src.base + j] += sum;
+__global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs a) {
+  extern __shared__ float lse2[];                  // base-2 log-sum-exp of each row (mass blocks)
+  if (static_cast<int>(blockIdx.y + blockIdx.z * 65535) >= a.U) return;
+  const Unit un(a, blockIdx.y + blockIdx.z * 65535);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (static_cast<int>(blockIdx.x) < a.merge_blocks) {
+    const int r = blockIdx.x * (kFinThreads / 32) + warp;
+    if (r >= un.R) return;
+    const float2* ml = a.part_ml + (static_cast<int64_t>(un.u) * un.R + r) * a.splits;
+    float top = -INFINITY;
+    for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, ml[i].x);
+    for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
+    float x[D / 32] = {}, sum = 0.f;
+    for (int i = 0; i < a.splits; ++i) {
+      const float2 v = ml[i];
+      if (v.x == -INFINITY) continue;
+      const float w = ex2_approx(v.x - top);
+      sum = fmaf(v.y, w, sum);
+      const float* src = a.part_o + ((static_cast<int64_t>(un.u) * un.R + r) * a.splits + i) * D + lane * (D / 32);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) x[c] = fmaf(src[c], w, x[c]);
     }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    __nv_bfloat16* out = a.out + un.q_at(a, a.os, r) + lane * (D / 32);
+#pragma unroll
+    for (int c = 0; c < D / 32; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(x[c] * inv, x[c + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[un.lse_at(a, r)] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    return;
   }
+  const int j0 = (blockIdx.x - a.merge_blocks) * a.mass_keys;
+  if (j0 >= un.n) return;
+  for (int r = warp; r < un.R; r += kFinThreads / 32) {
+    const float2* ml = a.part_ml + (static_cast<int64_t>(un.u) * un.R + r) * a.splits;
+    float top = -INFINITY, sum = 0.f;
+    for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, ml[i].x);
+    for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
+    for (int i = lane; i < a.splits; i += 32)
+      if (ml[i].x != -INFINITY) sum += ml[i].y * ex2_approx(ml[i].x - top);
+    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(kFull, sum, k);
+    if (lane == 0) lse2[r] = sum > 0.f ? top + log2f(sum) : 0.f;      // nothing seen: every logit is -inf
+  }
+  __syncthreads();
+  const int j1 = min(un.n, j0 + a.mass_keys);
+  for (int j = j0 + threadIdx.x; j < j1; j += kFinThreads) {
+    const float* y = a.logits + (un.base + j) * a.logit_stride;
+    float sum = 0.f;
+    for (int r = 0; r < un.R; ++r) sum += ex2_approx(y[r] - lse2[r]);
+    a.rows.mass[un.base + j] += sum;
+  }
+}
+
+template <int D, int NT, bool ROW>
+cudaError_t launch_one(const I4AttnArgs& a, cudaStream_t stream) {
+  auto kernel = i4_attn_kernel<D, NT, ROW>;
+  const int bytes = static_cast<int>(sizeof(Smem<D, NT, ROW>));
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  const int R = a.n_q * a.G;
+  const dim3 grid((R + NT * 8 - 1) / (NT * 8) * a.splits, std::min(a.U, 65535), (a.U + 65534) / 65535);
+  kernel<<<grid, kThreads, bytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, bool ROW>
+cudaError_t launch_rows(const I4AttnArgs& a, cudaStream_t stream) {
+  const int R = a.n_q * a.G;
+  if (R <= 8) return launch_one<D, 1, ROW>(a, stream);
+  if (R <= 16) return launch_one<D, 2, ROW>(a, stream);
+  return launch_one<D, 4, ROW>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(a.n_q) * a.G;
-  const unsigned y = a.U < 65535 ? a.U : 65535;
-  const dim3 grid(static_cast<unsigned>((rows + kPlainRows - 1) / kPlainRows), y);
-  const dim3 mgrid(static_cast<unsigned>((a.rows.capacity + 31) / 32), y);
-  if (a.d == 128) i4_plain_kernel<128><<<grid, kPlainThreads, 0, stream>>>(a);
-  else i4_plain_kernel<64><<<grid, kPlainThreads, 0, stream>>>(a);
-  if (a.add_mass) {
-    if (a.d == 128) i4_mass_kernel<128><<<mgrid, kPlainThreads, 0, stream>>>(a);
-    else i4_mass_kernel<64><<<mgrid, kPlainThreads, 0, stream>>>(a);
-  }
+  const bool row = a.rows.quant_mode == KVC_QUANT_ROW_FP16;
+  cudaError_t e = a.d == 128 ? (row ? launch_rows<128, true>(a, stream) : launch_rows<128, false>(a, stream))
+                             : (row ? launch_rows<64, true>(a, stream) : launch_rows<64, false>(a, stream));
+  const int mass_blocks = a.add_mass ? (a.rows.capacity + a.mass_keys - 1) / a.mass_keys : 0;
+  if (e != cudaSuccess || a.merge_blocks + mass_blocks == 0) return e;
+  const dim3 grid(a.merge_blocks + mass_blocks, std::min(a.U, 65535), (a.U + 65534) / 65535);
+  const size_t bytes = a.add_mass ? static_cast<size_t>(a.n_q) * a.G * sizeof(float) : 0;
+  if (a.d == 128) i4_finish_kernel<128><<<grid, kFinThreads, bytes, stream>>>(a);
+  else i4_finish_kernel<64><<<grid, kFinThreads, bytes, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -424,8 +424,36 @@ kvc_status encode_rows(CUtensorMap* map, const void* ptr, const kvc_shape* s, in
   return r == CUDA_SUCCESS ? KVC_OK : KVC_ERR_CUDA;
 }
 
-size_t i4_attn_lse_bytes(const kvc_shape* s, int64_t n_q) {
-  return static_cast<size_t>(s->batch) * s->n_layers * s->n_q_heads * n_q * sizeof(float);
+struct I4AttnPlan {
+  int32_t splits = 1, merge_blocks = 0, mass_keys = 0, logit_stride = 0;
+  size_t ws_ml = 0, ws_o = 0, ws_total = 0;
+};
+
+kvc_status plan_i4_attn(const kvc_shape* s, const kvc_i4_rows* r, int32_t n_q, uint32_t flags, I4AttnPlan* p) {
+  kvc_status st = check_i4(s, r);
+  if (st != KVC_OK) return st;
+  if ((st = check_queries(s, n_q)) != KVC_OK) return st;
+  const int64_t U = n_units(s), rows = static_cast<int64_t>(n_q) * (s->n_q_heads / s->n_kv_heads);
+  const bool mass = (flags & KVC_ATTN_ADD_MASS) != 0;
+  if (rows > (mass ? 12288 : 1 << 24)) return KVC_ERR_UNSUPPORTED;   // row statistics of a mass block in shared memory
+  DevInfo info;
+  if ((st = check_device(&info)) != KVC_OK) return st;
+  // three blocks of four warps per SM, each warp with at least two tiles of 32 keys
+  const int64_t blocks = U * ((rows + 31) / 32);
+  int64_t want = (6LL * info.sms + blocks - 1) / blocks;
+  want = std::min<int64_t>(want, r->capacity / 256);
+  p->splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(want, 128)));
+  p->logit_stride = static_cast<int32_t>((rows + 1) / 2 * 2);
+  p->mass_keys = 1024;
+  const size_t parts = static_cast<size_t>(U) * rows * p->splits;
+  if (p->splits > 1) {
+    p->merge_blocks = static_cast<int32_t>((rows + 7) / 8);
+    p->ws_o = (parts * s->head_dim * sizeof(float) + 255) / 256 * 256;
+  }
+  if (p->splits > 1 || mass) p->ws_ml = (parts * sizeof(float2) + 255) / 256 * 256;
+  p->ws_total = p->ws_ml + p->ws_o;
+  if (mass) p->ws_total += static_cast<size_t>(U) * r->capacity * p->logit_stride * sizeof(float);
+  return KVC_OK;
 }
 
 }  // namespace
@@ -1038,8 +1066,8 @@ kvc_status kvc_i4_read(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t 
 }
 
 size_t kvc_i4_attn_workspace_bytes(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t n_q, uint32_t flags) {
-  if (check_i4(shape, rows) != KVC_OK || check_queries(shape, n_q) != KVC_OK) return 0;
-  return (flags & KVC_ATTN_ADD_MASS) ? i4_attn_lse_bytes(shape, n_q) : 0;
+  I4AttnPlan p;
+  return plan_i4_attn(shape, rows, n_q, flags, &p) == KVC_OK ? p.ws_total : 0;
 }
 
 kvc_status kvc_i4_attn(const kvc_shape* shape, const kvc_i4_rows* rows, const void* q,
@@ -1057,10 +1085,9 @@ kvc_status kvc_i4_attn(const kvc_shape* shape, const kvc_i4_rows* rows, const vo
   if ((st = tensor_strides(shape, shape->n_q_heads, n_q, q_strides, &a.qs)) != KVC_OK) return st;
   if ((st = tensor_strides(shape, shape->n_q_heads, n_q, out_strides, &a.os)) != KVC_OK) return st;
   if ((st = check_mods(mods, &a.mods)) != KVC_OK) return st;
-  DevInfo info;
-  if ((st = check_device(&info)) != KVC_OK) return st;
-  const size_t need = kvc_i4_attn_workspace_bytes(shape, rows, n_q, flags);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return KVC_ERR_WORKSPACE;
+  I4AttnPlan p;
+  if ((st = plan_i4_attn(shape, rows, n_q, flags, &p)) != KVC_OK) return st;
+  if (p.ws_total > 0 && (!workspace || workspace_bytes < p.ws_total || !aligned(workspace, 256))) return KVC_ERR_WORKSPACE;
   if (!(softmax_scale > 0.f)) softmax_scale = 1.0f / sqrtf(static_cast<float>(shape->head_dim));
   a.U = static_cast<int32_t>(n_units(shape));
   a.L = shape->n_layers;
@@ -1075,7 +1102,15 @@ kvc_status kvc_i4_attn(const kvc_shape* shape, const kvc_i4_rows* rows, const vo
   a.q_pos = q_pos;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.add_mass = (flags & KVC_ATTN_ADD_MASS) != 0;
-  a.lse = row_lse ? row_lse : a.add_mass ? static_cast<float*>(workspace) : nullptr;
+  a.lse = row_lse;
+  a.splits = p.splits;
+  a.merge_blocks = p.merge_blocks;
+  a.mass_keys = p.mass_keys;
+  a.logit_stride = p.logit_stride;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (p.ws_ml) a.part_ml = reinterpret_cast<float2*>(ws);
+  if (p.ws_o) a.part_o = reinterpret_cast<float*>(ws + p.ws_ml);
+  if (a.add_mass) a.logits = reinterpret_cast<float*>(ws + p.ws_ml + p.ws_o);
   return launch_i4_attn(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 

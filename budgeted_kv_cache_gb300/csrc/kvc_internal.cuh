@@ -261,8 +261,15 @@ struct I4AttnArgs {
   const int32_t* q_pos;        // optional [B][n_q]
   Mods mods;
   __nv_bfloat16* out;
-  float* lse;                  // [B][L][H_q][n_q]: the caller's or the workspace's
+  float* lse;                  // optional [B][L][H_q][n_q]
   bool add_mass;
+  int32_t splits;              // blocks that share a unit's keys
+  int32_t merge_blocks;        // second kernel: blocks per unit that join splits (0: nothing to join)
+  int32_t mass_keys;           // second kernel: keys per block that adds mass
+  int32_t logit_stride;        // n_q G rounded up to even
+  float* part_o;               // splits > 1: [U][n_q G][splits][d]
+  float2* part_ml;             // splits > 1 or add_mass: [U][n_q G][splits]
+  float* logits;               // add_mass: [U][capacity][logit_stride], base 2
 };
 
 struct I4EvictArgs {
