@@ -146,6 +146,29 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh(z) / z from u = z^2 in [0, 1]: degree-6 polynomial fitted at Chebyshev
+// points (tanh within 1.8e-7 of its value).
+__device__ __forceinline__ uint64_t tanh_over_z(uint64_t u) {
+  const float c[7] = {0.9999999403953552f,  -0.33332857489585876f, 0.13325397670269012f, -0.05346517637372017f,
+                      0.020305519923567772f, -0.006217069923877716f, 0.0010455535957589746f};
+  uint64_t r = pair(c[6], c[6]);
+#pragma unroll
+  for (int k = 5; k >= 0; --k) r = fma2(r, u, pair(c[k], c[k]));
+  return r;
+}
+
 // Bits [lo, hi) of a 32-bit word, either end outside it allowed.
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   lo = max(lo, 0);
@@ -237,9 +260,8 @@ struct Bars {
   int q_min, q_max;
 };
 
-// D: head dimension.  MODS: a cap or slopes (the logits are transformed
-// before the softmax).
-template <int D, bool MODS>
+// D: head dimension.  CAP, BIAS: the logits are capped, or get slopes.
+template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
   using C = Cfg<D>;
@@ -466,10 +488,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     int my_doc = 0;
     if (docs) my_doc = p >= 0 && p < t.nk ? __ldg(docs + p) : -1;
     if (p < 0 || my_doc < 0) row_hi = row_lo = row_pre = 0;
-    const float cs = MODS ? 1.f : a.scale * kLog2e;
+    const float cs = CAP || BIAS ? 1.f : a.scale * kLog2e;
     const float cap = a.mods.softcap;
-    const float zs = MODS && cap > 0.f ? 2.f * kLog2e * a.scale / cap : 0.f;      // tanh argument x 2 log2 e
-    const float slope2 = MODS && a.mods.slopes ? a.mods.slopes[head] * kLog2e : 0.f;
+    const float zs = CAP ? a.scale / cap : 0.f;
+    const float slope2 = BIAS ? a.mods.slopes[head] * kLog2e : 0.f;
     float m = -INFINITY, l = 0.f;              // reference maximum (of y / cs) and sum of 2^(y - m cs)
     TileWalk walk(t, table, q_min, q_max);
     int n = 0;                                 // tiles of this stream
@@ -496,22 +518,37 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
       float (&y)[4][32] = reinterpret_cast<float (&)[4][32]>(sr);
       const int j0 = tile * kKeys;
-      if constexpr (MODS) {
-        const float far = static_cast<float>(p - j0);
+      if constexpr (CAP) {
+        // z = s scale / cap; the polynomial as long as the warp's |z| <= 1 (logits within the cap)
+        float big = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float x = y[c][e];
-            if (cap > 0.f) {
-              // cap tanh(z) = cap (1 - 2 / (1 + e^2z)): right at both infinities
-              const float ez = ex2_approx(x * zs);
-              x = fmaf(-2.f * cap, __frcp_rn(1.f + ez), cap) * kLog2e;
-            } else {
-              x *= a.scale * kLog2e;
+          for (int e = 0; e < 32; e += 2) big = fmaxf(big, fmaxf(fabsf(y[c][e]), fabsf(y[c][e + 1])));
+        if (__all_sync(0xffffffffu, big * zs <= 1.f || !valid)) {
+          const uint64_t zs2 = pair(zs, zs), out2 = pair(cap * kLog2e, cap * kLog2e);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const uint64_t z = mul2(pair(y[c][e], y[c][e + 1]), zs2);
+              unpair(mul2(mul2(z, out2), tanh_over_z(mul2(z, z))), &y[c][e], &y[c][e + 1]);
             }
-            y[c][e] = fmaf(-slope2, fabsf(far - static_cast<float>(c * 32 + e)), x);
-          }
+        } else {
+          // cap tanh(z) = cap (1 - 2 / (1 + e^2z)): right at both infinities
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              y[c][e] = fmaf(-2.f * cap, rcp_approx(1.f + ex2_approx(y[c][e] * (zs * (2.f * kLog2e)))), cap) * kLog2e;
+        }
+      }
+      if constexpr (BIAS) {
+        const float far = static_cast<float>(p - j0), by = CAP ? 1.f : a.scale * kLog2e;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[c][e] = fmaf(-slope2, fabsf(far - static_cast<float>(c * 32 + e)), y[c][e] * by);
       }
       // masks, unless every row of the warp sees the whole tile
       bool whole = j0 + kKeys <= row_pre || (j0 >= row_lo && j0 + kKeys <= row_hi);
@@ -521,18 +558,28 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         same = d.x == d.y && d.x == my_doc;
       }
       if (!__all_sync(0xffffffffu, (whole && same) || !valid)) {
-        const bool by_doc = !__all_sync(0xffffffffu, same || !valid);
+        uint32_t eq[4] = {~0u, ~0u, ~0u, ~0u};
+        if (docs && !__all_sync(0xffffffffu, same || !valid)) {
+          // the keys of each document that the warp's rows have, one document after another
+          int kd[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) kd[c] = j0 + c * 32 + lane < t.nk ? __ldg(docs + j0 + c * 32 + lane) : -1;
+          uint32_t left = 0xffffffffu;
+#pragma unroll 1
+          while (left) {
+            const int doc = __shfl_sync(0xffffffffu, my_doc, __ffs(left) - 1);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t hit = __ballot_sync(0xffffffffu, kd[c] == doc);
+              if (my_doc == doc) eq[c] = hit;
+            }
+            left &= ~__ballot_sync(0xffffffffu, my_doc == doc);
+          }
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int jc = j0 + c * 32;
-          uint32_t bits = bit_range(row_lo - jc, row_hi - jc) | bit_range(0, row_pre - jc);
-          if (by_doc) {
-            uint32_t eq = 0;
-#pragma unroll 8
-            for (int e = 0; e < 32; ++e)
-              eq |= (jc + e < t.nk && __ldg(docs + jc + e) == my_doc ? 1u : 0u) << e;
-            bits &= eq;
-          }
+          const uint32_t bits = (bit_range(row_lo - jc, row_hi - jc) | bit_range(0, row_pre - jc)) & eq[c];
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!(bits & (1u << e))) y[c][e] = -INFINITY;
@@ -760,7 +807,6 @@ size_t prompt_smem_bytes(int d) { return d == 128 ? Cfg<128>::kSmem : Cfg<64>::k
 cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream) {
   if (a.docs)
     doc_tiles_kernel<<<dim3((a.n_tiles + 7) / 8, std::min(a.B, 65535)), 256, 0, stream>>>(a);
-  const bool mods = a.mods.softcap > 0.f || a.mods.slopes;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.n_blocks) * a.U * a.splits);
   auto go = [&](auto kernel) -> cudaError_t {
     const int bytes = static_cast<int>(prompt_smem_bytes(a.d));
@@ -769,8 +815,14 @@ cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_k, const C
     kernel<<<grid, kThreads, bytes, stream>>>(map_k, map_v, a);
     return cudaGetLastError();
   };
-  cudaError_t e = a.d == 128 ? (mods ? go(prompt_kernel<128, true>) : go(prompt_kernel<128, false>))
-                             : (mods ? go(prompt_kernel<64, true>) : go(prompt_kernel<64, false>));
+  const bool cap = a.mods.softcap > 0.f, bias = a.mods.slopes != nullptr;
+  cudaError_t e;
+  if (a.d == 128)
+    e = cap ? (bias ? go(prompt_kernel<128, true, true>) : go(prompt_kernel<128, true, false>))
+            : (bias ? go(prompt_kernel<128, false, true>) : go(prompt_kernel<128, false, false>));
+  else
+    e = cap ? (bias ? go(prompt_kernel<64, true, true>) : go(prompt_kernel<64, true, false>))
+            : (bias ? go(prompt_kernel<64, false, true>) : go(prompt_kernel<64, false, false>));
   if (e != cudaSuccess || a.splits == 1) return e;
   const int64_t rows = static_cast<int64_t>(a.U) * a.n_q * a.G;
   const unsigned blocks = static_cast<unsigned>((rows + 7) / 8);
