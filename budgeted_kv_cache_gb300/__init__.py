@@ -174,8 +174,14 @@ def _p(t) -> Optional[int]:
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object (3 us of a call), where torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -528,9 +534,10 @@ class I4Rows:
                 raise KvcError("I4Rows", 1)
 
     def c(self) -> kvc_i4_rows:
-        return kvc_i4_rows(_p(self.k), _p(self.v), _p(self.k_scale), _p(self.v_scale), _p(self.pos),
-                           _p(self.mass), _p(self.count), _p(self.next_pos), int(self.pos.shape[-1]),
-                           int(self.quant_mode))
+        pos, mass = self.pos, self.mass
+        return kvc_i4_rows(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                           pos.data_ptr(), None if mass is None else mass.data_ptr(), self.count.data_ptr(),
+                           self.next_pos.data_ptr(), pos.shape[1], self.quant_mode)
 
     @staticmethod
     def allocate(shape: kvc_shape, capacity: int, quant_mode: int = QUANT_G32_BF16, device="cuda",
@@ -555,39 +562,56 @@ class I4Rows:
                       pools.pos_out[POOL_INT4], kept_count[POOL_INT4], next_pos, mass, policy.quant_mode)
 
 
-def _strides(fn: str, t: torch.Tensor, shape: kvc_shape, heads: int, n: int):
-    """Strides of a bf16 [B][L][H][n][d] tensor of the current device; n < 0 takes the tensor's."""
-    if t.dtype != torch.bfloat16 or t.dim() != 5 or not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise KvcError(fn, 1)
-    st = t.stride()
-    if tuple(t.shape) != (shape.batch, shape.n_layers, heads, t.shape[3] if n < 0 else n, shape.head_dim) or st[4] != 1:
-        raise KvcError(fn, 1)
-    return ctypes.byref(kvc_strides(*st[:4]))
+class _Call:
+    """Checks of one call's tensors: types, shapes, the current device."""
 
+    def __init__(self, fn: str, shape: kvc_shape):
+        self.fn, self.shape, self.dev = fn, shape, torch.cuda.current_device() if torch.cuda.is_initialized() else -2
 
-def _dense(fn: str, t: Optional[torch.Tensor], dtype, n: int) -> Optional[int]:
-    """Address of an optional contiguous device tensor of n elements."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != torch.cuda.current_device():
-        raise KvcError(fn, 1)
-    return t.data_ptr()
+    def refuse(self):
+        raise KvcError(self.fn, 1)
 
+    def rows(self, t: torch.Tensor, heads: int, n: int = -1):
+        """Strides of a bf16 [B][L][H][n][d] tensor; n < 0 takes the tensor's."""
+        size, st, s = t.shape, t.stride(), self.shape
+        if (t.dtype is not torch.bfloat16 or t.get_device() != self.dev or len(size) != 5 or st[4] != 1 or
+                size[4] != s.head_dim or size[2] != heads or size[1] != s.n_layers or size[0] != s.batch or
+                (n >= 0 and size[3] != n)):
+            self.refuse()
+        return ctypes.byref(kvc_strides(st[0], st[1], st[2], st[3]))
 
-def _mods(fn: str, mods: Optional[ScoreMods], shape: kvc_shape):
-    if mods is None:
-        return None
-    return ctypes.byref(kvc_score_mods(
-        float(mods.softcap), _dense(fn, mods.slopes, torch.float32, shape.n_q_heads), int(mods.window),
-        _dense(fn, mods.prefix_len, torch.int32, shape.batch)))
+    def dense(self, t: Optional[torch.Tensor], dtype, n: int) -> Optional[int]:
+        """Address of an optional contiguous tensor of n elements."""
+        if t is None:
+            return None
+        if t.dtype is not dtype or t.numel() != n or t.get_device() != self.dev or not t.is_contiguous():
+            self.refuse()
+        return t.data_ptr()
 
+    def cache(self, rows: I4Rows):
+        if rows.k.get_device() != self.dev or rows.k.shape[0] != self.units or rows.k.shape[2] * 2 != self.shape.head_dim:
+            self.refuse()
+        return ctypes.byref(rows.c())
 
-def _units(shape: kvc_shape) -> int:
-    return shape.batch * shape.n_layers * shape.n_kv_heads
+    def mods(self, m: Optional[ScoreMods]):
+        if m is None:
+            return None
+        s = self.shape
+        return ctypes.byref(kvc_score_mods(m.softcap, self.dense(m.slopes, torch.float32, s.n_q_heads), m.window,
+                                           self.dense(m.prefix_len, torch.int32, s.batch)))
 
+    def space(self, workspace: Optional[torch.Tensor]):
+        """Address and bytes of a workspace."""
+        if workspace is None:
+            return None, 0
+        if workspace.get_device() != self.dev or not workspace.is_contiguous():
+            self.refuse()
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
-def _bytes(workspace) -> int:
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+    @property
+    def units(self) -> int:
+        s = self.shape
+        return s.batch * s.n_layers * s.n_kv_heads
 
 
 def kvc_prompt_attn_workspace_bytes(shape, n_q: int, with_docs: bool = False) -> int:
@@ -598,38 +622,40 @@ def kvc_prompt_attn(shape, q, k, v, out, q_len=None, kv_len=None, docs=None, mod
                     softmax_scale=0.0, row_lse=None, unit_status=None, workspace=None, stream=None):
     """Attention of q [B][L][H_q][n_q][d] over k, v [B][L][H_kv][T][d] (any strides whose innermost is 1;
     k and v alike) with score modifiers and documents (see include/kvc.h)."""
-    f, n_q = "kvc_prompt_attn", int(q.shape[3]) if q.dim() == 5 else 0
-    if v.stride() != k.stride() or v.shape != k.shape:
-        raise KvcError(f, 1)
-    _check(f, _load().kvc_prompt_attn(
-        ctypes.byref(shape), _p(q), _strides(f, q, shape, shape.n_q_heads, n_q), n_q, _p(k), _p(v),
-        _strides(f, k, shape, shape.n_kv_heads, shape.n_tokens),
-        _dense(f, q_len, torch.int32, shape.batch), _dense(f, kv_len, torch.int32, shape.batch),
-        _dense(f, docs, torch.int32, shape.batch * shape.n_tokens), _mods(f, mods, shape), float(softmax_scale),
-        _p(out), _strides(f, out, shape, shape.n_q_heads, n_q),
-        _dense(f, row_lse, torch.float32, shape.batch * shape.n_layers * shape.n_q_heads * n_q),
-        _dense(f, unit_status, torch.int32, _units(shape)), _p(workspace), _bytes(workspace), _stream(stream)))
+    c = _Call("kvc_prompt_attn", shape)
+    if q.dim() != 5 or v.stride() != k.stride():
+        c.refuse()
+    B, Hq, Hkv, T, n_q, i32 = shape.batch, shape.n_q_heads, shape.n_kv_heads, shape.n_tokens, q.shape[3], torch.int32
+    c.rows(v, Hkv, T)
+    ws, ws_bytes = c.space(workspace)
+    _check(c.fn, _load().kvc_prompt_attn(
+        ctypes.byref(shape), q.data_ptr(), c.rows(q, Hq), n_q, k.data_ptr(), v.data_ptr(), c.rows(k, Hkv, T),
+        c.dense(q_len, i32, B), c.dense(kv_len, i32, B), c.dense(docs, i32, B * T), c.mods(mods), softmax_scale,
+        out.data_ptr(), c.rows(out, Hq, n_q), c.dense(row_lse, torch.float32, B * shape.n_layers * Hq * n_q),
+        c.dense(unit_status, i32, c.units), ws, ws_bytes, _stream(stream)))
 
 
 def kvc_i4_append(shape, rows: I4Rows, k, v, n_new=None, unit_status=None, stream=None):
     """Quantise k, v [B][L][H_kv][n][d] into the rows behind those in use (see include/kvc.h)."""
-    f, r = "kvc_i4_append", rows.c()
+    c = _Call("kvc_i4_append", shape)
     if v.stride() != k.stride() or v.shape != k.shape:
-        raise KvcError(f, 1)
-    _check(f, _load().kvc_i4_append(
-        ctypes.byref(shape), ctypes.byref(r), _p(k), _p(v), _strides(f, k, shape, shape.n_kv_heads, -1),
-        int(k.shape[3]), _dense(f, n_new, torch.int32, shape.batch), _dense(f, unit_status, torch.int32, _units(shape)),
-        _stream(stream)))
+        c.refuse()
+    strides = c.rows(k, shape.n_kv_heads)
+    c.rows(v, shape.n_kv_heads)
+    _check(c.fn, _load().kvc_i4_append(
+        ctypes.byref(shape), c.cache(rows), k.data_ptr(), v.data_ptr(), strides, k.shape[3],
+        c.dense(n_new, torch.int32, shape.batch), c.dense(unit_status, torch.int32, c.units), _stream(stream)))
 
 
 def kvc_i4_read(shape, rows: I4Rows, k_out, v_out, stream=None):
     """Rows 0 .. n-1 of every unit as bf16 into k_out, v_out [B][L][H_kv][n][d] (see include/kvc.h)."""
-    f, r = "kvc_i4_read", rows.c()
+    c = _Call("kvc_i4_read", shape)
     if v_out.stride() != k_out.stride() or v_out.shape != k_out.shape:
-        raise KvcError(f, 1)
-    _check(f, _load().kvc_i4_read(
-        ctypes.byref(shape), ctypes.byref(r), int(k_out.shape[3]) if k_out.dim() == 5 else 0, _p(k_out),
-        _p(v_out), _strides(f, k_out, shape, shape.n_kv_heads, -1), _stream(stream)))
+        c.refuse()
+    strides = c.rows(k_out, shape.n_kv_heads)
+    c.rows(v_out, shape.n_kv_heads)
+    _check(c.fn, _load().kvc_i4_read(ctypes.byref(shape), c.cache(rows), k_out.shape[3], k_out.data_ptr(),
+                                     v_out.data_ptr(), strides, _stream(stream)))
 
 
 def kvc_i4_attn_workspace_bytes(shape, rows: I4Rows, n_q: int, add_mass: bool = False) -> int:
@@ -642,13 +668,15 @@ def kvc_i4_attn(shape, rows: I4Rows, q, out, q_pos=None, mods: Optional[ScoreMod
                 add_mass: bool = False, row_lse=None, workspace=None, stream=None):
     """Attention of q [B][L][H_q][n_q][d] over a 4-bit cache; add_mass adds the softmax weights to
     rows.mass (see include/kvc.h)."""
-    f, r, n_q = "kvc_i4_attn", rows.c(), int(q.shape[3]) if q.dim() == 5 else 0
-    _check(f, _load().kvc_i4_attn(
-        ctypes.byref(shape), ctypes.byref(r), _p(q), _strides(f, q, shape, shape.n_q_heads, n_q), n_q,
-        _dense(f, q_pos, torch.int32, shape.batch * n_q), _mods(f, mods, shape), float(softmax_scale),
-        ATTN_ADD_MASS if add_mass else 0, _p(out), _strides(f, out, shape, shape.n_q_heads, n_q),
-        _dense(f, row_lse, torch.float32, shape.batch * shape.n_layers * shape.n_q_heads * n_q), _p(workspace),
-        _bytes(workspace), _stream(stream)))
+    c = _Call("kvc_i4_attn", shape)
+    if q.dim() != 5:
+        c.refuse()
+    B, Hq, n_q = shape.batch, shape.n_q_heads, q.shape[3]
+    ws, ws_bytes = c.space(workspace)
+    _check(c.fn, _load().kvc_i4_attn(
+        ctypes.byref(shape), c.cache(rows), q.data_ptr(), c.rows(q, Hq), n_q, c.dense(q_pos, torch.int32, B * n_q),
+        c.mods(mods), softmax_scale, ATTN_ADD_MASS if add_mass else 0, out.data_ptr(), c.rows(out, Hq, n_q),
+        c.dense(row_lse, torch.float32, B * shape.n_layers * Hq * n_q), ws, ws_bytes, _stream(stream)))
 
 
 def kvc_i4_evict_workspace_bytes(shape, rows: I4Rows, budget: int) -> int:
@@ -659,8 +687,7 @@ def kvc_i4_evict_workspace_bytes(shape, rows: I4Rows, budget: int) -> int:
 def kvc_i4_evict(shape, rows: I4Rows, budget: int, n_sink: int, n_recent: int, unit_status=None, workspace=None,
                  stream=None):
     """Evict in place the rows of least mass above `budget` rows per unit (see include/kvc.h)."""
-    r = rows.c()
-    _check("kvc_i4_evict", _load().kvc_i4_evict(
-        ctypes.byref(shape), ctypes.byref(r), int(budget), int(n_sink), int(n_recent),
-        _dense("kvc_i4_evict", unit_status, torch.int32, _units(shape)), _p(workspace), _bytes(workspace),
-        _stream(stream)))
+    c = _Call("kvc_i4_evict", shape)
+    ws, ws_bytes = c.space(workspace)
+    _check(c.fn, _load().kvc_i4_evict(ctypes.byref(shape), c.cache(rows), budget, n_sink, n_recent,
+                                      c.dense(unit_status, torch.int32, c.units), ws, ws_bytes, _stream(stream)))

@@ -17,38 +17,67 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRowThreads = 256;
+constexpr int kBatch = 4;                        // rows of a thread whose loads are in flight together
 
-__device__ __forceinline__ float scale_of(uint16_t bits, bool row_mode) {
-  return row_mode ? __half2float(__ushort_as_half(bits)) : bf16_bits_to_float(bits);
-}
-
-// Quantises the 8 elements of this lane (lanes_per_group adjacent lanes share
-// a scale): packed codes, and the scale's bits.
-__device__ __forceinline__ uint32_t quantise8(const uint4& w, bool row_mode, int lanes_per_group, uint16_t* bits) {
+// Quantises the 8 elements of this lane (`lanes` adjacent lanes share a
+// scale): packed codes, and the scale's bits.
+//   scale = max / 7 rounded to the scale's format, code = rint(x / scale).
+// Both quotients come from a reciprocal and Markstein's correction, within
+// one ulp: the codes equal those of IEEE division (see div_by_recip), and so
+// does the rounded scale, because a / 7 for a bf16 a is never within an ulp of
+// a tie of either format (checked for every a).  rint is an addition of
+// 1.5 x 2^23 (a conversion to integer runs at a quarter of the rate); the
+// eight sums, 8 larger than their codes, are packed by shifted additions and
+// the offset is taken out at the end.  11 operations an element against 20.
+// Scales that are subnormal or clipped (where the quotient may exceed 7.5)
+// take the slow way.
+__device__ __forceinline__ uint32_t quantise8(const uint4& w, bool row_mode, int lanes, uint16_t* bits) {
   const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+  __nv_bfloat162 mx = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&r[0]));
+#pragma unroll
+  for (int i = 1; i < 4; ++i) mx = __hmax2(mx, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&r[i])));
+  float amax = fmaxf(__low2float(mx), __high2float(mx));
+  for (int o = 1; o < lanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+  float sc = div_by_recip(amax, 7.f, 0x1.24924ap-3f);       // the reciprocal of 7, rounded
+  uint16_t sb;
+  if (row_mode) {
+    sb = __half_as_ushort(__float2half_rn(sc));
+    sc = __half2float(__ushort_as_half(sb));
+  } else {
+    sb = float_to_bf16_bits(sc);
+    sc = bf16_bits_to_float(sb);
+  }
+  if (!(amax > 0.f)) {                           // a group of zeros: codes 0, scale 1
+    sc = 1.f;
+    sb = row_mode ? 0x3c00 : 0x3f80;
+  }
   float x[8];
-  float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(r[i] << 16);
     x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-    amax = fmaxf(amax, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
   }
-  for (int o = 1; o < lanes_per_group; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-  float sc = 1.f;
+  const bool fast = row_mode ? sc >= 0x1p-14f && sc < 65504.f : recip_div_ok(sc);
+  if (__all_sync(kFull, fast)) {
+    const float y = __frcp_rn(sc);
+    uint32_t pk = 0u - 0x3f400000u;                          // the exponents' part of the sum below
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      pk += __float_as_uint(__fadd_rn(div_by_recip(x[i], sc, y), 12582920.f)) << (4 * i);
+    *bits = sb;
+    return pk ^ 0x88888888u;
+  }
+  sc = 1.f;
   if (amax > 0.f) {
     const float s = __fdiv_rn(amax, 7.f);
     if (row_mode) sc = fmaxf(fminf(__half2float(__float2half_rn(s)), 65504.f), 0x1p-24f);
     else sc = fmaxf(bf16_bits_to_float(float_to_bf16_bits(s)), __uint_as_float(0x00010000u));   // 2^-133
   }
   *bits = row_mode ? __half_as_ushort(__float2half_rn(sc)) : float_to_bf16_bits(sc);
-  const bool fast = recip_div_ok(sc);
-  const float y = __fdiv_rn(1.f, sc);
   uint32_t pk = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    int q = __float2int_rn(fast ? div_by_recip(x[i], sc, y) : __fdiv_rn(x[i], sc));
-    q = max(-7, min(7, amax > 0.f ? q : 0));
+    const int q = max(-7, min(7, amax > 0.f ? __float2int_rn(__fdiv_rn(x[i], sc)) : 0));
     pk |= static_cast<uint32_t>(q & 0xf) << (4 * i);
   }
   return pk;
@@ -95,33 +124,40 @@ __global__ void __launch_bounds__(kRowThreads) i4_append_kernel(const I4AppendAr
   const int64_t src0 = b * a.st.batch + l * a.st.layer + h * a.st.head;
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   const bool row_mode = a.rows.quant_mode == KVC_QUANT_ROW_FP16;
-  const int i_end = (min(r.n, static_cast<int>((blockIdx.x + 1) * a.rows_per_block)) + RPB - 1) / RPB * RPB;
-  for (int i = blockIdx.x * a.rows_per_block + sub; i < i_end; i += RPB) {
-    const bool ok = i < r.n;
-    const int64_t src = src0 + static_cast<int64_t>(ok ? i : 0) * a.st.token + lane * 8;
-    const int64_t row = static_cast<int64_t>(u) * a.rows.capacity + r.slot + i;
-    uint4 w[2] = {};
-    if (ok) {
-      w[0] = __ldg(reinterpret_cast<const uint4*>(a.k + src));
-      w[1] = __ldg(reinterpret_cast<const uint4*>(a.v + src));
+  const int i_end = min(r.n, static_cast<int>((blockIdx.x + 1) * a.rows_per_block));
+  for (int i0 = blockIdx.x * a.rows_per_block; i0 < i_end; i0 += RPB * kBatch) {
+    uint4 w[kBatch][2];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * RPB + sub;
+      const int64_t src = src0 + static_cast<int64_t>(i) * a.st.token + lane * 8;
+      w[k][0] = i < i_end ? __ldcs(reinterpret_cast<const uint4*>(a.k + src)) : make_uint4(0, 0, 0, 0);
+      w[k][1] = i < i_end ? __ldcs(reinterpret_cast<const uint4*>(a.v + src)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      uint16_t bits;
-      const uint32_t pk = quantise8(w[v], row_mode, row_mode ? LPR : 4, &bits);
-      if (ok) {
-        static_cast<uint32_t*>(v ? a.rows.v : a.rows.k)[row * LPR + lane] = pk;
-        uint16_t* sp = static_cast<uint16_t*>(v ? a.rows.v_scale : a.rows.k_scale);
-        if (row_mode) {
-          if (lane == 0) sp[row] = bits;
-        } else if ((lane & 3) == 0) {
-          sp[row * (D / 32) + lane / 4] = bits;
+    for (int k = 0; k < kBatch; ++k) {
+      if (i0 + k * RPB >= i_end) break;            // for the whole block
+      const int i = i0 + k * RPB + sub;
+      const bool ok = i < i_end;
+      const int64_t row = static_cast<int64_t>(u) * a.rows.capacity + r.slot + i;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        uint16_t bits;
+        const uint32_t pk = quantise8(w[k][v], row_mode, row_mode ? LPR : 4, &bits);
+        if (ok) {
+          static_cast<uint32_t*>(v ? a.rows.v : a.rows.k)[row * LPR + lane] = pk;
+          uint16_t* sp = static_cast<uint16_t*>(v ? a.rows.v_scale : a.rows.k_scale);
+          if (row_mode) {
+            if (lane == 0) sp[row] = bits;
+          } else if ((lane & 3) == 0) {
+            sp[row * (D / 32) + lane / 4] = bits;
+          }
         }
       }
-    }
-    if (ok && lane == 0) {
-      a.rows.pos[row] = p0 + i;
-      if (a.rows.mass) a.rows.mass[row] = 0.f;
+      if (ok && lane == 0) {
+        a.rows.pos[row] = p0 + i;
+        if (a.rows.mass) a.rows.mass[row] = 0.f;
+      }
     }
   }
   if (gridDim.x == 1) {
@@ -135,6 +171,32 @@ __global__ void i4_advance_kernel(const I4AppendArgs a) {
   if (u < a.U) advance(a, u, room_of(a, u));
 }
 
+// The 8 codes of a word times their scale, as bf16 in element order, each
+// rounded once: codes are exact in bf16 (136 + code - 136), a bf16 scale
+// multiplies them in bf16, an fp16 scale in fp32.
+__device__ __forceinline__ uint4 dequantise8(uint32_t w, uint16_t scale, bool row_mode) {
+  uint32_t c[4];                                 // elements (0,4), (1,5), (2,6), (3,7)
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t x = ((w >> (4 * k)) & 0x000f000fu) ^ 0x43084308u;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c[k]) : "r"(x), "r"(0x43084308u));
+  }
+  if (row_mode) {
+    const float s = __half2float(__ushort_as_half(scale));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(c[k] << 16) * s, __uint_as_float(c[k] & 0xffff0000u) * s);
+      c[k] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+  } else {
+    const uint32_t s2 = scale * 0x10001u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(c[k]) : "r"(s2));
+  }
+  return make_uint4(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410), __byte_perm(c[0], c[1], 0x7632),
+                    __byte_perm(c[2], c[3], 0x7632));
+}
+
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) i4_read_kernel(const I4ReadArgs a) {
   constexpr int LPR = D / 8, RPB = kRowThreads / LPR;
@@ -146,45 +208,62 @@ __global__ void __launch_bounds__(kRowThreads) i4_read_kernel(const I4ReadArgs a
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   const bool row_mode = a.rows.quant_mode == KVC_QUANT_ROW_FP16;
   const int i_end = min(n, static_cast<int>((blockIdx.x + 1) * a.rows_per_block));
-  for (int i = blockIdx.x * a.rows_per_block + sub; i < i_end; i += RPB) {
-    const int64_t row = static_cast<int64_t>(u) * a.rows.capacity + i;
-    const int64_t dst = dst0 + static_cast<int64_t>(i) * a.st.token + lane * 8;
+  const int64_t row0 = static_cast<int64_t>(u) * a.rows.capacity;
+  for (int i0 = blockIdx.x * a.rows_per_block + sub; i0 < i_end; i0 += RPB * kBatch) {
+    uint32_t pk[kBatch][2];
+    uint16_t sb[kBatch][2];
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const uint32_t pk = __ldg(static_cast<const uint32_t*>(v ? a.rows.v : a.rows.k) + row * LPR + lane);
-      const uint16_t* sp = static_cast<const uint16_t*>(v ? a.rows.v_scale : a.rows.k_scale);
-      const float sc = scale_of(__ldg(sp + (row_mode ? row : row * (D / 32) + lane / 4)), row_mode);
-      uint32_t o[4];
+    for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-      for (int i2 = 0; i2 < 4; ++i2) {
-        const float lo = static_cast<float>(static_cast<int32_t>(pk << (28 - 8 * i2)) >> 28) * sc;
-        const float hi = static_cast<float>(static_cast<int32_t>(pk << (24 - 8 * i2)) >> 28) * sc;
-        o[i2] = float_to_bf16_bits(lo) | static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16;
+      for (int v = 0; v < 2; ++v) {
+        const int64_t row = row0 + min(i0 + k * RPB, i_end - 1);
+        pk[k][v] = __ldg(static_cast<const uint32_t*>(v ? a.rows.v : a.rows.k) + row * LPR + lane);
+        sb[k][v] = __ldg(static_cast<const uint16_t*>(v ? a.rows.v_scale : a.rows.k_scale) +
+                         (row_mode ? row : row * (D / 32) + lane / 4));
       }
-      *reinterpret_cast<uint4*>((v ? a.v : a.k) + dst) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * RPB;
+      if (i >= i_end) break;
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+        __stcs(reinterpret_cast<uint4*>((v ? a.v : a.k) + dst0 + static_cast<int64_t>(i) * a.st.token + lane * 8),
+               dequantise8(pk[k][v], sb[k][v], row_mode));
     }
   }
 }
 
 // ----------------------------------------------------------------------------
-// Eviction.  One block per unit.  The key of a row that may leave is (mass,
-// -pos) as one 64-bit number, so the rows that leave are the `over` smallest:
-// a radix select by 8-bit digits finds the `over`-th, and one ordered pass
-// over the slots lists the holes below the budget and the remaining rows
-// behind it.  Both lists have the same length; hole i takes row i.
+// Eviction.  One block per unit.  A row that may leave has the 64-bit key
+// (mass, -pos); the `over` rows of smallest key leave.
+//   * over = 1 (a token in, a row out): one reduction finds the row, and the
+//     row in slot `budget` takes its place.
+//   * else a radix select by 8-bit digits finds the `over`-th smallest key:
+//     four passes over the mass, which stops as soon as a digit's rows leave
+//     all together, and four over the positions where rows of equal mass have
+//     to be told apart.  Then every 32 slots give a word of leaving rows, and
+//     one prefix sum over the words lists the holes below the budget and the
+//     remaining rows behind it; hole i takes row i.
+// Bound by the latency of its few dependent steps for the caches it is meant
+// for (thousands of rows per unit).
 // ----------------------------------------------------------------------------
 constexpr int kEvictThreads = 1024;
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kHeld = 8;                         // mass keys of a thread kept in registers
+constexpr uint32_t kStays = 0xffffffffu;         // no key: above that of +inf
 
-__device__ __forceinline__ uint64_t evict_key(float mass, int32_t pos) {
+__device__ __forceinline__ uint32_t mass_key(float mass) {
   uint32_t b = __float_as_uint(mass);
   if (mass != mass) b = 0xff800000u;            // NaN: -inf
   if (b == 0x80000000u) b = 0u;                 // -0: +0
-  b = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return static_cast<uint64_t>(b) << 32 | ~(static_cast<uint32_t>(pos) ^ 0x80000000u);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// Exclusive prefix sum of v over the block, and the total.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
+__device__ __forceinline__ uint32_t pos_key(int32_t pos) { return ~(static_cast<uint32_t>(pos) ^ 0x80000000u); }
+
+// Exclusive prefix sum of v over the block, and the total.  A barrier has to
+// separate two calls' use of `sums`; the call ends with one.
+__device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -192,29 +271,79 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
     const int y = __shfl_up_sync(kFull, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) warp_sums[warp] = x;
+  if (lane == 31) sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
+  int s = sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, s, o);
+    if (lane >= o) s += y;
+  }
+  *total = __shfl_sync(kFull, s, 31);
+  const int before = warp ? __shfl_sync(kFull, s, warp - 1) : 0;
+  __syncthreads();
+  return before + x - v;
+}
+
+struct EvictSmem {
+  int hist[256];
+  int sums[kEvictWarps];
+  unsigned long long best[kEvictWarps];
+  int slot[kEvictWarps];
+  int bin, before, count;
+};
+
+// The digit of the `need`-th smallest among hist, and the number of keys
+// below it (warp 0; hist holds at least `need`).
+__device__ __forceinline__ void find_bin(EvictSmem& s, int need) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int h[8], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += h[k] = s.hist[lane * 8 + k];
+    int x = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, s, o);
-      if (lane >= o) s += y;
+      const int y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
     }
-    warp_sums[32 + lane] = s;
+    int before = x - sum;
+    if (before < need && need <= x) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (before < need && need <= before + h[k]) {
+          s.bin = lane * 8 + k;
+          s.before = before;
+          s.count = h[k];
+        }
+        before += h[k];
+      }
+    }
+    if (lane == 31 && x < need) s.bin = -1;
   }
-  __syncthreads();
-  *total = warp_sums[63];
-  const int before = x - v + (warp ? warp_sums[32 + warp - 1] : 0);
-  __syncthreads();
-  return before;
+}
+
+// Row `from` of the unit to slot `to` (one warp).
+__device__ __forceinline__ void move_row(const I4EvictArgs& a, int64_t to, int64_t from) {
+  const int lane = threadIdx.x & 31, words = a.d / 8;
+  const int sb = a.rows.quant_mode == KVC_QUANT_ROW_FP16 ? 1 : a.d / 32;
+  if (lane < words) {
+    static_cast<uint32_t*>(a.rows.k)[to * words + lane] = static_cast<const uint32_t*>(a.rows.k)[from * words + lane];
+    static_cast<uint32_t*>(a.rows.v)[to * words + lane] = static_cast<const uint32_t*>(a.rows.v)[from * words + lane];
+  } else if (lane >= 16 && lane < 16 + sb) {
+    const int g = lane - 16;
+    static_cast<uint16_t*>(a.rows.k_scale)[to * sb + g] = static_cast<const uint16_t*>(a.rows.k_scale)[from * sb + g];
+    static_cast<uint16_t*>(a.rows.v_scale)[to * sb + g] = static_cast<const uint16_t*>(a.rows.v_scale)[from * sb + g];
+  } else if (lane == 30) {
+    a.rows.pos[to] = a.rows.pos[from];
+  } else if (lane == 31) {
+    a.rows.mass[to] = a.rows.mass[from];
+  }
 }
 
 __global__ void __launch_bounds__(kEvictThreads) i4_evict_kernel(const I4EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int warp_sums[64];
-  __shared__ int s_bin, s_before, s_free;
-  const int u = blockIdx.x, tid = threadIdx.x;
+  __shared__ EvictSmem s;
+  const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cap = a.rows.capacity;
   const int cnt = a.rows.count[u];
   if (cnt < 0 || cnt > cap) {
@@ -224,96 +353,167 @@ __global__ void __launch_bounds__(kEvictThreads) i4_evict_kernel(const I4EvictAr
   const int over = cnt - a.budget;
   if (over <= 0) return;
   const int64_t base = static_cast<int64_t>(u) * cap;
-  int32_t* pos = a.rows.pos + base;
-  float* mass = a.rows.mass + base;
+  const int32_t* pos = a.rows.pos + base;
+  const float* mass = a.rows.mass + base;
   const int64_t first_recent = static_cast<int64_t>(a.rows.next_pos[u]) - a.n_recent;
-  auto may_leave = [&](int32_t p) { return p >= a.n_sink && p < first_recent; };
+  auto key_of = [&](int i) -> uint32_t {
+    const int32_t p = pos[i];
+    const float m = mass[i];
+    return p >= a.n_sink && p < first_recent ? mass_key(m) : kStays;
+  };
 
-  uint64_t prefix = 0;
-  int need = over;                     // rank of the threshold key among those that match the prefix
-  int shift = 56;
-#pragma unroll 1
-  for (; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
-    if (tid == 0) s_free = 0;
-    __syncthreads();
-    int mine = 0;
+  if (over == 1) {
+    unsigned long long best = ~0ull;
+    int at = -1;
     for (int i = tid; i < cnt; i += kEvictThreads) {
       const int32_t p = pos[i];
-      if (!may_leave(p)) continue;
-      const uint64_t key = evict_key(mass[i], p);
-      if (shift < 56 && (key >> (shift + 8)) != (prefix >> (shift + 8))) continue;
-      atomicAdd(&hist[(key >> shift) & 255], 1);
-      ++mine;
+      const float m = mass[i];
+      if (!(p >= a.n_sink && p < first_recent)) continue;
+      const unsigned long long key = static_cast<unsigned long long>(mass_key(m)) << 32 | pos_key(p);
+      if (key < best || at < 0) best = key, at = i;          // ascending slots: the lower of equal keys stays first
     }
-    if (mine) atomicAdd(&s_free, mine);
+    auto merge = [&](unsigned long long k2, int a2) {
+      if (a2 >= 0 && (at < 0 || k2 < best || (k2 == best && a2 < at))) best = k2, at = a2;
+    };
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const unsigned long long k2 = __shfl_xor_sync(kFull, best, o);
+      const int a2 = __shfl_xor_sync(kFull, at, o);
+      merge(k2, a2);
+    }
+    if (lane == 0) s.best[warp] = best, s.slot[warp] = at;
     __syncthreads();
-    if (s_free < need) {               // only at the first digit: too few rows may leave
+    if (warp) return;
+    best = s.best[lane], at = s.slot[lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const unsigned long long k2 = __shfl_xor_sync(kFull, best, o);
+      const int a2 = __shfl_xor_sync(kFull, at, o);
+      merge(k2, a2);
+    }
+    if (at < 0) {
+      if (lane == 0 && a.unit_status) a.unit_status[u] = KVC_UNIT_OVER_BUDGET;
+      return;
+    }
+    if (at < a.budget) move_row(a, base + at, base + a.budget);
+    if (lane == 0) a.rows.count[u] = a.budget;
+    return;
+  }
+
+  const bool held = cnt <= kEvictThreads * kHeld;
+  uint32_t key[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) key[k] = held && k * kEvictThreads + tid < cnt ? key_of(k * kEvictThreads + tid) : kStays;
+
+  // the threshold: rows whose key's top bits are below thr leave, and `need` of those that equal it
+  uint32_t thr = 0, thr_pos = 0;
+  int need = over, shift = 32, shift_pos = 32;
+  bool whole = false;
+#pragma unroll 1
+  while (shift > 0 && !whole) {
+    shift -= 8;
+    if (tid < 256) s.hist[tid] = 0;
+    __syncthreads();
+    auto count = [&](uint32_t x) {
+      if (x != kStays && (shift == 24 || x >> (shift + 8) == thr)) atomicAdd(&s.hist[(x >> shift) & 255], 1);
+    };
+    if (held) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) count(key[k]);
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < cnt; i += kEvictThreads) count(key_of(i));
+    }
+    __syncthreads();
+    find_bin(s, need);
+    __syncthreads();
+    if (s.bin < 0) {                    // only at the first digit: too few rows may leave
       if (tid == 0 && a.unit_status) a.unit_status[u] = KVC_UNIT_OVER_BUDGET;
       return;
     }
-    if (tid == 0) {
-      int before = 0, bin = 0;
-      while (before + hist[bin] < need) before += hist[bin++];
-      s_bin = bin;
-      s_before = before;
+    thr = thr << 8 | static_cast<uint32_t>(s.bin);
+    need -= s.before;
+    whole = s.count == need;
+    __syncthreads();
+  }
+  // equal mass: the later positions
+#pragma unroll 1
+  while (shift_pos > 0 && !whole) {
+    shift_pos -= 8;
+    if (tid < 256) s.hist[tid] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < cnt; i += kEvictThreads) {
+      if (key_of(i) != thr) continue;
+      const uint32_t x = pos_key(pos[i]);
+      if (shift_pos == 24 || x >> (shift_pos + 8) == thr_pos) atomicAdd(&s.hist[(x >> shift_pos) & 255], 1);
     }
     __syncthreads();
-    prefix |= static_cast<uint64_t>(s_bin) << shift;
-    need -= s_before;
-    const bool whole = hist[s_bin] == need;
+    find_bin(s, need);
     __syncthreads();
-    if (whole) break;
+    thr_pos = thr_pos << 8 | static_cast<uint32_t>(s.bin);
+    need -= s.before;
+    whole = s.count == need;
+    __syncthreads();
   }
-  // rows with key >> shift below the threshold's leave, and the first `need` that equal it
-  if (shift < 0) shift = 0;
-  const uint64_t thr = prefix >> shift;
+  const bool by_pos = shift_pos < 32;
+  auto below = [&](uint32_t x, int i) { return x != kStays && ((x >> shift) < thr || (by_pos && x == thr && (pos_key(pos[i]) >> shift_pos) < thr_pos)); };
+  auto equal = [&](uint32_t x, int i) { return x != kStays && (x >> shift) == thr && (!by_pos || (pos_key(pos[i]) >> shift_pos) == thr_pos); };
+
+  // a word of leaving rows per 32 slots; rows of one key and position leave in slot order
+  const int words = (cnt + 31) / 32;
+  uint32_t* leaves = a.words + static_cast<int64_t>(u) * a.n_words;
   int32_t* holes = a.lists + static_cast<int64_t>(u) * 2 * a.max_moves;
   int32_t* donors = holes + a.max_moves;
-  int n_eq = 0, n_holes = 0, n_donors = 0;
-  for (int i0 = 0; i0 < cnt; i0 += kEvictThreads) {
+  int n_eq = 0;
+  auto mark = [&](int i0, uint32_t x) {
     const int i = i0 + tid;
-    bool less = false, eq = false;
-    if (i < cnt) {
-      const int32_t p = pos[i];
-      if (may_leave(p)) {
-        const uint64_t key = evict_key(mass[i], p) >> shift;
-        less = key < thr;
-        eq = key == thr;
-      }
+    bool gone = i < cnt && below(x, i);
+    const bool eq = i < cnt && equal(x, i);
+    if (whole) {
+      gone |= eq;
+    } else {
+      int total;
+      const int rank = n_eq + block_scan(eq, s.sums, &total);
+      n_eq += total;
+      gone |= eq && rank < need;
     }
-    int total;
-    const int rank = n_eq + block_scan(eq, warp_sums, &total);
-    n_eq += total;
-    const bool leaves = less || (eq && rank < need);
-    const bool hole = leaves && i < a.budget, donor = i < cnt && !leaves && i >= a.budget;
-    const int at_h = n_holes + block_scan(hole, warp_sums, &total);
-    n_holes += total;
-    if (hole) holes[at_h] = i;
-    const int at_d = n_donors + block_scan(donor, warp_sums, &total);
-    n_donors += total;
-    if (donor) donors[at_d] = i;
+    const uint32_t word = __ballot_sync(kFull, gone);
+    if (lane == 0 && i < cnt) leaves[i >> 5] = word;
+  };
+  if (held) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (k * kEvictThreads < cnt) mark(k * kEvictThreads, key[k]);
+  } else {
+#pragma unroll 1
+    for (int i0 = 0; i0 < cnt; i0 += kEvictThreads) mark(i0, i0 + tid < cnt ? key_of(i0 + tid) : kStays);
   }
   __syncthreads();
-  const int half = a.d / 2, lane = tid & 31;
-  const int sb = a.rows.quant_mode == KVC_QUANT_ROW_FP16 ? 1 : a.d / 32;
-  for (int m = tid >> 5; m < n_holes; m += kEvictThreads / 32) {
-    const int64_t to = base + holes[m], from = base + donors[m];
-    const uint32_t* ks = static_cast<const uint32_t*>(a.rows.k) + from * (half / 4);
-    const uint32_t* vs = static_cast<const uint32_t*>(a.rows.v) + from * (half / 4);
-    if (lane < half / 4) {
-      static_cast<uint32_t*>(a.rows.k)[to * (half / 4) + lane] = ks[lane];
-      static_cast<uint32_t*>(a.rows.v)[to * (half / 4) + lane] = vs[lane];
-    } else if (lane >= 16 && lane < 16 + sb) {
-      const int g = lane - 16;
-      static_cast<uint16_t*>(a.rows.k_scale)[to * sb + g] = static_cast<const uint16_t*>(a.rows.k_scale)[from * sb + g];
-      static_cast<uint16_t*>(a.rows.v_scale)[to * sb + g] = static_cast<const uint16_t*>(a.rows.v_scale)[from * sb + g];
-    } else if (lane == 30) {
-      a.rows.pos[to] = a.rows.pos[from];
-    } else if (lane == 31) {
-      a.rows.mass[to] = a.rows.mass[from];
+  int n_holes = 0, n_donors = 0;
+#pragma unroll 1
+  for (int w0 = 0; w0 < words; w0 += kEvictThreads) {
+    const int w = w0 + tid, i0 = w * 32;
+    uint32_t h = 0, d = 0;
+    if (w < words) {
+      const uint32_t gone = leaves[w];
+      const int used = min(32, cnt - i0);
+      const uint32_t in_use = used == 32 ? ~0u : (1u << used) - 1;
+      const int below_budget = max(0, min(32, a.budget - i0));
+      const uint32_t front = below_budget == 32 ? ~0u : (1u << below_budget) - 1;
+      h = gone & front;
+      d = ~gone & in_use & ~front;
     }
+    int total;
+    int at = n_holes + block_scan(__popc(h), s.sums, &total);
+    n_holes += total;
+    for (; h; h &= h - 1) holes[at++] = i0 + __ffs(h) - 1;
+    at = n_donors + block_scan(__popc(d), s.sums, &total);
+    n_donors += total;
+    for (; d; d &= d - 1) donors[at++] = i0 + __ffs(d) - 1;
   }
+  __syncthreads();
+  for (int m = warp; m < n_holes; m += kEvictWarps) move_row(a, base + holes[m], base + donors[m]);
   if (tid == 0) a.rows.count[u] = a.budget;
 }
 
@@ -321,9 +521,9 @@ __global__ void __launch_bounds__(kEvictThreads) i4_evict_kernel(const I4EvictAr
 
 cudaError_t launch_i4_append(const I4AppendArgs& a0, cudaStream_t stream) {
   I4AppendArgs a = a0;
-  // up to 256 rows per block: enough blocks to fill the device from a few
-  // thousand rows on, and the rows of a short append in one launch
-  a.rows_per_block = 256;
+  // up to 256 rows of a unit in one block, which advances the counters itself
+  // (one launch); longer ones in blocks of 128 rows and a second launch
+  a.rows_per_block = a.n <= 256 ? 256 : 128;
   const dim3 grid((a.n + a.rows_per_block - 1) / a.rows_per_block, std::min(a.U, 65535), (a.U + 65534) / 65535);
   if (a.d == 128) i4_append_kernel<128><<<grid, kRowThreads, 0, stream>>>(a);
   else i4_append_kernel<64><<<grid, kRowThreads, 0, stream>>>(a);
@@ -333,7 +533,8 @@ cudaError_t launch_i4_append(const I4AppendArgs& a0, cudaStream_t stream) {
 
 cudaError_t launch_i4_read(const I4ReadArgs& a0, cudaStream_t stream) {
   I4ReadArgs a = a0;
-  a.rows_per_block = 256;
+  // one batch of rows per thread: blocks of 64 rows (128 at d = 64)
+  a.rows_per_block = kRowThreads / (a.d / 8) * kBatch;
   const dim3 grid((a.n + a.rows_per_block - 1) / a.rows_per_block, std::min(a.U, 65535), (a.U + 65534) / 65535);
   if (a.d == 128) i4_read_kernel<128><<<grid, kRowThreads, 0, stream>>>(a);
   else i4_read_kernel<64><<<grid, kRowThreads, 0, stream>>>(a);

@@ -1116,7 +1116,8 @@ kvc_status kvc_i4_attn(const kvc_shape* shape, const kvc_i4_rows* rows, const vo
 
 size_t kvc_i4_evict_workspace_bytes(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t budget) {
   if (check_i4(shape, rows) != KVC_OK || budget < 1 || budget >= rows->capacity) return 0;
-  return static_cast<size_t>(n_units(shape)) * 2 * std::min(budget, rows->capacity - budget) * sizeof(int32_t);
+  const int64_t moves = std::min(budget, rows->capacity - budget), words = (static_cast<int64_t>(rows->capacity) + 31) / 32;
+  return static_cast<size_t>(n_units(shape)) * (2 * moves + words) * sizeof(int32_t);
 }
 
 kvc_status kvc_i4_evict(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t budget,
@@ -1137,7 +1138,9 @@ kvc_status kvc_i4_evict(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t
   a.n_recent = n_recent;
   a.max_moves = budget < rows->capacity ? std::min(budget, rows->capacity - budget) : 0;
   a.rows = *rows;
+  a.n_words = static_cast<int32_t>((static_cast<int64_t>(rows->capacity) + 31) / 32);
   a.lists = static_cast<int32_t*>(workspace);
+  a.words = reinterpret_cast<uint32_t*>(a.lists) + static_cast<int64_t>(a.U) * 2 * a.max_moves;
   a.unit_status = unit_status;
   return launch_i4_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }

@@ -276,7 +276,9 @@ struct I4EvictArgs {
   int32_t U, d, budget, n_sink, n_recent;
   int32_t max_moves;           // entries of each list
   kvc_i4_rows rows;
+  int32_t n_words;             // words of 32 slots
   int32_t* lists;              // [U][2][max_moves]: holes, donors
+  uint32_t* words;             // [U][n_words]: bits of the rows that leave
   int32_t* unit_status;        // optional [U]
 };
 
