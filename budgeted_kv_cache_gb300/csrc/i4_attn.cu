@@ -77,6 +77,17 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Scales of one key times `by`, as fp32.
+__device__ __forceinline__ void put_scales(float* to, uint2 s, float by) {
+  *reinterpret_cast<float4*>(to) =
+      make_float4(__uint_as_float(s.x << 16) * by, __uint_as_float(s.x & 0xffff0000u) * by, __uint_as_float(s.y << 16) * by,
+                  __uint_as_float(s.y & 0xffff0000u) * by);
+}
+__device__ __forceinline__ void put_scales(float* to, uint32_t s, float by) {
+  *reinterpret_cast<float2*>(to) = make_float2(__uint_as_float(s << 16) * by, __uint_as_float(s & 0xffff0000u) * by);
+}
+__device__ __forceinline__ void put_scales(float* to, uint16_t s, float by) { *to = __half2float(__ushort_as_half(s)) * by; }
+
 struct Unit {
   int u, b, l, g, n, R;
   int64_t base;
@@ -106,7 +117,7 @@ __device__ __forceinline__ void split_range(const I4AttnArgs& a, int n, int spli
 template <int D, int NT, bool ROW>
 struct Smem {
   alignas(128) uint8_t codes[kWarps][kStages][2][kTile][D / 2];
-  alignas(16) uint16_t scale[kWarps][2][kTile][ROW ? 1 : D / 32];
+  alignas(16) float scale[kWarps][2][kTile][ROW ? 1 : D / 32];
   int32_t pos[kWarps][kTile];
   float m[kWarps][NT * 8], l[kWarps][NT * 8];
   alignas(16) float o[NT * 8][D + 4];
@@ -126,17 +137,32 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
   int t0, t1;
   split_range(a, un.n, split, &t0, &t1);
 
-  // one warp's copies of tile i: 16-byte chunks of key and value codes, rows past n filled with zeros
+  // one warp's copies of tile i: this lane's 16-byte chunk of every 32 / CH rows; rows past n filled with zeros
   auto swz = [](int row, int chunk) { return D == 128 ? chunk ^ ((row >> 1) & 3) : chunk ^ ((row >> 2) & 1); };
+  constexpr int RPC = 32 / CH;                     // rows per copy instruction of a warp
+  const int c_row = lane / CH, c_chunk = lane % CH;
+  const uint32_t c_dst = smem_u32(&s.codes[warp][0][0][c_row][swz(c_row, c_chunk) * 16]);
+  const int64_t c_src = (un.base + c_row) * (D / 2) + c_chunk * 16;
+  const uint8_t* const c_k = static_cast<const uint8_t*>(a.rows.k) + c_src;
+  const uint8_t* const c_v = static_cast<const uint8_t*>(a.rows.v) + c_src;
   auto copy_tile = [&](int i, int st) {
     if (i < t1) {
+      const int64_t at = static_cast<int64_t>(i) * (kTile * D / 2);
+      const uint32_t dst = c_dst + st * (2 * kTile * D / 2);
+      const int left = un.n - i * kTile - c_row;   // rows from this lane's first on
+      if (i * kTile + kTile <= un.n) {
 #pragma unroll
-      for (int c = lane; c < kTile * CH; c += 32) {
-        const int row = c / CH, chunk = c % CH, j = i * kTile + row;
-        const bool ok = j < un.n;
-        const int64_t at = (un.base + (ok ? j : 0)) * (D / 2) + chunk * 16;
-        cp_async16(smem_u32(&s.codes[warp][st][0][row][swz(row, chunk) * 16]), static_cast<const uint8_t*>(a.rows.k) + at, ok);
-        cp_async16(smem_u32(&s.codes[warp][st][1][row][swz(row, chunk) * 16]), static_cast<const uint8_t*>(a.rows.v) + at, ok);
+        for (int r = 0; r < kTile; r += RPC) {
+          cp_async16(dst + r * (D / 2), c_k + at + r * (D / 2), true);
+          cp_async16(dst + (kTile + r) * (D / 2), c_v + at + r * (D / 2), true);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < kTile; r += RPC) {
+          const bool ok = r < left;
+          cp_async16(dst + r * (D / 2), ok ? c_k + at + r * (D / 2) : c_k, ok);
+          cp_async16(dst + (kTile + r) * (D / 2), ok ? c_v + at + r * (D / 2) : c_v, ok);
+        }
       }
     }
     cp_async_commit();
@@ -147,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
   int32_t pos_next = 0;
   auto fetch = [&](int i) {
     const int j = i * kTile + lane;
+    ks_next = vs_next = Scales{};                  // rows behind those in use: no garbage meets a zero weight
     if (i < t1 && j < un.n) {
       ks_next = __ldg(static_cast<const Scales*>(a.rows.k_scale) + un.base + j);
       vs_next = __ldg(static_cast<const Scales*>(a.rows.v_scale) + un.base + j);
@@ -189,7 +216,19 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
   }
 
   const bool capped = a.mods.softcap > 0.f, biased = a.mods.slopes != nullptr;
-  const float cs = a.scale * kLog2e;
+  const bool modified = capped || biased;
+  const float pre = capped ? a.scale : a.scale * kLog2e;      // goes into the key scales
+  int hi_min = INT32_MAX, lo_max = INT32_MIN;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      hi_min = min(hi_min, q_hi[nt][e]);
+      lo_max = max(lo_max, q_lo[nt][e]);
+    }
+  hi_min = __reduce_min_sync(kFull, hi_min);
+  lo_max = __reduce_max_sync(kFull, lo_max);
+  float* const log_row = a.logits + (un.base + g) * a.logit_stride + r0 + 2 * t;
   const uint32_t half_sel = (g >> 2) ? 0x7632u : 0x5410u;
   float m[NT][2], l[NT][2], o[NG][2][NT][4];
 #pragma unroll
@@ -207,24 +246,26 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
   for (int i = t0 + warp; i < t1; i += kWarps) {
     copy_tile(i + (kStages - 1) * kWarps, (st + kStages - 1) % kStages);
     // scales and positions of this tile: one lane per key, then to all
-    *reinterpret_cast<Scales*>(&s.scale[warp][0][lane][0]) = ks_next;
-    *reinterpret_cast<Scales*>(&s.scale[warp][1][lane][0]) = vs_next;
+    put_scales(&s.scale[warp][0][lane][0], ks_next, pre);
+    put_scales(&s.scale[warp][1][lane][0], vs_next, 1.f);
     s.pos[warp][lane] = pos_next;
+    // does every query row see every key of the tile?
+    const bool clear = __all_sync(kFull, i * kTile + lane < un.n && pos_next <= hi_min && pos_next >= lo_max);
     fetch(i + kWarps);
     cp_async_wait<kStages - 1>();
     __syncwarp();
     const uint8_t* kc = &s.codes[warp][st][0][0][0];
     const uint8_t* vc = &s.codes[warp][st][1][0][0];
     auto scale_f = [&](int which, int key, float (&f)[NG]) {
+      const float* w = &s.scale[warp][which][key][0];
       if constexpr (ROW) {
-        f[0] = __half2float(__ushort_as_half(s.scale[warp][which][key][0]));
+        f[0] = w[0];
+      } else if constexpr (NG == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(w);
+        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
       } else {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&s.scale[warp][which][key][0]);
-#pragma unroll
-        for (int k = 0; k < NG / 2; ++k) {
-          f[2 * k] = __uint_as_float(w[k] << 16);
-          f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        }
+        const float2 v = *reinterpret_cast<const float2*>(w);
+        f[0] = v.x, f[1] = v.y;
       }
     };
 
@@ -262,31 +303,41 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
           }
         }
       }
-      const int pk[2] = {s.pos[warp][k0], s.pos[warp][k1]};
-      const bool in_use[2] = {i * kTile + k0 < un.n, i * kTile + k1 < un.n};
+      if constexpr (ROW) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int e = c & 1, k = c >> 1;
-          float x = y[sub][nt][c];
-          if constexpr (ROW) x *= k ? f1[0] : f0[0];
-          if (capped) x = a.mods.softcap * tanhf(x * a.scale / a.mods.softcap) * kLog2e;
-          else x *= cs;
-          if (biased) x = fmaf(-slope[nt][e], fabsf(static_cast<float>(q_hi[nt][e] - pk[k])), x);
-          const bool seen = in_use[k] && ((pk[k] <= q_hi[nt][e] && pk[k] >= q_lo[nt][e]) || pk[k] < prefix);
-          y[sub][nt][c] = seen ? x : -INFINITY;
-        }
+          for (int c = 0; c < 4; ++c) y[sub][nt][c] *= c < 2 ? f0[0] : f1[0];
+      }
+      if (modified || !clear) {
+        const int pk[2] = {s.pos[warp][k0], s.pos[warp][k1]};
+        const bool in_use[2] = {i * kTile + k0 < un.n, i * kTile + k1 < un.n};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int e = c & 1, k = c >> 1;
+            float x = y[sub][nt][c];
+            if (capped) x = a.mods.softcap * tanhf(x / a.mods.softcap) * kLog2e;
+            if (biased) x = fmaf(-slope[nt][e], fabsf(static_cast<float>(q_hi[nt][e] - pk[k])), x);
+            const bool seen = in_use[k] && ((pk[k] <= q_hi[nt][e] && pk[k] >= q_lo[nt][e]) || pk[k] < prefix);
+            y[sub][nt][c] = seen ? x : -INFINITY;
+          }
+      }
       if (a.logits) {
         // [unit][key][R rounded up to even]
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (!in_use[k]) continue;
-          float* dst = a.logits + (un.base + i * kTile + (k ? k1 : k0)) * a.logit_stride + r0 + 2 * t;
+        float* dst = log_row + (static_cast<int64_t>(i) * kTile + sub * 16) * a.logit_stride;
+        if (clear || i * kTile + k0 < un.n) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             if (r0 + nt * 8 + 2 * t < a.logit_stride)
-              *reinterpret_cast<float2*>(dst + nt * 8) = make_float2(y[sub][nt][2 * k], y[sub][nt][2 * k + 1]);
+              *reinterpret_cast<float2*>(dst + nt * 8) = make_float2(y[sub][nt][0], y[sub][nt][1]);
+        }
+        if (clear || i * kTile + k1 < un.n) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            if (r0 + nt * 8 + 2 * t < a.logit_stride)
+              *reinterpret_cast<float2*>(dst + 8 * a.logit_stride + nt * 8) = make_float2(y[sub][nt][2], y[sub][nt][3]);
         }
       }
     }
@@ -323,15 +374,17 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
         }
     }
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int e = 0; e < 2; ++e) {
+        const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float ref = m[nt][c & 1];
-          y[sub][nt][c] = ex2_approx(y[sub][nt][c] - (ref == -INFINITY ? 0.f : ref));
-          l[nt][c & 1] += y[sub][nt][c];
+        for (int k = 0; k < 4; ++k) {
+          float& x = y[k >> 1][nt][(k & 1) * 2 + e];
+          x = ex2_approx(x - ref);
+          l[nt][e] += x;
         }
+      }
 
     // ---- O^T += V^T P^T
 #pragma unroll
@@ -340,12 +393,6 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
       float f0[NG], f1[NG];
       scale_f(1, k0, f0);
       scale_f(1, k1, f1);
-      const bool in0 = i * kTile + k0 < un.n, in1 = i * kTile + k1 < un.n;
-#pragma unroll
-      for (int gr = 0; gr < (ROW ? 1 : NG); ++gr) {
-        if (!in0) f0[gr] = 0.f;                    // scales behind the rows in use may be NaN
-        if (!in1) f1[gr] = 0.f;
-      }
       uint32_t pb[NT][2];
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
@@ -451,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
 // Second kernel: blocks [0, a.merge_blocks) of a unit join the splits of its
 // rows, the others add the weights of their keys to the mass.
 constexpr int kFinThreads = 256;
+constexpr int kMassKeys = 1024;                  // keys of a block that adds mass
 
 template <int D>
 __global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs a) {
@@ -461,20 +509,26 @@ __global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs
   if (static_cast<int>(blockIdx.x) < a.merge_blocks) {
     const int r = blockIdx.x * (kFinThreads / 32) + warp;
     if (r >= un.R) return;
-    const float2* ml = a.part_ml + (static_cast<int64_t>(un.u) * un.R + r) * a.splits;
+    const int64_t part = (static_cast<int64_t>(un.u) * un.R + r) * a.splits;
     float top = -INFINITY;
-    for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, ml[i].x);
+    for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, a.part_ml[part + i].x);
     for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
     float x[D / 32] = {}, sum = 0.f;
-    for (int i = 0; i < a.splits; ++i) {
-      const float2 v = ml[i];
-      if (v.x == -INFINITY) continue;
-      const float w = ex2_approx(v.x - top);
+    for (int i0 = 0; i0 < a.splits; i0 += 32) {
+      // lane i holds split i's weight; the outputs of eight splits are on their way together
+      const float2 v = i0 + lane < a.splits ? a.part_ml[part + i0 + lane] : make_float2(-INFINITY, 0.f);
+      const float w = v.x == -INFINITY ? 0.f : ex2_approx(v.x - top);
       sum = fmaf(v.y, w, sum);
-      const float* src = a.part_o + ((static_cast<int64_t>(un.u) * un.R + r) * a.splits + i) * D + lane * (D / 32);
+      const int n = min(32, a.splits - i0);
+      const float* src = a.part_o + (part + i0) * D + lane * (D / 32);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(kFull, w, i);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) x[c] = fmaf(src[c], w, x[c]);
+        for (int c = 0; c < D / 32; ++c) x[c] = fmaf(src[i * D + c], wi, x[c]);
+      }
     }
+    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(kFull, sum, k);
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     __nv_bfloat16* out = a.out + un.q_at(a, a.os, r) + lane * (D / 32);
 #pragma unroll
@@ -482,7 +536,7 @@ __global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs
     if (lane == 0 && a.lse) a.lse[un.lse_at(a, r)] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
     return;
   }
-  const int j0 = (blockIdx.x - a.merge_blocks) * a.mass_keys;
+  const int j0 = (blockIdx.x - a.merge_blocks) * kMassKeys;
   if (j0 >= un.n) return;
   for (int r = warp; r < un.R; r += kFinThreads / 32) {
     const float2* ml = a.part_ml + (static_cast<int64_t>(un.u) * un.R + r) * a.splits;
@@ -495,12 +549,23 @@ __global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs
     if (lane == 0) lse2[r] = sum > 0.f ? top + log2f(sum) : 0.f;      // nothing seen: every logit is -inf
   }
   __syncthreads();
-  const int j1 = min(un.n, j0 + a.mass_keys);
-  for (int j = j0 + threadIdx.x; j < j1; j += kFinThreads) {
-    const float* y = a.logits + (un.base + j) * a.logit_stride;
-    float sum = 0.f;
-    for (int r = 0; r < un.R; ++r) sum += ex2_approx(y[r] - lse2[r]);
-    a.rows.mass[un.base + j] += sum;
+  // four keys of a thread at once, two query rows per load
+  for (int j = j0 + threadIdx.x; j < j0 + kMassKeys; j += kFinThreads * 4) {
+    float sum[4] = {};
+    for (int r = 0; r < un.R; r += 2) {
+      float2 y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int jk = min(j + k * kFinThreads, un.n - 1);
+        y[k] = *reinterpret_cast<const float2*>(a.logits + (un.base + jk) * a.logit_stride + r);
+      }
+      const float l0 = lse2[r], l1 = lse2[min(r + 1, un.R - 1)];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum[k] += ex2_approx(y[k].x - l0) + (r + 1 < un.R ? ex2_approx(y[k].y - l1) : 0.f);   // a padding column adds nothing
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (j + k * kFinThreads < un.n) a.rows.mass[un.base + j + k * kFinThreads] += sum[k];
   }
 }
 
@@ -530,7 +595,7 @@ cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream) {
   const bool row = a.rows.quant_mode == KVC_QUANT_ROW_FP16;
   cudaError_t e = a.d == 128 ? (row ? launch_rows<128, true>(a, stream) : launch_rows<128, false>(a, stream))
                              : (row ? launch_rows<64, true>(a, stream) : launch_rows<64, false>(a, stream));
-  const int mass_blocks = a.add_mass ? (a.rows.capacity + a.mass_keys - 1) / a.mass_keys : 0;
+  const int mass_blocks = a.add_mass ? (a.rows.capacity + kMassKeys - 1) / kMassKeys : 0;
   if (e != cudaSuccess || a.merge_blocks + mass_blocks == 0) return e;
   const dim3 grid(a.merge_blocks + mass_blocks, std::min(a.U, 65535), (a.U + 65534) / 65535);
   const size_t bytes = a.add_mass ? static_cast<size_t>(a.n_q) * a.G * sizeof(float) : 0;

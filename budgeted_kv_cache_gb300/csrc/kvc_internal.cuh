@@ -265,7 +265,6 @@ struct I4AttnArgs {
   bool add_mass;
   int32_t splits;              // blocks that share a unit's keys
   int32_t merge_blocks;        // second kernel: blocks per unit that join splits (0: nothing to join)
-  int32_t mass_keys;           // second kernel: keys per block that adds mass
   int32_t logit_stride;        // n_q G rounded up to even
   float* part_o;               // splits > 1: [U][n_q G][splits][d]
   float2* part_ml;             // splits > 1 or add_mass: [U][n_q G][splits]
