@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "kvc_internal.cuh"
+#include "packed_math.cuh"
 
 namespace kvc {
 
@@ -70,11 +71,6 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   asm("lop3.b32 %0, %1, 0x000f000f, 0x43084308, 0x6a;" : "=r"(r) : "r"(w));      // (w & mask) ^ magic
   asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0x43084308u));
   return r;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Scales of one key times `by`, as fp32.
@@ -218,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
   const bool capped = a.mods.softcap > 0.f, biased = a.mods.slopes != nullptr;
   const bool modified = capped || biased;
   const float pre = capped ? a.scale : a.scale * kLog2e;      // goes into the key scales
+  const float inv_cap = capped ? 1.f / a.mods.softcap : 0.f;
   int hi_min = INT32_MAX, lo_max = INT32_MIN;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -310,6 +307,16 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
           for (int c = 0; c < 4; ++c) y[sub][nt][c] *= c < 2 ? f0[0] : f1[0];
       }
       if (modified || !clear) {
+        // cap tanh(x / cap): a polynomial while the warp's |x| <= cap, else cap (1 - 2 / (1 + e^(2 x / cap)))
+        bool small = true;
+        if (capped) {
+          float big = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) big = fmaxf(big, fabsf(y[sub][nt][c]));
+          small = __all_sync(kFull, big * inv_cap <= 1.f);
+        }
         const int pk[2] = {s.pos[warp][k0], s.pos[warp][k1]};
         const bool in_use[2] = {i * kTile + k0 < un.n, i * kTile + k1 < un.n};
 #pragma unroll
@@ -318,7 +325,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
           for (int c = 0; c < 4; ++c) {
             const int e = c & 1, k = c >> 1;
             float x = y[sub][nt][c];
-            if (capped) x = a.mods.softcap * tanhf(x / a.mods.softcap) * kLog2e;
+            if (capped) x = small ? x * poly_tanh_over_z(x * inv_cap) * kLog2e
+                                  : fmaf(-2.f * a.mods.softcap, rcp_approx(1.f + ex2_approx(x * (inv_cap * (2.f * kLog2e)))),
+                                         a.mods.softcap) * kLog2e;
             if (biased) x = fmaf(-slope[nt][e], fabsf(static_cast<float>(q_hi[nt][e] - pk[k])), x);
             const bool seen = in_use[k] && ((pk[k] <= q_hi[nt][e] && pk[k] >= q_lo[nt][e]) || pk[k] < prefix);
             y[sub][nt][c] = seen ? x : -INFINITY;

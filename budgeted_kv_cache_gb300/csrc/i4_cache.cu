@@ -10,6 +10,7 @@
 #include <algorithm>
 
 #include "kvc_internal.cuh"
+#include "packed_math.cuh"
 
 namespace kvc {
 
@@ -19,28 +20,32 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRowThreads = 256;
 constexpr int kBatch = 4;                        // rows of a thread whose loads are in flight together
 
-// Quantises the 8 elements of this lane (`lanes` adjacent lanes share a
+// Quantises the 8 elements of this lane (`LANES` adjacent lanes share a
 // scale): packed codes, and the scale's bits.
 //   scale = max / 7 rounded to the scale's format, code = rint(x / scale).
-// Both quotients come from a reciprocal and Markstein's correction, within
-// one ulp: the codes equal those of IEEE division (see div_by_recip), and so
-// does the rounded scale, because a / 7 for a bf16 a is never within an ulp of
-// a tie of either format (checked for every a).  rint is an addition of
-// 1.5 x 2^23 (a conversion to integer runs at a quarter of the rate); the
-// eight sums, 8 larger than their codes, are packed by shifted additions and
-// the offset is taken out at the end.  11 operations an element against 20.
+// Both quotients are q0 = x y, q = q0 + (x - q0 b) y (Markstein) with y within
+// one ulp of 1 / b.  The codes equal those of IEEE division: checked for every
+// bf16 mantissa against every bf16 and fp16 scale mantissa with y one ulp off
+// either way; and so does the rounded scale, because a / 7 for a bf16 a is
+// never within an ulp of a tie of either format (checked for every a).  rint
+// is an addition of 1.5 x 2^23 (a conversion to integer runs at a quarter of
+// the rate); the eight sums, 8 larger than their codes, are packed by shifted
+// additions and the offset is taken out at the end.  Everything but the
+// packing works on two elements per instruction.
 // Scales that are subnormal or clipped (where the quotient may exceed 7.5)
 // take the slow way.
-__device__ __forceinline__ uint32_t quantise8(const uint4& w, bool row_mode, int lanes, uint16_t* bits) {
+template <bool ROW, int LANES>
+__device__ __forceinline__ uint32_t quantise8(const uint4& w, uint16_t* bits) {
   const uint32_t r[4] = {w.x, w.y, w.z, w.w};
   __nv_bfloat162 mx = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&r[0]));
 #pragma unroll
   for (int i = 1; i < 4; ++i) mx = __hmax2(mx, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&r[i])));
   float amax = fmaxf(__low2float(mx), __high2float(mx));
-  for (int o = 1; o < lanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
   float sc = div_by_recip(amax, 7.f, 0x1.24924ap-3f);       // the reciprocal of 7, rounded
   uint16_t sb;
-  if (row_mode) {
+  if (ROW) {
     sb = __half_as_ushort(__float2half_rn(sc));
     sc = __half2float(__ushort_as_half(sb));
   } else {
@@ -49,35 +54,36 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& w, bool row_mode, int
   }
   if (!(amax > 0.f)) {                           // a group of zeros: codes 0, scale 1
     sc = 1.f;
-    sb = row_mode ? 0x3c00 : 0x3f80;
+    sb = ROW ? 0x3c00 : 0x3f80;
   }
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(r[i] << 16);
-    x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-  }
-  const bool fast = row_mode ? sc >= 0x1p-14f && sc < 65504.f : recip_div_ok(sc);
+  const bool fast = ROW ? sc >= 0x1p-14f && sc < 65504.f : recip_div_ok(sc);
   if (__all_sync(kFull, fast)) {
-    const float y = __frcp_rn(sc);
+    const float y = rcp_approx(sc);
+    const uint64_t y2 = pair(y, y), nb2 = pair(-sc, -sc), round2 = pair(12582920.f, 12582920.f);
     uint32_t pk = 0u - 0x3f400000u;                          // the exponents' part of the sum below
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      pk += __float_as_uint(__fadd_rn(div_by_recip(x[i], sc, y), 12582920.f)) << (4 * i);
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t x2 = pair(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xffff0000u));
+      const uint64_t q0 = mul2(x2, y2);
+      float lo, hi;
+      unpair(add2(fma2(fma2(q0, nb2, x2), y2, q0), round2), &lo, &hi);
+      pk += (__float_as_uint(lo) << (8 * i)) + (__float_as_uint(hi) << (8 * i + 4));
+    }
     *bits = sb;
     return pk ^ 0x88888888u;
   }
   sc = 1.f;
   if (amax > 0.f) {
     const float s = __fdiv_rn(amax, 7.f);
-    if (row_mode) sc = fmaxf(fminf(__half2float(__float2half_rn(s)), 65504.f), 0x1p-24f);
+    if (ROW) sc = fmaxf(fminf(__half2float(__float2half_rn(s)), 65504.f), 0x1p-24f);
     else sc = fmaxf(bf16_bits_to_float(float_to_bf16_bits(s)), __uint_as_float(0x00010000u));   // 2^-133
   }
-  *bits = row_mode ? __half_as_ushort(__float2half_rn(sc)) : float_to_bf16_bits(sc);
+  *bits = ROW ? __half_as_ushort(__float2half_rn(sc)) : float_to_bf16_bits(sc);
   uint32_t pk = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int q = max(-7, min(7, amax > 0.f ? __float2int_rn(__fdiv_rn(x[i], sc)) : 0));
+    const float x = __uint_as_float(i & 1 ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
+    const int q = max(-7, min(7, amax > 0.f ? __float2int_rn(__fdiv_rn(x, sc)) : 0));
     pk |= static_cast<uint32_t>(q & 0xf) << (4 * i);
   }
   return pk;
@@ -113,51 +119,64 @@ __device__ __forceinline__ void advance(const I4AppendArgs& a, int u, const Room
 // Row block blockIdx.x of unit blockIdx.y (+ 65535 blockIdx.z).  A unit of
 // one block advances its own counters; those of several blocks are advanced
 // by the next kernel, after every block has read them.
-template <int D>
-__global__ void __launch_bounds__(kRowThreads) i4_append_kernel(const I4AppendArgs a) {
-  constexpr int LPR = D / 8, RPB = kRowThreads / LPR;
+template <int D, bool ROW, int THREADS>
+__global__ void __launch_bounds__(THREADS) i4_append_kernel(const I4AppendArgs a) {
+  constexpr int LPR = D / 8, RPB = THREADS / LPR, NS = ROW ? 1 : D / 32;
   const int u = blockIdx.y + blockIdx.z * 65535;
   if (u >= a.U) return;
   const Room r = room_of(a, u);
-  const int32_t p0 = a.rows.next_pos[u];
   const int h = u % a.Hkv, l = u / a.Hkv % a.L, b = u / (a.Hkv * a.L);
-  const int64_t src0 = b * a.st.batch + l * a.st.layer + h * a.st.head;
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
-  const bool row_mode = a.rows.quant_mode == KVC_QUANT_ROW_FP16;
   const int i_end = min(r.n, static_cast<int>((blockIdx.x + 1) * a.rows_per_block));
-  for (int i0 = blockIdx.x * a.rows_per_block; i0 < i_end; i0 += RPB * kBatch) {
-    uint4 w[kBatch][2];
+  const int first = blockIdx.x * a.rows_per_block;
+  const int64_t src = b * a.st.batch + l * a.st.layer + h * a.st.head + (first + sub) * a.st.token + lane * 8;
+  const int64_t step = RPB * a.st.token;
+  const uint16_t* ks = reinterpret_cast<const uint16_t*>(a.k) + src;
+  const uint16_t* vs = reinterpret_cast<const uint16_t*>(a.v) + src;
+  const int64_t row = static_cast<int64_t>(u) * a.rows.capacity + r.slot + first + sub;
+  uint32_t* codes[2] = {static_cast<uint32_t*>(a.rows.k) + row * LPR + lane, static_cast<uint32_t*>(a.rows.v) + row * LPR + lane};
+  const bool has_scale = ROW ? lane == 0 : (lane & 3) == 0;
+  uint16_t* scales[2] = {static_cast<uint16_t*>(a.rows.k_scale) + row * NS + (ROW ? 0 : lane / 4),
+                         static_cast<uint16_t*>(a.rows.v_scale) + row * NS + (ROW ? 0 : lane / 4)};
+  int32_t* pos = a.rows.pos + row;
+  float* mass = a.rows.mass + row;
+  int32_t p = a.rows.next_pos[u] + first + sub;
+#pragma unroll 1
+  for (int left = i_end - first; left > 0; left -= RPB * kBatch) {       // rows of the block still to do
+    uint4 w[kBatch][2] = {};
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (k * RPB + sub < left) {
+        w[k][0] = __ldcs(reinterpret_cast<const uint4*>(ks + k * step));
+        w[k][1] = __ldcs(reinterpret_cast<const uint4*>(vs + k * step));
+      }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * RPB + sub;
-      const int64_t src = src0 + static_cast<int64_t>(i) * a.st.token + lane * 8;
-      w[k][0] = i < i_end ? __ldcs(reinterpret_cast<const uint4*>(a.k + src)) : make_uint4(0, 0, 0, 0);
-      w[k][1] = i < i_end ? __ldcs(reinterpret_cast<const uint4*>(a.v + src)) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (i0 + k * RPB >= i_end) break;            // for the whole block
-      const int i = i0 + k * RPB + sub;
-      const bool ok = i < i_end;
-      const int64_t row = static_cast<int64_t>(u) * a.rows.capacity + r.slot + i;
+      if (k * RPB >= left) break;                  // for the whole block
+      const bool ok = k * RPB + sub < left;
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         uint16_t bits;
-        const uint32_t pk = quantise8(w[k][v], row_mode, row_mode ? LPR : 4, &bits);
+        const uint32_t pk = quantise8<ROW, ROW ? LPR : 4>(w[k][v], &bits);
         if (ok) {
-          static_cast<uint32_t*>(v ? a.rows.v : a.rows.k)[row * LPR + lane] = pk;
-          uint16_t* sp = static_cast<uint16_t*>(v ? a.rows.v_scale : a.rows.k_scale);
-          if (row_mode) {
-            if (lane == 0) sp[row] = bits;
-          } else if ((lane & 3) == 0) {
-            sp[row * (D / 32) + lane / 4] = bits;
-          }
+          codes[v][k * RPB * LPR] = pk;
+          if (has_scale) scales[v][k * RPB * NS] = bits;
         }
       }
       if (ok && lane == 0) {
-        a.rows.pos[row] = p0 + i;
-        if (a.rows.mass) a.rows.mass[row] = 0.f;
+        pos[k * RPB] = p + k * RPB;
+        if (a.rows.mass) mass[k * RPB] = 0.f;
       }
+    }
+    ks += kBatch * step;
+    vs += kBatch * step;
+    pos += kBatch * RPB;
+    mass += kBatch * RPB;
+    p += kBatch * RPB;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      codes[v] += kBatch * RPB * LPR;
+      scales[v] += kBatch * RPB * NS;
     }
   }
   if (gridDim.x == 1) {
@@ -247,7 +266,7 @@ __global__ void __launch_bounds__(kRowThreads) i4_read_kernel(const I4ReadArgs a
 // Bound by the latency of its few dependent steps for the caches it is meant
 // for (thousands of rows per unit).
 // ----------------------------------------------------------------------------
-constexpr int kEvictThreads = 1024;
+constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kHeld = 8;                         // mass keys of a thread kept in registers
 constexpr uint32_t kStays = 0xffffffffu;         // no key: above that of +inf
@@ -273,7 +292,7 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
   }
   if (lane == 31) sums[warp] = x;
   __syncthreads();
-  int s = sums[lane];
+  int s = lane < kEvictWarps ? sums[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(kFull, s, o);
@@ -341,7 +360,7 @@ __device__ __forceinline__ void move_row(const I4EvictArgs& a, int64_t to, int64
   }
 }
 
-__global__ void __launch_bounds__(kEvictThreads) i4_evict_kernel(const I4EvictArgs a) {
+__global__ void __launch_bounds__(kEvictThreads, 2) i4_evict_kernel(const I4EvictArgs a) {
   __shared__ EvictSmem s;
   const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cap = a.rows.capacity;
@@ -384,7 +403,8 @@ __global__ void __launch_bounds__(kEvictThreads) i4_evict_kernel(const I4EvictAr
     if (lane == 0) s.best[warp] = best, s.slot[warp] = at;
     __syncthreads();
     if (warp) return;
-    best = s.best[lane], at = s.slot[lane];
+    best = ~0ull, at = -1;
+    if (lane < kEvictWarps) best = s.best[lane], at = s.slot[lane];
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       const unsigned long long k2 = __shfl_xor_sync(kFull, best, o);
@@ -519,14 +539,26 @@ __global__ void __launch_bounds__(kEvictThreads) i4_evict_kernel(const I4EvictAr
 
 }  // namespace
 
+namespace {
+
+template <int D, bool ROW>
+void append(const I4AppendArgs& a, dim3 grid, bool wide, cudaStream_t stream) {
+  if (wide) i4_append_kernel<D, ROW, 512><<<grid, 512, 0, stream>>>(a);
+  else i4_append_kernel<D, ROW, 256><<<grid, 256, 0, stream>>>(a);
+}
+
+}  // namespace
+
 cudaError_t launch_i4_append(const I4AppendArgs& a0, cudaStream_t stream) {
   I4AppendArgs a = a0;
   // up to 256 rows of a unit in one block, which advances the counters itself
-  // (one launch); longer ones in blocks of 128 rows and a second launch
+  // (one launch), 512 threads from 64 rows on; longer ones in blocks of 128
+  // rows and a second launch
   a.rows_per_block = a.n <= 256 ? 256 : 128;
+  const bool wide = a.n > 64 && a.n <= 256, row = a.rows.quant_mode == KVC_QUANT_ROW_FP16;
   const dim3 grid((a.n + a.rows_per_block - 1) / a.rows_per_block, std::min(a.U, 65535), (a.U + 65534) / 65535);
-  if (a.d == 128) i4_append_kernel<128><<<grid, kRowThreads, 0, stream>>>(a);
-  else i4_append_kernel<64><<<grid, kRowThreads, 0, stream>>>(a);
+  if (a.d == 128) row ? append<128, true>(a, grid, wide, stream) : append<128, false>(a, grid, wide, stream);
+  else row ? append<64, true>(a, grid, wide, stream) : append<64, false>(a, grid, wide, stream);
   if (grid.x > 1) i4_advance_kernel<<<(a.U + 255) / 256, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }

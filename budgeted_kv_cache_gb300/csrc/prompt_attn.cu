@@ -35,6 +35,7 @@
 #include <algorithm>
 
 #include "kvc_internal.cuh"
+#include "packed_math.cuh"
 
 namespace kvc {
 
@@ -90,9 +91,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// mbar_wait by a whole warp, with one answer for all lanes (what follows is
+__device__ __forceinline__ bool try_once(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait by a whole warp, with one answer for all lanes (what follows is
 // executed by the warp together).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (__all_sync(0xffffffffu, try_once(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
@@ -116,57 +132,6 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
   return d;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-
-__device__ __forceinline__ void unpair(uint64_t v, float* lo, float* hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// tanh(z) / z from u = z^2 in [0, 1]: degree-6 polynomial fitted at Chebyshev
-// points (tanh within 1.8e-7 of its value).
-__device__ __forceinline__ uint64_t tanh_over_z(uint64_t u) {
-  const float c[7] = {0.9999999403953552f,  -0.33332857489585876f, 0.13325397670269012f, -0.05346517637372017f,
-                      0.020305519923567772f, -0.006217069923877716f, 0.0010455535957589746f};
-  uint64_t r = pair(c[6], c[6]);
-#pragma unroll
-  for (int k = 5; k >= 0; --k) r = fma2(r, u, pair(c[k], c[k]));
-  return r;
 }
 
 // Bits [lo, hi) of a 32-bit word, either end outside it allowed.
