@@ -69,14 +69,51 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A bf16, two elements of K per column.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// The MMA warp stays converged and lets one elected lane issue, by predicate:
+// under `if (lane == 0)` the compiler keeps descriptors in per-thread
+// registers and moves each to the uniform ones in front of every instruction
+// (58 cycles an MMA measured, 118 in this kernel, whatever its size; 30 for
+// 128 x 64 x 16 this way, which is the tensor core's own time).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(p));
+  return p;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A bf16, two elements of K per column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(elected)
       : "memory");
 }
 
@@ -351,6 +388,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     const uint32_t idesc_o = mma_idesc_bf16(128, D) | (1u << 16);     // B (values) MN-major
     TileWalk walk(t, table, q_min, q_max), walk_v(t, table, q_min, q_max);
     bool ok = warp_wait(smem_u32(&s.qfull), 0, abort_flag);
+    const uint32_t elected = elect_one();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t q_desc = sw128_desc(smem_u32(sq)), k_desc = sw128_desc(smem_u32(sk)), val_desc = v_desc(smem_u32(sv));
     int n_k = 0, n_v = 0;                // K and V tiles taken up
     bool k_more = true;
     // the scores of step x (stream x & 1); false when there is no such step
@@ -365,20 +405,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       } else if (!k_more) {
         return false;
       }
-      if (lane == 0) {
-        tc_fence_after();
-        const uint32_t st = (n_k - 1) % C::kNk;
-        const uint64_t qd = sw128_desc(smem_u32(sq + (share ? h : 0) * C::kTile));
-        const uint64_t kd = sw128_desc(smem_u32(sk + st * C::kTile));
+      tc_fence_after();
+      const uint32_t st = (n_k - 1) % C::kNk;
+      const uint64_t qd = q_desc + (share ? h : 0) * (C::kTile >> 4), kd = k_desc + st * (C::kTile >> 4);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * (kChunkBytes >> 4) + (ks & 3) * 2;
-          tc_mma_bf16(tmem + h * 128, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u);
-        }
-        tc_commit(smem_u32(&s.sfull[h]));
-        if (!share || h == 1) tc_commit(smem_u32(&s.kempty[st]));
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t off = (ks >> 2) * (kChunkBytes >> 4) + (ks & 3) * 2;
+        mma_ss(tm + h * 128, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u, elected);
       }
-      __syncwarp();
+      commit(smem_u32(&s.sfull[h]), elected);
+      if (!share || h == 1) commit(smem_u32(&s.kempty[st]), elected);
       return true;
     };
     auto values = [&](int x) -> bool {
@@ -407,18 +443,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         }
       }
       if (!warp_wait(smem_u32(&s.pfull[h]), (x >> 1) & 1, abort_flag)) return false;
-      if (lane == 0) {
-        tc_fence_after();
-        const uint32_t st = (n_v - 1) % C::kNv;
-        const uint64_t vd = v_desc(smem_u32(sv + st * C::kTile));
+      tc_fence_after();
+      const uint32_t st = (n_v - 1) % C::kNv;
+      const uint64_t vd = val_desc + st * (C::kTile >> 4);
+      const uint32_t more = x > 1 ? 1u : 0u;
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks)
-          tc_mma_ts(tmem + kOCol + h * 128, tmem + h * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o,
-                    (x > 1 || ks > 0) ? 1u : 0u);
-        tc_commit(smem_u32(&s.odone[h]));
-        if (!share || h == 1) tc_commit(smem_u32(&s.vempty[st]));
-      }
-      __syncwarp();
+      for (int ks = 0; ks < kKeys / 16; ++ks)
+        mma_ts(tm + kOCol + h * 128, tm + h * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o, ks > 0 ? 1u : more,
+               elected);
+      commit(smem_u32(&s.odone[h]), elected);
+      if (!share || h == 1) commit(smem_u32(&s.vempty[st]), elected);
       return true;
     };
     if (ok) {
@@ -430,8 +464,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       }
     }
     // all MMAs issued above complete before tensor memory is freed
-    if (lane == 0) tc_commit(smem_u32(&s.done));
-    __syncwarp();
+    commit(smem_u32(&s.done), elected);
     drain(smem_u32(&s.done), 0);
   }
   } else {
