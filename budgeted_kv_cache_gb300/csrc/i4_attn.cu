@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
           for (int c = 0; c < 4; ++c) y[sub][nt][c] *= c < 2 ? f0[0] : f1[0];
       }
       if (modified || !clear) {
-        // cap tanh(x / cap): a polynomial while the warp's |x| <= cap, else cap (1 - 2 / (1 + e^(2 x / cap)))
+        // cap tanh(x / cap): a polynomial while the warp's |x / cap| is small, else cap (1 - 2 / (1 + e^(2 x / cap)))
         bool small = true;
         if (capped) {
           float big = 0.f;
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c) big = fmaxf(big, fabsf(y[sub][nt][c]));
-          small = __all_sync(kFull, big * inv_cap <= 1.f);
+          small = __all_sync(kFull, big * inv_cap <= kTanhRange);
         }
         const int pk[2] = {s.pos[warp][k0], s.pos[warp][k1]};
         const bool in_use[2] = {i * kTile + k0 < un.n, i * kTile + k1 < un.n};
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
           for (int c = 0; c < 4; ++c) {
             const int e = c & 1, k = c >> 1;
             float x = y[sub][nt][c];
-            if (capped) x = small ? x * poly_tanh_over_z(x * inv_cap) * kLog2e
+            if (capped) x = small ? x * tanh_over_z(x * inv_cap) * kLog2e
                                   : fmaf(-2.f * a.mods.softcap, rcp_approx(1.f + ex2_approx(x * (inv_cap * (2.f * kLog2e)))),
                                          a.mods.softcap) * kLog2e;
             if (biased) x = fmaf(-slope[nt][e], fabsf(static_cast<float>(q_hi[nt][e] - pk[k])), x);

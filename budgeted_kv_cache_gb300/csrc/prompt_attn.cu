@@ -256,7 +256,7 @@ struct TileWalk {
 
 struct Bars {
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
-  uint64_t sfull[2], pfull[2], odone[2], qfull, done;
+  uint64_t sfull[2], phalf[2], pfull[2], odone[2], qfull, done;
   uint32_t tmem;
   int abort_flag;
   int q_min, q_max;
@@ -288,6 +288,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.sfull[i]), 1);
+      mbar_init(smem_u32(&s.phalf[i]), 4);
       mbar_init(smem_u32(&s.pfull[i]), 4);
       mbar_init(smem_u32(&s.odone[i]), 1);
     }
@@ -442,15 +443,20 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
           __syncwarp();
         }
       }
-      if (!warp_wait(smem_u32(&s.pfull[h]), (x >> 1) & 1, abort_flag)) return false;
+      if (!warp_wait(smem_u32(&s.phalf[h]), (x >> 1) & 1, abort_flag)) return false;
       tc_fence_after();
       const uint32_t st = (n_v - 1) % C::kNv;
       const uint64_t vd = val_desc + st * (C::kTile >> 4);
       const uint32_t more = x > 1 ? 1u : 0u;
 #pragma unroll
-      for (int ks = 0; ks < kKeys / 16; ++ks)
+      for (int ks = 0; ks < kKeys / 32; ++ks)
         mma_ts(tm + kOCol + h * 128, tm + h * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o, ks > 0 ? 1u : more,
                elected);
+      if (!warp_wait(smem_u32(&s.pfull[h]), (x >> 1) & 1, abort_flag)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = kKeys / 32; ks < kKeys / 16; ++ks)
+        mma_ts(tm + kOCol + h * 128, tm + h * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o, 1u, elected);
       commit(smem_u32(&s.odone[h]), elected);
       if (!share || h == 1) commit(smem_u32(&s.vempty[st]), elected);
       return true;
@@ -486,9 +492,19 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     int my_doc = 0;
     if (docs) my_doc = p >= 0 && p < t.nk ? __ldg(docs + p) : -1;
     if (p < 0 || my_doc < 0) row_hi = row_lo = row_pre = 0;
+    // tiles that every row of the warp sees whole: keys [all_lo, all_hi) and [0, all_pre)
+    const int all_lo = __reduce_max_sync(0xffffffffu, valid ? row_lo : 0);
+    const int all_hi = __reduce_min_sync(0xffffffffu, valid ? row_hi : INT32_MAX);
+    const int all_pre = __reduce_min_sync(0xffffffffu, valid ? row_pre : INT32_MAX);
     const float cs = CAP || BIAS ? 1.f : a.scale * kLog2e;
     const float cap = a.mods.softcap;
     const float zs = CAP ? a.scale / cap : 0.f;
+    float tc[5];                               // the polynomial's coefficients for s
+    if constexpr (CAP) {
+      float f = zs * cap * kLog2e;
+#pragma unroll
+      for (int k = 0; k < 5; ++k, f *= zs * zs) tc[k] = kTanh[k] * f;
+    }
     const float slope2 = BIAS ? a.mods.slopes[head] * kLog2e : 0.f;
     float m = -INFINITY, l = 0.f;              // reference maximum (of y / cs) and sum of 2^(y - m cs)
     TileWalk walk(t, table, q_min, q_max);
@@ -506,7 +522,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       tc_fence_after();
       if (!warp_valid) {                       // nothing of this warp is a row: the product's result is not read
         tc_fence_before();
-        if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&s.phalf[h]));
+          mbar_arrive(smem_u32(&s.pfull[h]));
+        }
         continue;
       }
       uint32_t sr[4][32];
@@ -517,20 +536,21 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       float (&y)[4][32] = reinterpret_cast<float (&)[4][32]>(sr);
       const int j0 = tile * kKeys;
       if constexpr (CAP) {
-        // z = s scale / cap; the polynomial as long as the warp's |z| <= 1 (logits within the cap)
+        // z = s scale / cap; cap tanh(z) log2 e = s times a polynomial in s^2 as long as the warp's |z| are small
         float big = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) big = fmaxf(big, fmaxf(fabsf(y[c][e]), fabsf(y[c][e + 1])));
-        if (__all_sync(0xffffffffu, big * zs <= 1.f || !valid)) {
-          const uint64_t zs2 = pair(zs, zs), out2 = pair(cap * kLog2e, cap * kLog2e);
+        if (__all_sync(0xffffffffu, (big * zs <= kTanhRange && big < 1e18f) || !valid)) {
+          const uint64_t k4 = pair(tc[4], tc[4]), k3 = pair(tc[3], tc[3]), k2 = pair(tc[2], tc[2]), k1 = pair(tc[1], tc[1]),
+                         k0 = pair(tc[0], tc[0]);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const uint64_t z = mul2(pair(y[c][e], y[c][e + 1]), zs2);
-              unpair(mul2(mul2(z, out2), tanh_over_z(mul2(z, z))), &y[c][e], &y[c][e + 1]);
+              const uint64_t x = pair(y[c][e], y[c][e + 1]), w = mul2(x, x);
+              unpair(mul2(x, fma2(fma2(fma2(fma2(k4, w, k3), w, k2), w, k1), w, k0)), &y[c][e], &y[c][e + 1]);
             }
         } else {
           // cap tanh(z) = cap (1 - 2 / (1 + e^2z)): right at both infinities
@@ -549,15 +569,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
           for (int e = 0; e < 32; ++e) y[c][e] = fmaf(-slope2, fabsf(far - static_cast<float>(c * 32 + e)), y[c][e] * by);
       }
       // masks, unless every row of the warp sees the whole tile
-      bool whole = j0 + kKeys <= row_pre || (j0 >= row_lo && j0 + kKeys <= row_hi);
+      const bool whole = j0 + kKeys <= all_pre || (j0 >= all_lo && j0 + kKeys <= all_hi);
       bool same = true;
       if (docs) {
         const int2 d = __ldg(table + tile);
-        same = d.x == d.y && d.x == my_doc;
+        same = __all_sync(0xffffffffu, (d.x == d.y && d.x == my_doc) || !valid);
       }
-      if (!__all_sync(0xffffffffu, (whole && same) || !valid)) {
+      if (!whole || !same) {
         uint32_t eq[4] = {~0u, ~0u, ~0u, ~0u};
-        if (docs && !__all_sync(0xffffffffu, same || !valid)) {
+        if (!same) {
           // the keys of each document that the warp's rows have, one document after another
           int kd[4];
 #pragma unroll
@@ -631,6 +651,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
           pk[e / 2] = pack_bf16x2(p0, p1);
         }
         tmem_st16(s_col + c * 16, pk);
+        if (c == 1) {                          // the product may start on the first half of the keys
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s.phalf[h]));
+        }
       }
       float s0, s1;
       unpair(add2(sum[0], sum[1]), &s0, &s1);
