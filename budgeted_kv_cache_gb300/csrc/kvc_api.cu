@@ -406,17 +406,21 @@ kvc_status plan_prompt(const kvc_shape* s, int32_t n_q, bool with_docs, PromptPl
   return KVC_OK;
 }
 
-// [B][L][H][n][d] bf16 tensor as (d, n, H, L, B) in boxes of 64 x 128 rows.
+// [B][L][H][n][d] bf16 tensor in boxes of 64 columns, `rows` tokens and
+// `group` heads: token by token within a head, as (d, n, H, L, B), or head by
+// head within a token, as (d, H, n, L, B).
 kvc_status encode_rows(CUtensorMap* map, const void* ptr, const kvc_shape* s, int64_t heads, int64_t n,
-                       const kvc_strides& st) {
+                       const kvc_strides& st, int rows, int group, bool by_token) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return KVC_ERR_CUDA;
-  cuuint64_t dims[5] = {static_cast<cuuint64_t>(s->head_dim), static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(heads),
-                        static_cast<cuuint64_t>(s->n_layers), static_cast<cuuint64_t>(s->batch)};
-  const int64_t given[4] = {st.token, st.head, st.layer, st.batch};
+  const cuuint64_t d = static_cast<cuuint64_t>(s->head_dim), nn = static_cast<cuuint64_t>(n),
+                   hh = static_cast<cuuint64_t>(heads);
+  cuuint64_t dims[5] = {d, by_token ? hh : nn, by_token ? nn : hh, static_cast<cuuint64_t>(s->n_layers),
+                        static_cast<cuuint64_t>(s->batch)};
+  const int64_t given[4] = {by_token ? st.head : st.token, by_token ? st.token : st.head, st.layer, st.batch};
   cuuint64_t strides[4];
   for (int i = 0; i < 4; ++i) strides[i] = given[i] > 0 ? given[i] * 2 : s->head_dim * 2;   // 0: a dimension of size 1
-  cuuint32_t box[5] = {64, kTileTokens, 1, 1, 1};
+  cuuint32_t box[5] = {64, static_cast<cuuint32_t>(by_token ? group : rows), static_cast<cuuint32_t>(by_token ? rows : group), 1, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1010,10 +1014,12 @@ kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_stri
     a.part_ml = reinterpret_cast<float2*>(ws + p.ws_docs);
     a.part_o = reinterpret_cast<float*>(ws + p.ws_docs + p.ws_ml);
   }
-  CUtensorMap mk, mv;
-  if ((st = encode_rows(&mk, k, shape, shape->n_kv_heads, shape->n_tokens, a.kvs)) != KVC_OK) return st;
-  if ((st = encode_rows(&mv, v, shape, shape->n_kv_heads, shape->n_tokens, a.kvs)) != KVC_OK) return st;
-  return launch_prompt(a, mk, mv, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+  a.q_tma = 128 % a.G == 0;
+  CUtensorMap mq = {}, mk, mv;
+  if (a.q_tma && (st = encode_rows(&mq, q, shape, shape->n_q_heads, n_q, a.qs, 128 / a.G, a.G, true)) != KVC_OK) return st;
+  if ((st = encode_rows(&mk, k, shape, shape->n_kv_heads, shape->n_tokens, a.kvs, kTileTokens, 1, false)) != KVC_OK) return st;
+  if ((st = encode_rows(&mv, v, shape, shape->n_kv_heads, shape->n_tokens, a.kvs, kTileTokens, 1, false)) != KVC_OK) return st;
+  return launch_prompt(a, mq, mk, mv, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
 kvc_status kvc_i4_append(const kvc_shape* shape, const kvc_i4_rows* rows, const void* k,

@@ -230,6 +230,7 @@ struct PromptArgs {
   float* part_o;               // splits > 1: [U][n_q G][splits][d] unnormalised outputs
   float2* part_ml;             // [U][n_q G][splits] (log2-domain maximum, sum)
   int2* doc_tiles;             // with docs: [B][n_tiles] (min, max) document
+  bool q_tma;                  // G divides 128: a tile of rows is a box of whole queries
 };
 
 struct I4AppendArgs {
@@ -303,7 +304,8 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_engine(const DecodeArgs& a, cudaStream_t stream);
 size_t prompt_smem_bytes(int d);
-cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream);
+cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v,
+                          cudaStream_t stream);
 cudaError_t launch_i4_append(const I4AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_read(const I4ReadArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream);

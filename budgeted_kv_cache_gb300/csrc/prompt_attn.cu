@@ -27,8 +27,8 @@
 // the item sees are zeroed in shared memory (0 x NaN is NaN in a product).
 //
 // Warp roles (12 warps): 0-3 and 4-7 softmax of stream 0 and 1 (a row of 128
-// scores per thread in registers: their warpgroups take 208 registers a
-// thread, the third gives them up and keeps 88; 2 x 208 + 88 = 3 x 168, what
+// scores per thread in registers: their warpgroups take 200 registers a
+// thread, the third gives them up and keeps 104; 2 x 200 + 104 = 3 x 168, what
 // the block was launched with), 8 TMA producer, 9 TMEM owner and MMA issuer.  Every wait is bounded; one that
 // gives up raises a shared abort flag, the unit is marked KVC_UNIT_TIMEOUT
 // and the CTA drains its copies and MMAs before it frees tensor memory.
@@ -217,30 +217,43 @@ __device__ __forceinline__ Item make_item(const PromptArgs& a, int id) {
   t.skip = max(0, lo_tile - pre_tiles);
   t.n = max(pre_tiles, hi_tile) - t.skip;
   if (hi_tile <= lo_tile) t.n = pre_tiles, t.skip = 0;
-  t.i0 = static_cast<int>(static_cast<int64_t>(t.n) * t.split / a.splits);
-  t.i1 = static_cast<int>(static_cast<int64_t>(t.n) * (t.split + 1) / a.splits);
+  t.i0 = static_cast<int>(static_cast<uint32_t>(t.n) * t.split / a.splits);     // tiles < 2^24, splits <= 256
+  t.i1 = t.split + 1 == a.splits ? t.n : static_cast<int>(static_cast<uint32_t>(t.n) * (t.split + 1) / a.splits);
+  return t;
+}
+
+// The same value in every lane, known as such to the compiler (uniform
+// registers, and no divergence after a branch on it).
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+__device__ __forceinline__ Item uniform_item(const Item& from) {
+  static_assert(sizeof(Item) % 4 == 0, "an Item is ints");
+  Item t;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(Item) / 4); ++i)
+    reinterpret_cast<int*>(&t)[i] = uniform(reinterpret_cast<const int*>(&from)[i]);
   return t;
 }
 
 // The tiles of an item that may be seen, in order; every lane of the warp
 // calls next() together.
 struct TileWalk {
-  const Item& t;
+  int skip_at, skip, end;
   const int2* table;           // [tiles] (min, max) document of each key tile, or null
   int q_min, q_max;            // documents of the item's queries
   int at, base;
   uint32_t mask;
-  __device__ TileWalk(const Item& t_, const int2* table_, int q_min_, int q_max_)
-      : t(t_), table(table_), q_min(q_min_), q_max(q_max_), at(t_.i0), base(0), mask(0) {}
-  __device__ __forceinline__ int tile(int i) const { return i + (i >= t.skip_at ? t.skip : 0); }
+  __device__ TileWalk(const Item& t, const int2* table_, int q_min_, int q_max_)
+      : skip_at(t.skip_at), skip(t.skip), end(t.i1), table(table_), q_min(q_min_), q_max(q_max_), at(t.i0), base(0), mask(0) {}
+  __device__ __forceinline__ int tile(int i) const { return i + (i >= skip_at ? skip : 0); }
   __device__ __forceinline__ int next() {
-    if (!table) return at < t.i1 ? tile(at++) : -1;
+    if (!table) return at < end ? tile(at++) : -1;
 #pragma unroll 1
     while (mask == 0) {
-      if (at >= t.i1) return -1;
+      if (at >= end) return -1;
       const int i = at + (threadIdx.x & 31);
       bool ok = false;
-      if (i < t.i1) {
+      if (i < end) {
         const int2 d = __ldg(table + tile(i));
         ok = d.y >= q_min && d.x <= q_max;
       }
@@ -248,7 +261,7 @@ struct TileWalk {
       base = at;
       at += 32;
     }
-    const int i = base + __ffs(mask) - 1;
+    const int i = base + __ffs(mask) - 1;          // uniform: a ballot's bits
     mask &= mask - 1;
     return tile(i);
   }
@@ -260,12 +273,14 @@ struct Bars {
   uint32_t tmem;
   int abort_flag;
   int q_min, q_max;
+  Item item;
 };
 
 // D: head dimension.  CAP, BIAS: the logits are capped, or get slopes.
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
-prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+              const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -275,10 +290,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
   Bars& s = *reinterpret_cast<Bars*>(sv + C::kNv * C::kTile);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &s.abort_flag;
-  const Item t = make_item(a, blockIdx.x);
-  if (t.rows == 0) return;                             // rows past the sequence's queries
-  const bool share = t.rows > kTileRows;               // two Q tiles, or two streams over one
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&s.kfull[i]), 1);
@@ -292,7 +303,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       mbar_init(smem_u32(&s.pfull[i]), 4);
       mbar_init(smem_u32(&s.odone[i]), 1);
     }
-    mbar_init(smem_u32(&s.qfull), 8);
+    mbar_init(smem_u32(&s.qfull), a.q_tma ? 1 : 8);
     mbar_init(smem_u32(&s.done), 1);
     s.abort_flag = 0;
     s.q_min = INT32_MAX;
@@ -303,47 +314,78 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     tmem_alloc(smem_u32(&s.tmem), kTmemCols);
     tmem_relinquish();
   }
+  if (threadIdx.x == 0) s.item = make_item(a, blockIdx.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s.tmem;
+  const uint32_t tmem = uniform(s.tmem);
+  const Item t = uniform_item(s.item);
+  const bool share = t.rows > kTileRows;               // two Q tiles, or two streams over one
+  if (t.rows == 0) {                                   // rows past the sequence's queries
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
   const int32_t* docs = a.docs ? a.docs + static_cast<int64_t>(t.b) * a.T : nullptr;
   const int2* table = a.docs ? a.doc_tiles + static_cast<int64_t>(t.b) * a.n_tiles : nullptr;
 
-  // Q tiles (softmax warps, one row per thread) and the documents of their positions
+  // Q tiles: one copy per 64 columns and tile where whole queries fill a tile's rows (the producer issues it), else
+  // the softmax warps load their 32 rows, two at a time (16 lanes a row; four at d = 64), and store them in the
+  // operand's swizzled chunks.  And the documents of the queries' positions.
   if (warp < 8) {
-    const int tile = warp >> 2, r = threadIdx.x & 127;
-    const int row = tile * kTileRows + r;
+    const int tile = warp >> 2, row = tile * kTileRows + (threadIdx.x & 127);
     if (tile == 0 || share) {
-      uint8_t* dst = sq + tile * C::kTile + r * 128;
       const bool ok = row < t.rows;
       const int pr = t.row0 + (ok ? row : 0);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + t.b * a.qs.batch + t.l * a.qs.layer + static_cast<int64_t>(t.g * a.G + pr % a.G) * a.qs.head +
-          static_cast<int64_t>(pr / a.G) * a.qs.token);
+      if (!a.q_tma) {
+        const __nv_bfloat16* q = a.q + t.b * a.qs.batch + t.l * a.qs.layer;
+        const int64_t own = static_cast<int64_t>(t.g * a.G + pr % a.G) * a.qs.head + static_cast<int64_t>(pr / a.G) * a.qs.token;
+        constexpr int LPR = D / 8;
+        const int chunk = lane % LPR;
+        uint8_t* dst = sq + tile * C::kTile + (chunk >> 3) * kChunkBytes;
+#pragma unroll 1
+        for (int i0 = 0; i0 < LPR; i0 += 8) {
+          uint4 w[8];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 w = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * kChunkBytes + (((c & 7) ^ (r & 7)) << 4)) = w;
+          for (int i = 0; i < 8; ++i) {
+            const int r = (i0 + i) * (32 / LPR) + lane / LPR;
+            const int64_t at = __shfl_sync(0xffffffffu, own, r);
+            w[i] = row - lane + r < t.rows ? __ldg(reinterpret_cast<const uint4*>(q + at) + chunk) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rt = (warp & 3) * 32 + (i0 + i) * (32 / LPR) + lane / LPR;
+            *reinterpret_cast<uint4*>(dst + rt * 128 + (((chunk & 7) ^ (rt & 7)) << 4)) = w[i];
+          }
+        }
       }
-      if (docs && ok) {
+      if (docs) {
         const int p = t.first + pr / a.G;
-        const int doc = p >= 0 ? __ldg(docs + p) : -1;
-        if (doc >= 0) {
-          atomicMin(&s.q_min, doc);
-          atomicMax(&s.q_max, doc);
+        const int doc = ok && p >= 0 ? __ldg(docs + p) : -1;
+        const int lo = __reduce_min_sync(0xffffffffu, doc >= 0 ? doc : INT32_MAX), hi = __reduce_max_sync(0xffffffffu, doc);
+        if (lane == 0) {
+          atomicMin(&s.q_min, lo);
+          atomicMax(&s.q_max, hi);
         }
       }
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s.qfull));
+    if (!a.q_tma) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.qfull));
+    }
+  } else if (a.q_tma && warp == kLoadWarp && lane == 0) {
+    const int tiles = share ? 2 : 1;
+    mbar_arrive_expect_tx(smem_u32(&s.qfull), tiles * C::kTile);
+    for (int i = 0; i < tiles; ++i)
+      for (int c = 0; c < C::kChunks; ++c)
+        tma_load_5d(smem_u32(sq + i * C::kTile + c * kChunkBytes), &map_q, smem_u32(&s.qfull), c * 64, t.g * a.G,
+                    (t.row0 + i * kTileRows) / a.G, t.l, t.b);
   }
   if (docs) __syncthreads();
-  const int q_min = docs ? s.q_min : 0, q_max = docs ? s.q_max : 0;
+  const int q_min = docs ? uniform(s.q_min) : 0, q_max = docs ? uniform(s.q_max) : 0;
 
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == kLoadWarp) {
     // -------------------------------------------------------------- TMA producer: K(i + 1) before V(i)
     if (lane == 0) {
@@ -379,6 +421,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       cur = nxt;
     }
     // every copy issued above lands before the CTA exits
+    if (a.q_tma) drain(smem_u32(&s.qfull), 0);
     for (int i = max(0, nk - C::kNk); i < nk; ++i)
       drain(smem_u32(&s.kfull[i % C::kNk]), (i / C::kNk) & 1);
     for (int i = max(0, nv - C::kNv); i < nv; ++i)
@@ -390,7 +433,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     TileWalk walk(t, table, q_min, q_max), walk_v(t, table, q_min, q_max);
     bool ok = warp_wait(smem_u32(&s.qfull), 0, abort_flag);
     const uint32_t elected = elect_one();
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t q_desc = sw128_desc(smem_u32(sq)), k_desc = sw128_desc(smem_u32(sk)), val_desc = v_desc(smem_u32(sv));
     int n_k = 0, n_v = 0;                // K and V tiles taken up
     bool k_more = true;
@@ -412,7 +454,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = (ks >> 2) * (kChunkBytes >> 4) + (ks & 3) * 2;
-        mma_ss(tm + h * 128, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u, elected);
+        mma_ss(tmem + h * 128, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u, elected);
       }
       commit(smem_u32(&s.sfull[h]), elected);
       if (!share || h == 1) commit(smem_u32(&s.kempty[st]), elected);
@@ -450,13 +492,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       const uint32_t more = x > 1 ? 1u : 0u;
 #pragma unroll
       for (int ks = 0; ks < kKeys / 32; ++ks)
-        mma_ts(tm + kOCol + h * 128, tm + h * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o, ks > 0 ? 1u : more,
+        mma_ts(tmem + kOCol + h * 128, tmem + h * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o, ks > 0 ? 1u : more,
                elected);
       if (!warp_wait(smem_u32(&s.pfull[h]), (x >> 1) & 1, abort_flag)) return false;
       tc_fence_after();
 #pragma unroll
       for (int ks = kKeys / 32; ks < kKeys / 16; ++ks)
-        mma_ts(tm + kOCol + h * 128, tm + h * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o, 1u, elected);
+        mma_ts(tmem + kOCol + h * 128, tmem + h * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o, 1u, elected);
       commit(smem_u32(&s.odone[h]), elected);
       if (!share || h == 1) commit(smem_u32(&s.vempty[st]), elected);
       return true;
@@ -475,14 +517,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
   }
   } else {
     // -------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int h = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const int row = (share ? h * kTileRows : 0) + r;
     const bool valid = row < t.rows;
-    const int pr = t.row0 + (valid ? row : 0);
-    const int p = t.first + pr / a.G;
-    const int head = t.g * a.G + pr % a.G;
+    const int p = t.first + (t.row0 + (valid ? row : 0)) / a.G;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_col = tmem + lanes + h * 128, o_col = tmem + lanes + kOCol + h * 128;
     const bool warp_valid = __any_sync(0xffffffffu, valid);
@@ -505,7 +545,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 #pragma unroll
       for (int k = 0; k < 5; ++k, f *= zs * zs) tc[k] = kTanh[k] * f;
     }
-    const float slope2 = BIAS ? a.mods.slopes[head] * kLog2e : 0.f;
+    const float slope2 = BIAS ? a.mods.slopes[t.g * a.G + (t.row0 + (valid ? row : 0)) % a.G] * kLog2e : 0.f;
     float m = -INFINITY, l = 0.f;              // reference maximum (of y / cs) and sum of 2^(y - m cs)
     TileWalk walk(t, table, q_min, q_max);
     int n = 0;                                 // tiles of this stream
@@ -696,6 +736,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       named_bar_sync(2, 256);
     }
     if (!fail && warp_valid && (share || h == 0)) {
+      const int pr = t.row0 + (valid ? row : 0);
+      const int head = t.g * a.G + pr % a.G;
       float f0 = 1.f, f1 = 0.f;
       const float* box = reinterpret_cast<const float*>(sk) + r * (D + 4);
       if (!share && valid) {
@@ -713,8 +755,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         f1 *= inv;
       }
       const int64_t prow = static_cast<int64_t>(t.u) * a.n_q * a.G + pr;
-      __nv_bfloat16* out = a.out + t.b * a.os.batch + t.l * a.os.layer + static_cast<int64_t>(head) * a.os.head +
-                           static_cast<int64_t>(pr / a.G) * a.os.token;
+      const int64_t own = static_cast<int64_t>(head) * a.os.head + static_cast<int64_t>(pr / a.G) * a.os.token;
+      uint8_t* stage = sq + (share ? h : 0) * C::kTile + r * (2 * D);       // Q is not read any more
       float* part_o = a.part_o + (prow * a.splits + t.split) * D;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -744,9 +786,25 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         } else {
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(out + c * 32 + e) =
+            *reinterpret_cast<uint4*>(stage + (((c * 4 + e / 8) ^ (r & 7)) << 4)) =
                 make_uint4(pack_bf16x2(x[e], x[e + 1]), pack_bf16x2(x[e + 2], x[e + 3]),
                            pack_bf16x2(x[e + 4], x[e + 5]), pack_bf16x2(x[e + 6], x[e + 7]));
+        }
+      }
+      if (!part) {
+        // the warp's rows from shared memory, whole rows per store
+        __syncwarp();
+        constexpr int LPR = D / 8;
+        const int chunk = lane % LPR;
+        __nv_bfloat16* out = a.out + t.b * a.os.batch + t.l * a.os.layer;
+        const uint8_t* rows = sq + (share ? h : 0) * C::kTile;
+#pragma unroll 4
+        for (int i = 0; i < LPR; ++i) {
+          const int rr = i * (32 / LPR) + lane / LPR, rt = quarter * 32 + rr;
+          const int64_t at = __shfl_sync(0xffffffffu, own, rr);
+          if ((share ? h * kTileRows : 0) + rt < t.rows)
+            *(reinterpret_cast<uint4*>(out + at) + chunk) =
+                *reinterpret_cast<const uint4*>(rows + rt * (2 * D) + ((chunk ^ (rt & 7)) << 4));
         }
       }
       if (valid && part) {
@@ -756,7 +814,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
       }
     }
-    if (fail && lane == 0 && a.unit_status) a.unit_status[t.u] = KVC_UNIT_TIMEOUT;
+    if (fail && lane == 0 && a.unit_status) a.unit_status[s.item.u] = KVC_UNIT_TIMEOUT;
   }
   tc_fence_before();
   __syncthreads();
@@ -828,7 +886,8 @@ __global__ void __launch_bounds__(256) doc_tiles_kernel(const PromptArgs a) {
 
 size_t prompt_smem_bytes(int d) { return d == 128 ? Cfg<128>::kSmem : Cfg<64>::kSmem; }
 
-cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream) {
+cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v,
+                          cudaStream_t stream) {
   if (a.docs)
     doc_tiles_kernel<<<dim3((a.n_tiles + 7) / 8, std::min(a.B, 65535)), 256, 0, stream>>>(a);
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.n_blocks) * a.U * a.splits);
@@ -836,7 +895,7 @@ cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_k, const C
     const int bytes = static_cast<int>(prompt_smem_bytes(a.d));
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, bytes, stream>>>(map_k, map_v, a);
+    kernel<<<grid, kThreads, bytes, stream>>>(map_q, map_k, map_v, a);
     return cudaGetLastError();
   };
   const bool cap = a.mods.softcap > 0.f, bias = a.mods.slopes != nullptr;
