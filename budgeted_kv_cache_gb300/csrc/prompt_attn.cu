@@ -269,7 +269,7 @@ struct TileWalk {
 
 struct Bars {
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
-  uint64_t sfull[2], phalf[2], pfull[2], odone[2], qfull, done;
+  uint64_t sfull[2], phalf[2], pfull[2], odone[2], qfull[2], done;
   uint32_t tmem;
   int abort_flag;
   int q_min, q_max;
@@ -303,7 +303,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       mbar_init(smem_u32(&s.pfull[i]), 4);
       mbar_init(smem_u32(&s.odone[i]), 1);
     }
-    mbar_init(smem_u32(&s.qfull), a.q_tma ? 1 : 8);
+    mbar_init(smem_u32(&s.qfull[0]), a.q_tma ? 1 : 4);
+    mbar_init(smem_u32(&s.qfull[1]), a.q_tma ? 1 : 4);
     mbar_init(smem_u32(&s.done), 1);
     s.abort_flag = 0;
     s.q_min = INT32_MAX;
@@ -371,15 +372,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     if (!a.q_tma) {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.qfull));
+      if (lane == 0) mbar_arrive(smem_u32(&s.qfull[tile]));
     }
-  } else if (a.q_tma && warp == kLoadWarp && lane == 0) {
-    const int tiles = share ? 2 : 1;
-    mbar_arrive_expect_tx(smem_u32(&s.qfull), tiles * C::kTile);
-    for (int i = 0; i < tiles; ++i)
-      for (int c = 0; c < C::kChunks; ++c)
-        tma_load_5d(smem_u32(sq + i * C::kTile + c * kChunkBytes), &map_q, smem_u32(&s.qfull), c * 64, t.g * a.G,
-                    (t.row0 + i * kTileRows) / a.G, t.l, t.b);
   }
   if (docs) __syncthreads();
   const int q_min = docs ? uniform(s.q_min) : 0, q_max = docs ? uniform(s.q_max) : 0;
@@ -406,9 +400,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       __syncwarp();
       return true;
     };
+    auto load_q = [&](int i) {
+      if (!a.q_tma || lane) return;
+      mbar_arrive_expect_tx(smem_u32(&s.qfull[i]), C::kTile);
+      for (int c = 0; c < C::kChunks; ++c)
+        tma_load_5d(smem_u32(sq + i * C::kTile + c * kChunkBytes), &map_q, smem_u32(&s.qfull[i]), c * 64, t.g * a.G,
+                    (t.row0 + i * kTileRows) / a.G, t.l, t.b);
+    };
     int nk = 0, nv = 0;
+    load_q(0);
     int cur = walk.next();
     bool ok = cur < 0 || load(&map_k, sk, s.kfull, s.kempty, C::kNk, nk++, cur);
+    if (share) load_q(1);
     if (cur < 0 || !ok) nk = 0;
     while (cur >= 0 && ok) {
       const int nxt = walk.next();
@@ -421,7 +424,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       cur = nxt;
     }
     // every copy issued above lands before the CTA exits
-    if (a.q_tma) drain(smem_u32(&s.qfull), 0);
+    if (a.q_tma) drain(smem_u32(&s.qfull[0]), 0);
+    if (a.q_tma && share) drain(smem_u32(&s.qfull[1]), 0);
     for (int i = max(0, nk - C::kNk); i < nk; ++i)
       drain(smem_u32(&s.kfull[i % C::kNk]), (i / C::kNk) & 1);
     for (int i = max(0, nv - C::kNv); i < nv; ++i)
@@ -431,7 +435,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const uint32_t idesc_s = mma_idesc_bf16(128, kKeys);
     const uint32_t idesc_o = mma_idesc_bf16(128, D) | (1u << 16);     // B (values) MN-major
     TileWalk walk(t, table, q_min, q_max), walk_v(t, table, q_min, q_max);
-    bool ok = warp_wait(smem_u32(&s.qfull), 0, abort_flag);
+    bool ok = warp_wait(smem_u32(&s.qfull[0]), 0, abort_flag);
     const uint32_t elected = elect_one();
     const uint64_t q_desc = sw128_desc(smem_u32(sq)), k_desc = sw128_desc(smem_u32(sk)), val_desc = v_desc(smem_u32(sv));
     int n_k = 0, n_v = 0;                // K and V tiles taken up
@@ -448,6 +452,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       } else if (!k_more) {
         return false;
       }
+      if (share && x == 1 && !warp_wait(smem_u32(&s.qfull[1]), 0, abort_flag)) return ok = false;
       tc_fence_after();
       const uint32_t st = (n_k - 1) % C::kNk;
       const uint64_t qd = q_desc + (share ? h : 0) * (C::kTile >> 4), kd = k_desc + st * (C::kTile >> 4);
@@ -716,7 +721,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       float* box = reinterpret_cast<float*>(sk) + r * (D + 4);
       if (named_bar_or(1, 256, fail)) fail = true;           // both streams' products are done
       if (h == 1 && !fail && warp_valid) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           if (n > 0) {
@@ -758,7 +763,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       const int64_t own = static_cast<int64_t>(head) * a.os.head + static_cast<int64_t>(pr / a.G) * a.os.token;
       uint8_t* stage = sq + (share ? h : 0) * C::kTile + r * (2 * D);       // Q is not read any more
       float* part_o = a.part_o + (prow * a.splits + t.split) * D;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         if (n > 0) {
