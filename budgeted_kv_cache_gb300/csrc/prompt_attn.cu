@@ -541,7 +541,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const int all_lo = __reduce_max_sync(0xffffffffu, valid ? row_lo : 0);
     const int all_hi = __reduce_min_sync(0xffffffffu, valid ? row_hi : INT32_MAX);
     const int all_pre = __reduce_min_sync(0xffffffffu, valid ? row_pre : INT32_MAX);
-    const float cs = CAP || BIAS ? 1.f : a.scale * kLog2e;
+    const float cs = CAP ? 1.f : a.scale * kLog2e;
     const float cap = a.mods.softcap;
     const float zs = CAP ? a.scale / cap : 0.f;
     float tc[5];                               // the polynomial's coefficients for s
@@ -550,7 +550,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 #pragma unroll
       for (int k = 0; k < 5; ++k, f *= zs * zs) tc[k] = kTanh[k] * f;
     }
-    const float slope2 = BIAS ? a.mods.slopes[t.g * a.G + (t.row0 + (valid ? row : 0)) % a.G] * kLog2e : 0.f;
+    // slope in units of y: base 2 behind a cap, raw scores otherwise
+    const float bias = BIAS ? a.mods.slopes[t.g * a.G + (t.row0 + (valid ? row : 0)) % a.G] * (CAP ? kLog2e : 1.f / a.scale) : 0.f;
+    const int all_pre_max = BIAS ? __reduce_max_sync(0xffffffffu, row_pre) : 0;
     float m = -INFINITY, l = 0.f;              // reference maximum (of y / cs) and sum of 2^(y - m cs)
     TileWalk walk(t, table, q_min, q_max);
     int n = 0;                                 // tiles of this stream
@@ -607,11 +609,23 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         }
       }
       if constexpr (BIAS) {
-        const float far = static_cast<float>(p - j0), by = CAP ? 1.f : a.scale * kLog2e;
+        if (all_pre_max == 0) {
+          // keys that are seen lie at or before the row: -slope |p - j| = slope (j - j0) - slope (p - j0)
+          const float b0 = -bias * static_cast<float>(p - j0);
+          const uint64_t s2 = pair(bias, bias), b2 = pair(b0, b0);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[c][e] = fmaf(-slope2, fabsf(far - static_cast<float>(c * 32 + e)), y[c][e] * by);
+            for (int e = 0; e < 32; e += 2)
+              unpair(add2(fma2(s2, pair(static_cast<float>(c * 32 + e), static_cast<float>(c * 32 + e + 1)), b2),
+                          pair(y[c][e], y[c][e + 1])), &y[c][e], &y[c][e + 1]);
+        } else {
+          const float far = static_cast<float>(p - j0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[c][e] = fmaf(-bias, fabsf(far - static_cast<float>(c * 32 + e)), y[c][e]);
+        }
       }
       // masks, unless every row of the warp sees the whole tile
       const bool whole = j0 + kKeys <= all_pre || (j0 >= all_lo && j0 + kKeys <= all_hi);
