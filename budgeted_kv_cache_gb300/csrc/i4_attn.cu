@@ -37,7 +37,6 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTile = 32;                        // keys per warp tile
-constexpr int kStages = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;                     // log2 growth of the maximum that forces a rescale
@@ -112,21 +111,27 @@ __device__ __forceinline__ void split_range(const I4AttnArgs& a, int n, int spli
 // NT: query rows of a block / 8.  ROW: one scale per row.
 template <int D, int NT, bool ROW>
 struct Smem {
-  alignas(128) uint8_t codes[kWarps][kStages][2][kTile][D / 2];
+  // NT = 1: four blocks (of 128 registers a thread) per SM with three stages; else fewer and larger
+  static constexpr int kStages = NT == 1 ? 3 : 4, kBlocks = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  union {
+    alignas(128) uint8_t codes[kWarps][kStages][2][kTile][D / 2];
+    alignas(16) float o[NT * 8][D + 4];            // after the loop
+  };
   alignas(16) float scale[kWarps][2][kTile][ROW ? 1 : D / 32];
   int32_t pos[kWarps][kTile];
   float m[kWarps][NT * 8], l[kWarps][NT * 8];
-  alignas(16) float o[NT * 8][D + 4];
 };
 
 template <int D, int NT, bool ROW>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(const I4AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn_kernel(const I4AttnArgs a) {
   constexpr int NG = D / 32;                       // scale groups
   constexpr int CH = D / 32;                       // 16-byte chunks per row
   extern __shared__ __align__(128) uint8_t raw[];
   using S = Smem<D, NT, ROW>;
+  constexpr int kStages = S::kStages;
   S& s = *reinterpret_cast<S*>(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  let_next_kernel_start();
   if (static_cast<int>(blockIdx.y + blockIdx.z * 65535) >= a.U) return;
   const Unit un(a, blockIdx.y + blockIdx.z * 65535);
   const int split = blockIdx.x % a.splits, r0 = blockIdx.x / a.splits * (NT * 8);
@@ -507,7 +512,6 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) i4_attn_kernel(cons
 // Second kernel: blocks [0, a.merge_blocks) of a unit join the splits of its
 // rows, the others add the weights of their keys to the mass.
 constexpr int kFinThreads = 256;
-constexpr int kMassKeys = 1024;                  // keys of a block that adds mass
 
 template <int D>
 __global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs a) {
@@ -515,6 +519,7 @@ __global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs
   if (static_cast<int>(blockIdx.y + blockIdx.z * 65535) >= a.U) return;
   const Unit un(a, blockIdx.y + blockIdx.z * 65535);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_for_previous_kernel();
   if (static_cast<int>(blockIdx.x) < a.merge_blocks) {
     const int r = blockIdx.x * (kFinThreads / 32) + warp;
     if (r >= un.R) return;
@@ -545,36 +550,44 @@ __global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs
     if (lane == 0 && a.lse) a.lse[un.lse_at(a, r)] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
     return;
   }
-  const int j0 = (blockIdx.x - a.merge_blocks) * kMassKeys;
-  if (j0 >= un.n) return;
+  const int j0 = (blockIdx.x - a.merge_blocks) * a.mass_keys, j1 = min(un.n, j0 + a.mass_keys);
+  if (j0 >= j1) return;
   for (int r = warp; r < un.R; r += kFinThreads / 32) {
+    // splits <= kMaxSplits: four per lane, read once
     const float2* ml = a.part_ml + (static_cast<int64_t>(un.u) * un.R + r) * a.splits;
+    float2 v[kMaxSplits / 32];
     float top = -INFINITY, sum = 0.f;
-    for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, ml[i].x);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / 32; ++k) {
+      v[k] = k * 32 + lane < a.splits ? ml[k * 32 + lane] : make_float2(-INFINITY, 0.f);
+      top = fmaxf(top, v[k].x);
+    }
     for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
-    for (int i = lane; i < a.splits; i += 32)
-      if (ml[i].x != -INFINITY) sum += ml[i].y * ex2_approx(ml[i].x - top);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / 32; ++k)
+      if (v[k].x != -INFINITY) sum = fmaf(v[k].y, ex2_approx(v[k].x - top), sum);
     for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(kFull, sum, k);
     if (lane == 0) lse2[r] = sum > 0.f ? top + log2f(sum) : 0.f;      // nothing seen: every logit is -inf
   }
   __syncthreads();
   // four keys of a thread at once, two query rows per load
-  for (int j = j0 + threadIdx.x; j < j0 + kMassKeys; j += kFinThreads * 4) {
-    float sum[4] = {};
+  for (int j = j0 + threadIdx.x; j < j1; j += kFinThreads * 4) {
+    float sum[4] = {}, old[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) old[k] = a.rows.mass[un.base + min(j + k * kFinThreads, j1 - 1)];
     for (int r = 0; r < un.R; r += 2) {
       float2 y[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int jk = min(j + k * kFinThreads, un.n - 1);
-        y[k] = *reinterpret_cast<const float2*>(a.logits + (un.base + jk) * a.logit_stride + r);
-      }
-      const float l0 = lse2[r], l1 = lse2[min(r + 1, un.R - 1)];
+      for (int k = 0; k < 4; ++k)
+        y[k] = *reinterpret_cast<const float2*>(a.logits + (un.base + min(j + k * kFinThreads, j1 - 1)) * a.logit_stride + r);
+      const bool two = r + 1 < un.R;             // a padding column adds nothing
+      const float l0 = lse2[r], l1 = two ? lse2[r + 1] : 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum[k] += ex2_approx(y[k].x - l0) + (r + 1 < un.R ? ex2_approx(y[k].y - l1) : 0.f);   // a padding column adds nothing
+      for (int k = 0; k < 4; ++k) sum[k] += ex2_approx(y[k].x - l0) + (two ? ex2_approx(y[k].y - l1) : 0.f);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (j + k * kFinThreads < un.n) a.rows.mass[un.base + j + k * kFinThreads] += sum[k];
+      if (j + k * kFinThreads < j1) a.rows.mass[un.base + j + k * kFinThreads] = old[k] + sum[k];
   }
 }
 
@@ -604,13 +617,11 @@ cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream) {
   const bool row = a.rows.quant_mode == KVC_QUANT_ROW_FP16;
   cudaError_t e = a.d == 128 ? (row ? launch_rows<128, true>(a, stream) : launch_rows<128, false>(a, stream))
                              : (row ? launch_rows<64, true>(a, stream) : launch_rows<64, false>(a, stream));
-  const int mass_blocks = a.add_mass ? (a.rows.capacity + kMassKeys - 1) / kMassKeys : 0;
+  const int mass_blocks = a.add_mass ? (a.rows.capacity + a.mass_keys - 1) / a.mass_keys : 0;
   if (e != cudaSuccess || a.merge_blocks + mass_blocks == 0) return e;
   const dim3 grid(a.merge_blocks + mass_blocks, std::min(a.U, 65535), (a.U + 65534) / 65535);
   const size_t bytes = a.add_mass ? static_cast<size_t>(a.n_q) * a.G * sizeof(float) : 0;
-  if (a.d == 128) i4_finish_kernel<128><<<grid, kFinThreads, bytes, stream>>>(a);
-  else i4_finish_kernel<64><<<grid, kFinThreads, bytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(a.d == 128 ? i4_finish_kernel<128> : i4_finish_kernel<64>, grid, kFinThreads, bytes, stream, a);
 }
 
 }  // namespace kvc

@@ -266,11 +266,14 @@ struct I4AttnArgs {
   bool add_mass;
   int32_t splits;              // blocks that share a unit's keys
   int32_t merge_blocks;        // second kernel: blocks per unit that join splits (0: nothing to join)
+  int32_t mass_keys;           // second kernel: keys per block that adds mass
   int32_t logit_stride;        // n_q G rounded up to even
   float* part_o;               // splits > 1: [U][n_q G][splits][d]
   float2* part_ml;             // splits > 1 or add_mass: [U][n_q G][splits]
   float* logits;               // add_mass: [U][capacity][logit_stride], base 2
 };
+
+constexpr int kMaxSplits = 128;      // blocks that share a unit's keys in the 4-bit attention
 
 struct I4EvictArgs {
   int32_t U, d, budget, n_sink, n_recent;
@@ -317,9 +320,32 @@ cudaError_t launch_commit(const CommitArgs& a, cudaStream_t stream);
 cudaError_t launch_protect(const ProtectArgs& a, cudaStream_t stream);
 cudaError_t launch_flags(const FlagArgs& a, cudaStream_t stream);
 
+// Launches a kernel that may begin while the one before it in the stream still
+// runs (it has to call wait_for_previous_kernel before it touches anything of
+// that one's): the launch costs no gap.
+template <typename K, typename... A>
+cudaError_t launch_after(K kernel, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ----------------------------------------------------------------------------
 // device helpers
 // ----------------------------------------------------------------------------
+
+// The next kernel, launched with launch_after, may begin once every block has
+// called this; and it waits here until this one's results are there.
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
               const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
   using C = Cfg<D>;
+  let_next_kernel_start();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sq = base;                                  // two Q tiles
@@ -316,6 +317,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     tmem_relinquish();
   }
   if (threadIdx.x == 0) s.item = make_item(a, blockIdx.x);
+  if (a.docs) wait_for_previous_kernel();                // the documents of the key tiles
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -850,6 +852,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
   const int64_t prow = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (prow >= rows) return;
   const int lane = threadIdx.x & 31;
+  wait_for_previous_kernel();
   const int u = static_cast<int>(prow / (static_cast<int64_t>(a.n_q) * a.G));
   const int pr = static_cast<int>(prow % (static_cast<int64_t>(a.n_q) * a.G));
   const int b = u / (a.L * a.Hkv), l = u / a.Hkv % a.L, g = u % a.Hkv;
@@ -859,17 +862,21 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
   for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, ml[i].x);
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float x[D / 32] = {}, sum = 0.f;
-  if (top > -INFINITY) {
-    for (int i = 0; i < a.splits; ++i) {
-      const float2 v = ml[i];
-      if (v.x == -INFINITY) continue;
-      const float f = ex2_approx(v.x - top);
-      sum += v.y * f;
-      const float* o = a.part_o + (prow * a.splits + i) * D + lane * (D / 32);
+  for (int i0 = 0; i0 < a.splits; i0 += 32) {
+    // lane i holds split i's weight; the outputs of eight splits are on their way together
+    const float2 v = i0 + lane < a.splits ? ml[i0 + lane] : make_float2(-INFINITY, 0.f);
+    const float w = v.x == -INFINITY ? 0.f : ex2_approx(v.x - top);
+    sum = fmaf(v.y, w, sum);
+    const int n = min(32, a.splits - i0);
+    const float* src = a.part_o + (prow * a.splits + i0) * D + lane * (D / 32);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) x[c] = fmaf(o[c], f, x[c]);
+      for (int c = 0; c < D / 32; ++c) x[c] = fmaf(src[i * D + c], wi, x[c]);
     }
   }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   const int head = g * a.G + pr % a.G;
   __nv_bfloat16* out = a.out + b * a.os.batch + l * a.os.layer + static_cast<int64_t>(head) * a.os.head +
@@ -884,6 +891,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
 
 // Smallest and largest document of each key tile: one warp per tile.
 __global__ void __launch_bounds__(256) doc_tiles_kernel(const PromptArgs a) {
+  let_next_kernel_start();
   const int tile = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (tile >= a.n_tiles) return;
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
@@ -914,6 +922,7 @@ cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const C
     const int bytes = static_cast<int>(prompt_smem_bytes(a.d));
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
+    if (a.docs) return launch_after(kernel, dim3(grid), kThreads, bytes, stream, map_q, map_k, map_v, a);
     kernel<<<grid, kThreads, bytes, stream>>>(map_q, map_k, map_v, a);
     return cudaGetLastError();
   };
@@ -928,9 +937,7 @@ cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const C
   if (e != cudaSuccess || a.splits == 1) return e;
   const int64_t rows = static_cast<int64_t>(a.U) * a.n_q * a.G;
   const unsigned blocks = static_cast<unsigned>((rows + 7) / 8);
-  if (a.d == 128) prompt_merge_kernel<128><<<blocks, 256, 0, stream>>>(a);
-  else prompt_merge_kernel<64><<<blocks, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(a.d == 128 ? prompt_merge_kernel<128> : prompt_merge_kernel<64>, blocks, 256, 0, stream, a);
 }
 
 }  // namespace kvc
