@@ -562,56 +562,78 @@ class I4Rows:
                       pools.pos_out[POOL_INT4], kept_count[POOL_INT4], next_pos, mass, policy.quant_mode)
 
 
-class _Call:
-    """Checks of one call's tensors: types, shapes, the current device."""
+# Checks of the tensors of one call (types, shapes, the current device).  They run in front of kernels of a few
+# microseconds, so each tensor is looked at once and nothing is built that is not passed on.
 
-    def __init__(self, fn: str, shape: kvc_shape):
-        self.fn, self.shape, self.dev = fn, shape, torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+def _refuse(fn: str):
+    raise KvcError(fn, 1)
 
-    def refuse(self):
-        raise KvcError(self.fn, 1)
 
-    def rows(self, t: torch.Tensor, heads: int, n: int = -1):
-        """Strides of a bf16 [B][L][H][n][d] tensor; n < 0 takes the tensor's."""
-        size, st, s = t.shape, t.stride(), self.shape
-        if (t.dtype is not torch.bfloat16 or t.get_device() != self.dev or len(size) != 5 or st[4] != 1 or
-                size[4] != s.head_dim or size[2] != heads or size[1] != s.n_layers or size[0] != s.batch or
-                (n >= 0 and size[3] != n)):
-            self.refuse()
-        return ctypes.byref(kvc_strides(st[0], st[1], st[2], st[3]))
+def _device(fn: str) -> int:
+    """The current device; a program that has not used one has no tensors on it either."""
+    if not torch.cuda.is_initialized():
+        _refuse(fn)
+    return torch.cuda.current_device()
 
-    def dense(self, t: Optional[torch.Tensor], dtype, n: int) -> Optional[int]:
-        """Address of an optional contiguous tensor of n elements."""
-        if t is None:
-            return None
-        if t.dtype is not dtype or t.numel() != n or t.get_device() != self.dev or not t.is_contiguous():
-            self.refuse()
-        return t.data_ptr()
 
-    def cache(self, rows: I4Rows):
-        if rows.k.get_device() != self.dev or rows.k.shape[0] != self.units or rows.k.shape[2] * 2 != self.shape.head_dim:
-            self.refuse()
-        return ctypes.byref(rows.c())
+def _rows(fn: str, dev: int, t: torch.Tensor, s: kvc_shape, heads: int, n: int = -1):
+    """Strides of a bf16 [B][L][H][n][d] tensor (None: dense); n < 0 takes the tensor's."""
+    size = t.shape
+    if (len(size) != 5 or t.dtype is not torch.bfloat16 or size[4] != s.head_dim or size[2] != heads or
+            size[1] != s.n_layers or size[0] != s.batch or (n >= 0 and size[3] != n) or t.get_device() != dev):
+        _refuse(fn)
+    if t.is_contiguous():
+        return None
+    st = t.stride()
+    if st[4] != 1:
+        _refuse(fn)
+    return ctypes.byref(kvc_strides(st[0], st[1], st[2], st[3]))
 
-    def mods(self, m: Optional[ScoreMods]):
-        if m is None:
-            return None
-        s = self.shape
-        return ctypes.byref(kvc_score_mods(m.softcap, self.dense(m.slopes, torch.float32, s.n_q_heads), m.window,
-                                           self.dense(m.prefix_len, torch.int32, s.batch)))
 
-    def space(self, workspace: Optional[torch.Tensor]):
-        """Address and bytes of a workspace."""
-        if workspace is None:
-            return None, 0
-        if workspace.get_device() != self.dev or not workspace.is_contiguous():
-            self.refuse()
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+def _pair(fn: str, dev: int, k: torch.Tensor, v: torch.Tensor, s: kvc_shape, n: int = -1):
+    """Strides that keys and values share."""
+    if v.shape != k.shape or v.dtype is not k.dtype or v.get_device() != dev:
+        _refuse(fn)
+    strides = _rows(fn, dev, k, s, s.n_kv_heads, n)
+    if not v.is_contiguous() if strides is None else v.stride() != k.stride():
+        _refuse(fn)
+    return strides
 
-    @property
-    def units(self) -> int:
-        s = self.shape
-        return s.batch * s.n_layers * s.n_kv_heads
+
+def _dense(fn: str, dev: int, t: Optional[torch.Tensor], dtype, n: int) -> Optional[int]:
+    """Address of an optional contiguous tensor of n elements."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        _refuse(fn)
+    return t.data_ptr()
+
+
+def _units(s: kvc_shape) -> int:
+    return s.batch * s.n_layers * s.n_kv_heads
+
+
+def _cache(fn: str, dev: int, rows: I4Rows, s: kvc_shape):
+    size = rows.k.shape
+    if size[0] != s.batch * s.n_layers * s.n_kv_heads or size[2] * 2 != s.head_dim or rows.k.get_device() != dev:
+        _refuse(fn)
+    return ctypes.byref(rows.c())
+
+
+def _mods(fn: str, dev: int, m: Optional[ScoreMods], s: kvc_shape):
+    if m is None:
+        return None
+    return ctypes.byref(kvc_score_mods(m.softcap, _dense(fn, dev, m.slopes, torch.float32, s.n_q_heads), m.window,
+                                       _dense(fn, dev, m.prefix_len, torch.int32, s.batch)))
+
+
+def _space(fn: str, dev: int, workspace: Optional[torch.Tensor]):
+    """Address and bytes of a workspace."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(fn)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def kvc_prompt_attn_workspace_bytes(shape, n_q: int, with_docs: bool = False) -> int:
@@ -622,40 +644,42 @@ def kvc_prompt_attn(shape, q, k, v, out, q_len=None, kv_len=None, docs=None, mod
                     softmax_scale=0.0, row_lse=None, unit_status=None, workspace=None, stream=None):
     """Attention of q [B][L][H_q][n_q][d] over k, v [B][L][H_kv][T][d] (any strides whose innermost is 1;
     k and v alike) with score modifiers and documents (see include/kvc.h)."""
-    c = _Call("kvc_prompt_attn", shape)
-    if q.dim() != 5 or v.stride() != k.stride():
-        c.refuse()
-    B, Hq, Hkv, T, n_q, i32 = shape.batch, shape.n_q_heads, shape.n_kv_heads, shape.n_tokens, q.shape[3], torch.int32
-    c.rows(v, Hkv, T)
-    ws, ws_bytes = c.space(workspace)
-    _check(c.fn, _load().kvc_prompt_attn(
-        ctypes.byref(shape), q.data_ptr(), c.rows(q, Hq), n_q, k.data_ptr(), v.data_ptr(), c.rows(k, Hkv, T),
-        c.dense(q_len, i32, B), c.dense(kv_len, i32, B), c.dense(docs, i32, B * T), c.mods(mods), softmax_scale,
-        out.data_ptr(), c.rows(out, Hq, n_q), c.dense(row_lse, torch.float32, B * shape.n_layers * Hq * n_q),
-        c.dense(unit_status, i32, c.units), ws, ws_bytes, _stream(stream)))
+    f = "kvc_prompt_attn"
+    dev = _device(f)
+    B, Hq, T, i32 = shape.batch, shape.n_q_heads, shape.n_tokens, torch.int32
+    q_strides, n_q = _rows(f, dev, q, shape, Hq), q.shape[3]
+    ws, ws_bytes = _space(f, dev, workspace)
+    code = _load().kvc_prompt_attn(
+        ctypes.byref(shape), q.data_ptr(), q_strides, n_q, k.data_ptr(), v.data_ptr(), _pair(f, dev, k, v, shape, T),
+        _dense(f, dev, q_len, i32, B), _dense(f, dev, kv_len, i32, B), _dense(f, dev, docs, i32, B * T),
+        _mods(f, dev, mods, shape), softmax_scale, out.data_ptr(), _rows(f, dev, out, shape, Hq, n_q),
+        _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n_q),
+        _dense(f, dev, unit_status, i32, _units(shape)), ws, ws_bytes, _stream(stream))
+    if code:
+        raise KvcError(f, code)
 
 
 def kvc_i4_append(shape, rows: I4Rows, k, v, n_new=None, unit_status=None, stream=None):
     """Quantise k, v [B][L][H_kv][n][d] into the rows behind those in use (see include/kvc.h)."""
-    c = _Call("kvc_i4_append", shape)
-    if v.stride() != k.stride() or v.shape != k.shape:
-        c.refuse()
-    strides = c.rows(k, shape.n_kv_heads)
-    c.rows(v, shape.n_kv_heads)
-    _check(c.fn, _load().kvc_i4_append(
-        ctypes.byref(shape), c.cache(rows), k.data_ptr(), v.data_ptr(), strides, k.shape[3],
-        c.dense(n_new, torch.int32, shape.batch), c.dense(unit_status, torch.int32, c.units), _stream(stream)))
+    f = "kvc_i4_append"
+    dev = _device(f)
+    code = _load().kvc_i4_append(
+        ctypes.byref(shape), _cache(f, dev, rows, shape), k.data_ptr(), v.data_ptr(), _pair(f, dev, k, v, shape),
+        k.shape[3], _dense(f, dev, n_new, torch.int32, shape.batch),
+        _dense(f, dev, unit_status, torch.int32, _units(shape)), _stream(stream))
+    if code:
+        raise KvcError(f, code)
 
 
 def kvc_i4_read(shape, rows: I4Rows, k_out, v_out, stream=None):
     """Rows 0 .. n-1 of every unit as bf16 into k_out, v_out [B][L][H_kv][n][d] (see include/kvc.h)."""
-    c = _Call("kvc_i4_read", shape)
-    if v_out.stride() != k_out.stride() or v_out.shape != k_out.shape:
-        c.refuse()
-    strides = c.rows(k_out, shape.n_kv_heads)
-    c.rows(v_out, shape.n_kv_heads)
-    _check(c.fn, _load().kvc_i4_read(ctypes.byref(shape), c.cache(rows), k_out.shape[3], k_out.data_ptr(),
-                                     v_out.data_ptr(), strides, _stream(stream)))
+    f = "kvc_i4_read"
+    dev = _device(f)
+    strides = _pair(f, dev, k_out, v_out, shape)
+    code = _load().kvc_i4_read(ctypes.byref(shape), _cache(f, dev, rows, shape), k_out.shape[3], k_out.data_ptr(),
+                               v_out.data_ptr(), strides, _stream(stream))
+    if code:
+        raise KvcError(f, code)
 
 
 def kvc_i4_attn_workspace_bytes(shape, rows: I4Rows, n_q: int, add_mass: bool = False) -> int:
@@ -668,15 +692,18 @@ def kvc_i4_attn(shape, rows: I4Rows, q, out, q_pos=None, mods: Optional[ScoreMod
                 add_mass: bool = False, row_lse=None, workspace=None, stream=None):
     """Attention of q [B][L][H_q][n_q][d] over a 4-bit cache; add_mass adds the softmax weights to
     rows.mass (see include/kvc.h)."""
-    c = _Call("kvc_i4_attn", shape)
-    if q.dim() != 5:
-        c.refuse()
-    B, Hq, n_q = shape.batch, shape.n_q_heads, q.shape[3]
-    ws, ws_bytes = c.space(workspace)
-    _check(c.fn, _load().kvc_i4_attn(
-        ctypes.byref(shape), c.cache(rows), q.data_ptr(), c.rows(q, Hq), n_q, c.dense(q_pos, torch.int32, B * n_q),
-        c.mods(mods), softmax_scale, ATTN_ADD_MASS if add_mass else 0, out.data_ptr(), c.rows(out, Hq, n_q),
-        c.dense(row_lse, torch.float32, B * shape.n_layers * Hq * n_q), ws, ws_bytes, _stream(stream)))
+    f = "kvc_i4_attn"
+    dev = _device(f)
+    B, Hq = shape.batch, shape.n_q_heads
+    q_strides, n_q = _rows(f, dev, q, shape, Hq), q.shape[3]
+    ws, ws_bytes = _space(f, dev, workspace)
+    code = _load().kvc_i4_attn(
+        ctypes.byref(shape), _cache(f, dev, rows, shape), q.data_ptr(), q_strides, n_q,
+        _dense(f, dev, q_pos, torch.int32, B * n_q), _mods(f, dev, mods, shape), softmax_scale,
+        ATTN_ADD_MASS if add_mass else 0, out.data_ptr(), _rows(f, dev, out, shape, Hq, n_q),
+        _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n_q), ws, ws_bytes, _stream(stream))
+    if code:
+        raise KvcError(f, code)
 
 
 def kvc_i4_evict_workspace_bytes(shape, rows: I4Rows, budget: int) -> int:
@@ -687,7 +714,10 @@ def kvc_i4_evict_workspace_bytes(shape, rows: I4Rows, budget: int) -> int:
 def kvc_i4_evict(shape, rows: I4Rows, budget: int, n_sink: int, n_recent: int, unit_status=None, workspace=None,
                  stream=None):
     """Evict in place the rows of least mass above `budget` rows per unit (see include/kvc.h)."""
-    c = _Call("kvc_i4_evict", shape)
-    ws, ws_bytes = c.space(workspace)
-    _check(c.fn, _load().kvc_i4_evict(ctypes.byref(shape), c.cache(rows), budget, n_sink, n_recent,
-                                      c.dense(unit_status, torch.int32, c.units), ws, ws_bytes, _stream(stream)))
+    f = "kvc_i4_evict"
+    dev = _device(f)
+    ws, ws_bytes = _space(f, dev, workspace)
+    code = _load().kvc_i4_evict(ctypes.byref(shape), _cache(f, dev, rows, shape), budget, n_sink, n_recent,
+                                _dense(f, dev, unit_status, torch.int32, _units(shape)), ws, ws_bytes, _stream(stream))
+    if code:
+        raise KvcError(f, code)

@@ -47,7 +47,7 @@ constexpr int kKeys = 128;                       // keys per tile
 constexpr int kChunkBytes = 128 * 128;           // 128 rows x 64 bf16, 128-byte swizzle
 constexpr uint32_t kTmemCols = 512;              // S0, S1, O0, O1 of 128 columns each
 constexpr uint32_t kOCol = 256;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kItemWarp = 10;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;                     // log2 growth of the maximum that forces a rescale
@@ -57,7 +57,7 @@ struct Cfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kTile = kChunks * kChunkBytes;          // a Q, K or V tile
   static constexpr int kNk = D == 128 ? 2 : 4, kNv = D == 128 ? 3 : 4;
-  static constexpr int kSmem = (2 + kNk + kNv) * kTile + 1024 /* alignment */ + 512;
+  static constexpr int kSmem = (2 + kNk + kNv) * kTile + 1024 /* alignment */ + 512 /* Bars */;
 };
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
@@ -273,8 +273,10 @@ struct Bars {
   uint32_t tmem;
   int abort_flag;
   int q_min, q_max;
+  int tiles[2];                // of each stream
   Item item;
 };
+static_assert(sizeof(Bars) <= 512, "Cfg::kSmem");
 
 // D: head dimension.  CAP, BIAS: the logits are capped, or get slopes.
 template <int D, bool CAP, bool BIAS>
@@ -289,7 +291,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   uint8_t* sk = sq + 2 * C::kTile;
   uint8_t* sv = sk + C::kNk * C::kTile;
   Bars& s = *reinterpret_cast<Bars*>(sv + C::kNv * C::kTile);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile int* abort_flag = &s.abort_flag;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -316,7 +318,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     tmem_alloc(smem_u32(&s.tmem), kTmemCols);
     tmem_relinquish();
   }
-  if (threadIdx.x == 0) s.item = make_item(a, blockIdx.x);
+  if (warp == kItemWarp && lane == 0) s.item = make_item(a, blockIdx.x);
   if (a.docs) wait_for_previous_kernel();                // the documents of the key tiles
   tc_fence_before();
   __syncthreads();
@@ -731,44 +733,29 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     if (!fail && n > 0 && !warp_wait(smem_u32(&s.odone[h]), (n - 1) & 1, abort_flag)) fail = true;
     tc_fence_after();
     float m2 = m == -INFINITY ? -INFINITY : m * cs;
+    // One row tile: both streams hold an output for the same rows, in the same lanes of tensor memory.  They exchange
+    // (m, l) through the unused second Q tile, and each joins and writes one half of the columns.
+    int n_other = 0;
+    float f0 = 1.f, f1 = 0.f;
     if (!share) {
-      // two streams over one set of rows: stream 1 hands over through shared memory (the rings are empty by
-      // now: every tile was consumed by a product that has completed, of this stream or, below, the other)
-      float* box = reinterpret_cast<float*>(sk) + r * (D + 4);
-      if (named_bar_or(1, 256, fail)) fail = true;           // both streams' products are done
-      if (h == 1 && !fail && warp_valid) {
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          if (n > 0) {
-            tmem_ld32_issue(o_col + c * 32, o);
-            tmem_ld_wait(o);
-          }
-          if (valid) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(box + 4 + c * 32 + e) =
-                  n > 0 ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0, 0, 0, 0);
-          }
-        }
-        box[0] = m2;
-        box[1] = l;
-      }
-      named_bar_sync(2, 256);
+      float2* ml = reinterpret_cast<float2*>(sq + C::kTile);
+      ml[h * kTileRows + r] = make_float2(m2, l);
+      if (r == 0) s.tiles[h] = n;
+      tc_fence_before();
+      fail = named_bar_or(1, 256, fail);                     // both streams' products are done
+      tc_fence_after();
+      n_other = uniform(s.tiles[h ^ 1]);
+      const float2 o = ml[(h ^ 1) * kTileRows + r];
+      const float mm = fmaxf(m2, o.x);
+      f0 = m2 == -INFINITY ? 0.f : ex2_approx(m2 - mm);
+      f1 = o.x == -INFINITY ? 0.f : ex2_approx(o.x - mm);
+      // the same order of the sum on both sides
+      l = h == 0 ? fmaf(l, f0, o.y * f1) : fmaf(o.y, f1, l * f0);
+      m2 = mm;
     }
-    if (!fail && warp_valid && (share || h == 0)) {
+    if (!fail && warp_valid) {
       const int pr = t.row0 + (valid ? row : 0);
       const int head = t.g * a.G + pr % a.G;
-      float f0 = 1.f, f1 = 0.f;
-      const float* box = reinterpret_cast<const float*>(sk) + r * (D + 4);
-      if (!share && valid) {
-        const float mo = box[0], lo = box[1];
-        const float mm = fmaxf(m2, mo);
-        f0 = m2 == -INFINITY ? 0.f : ex2_approx(m2 - mm);
-        f1 = mo == -INFINITY ? 0.f : ex2_approx(mo - mm);
-        l = l * f0 + lo * f1;
-        m2 = mm;
-      }
       const bool part = a.splits > 1;
       if (!part) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -777,29 +764,29 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       }
       const int64_t prow = static_cast<int64_t>(t.u) * a.n_q * a.G + pr;
       const int64_t own = static_cast<int64_t>(head) * a.os.head + static_cast<int64_t>(pr / a.G) * a.os.token;
-      uint8_t* stage = sq + (share ? h : 0) * C::kTile + r * (2 * D);       // Q is not read any more
-      float* part_o = a.part_o + (prow * a.splits + t.split) * D;
+      // this stream's columns, staged in shared memory in 16-byte chunks (Q is not read any more)
+      const int cols = share ? D : D / 2, col0 = share ? 0 : h * (D / 2);
+      const int chunks = cols / 8, flip = min(chunks - 1, 7);
+      uint8_t* stage = sq + h * C::kTile + (share ? 0 : h * 4096);
+      float* part_o = a.part_o + (prow * a.splits + t.split) * D + col0;
+      const uint32_t mine = o_col + col0, other = tmem + lanes + kOCol + (h ^ 1) * 128 + col0;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < cols / 32; ++c) {
         uint32_t o[32];
+        float x[32];
         if (n > 0) {
-          tmem_ld32_issue(o_col + c * 32, o);
+          tmem_ld32_issue(mine + c * 32, o);
           tmem_ld_wait(o);
         }
-        if (!valid) continue;
-        float x[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] = n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
-        if (!share) {
+        if (n_other > 0) {
+          tmem_ld32_issue(other + c * 32, o);
+          tmem_ld_wait(o);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(box + 4 + c * 32 + e);
-            x[e] = fmaf(w.x, f1, x[e]);
-            x[e + 1] = fmaf(w.y, f1, x[e + 1]);
-            x[e + 2] = fmaf(w.z, f1, x[e + 2]);
-            x[e + 3] = fmaf(w.w, f1, x[e + 3]);
-          }
+          for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o[e]), f1, x[e]);
         }
+        if (!valid) continue;
         if (part) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
@@ -807,32 +794,31 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         } else {
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(stage + (((c * 4 + e / 8) ^ (r & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(stage + (r * chunks + ((c * 4 + e / 8) ^ (r & flip))) * 16) =
                 make_uint4(pack_bf16x2(x[e], x[e + 1]), pack_bf16x2(x[e + 2], x[e + 3]),
                            pack_bf16x2(x[e + 4], x[e + 5]), pack_bf16x2(x[e + 6], x[e + 7]));
         }
       }
       if (!part) {
-        // the warp's rows from shared memory, whole rows per store
+        // the warp's rows from shared memory, whole rows (or halves) per store
         __syncwarp();
-        constexpr int LPR = D / 8;
-        const int chunk = lane % LPR;
-        __nv_bfloat16* out = a.out + t.b * a.os.batch + t.l * a.os.layer;
-        const uint8_t* rows = sq + (share ? h : 0) * C::kTile;
+        const int chunk = lane & (chunks - 1), per = 32 / chunks;     // rows per instruction
+        __nv_bfloat16* out = a.out + t.b * a.os.batch + t.l * a.os.layer + col0;
 #pragma unroll 4
-        for (int i = 0; i < LPR; ++i) {
-          const int rr = i * (32 / LPR) + lane / LPR, rt = quarter * 32 + rr;
+        for (int i = 0; i < chunks; ++i) {
+          const int rr = i * per + lane / chunks, rt = quarter * 32 + rr;
           const int64_t at = __shfl_sync(0xffffffffu, own, rr);
           if ((share ? h * kTileRows : 0) + rt < t.rows)
             *(reinterpret_cast<uint4*>(out + at) + chunk) =
-                *reinterpret_cast<const uint4*>(rows + rt * (2 * D) + ((chunk ^ (rt & 7)) << 4));
+                *reinterpret_cast<const uint4*>(stage + (rt * chunks + (chunk ^ (rt & flip))) * 16);
         }
       }
-      if (valid && part) {
-        a.part_ml[prow * a.splits + t.split] = make_float2(m2, l);
-      } else if (valid && a.lse) {
-        a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n_q + pr / a.G] =
-            l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
+      if (valid && (share || h == 0)) {
+        if (part)
+          a.part_ml[prow * a.splits + t.split] = make_float2(m2, l);
+        else if (a.lse)
+          a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n_q + pr / a.G] =
+              l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
       }
     }
     if (fail && lane == 0 && a.unit_status) a.unit_status[s.item.u] = KVC_UNIT_TIMEOUT;
