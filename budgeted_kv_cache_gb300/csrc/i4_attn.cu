@@ -520,29 +520,51 @@ __global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs
   const Unit un(a, blockIdx.y + blockIdx.z * 65535);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_for_previous_kernel();
+  // Every load that does not depend on another is issued first: this kernel is a few latencies long.
   if (static_cast<int>(blockIdx.x) < a.merge_blocks) {
     const int r = blockIdx.x * (kFinThreads / 32) + warp;
     if (r >= un.R) return;
     const int64_t part = (static_cast<int64_t>(un.u) * un.R + r) * a.splits;
+    const float* src = a.part_o + part * D + lane * (D / 32);
+    float2 v[kMaxSplits / 32];
     float top = -INFINITY;
-    for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, a.part_ml[part + i].x);
-    for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
-    float x[D / 32] = {}, sum = 0.f;
-    for (int i0 = 0; i0 < a.splits; i0 += 32) {
-      // lane i holds split i's weight; the outputs of eight splits are on their way together
-      const float2 v = i0 + lane < a.splits ? a.part_ml[part + i0 + lane] : make_float2(-INFINITY, 0.f);
-      const float w = v.x == -INFINITY ? 0.f : ex2_approx(v.x - top);
-      sum = fmaf(v.y, w, sum);
-      const int n = min(32, a.splits - i0);
-      const float* src = a.part_o + (part + i0) * D + lane * (D / 32);
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(kFull, w, i);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) x[c] = fmaf(src[i * D + c], wi, x[c]);
-      }
+    for (int k = 0; k < kMaxSplits / 32; ++k)
+      v[k] = k * 32 + lane < a.splits ? a.part_ml[part + k * 32 + lane] : make_float2(-INFINITY, 0.f);
+    float x[D / 32] = {}, sum = 0.f;
+    constexpr int kAhead = 16;
+    using Vec = typename std::conditional<D == 128, float4, float2>::type;
+    Vec o[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) o[i] = *reinterpret_cast<const Vec*>(src + min(i, a.splits - 1) * D);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / 32; ++k) top = fmaxf(top, v[k].x);
+    for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
+    float w[kMaxSplits / 32];
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / 32; ++k) {
+      w[k] = v[k].x == -INFINITY ? 0.f : ex2_approx(v[k].x - top);
+      sum = fmaf(v[k].y, w[k], sum);
     }
     for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(kFull, sum, k);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / 32; ++k) {
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32 && k * 32 + i0 < a.splits; i0 += kAhead) {
+        if (k + i0 > 0) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+            o[i] = *reinterpret_cast<const Vec*>(src + static_cast<int64_t>(min(k * 32 + i0 + i, a.splits - 1)) * D);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const float wi = __shfl_sync(kFull, w[k], i0 + i);       // 0 past the last split
+          const float* e = reinterpret_cast<const float*>(&o[i]);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) x[c] = fmaf(e[c], wi, x[c]);
+        }
+      }
+    }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     __nv_bfloat16* out = a.out + un.q_at(a, a.os, r) + lane * (D / 32);
 #pragma unroll
@@ -550,8 +572,23 @@ __global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs
     if (lane == 0 && a.lse) a.lse[un.lse_at(a, r)] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
     return;
   }
-  const int j0 = (blockIdx.x - a.merge_blocks) * a.mass_keys, j1 = min(un.n, j0 + a.mass_keys);
-  if (j0 >= j1) return;
+  // Mass: four keys of a thread at once, two query rows per load; loads of keys past the rows in use stay inside the
+  // unit's logits (their values are not used).
+  const int j0 = (blockIdx.x - a.merge_blocks) * a.mass_keys, cap = a.rows.capacity;
+  auto key_at = [&](int j, int k) { return un.base + min(j + k * kFinThreads, cap - 1); };
+  float old[4];
+  float2 y[2][4];                                // of rows 0..3
+  auto load = [&](int j, int r, float2 (&to)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) to[k] = *reinterpret_cast<const float2*>(a.logits + key_at(j, k) * a.logit_stride + r);
+  };
+  auto load_first = [&](int j) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) old[k] = a.rows.mass[key_at(j, k)];
+    load(j, 0, y[0]);
+    load(j, min(2, a.logit_stride - 2), y[1]);
+  };
+  load_first(j0 + threadIdx.x);
   for (int r = warp; r < un.R; r += kFinThreads / 32) {
     // splits <= kMaxSplits: four per lane, read once
     const float2* ml = a.part_ml + (static_cast<int64_t>(un.u) * un.R + r) * a.splits;
@@ -569,21 +606,23 @@ __global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs
     for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(kFull, sum, k);
     if (lane == 0) lse2[r] = sum > 0.f ? top + log2f(sum) : 0.f;      // nothing seen: every logit is -inf
   }
+  const int j1 = min(un.n, j0 + a.mass_keys);
   __syncthreads();
-  // four keys of a thread at once, two query rows per load
   for (int j = j0 + threadIdx.x; j < j1; j += kFinThreads * 4) {
-    float sum[4] = {}, old[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) old[k] = a.rows.mass[un.base + min(j + k * kFinThreads, j1 - 1)];
+    if (j >= j0 + kFinThreads) load_first(j);
+    float sum[4] = {};
     for (int r = 0; r < un.R; r += 2) {
-      float2 y[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        y[k] = *reinterpret_cast<const float2*>(a.logits + (un.base + min(j + k * kFinThreads, j1 - 1)) * a.logit_stride + r);
+      if (r >= 4) {
+        if ((r >> 1) & 1) load(j, r, y[1]);
+        else load(j, r, y[0]);
+      }
       const bool two = r + 1 < un.R;             // a padding column adds nothing
       const float l0 = lse2[r], l1 = two ? lse2[r + 1] : 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum[k] += ex2_approx(y[k].x - l0) + (two ? ex2_approx(y[k].y - l1) : 0.f);
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = (r >> 1) & 1 ? y[1][k] : y[0][k];
+        sum[k] += ex2_approx(v.x - l0) + (two ? ex2_approx(v.y - l1) : 0.f);
+      }
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)

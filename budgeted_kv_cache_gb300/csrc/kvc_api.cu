@@ -442,10 +442,12 @@ kvc_status plan_i4_attn(const kvc_shape* s, const kvc_i4_rows* r, int32_t n_q, u
   if (rows > (mass ? 12288 : 1 << 24)) return KVC_ERR_UNSUPPORTED;   // row statistics of a mass block in shared memory
   DevInfo info;
   if ((st = check_device(&info)) != KVC_OK) return st;
-  // two rounds of the blocks (of four warps) that an SM holds, not a block more; each warp with a tile of 32 keys at
-  // least.  Measured at 32 units of up to 128K rows: 29 splits, a block more than two rounds, 195 us, 28 splits 163 us.
-  const int64_t blocks = U * ((rows + 31) / 32), per_sm = rows <= 8 ? 4 : rows <= 16 ? 3 : 2;
-  const int64_t want = std::min<int64_t>(2 * per_sm * info.sms / blocks, r->capacity / 128);
+  // One round of the blocks (of four warps) that the SMs hold, not a block more, each warp with a tile of 32 keys at
+  // least; a second round, which evens out ragged lengths, where a block still gets 1,024 keys.  Measured (128 wide, 4
+  // heads): 32 units of 100K to 128K rows 153 us in two rounds, 159 in one; 8 units of 32K rows 40 and 32 us.
+  const int64_t blocks = U * ((rows + 31) / 32), slots = (rows <= 8 ? 4 : rows <= 16 ? 3 : 2) * info.sms;
+  const int64_t want = std::max(std::min<int64_t>(slots / blocks, r->capacity / 128),
+                                std::min<int64_t>(2 * slots / blocks, r->capacity / 1024));
   p->splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(want, kMaxSplits)));
   p->logit_stride = static_cast<int32_t>((rows + 1) / 2 * 2);
   // mass: a key per thread for small caches, up to eight blocks of 256 threads per SM for long ones
