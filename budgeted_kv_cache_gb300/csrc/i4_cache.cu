@@ -304,7 +304,11 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
   return before + x - v;
 }
 
+constexpr int kEvictWords = 1024, kEvictMoves = 1024;        // kept in shared memory up to here, else in the workspace
+
 struct EvictSmem {
+  uint32_t words[kEvictWords];
+  int lists[2][kEvictMoves];
   int hist[256];
   int sums[kEvictWarps];
   unsigned long long best[kEvictWarps];
@@ -342,21 +346,41 @@ __device__ __forceinline__ void find_bin(EvictSmem& s, int need) {
   }
 }
 
-// Row `from` of the unit to slot `to` (one warp).
-__device__ __forceinline__ void move_row(const I4EvictArgs& a, int64_t to, int64_t from) {
+// What one lane moves of a row: words of the codes, a scale, the position or
+// the mass.
+struct RowPart {
+  uint32_t k, v;
+};
+
+__device__ __forceinline__ RowPart load_part(const I4EvictArgs& a, int64_t row) {
+  const int lane = threadIdx.x & 31, words = a.d / 8;
+  const int sb = a.rows.quant_mode == KVC_QUANT_ROW_FP16 ? 1 : a.d / 32;
+  RowPart p = {0, 0};
+  if (lane < words) {
+    p.k = static_cast<const uint32_t*>(a.rows.k)[row * words + lane];
+    p.v = static_cast<const uint32_t*>(a.rows.v)[row * words + lane];
+  } else if (lane >= 16 && lane < 16 + sb) {
+    p.k = static_cast<const uint16_t*>(a.rows.k_scale)[row * sb + lane - 16];
+    p.v = static_cast<const uint16_t*>(a.rows.v_scale)[row * sb + lane - 16];
+  } else if (lane == 31) {
+    p.k = static_cast<uint32_t>(a.rows.pos[row]);
+    p.v = __float_as_uint(a.rows.mass[row]);
+  }
+  return p;
+}
+
+__device__ __forceinline__ void store_part(const I4EvictArgs& a, int64_t row, const RowPart& p) {
   const int lane = threadIdx.x & 31, words = a.d / 8;
   const int sb = a.rows.quant_mode == KVC_QUANT_ROW_FP16 ? 1 : a.d / 32;
   if (lane < words) {
-    static_cast<uint32_t*>(a.rows.k)[to * words + lane] = static_cast<const uint32_t*>(a.rows.k)[from * words + lane];
-    static_cast<uint32_t*>(a.rows.v)[to * words + lane] = static_cast<const uint32_t*>(a.rows.v)[from * words + lane];
+    static_cast<uint32_t*>(a.rows.k)[row * words + lane] = p.k;
+    static_cast<uint32_t*>(a.rows.v)[row * words + lane] = p.v;
   } else if (lane >= 16 && lane < 16 + sb) {
-    const int g = lane - 16;
-    static_cast<uint16_t*>(a.rows.k_scale)[to * sb + g] = static_cast<const uint16_t*>(a.rows.k_scale)[from * sb + g];
-    static_cast<uint16_t*>(a.rows.v_scale)[to * sb + g] = static_cast<const uint16_t*>(a.rows.v_scale)[from * sb + g];
-  } else if (lane == 30) {
-    a.rows.pos[to] = a.rows.pos[from];
+    static_cast<uint16_t*>(a.rows.k_scale)[row * sb + lane - 16] = static_cast<uint16_t>(p.k);
+    static_cast<uint16_t*>(a.rows.v_scale)[row * sb + lane - 16] = static_cast<uint16_t>(p.v);
   } else if (lane == 31) {
-    a.rows.mass[to] = a.rows.mass[from];
+    a.rows.pos[row] = static_cast<int32_t>(p.k);
+    a.rows.mass[row] = __uint_as_float(p.v);
   }
 }
 
@@ -365,6 +389,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) i4_evict_kernel(const I4Evic
   const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cap = a.rows.capacity;
   const int cnt = a.rows.count[u];
+  const int64_t first_recent = static_cast<int64_t>(a.rows.next_pos[u]) - a.n_recent;
   if (cnt < 0 || cnt > cap) {
     if (tid == 0 && a.unit_status) a.unit_status[u] = KVC_UNIT_BAD_INDEX;
     return;
@@ -374,7 +399,6 @@ __global__ void __launch_bounds__(kEvictThreads, 2) i4_evict_kernel(const I4Evic
   const int64_t base = static_cast<int64_t>(u) * cap;
   const int32_t* pos = a.rows.pos + base;
   const float* mass = a.rows.mass + base;
-  const int64_t first_recent = static_cast<int64_t>(a.rows.next_pos[u]) - a.n_recent;
   auto key_of = [&](int i) -> uint32_t {
     const int32_t p = pos[i];
     const float m = mass[i];
@@ -415,7 +439,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) i4_evict_kernel(const I4Evic
       if (lane == 0 && a.unit_status) a.unit_status[u] = KVC_UNIT_OVER_BUDGET;
       return;
     }
-    if (at < a.budget) move_row(a, base + at, base + a.budget);
+    if (at < a.budget) store_part(a, base + at, load_part(a, base + a.budget));
     if (lane == 0) a.rows.count[u] = a.budget;
     return;
   }
@@ -482,9 +506,10 @@ __global__ void __launch_bounds__(kEvictThreads, 2) i4_evict_kernel(const I4Evic
 
   // a word of leaving rows per 32 slots; rows of one key and position leave in slot order
   const int words = (cnt + 31) / 32;
-  uint32_t* leaves = a.words + static_cast<int64_t>(u) * a.n_words;
-  int32_t* holes = a.lists + static_cast<int64_t>(u) * 2 * a.max_moves;
-  int32_t* donors = holes + a.max_moves;
+  uint32_t* leaves = words <= kEvictWords ? s.words : a.words + static_cast<int64_t>(u) * a.n_words;
+  const bool own_lists = over <= kEvictMoves;      // no list is longer than the rows that leave
+  int32_t* holes = own_lists ? s.lists[0] : a.lists + static_cast<int64_t>(u) * 2 * a.max_moves;
+  int32_t* donors = own_lists ? s.lists[1] : holes + a.max_moves;
   int n_eq = 0;
   auto mark = [&](int i0, uint32_t x) {
     const int i = i0 + tid;
@@ -533,7 +558,15 @@ __global__ void __launch_bounds__(kEvictThreads, 2) i4_evict_kernel(const I4Evic
     for (; d; d &= d - 1) donors[at++] = i0 + __ffs(d) - 1;
   }
   __syncthreads();
-  for (int m = warp; m < n_holes; m += kEvictWarps) move_row(a, base + holes[m], base + donors[m]);
+  // four rows of a warp on their way together
+  for (int m0 = warp; m0 < n_holes; m0 += kEvictWarps * 4) {
+    RowPart p[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) p[k] = load_part(a, base + donors[min(m0 + k * kEvictWarps, n_holes - 1)]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (m0 + k * kEvictWarps < n_holes) store_part(a, base + holes[m0 + k * kEvictWarps], p[k]);
+  }
   if (tid == 0) a.rows.count[u] = a.budget;
 }
 
