@@ -1015,9 +1015,14 @@ kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_stri
   a.block_rows = p.block_rows;
   a.n_blocks = p.n_blocks;
   a.splits = p.splits;
+  if (a.mods.window > 0 && !a.mods.prefix_len) {
+    // no item walks more tiles than the window and its rows' queries touch
+    const int64_t keys = static_cast<int64_t>(a.mods.window) + (p.block_rows + a.G - 1) / a.G;
+    a.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(p.splits, (keys / kTileTokens + 2) / 8)));
+  }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (docs) a.doc_tiles = reinterpret_cast<int2*>(ws);
-  if (p.splits > 1) {
+  if (a.splits > 1) {
     a.part_ml = reinterpret_cast<float2*>(ws + p.ws_docs);
     a.part_o = reinterpret_cast<float*>(ws + p.ws_docs + p.ws_ml);
   }

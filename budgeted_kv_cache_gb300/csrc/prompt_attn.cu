@@ -478,12 +478,19 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         ++n_v;
         // values of keys that no row of the item sees become zeros
         bool live = j0 + kKeys <= t.nk && (j0 + kKeys <= t.pre || (j0 >= t.lo && j0 + kKeys <= t.hi));
-        if (docs) live = live && __ldg(table + j0 / kKeys).x >= 0;
+        if (docs) {
+          const int2 d = __ldg(table + j0 / kKeys);
+          live = live && d.x >= q_min && d.y <= q_max;
+        }
         if (!live) {
 #pragma unroll 1
           for (int c = lane; c < kKeys; c += 32) {
             const int j = j0 + c;
-            const bool keep = j < t.nk && (j < t.pre || (j >= t.lo && j < t.hi)) && (!docs || __ldg(docs + j) >= 0);
+            bool keep = j < t.nk && (j < t.pre || (j >= t.lo && j < t.hi));
+            if (docs && keep) {
+              const int doc = __ldg(docs + j);
+              keep = doc >= q_min && doc <= q_max;         // 0 <= q_min
+            }
             if (!keep) {
               uint4* row = reinterpret_cast<uint4*>(sv + st * C::kTile + c * 128);
               for (int k = 0; k < C::kChunks; ++k)

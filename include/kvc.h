@@ -33,7 +33,8 @@
  *   - Every data pointer is DEVICE memory of the current CUDA device, owned
  *     by the caller, unless a call says otherwise.  The library keeps no pointer after a call returns and
  *     allocates no device memory; scratch space is the caller's workspace,
- *     sized by the matching *_workspace_bytes call.
+ *     sized by the matching *_workspace_bytes call.  Calls that may run at
+ *     the same time (on two streams, in two graphs) need one each.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy
  *     default stream) and never synchronise.  Results are valid once the
  *     caller synchronises the stream.
@@ -530,14 +531,14 @@ typedef struct {
  * q_len    optional int32 [B], limited to [0, n_q] (NULL: n_q).  Rows of out
  *          and row_lse at or past q_len[b] are left as they were.
  * kv_len   optional int32 [B], limited to [0, T] (NULL: T).  A query whose
- *          position is negative (q_len > kv_len) sees no key.
+ *          position is negative (q_len > kv_len) sees no key.  T < 2^31 - 256.
  * docs     optional int32 [B][T]: document of each key; a query (whose
  *          document is that of its position) sees only keys of the same
  *          document.  Tokens of a negative document see and are seen by
  *          nothing.
  * Rows of k and v at or past kv_len[b] and of negative documents may hold
- * any bits.  A row that some query sees is finite: a NaN or infinity in one
- * may also reach queries that do not see it.
+ * any bits.  Every other row is finite: a NaN or infinity in it may also
+ * reach queries that do not see it.
  * row_lse  optional fp32 [B][L][H_q][n_q], dense.
  * unit_status  optional int32 [U]; KVC_UNIT_TIMEOUT if a device wait gave up
  *          (its rows are then undefined); untouched otherwise.
@@ -607,6 +608,7 @@ kvc_status kvc_i4_read(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t 
  * q_pos    optional int32 [B][n_q] (NULL: the n_q tokens appended last, query
  *          i of unit u at position next_pos[u] - n_q + i).
  * mods     as above, with the rows' own positions; prefix_len [B].
+ * n_q G    at most 2^24, and 12,288 with KVC_ATTN_ADD_MASS.
  * KVC_ATTN_ADD_MASS: mass[u][r] += the sum over the unit's G heads and n_q
  *          queries of their softmax weight on row r, for every row in use
  *          (PACE Sec. 2: H2O's cumulative score; rows->mass is required).

@@ -213,6 +213,7 @@ ATTN = {
     "wide_group": dict(Hkv=1, G=33, cap=500, counts=[500], add=True),
     "draft": dict(B=2, Hkv=2, G=4, n_q=5, cap=800, counts=[800, 3], add=True),
     "chunk": dict(B=1, Hkv=1, G=4, n_q=70, cap=900, counts=[900], add=True),
+    "many_units": dict(B=5, L=7, Hkv=9, G=1, cap=40, counts=[40, 0, 33, 1, 32], add=True),
     "chunk_d64": dict(B=2, Hkv=2, G=2, n_q=33, cap=300, counts=[300, 128], d=64, mode=ROW),
     "softcap": dict(Hkv=2, G=4, n_q=3, cap=600, counts=[600], softcap=4.0, q_norm=8.0, add=True),
     "slopes": dict(Hkv=2, G=4, n_q=2, cap=600, counts=[600], slopes=True, add=True),
@@ -264,6 +265,28 @@ def test_attention_same_bits_twice_and_on_another_stream(kvc):
         torch.cuda.synchronize()
         got.append((out.clone(), lse.clone(), c.rows.mass.clone()))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_attention_on_two_streams_at_once(kvc):
+    """Calls that overlap over caches and workspaces of their own."""
+    cases = [attention_case(kvc, Hkv=2, G=4, cap=6000, counts=[6000], add=True, seed=s) for s in (1, 2)]
+    before = [c[0].rows.mass.clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for c, s in zip(cases, streams):
+        c[1](s)
+    torch.cuda.synchronize()
+    for c, m in zip(cases, before):
+        c[2](m)
+
+
+def test_mass_of_several_calls_adds_up(kvc):
+    c, run, check, _, _ = attention_case(kvc, Hkv=2, G=4, cap=700, counts=[700], add=True)
+    run()
+    torch.cuda.synchronize()
+    after_one = c.rows.mass.clone()
+    run()
+    check(after_one)
 
 
 def test_attention_extreme_scales(kvc):
@@ -346,6 +369,9 @@ EVICT = {
     "counts_out_of_range": dict(cap=100, counts=[101, -1, 100], budget=50),
     "budget_over_capacity": dict(cap=100, counts=[100], budget=1000),
     "same_positions": dict(cap=200, counts=[200], budget=90, same=True, equal=True),
+    "every_row_but_one_leaves": dict(cap=3000, counts=[3000], budget=1, n_sink=0, n_recent=1, U=2),
+    "more_moves_than_shared": dict(cap=9000, counts=[9000], budget=4500, U=2),
+    "more_words_than_shared": dict(cap=40000, counts=[40000], budget=39000, U=1, ties=True),
     "row_mode": dict(cap=400, counts=[400], budget=300, mode=ROW),
     "d64": dict(cap=400, counts=[400], budget=300, d=64),
 }

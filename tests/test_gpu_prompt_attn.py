@@ -148,6 +148,36 @@ def test_rows_that_nothing_sees_may_hold_any_bits(kvc, n_q):
     c.check()
 
 
+def test_documents_that_no_query_has_may_hold_any_bits(kvc):
+    """A chunk of the second document: the first one's rows, some in the same key tile, are NaN."""
+    c = Case(kvc, n_q=150, T=700, G=2, docs=[0] * 430 + [1] * 270)
+    for x in (c.k, c.v):
+        x[:, :, :, :430] = float("nan")
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("kw", [dict(window=200), dict(window=5000), dict(window=300, prefix=[700, 0])])
+def test_window_over_a_long_cache(kvc, kw):
+    """Splits of the keys follow the window where nothing else is seen."""
+    c = Case(kvc, B=2, n_q=2, T=30000, Hkv=1, G=4, d=64, kv_len=[30000, 17001], **kw)
+    c.run()
+    c.check()
+
+
+def test_two_streams_at_once(kvc):
+    """Two calls that overlap, each with its own workspace."""
+    cases = [Case(kvc, B=2, n_q=1, T=20000, seed=s) for s in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, s in zip(cases, streams):
+            c.run(stream=s)
+    torch.cuda.synchronize()
+    for c in cases:
+        c.check()
+
+
 def test_large_logits_stay_finite(kvc):
     c = Case(kvc, n_q=140, T=300, q_norm=60.0, seed=3)
     c.run()
