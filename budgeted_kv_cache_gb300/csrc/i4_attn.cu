@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
 constexpr int kFinThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs a) {
+__global__ void __launch_bounds__(kFinThreads, 4) i4_finish_kernel(const I4AttnArgs a) {
   extern __shared__ float lse2[];                  // base-2 log-sum-exp of each row (mass blocks)
   if (static_cast<int>(blockIdx.y + blockIdx.z * 65535) >= a.U) return;
   const Unit un(a, blockIdx.y + blockIdx.z * 65535);
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kFinThreads) i4_finish_kernel(const I4AttnArgs
     for (int k = 0; k < kMaxSplits / 32; ++k)
       v[k] = k * 32 + lane < a.splits ? a.part_ml[part + k * 32 + lane] : make_float2(-INFINITY, 0.f);
     float x[D / 32] = {}, sum = 0.f;
-    constexpr int kAhead = 16;
+    constexpr int kAhead = 8;
     using Vec = typename std::conditional<D == 128, float4, float2>::type;
     Vec o[kAhead];
 #pragma unroll

@@ -47,7 +47,7 @@ constexpr int kKeys = 128;                       // keys per tile
 constexpr int kChunkBytes = 128 * 128;           // 128 rows x 64 bf16, 128-byte swizzle
 constexpr uint32_t kTmemCols = 512;              // S0, S1, O0, O1 of 128 columns each
 constexpr uint32_t kOCol = 256;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kItemWarp = 10;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;                     // log2 growth of the maximum that forces a rescale
@@ -278,6 +278,23 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "Cfg::kSmem");
 
+// One tile of keys or values; one tile of queries (one thread).
+template <int D>
+__device__ __forceinline__ void load_tile(uint8_t* to, uint64_t* full, const CUtensorMap& map, const Item& t, int tile) {
+  mbar_arrive_expect_tx(smem_u32(full), Cfg<D>::kTile);
+  for (int c = 0; c < Cfg<D>::kChunks; ++c)
+    tma_load_5d(smem_u32(to + c * kChunkBytes), &map, smem_u32(full), c * 64, tile * kKeys, t.g, t.l, t.b);
+}
+
+template <int D>
+__device__ __forceinline__ void load_queries(Bars& s, uint8_t* sq, const CUtensorMap& map, const PromptArgs& a, const Item& t,
+                                             int i) {
+  mbar_arrive_expect_tx(smem_u32(&s.qfull[i]), Cfg<D>::kTile);
+  for (int c = 0; c < Cfg<D>::kChunks; ++c)
+    tma_load_5d(smem_u32(sq + i * Cfg<D>::kTile + c * kChunkBytes), &map, smem_u32(&s.qfull[i]), c * 64, t.g * a.G,
+                (t.row0 + i * kTileRows) / a.G, t.l, t.b);
+}
+
 // D: head dimension.  CAP, BIAS: the logits are capped, or get slopes.
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -293,7 +310,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   Bars& s = *reinterpret_cast<Bars*>(sv + C::kNv * C::kTile);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile int* abort_flag = &s.abort_flag;
-  if (threadIdx.x == 0) {
+  // One thread of the load warp sets up the barriers, works out the item and sends for the first queries and keys
+  // (the first tile of an item with documents depends on them), while another warp allocates tensor memory.
+  if (warp == kLoadWarp && lane == 0) {
+    if (a.q_tma) tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&s.kfull[i]), 1);
       mbar_init(smem_u32(&s.kempty[i]), 1);
@@ -305,20 +327,26 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       mbar_init(smem_u32(&s.phalf[i]), 4);
       mbar_init(smem_u32(&s.pfull[i]), 4);
       mbar_init(smem_u32(&s.odone[i]), 1);
+      mbar_init(smem_u32(&s.qfull[i]), a.q_tma ? 1 : 4);
     }
-    mbar_init(smem_u32(&s.qfull[0]), a.q_tma ? 1 : 4);
-    mbar_init(smem_u32(&s.qfull[1]), a.q_tma ? 1 : 4);
     mbar_init(smem_u32(&s.done), 1);
     s.abort_flag = 0;
     s.q_min = INT32_MAX;
     s.q_max = -1;
     fence_barrier_init();
+    const Item t = make_item(a, blockIdx.x);
+    s.item = t;
+    if (t.rows > 0) {
+      if (a.q_tma) load_queries<D>(s, sq, map_q, a, t, 0);
+      if (!a.docs && t.i0 < t.i1)
+        load_tile<D>(sk, &s.kfull[0], map_k, t, t.i0 + (t.i0 >= t.skip_at ? t.skip : 0));
+      if (a.q_tma && t.rows > kTileRows) load_queries<D>(s, sq, map_q, a, t, 1);
+    }
   }
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&s.tmem), kTmemCols);
     tmem_relinquish();
   }
-  if (warp == kItemWarp && lane == 0) s.item = make_item(a, blockIdx.x);
   if (a.docs) wait_for_previous_kernel();                // the documents of the key tiles
   tc_fence_before();
   __syncthreads();
@@ -386,44 +414,29 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == kLoadWarp) {
     // -------------------------------------------------------------- TMA producer: K(i + 1) before V(i)
-    if (lane == 0) {
-      tma_prefetch_desc(&map_k);
-      tma_prefetch_desc(&map_v);
-    }
     TileWalk walk(t, table, q_min, q_max);
-    auto load = [&](const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty, uint32_t n, int i,
+    auto load = [&](const CUtensorMap& map, uint8_t* ring, uint64_t* full, uint64_t* empty, uint32_t n, int i,
                     int tile) -> bool {
       const uint32_t st = i % n, ph = (i / n) & 1;
       if (!warp_wait(smem_u32(&empty[st]), ph ^ 1, abort_flag)) return false;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(smem_u32(&full[st]), C::kTile);
-        for (int c = 0; c < C::kChunks; ++c)
-          tma_load_5d(smem_u32(ring + st * C::kTile + c * kChunkBytes), map, smem_u32(&full[st]), c * 64, tile * kKeys,
-                      t.g, t.l, t.b);
-      }
+      if (lane == 0) load_tile<D>(ring + st * C::kTile, &full[st], map, t, tile);
       __syncwarp();
       return true;
     };
-    auto load_q = [&](int i) {
-      if (!a.q_tma || lane) return;
-      mbar_arrive_expect_tx(smem_u32(&s.qfull[i]), C::kTile);
-      for (int c = 0; c < C::kChunks; ++c)
-        tma_load_5d(smem_u32(sq + i * C::kTile + c * kChunkBytes), &map_q, smem_u32(&s.qfull[i]), c * 64, t.g * a.G,
-                    (t.row0 + i * kTileRows) / a.G, t.l, t.b);
-    };
     int nk = 0, nv = 0;
-    load_q(0);
     int cur = walk.next();
-    bool ok = cur < 0 || load(&map_k, sk, s.kfull, s.kempty, C::kNk, nk++, cur);
-    if (share) load_q(1);
-    if (cur < 0 || !ok) nk = 0;
+    bool ok = true;
+    if (cur >= 0) {
+      if (docs) ok = load(map_k, sk, s.kfull, s.kempty, C::kNk, 0, cur);      // else it is on its way
+      if (ok) nk = 1;
+    }
     while (cur >= 0 && ok) {
       const int nxt = walk.next();
       if (nxt >= 0) {
-        if (!(ok = load(&map_k, sk, s.kfull, s.kempty, C::kNk, nk, nxt))) break;
+        if (!(ok = load(map_k, sk, s.kfull, s.kempty, C::kNk, nk, nxt))) break;
         ++nk;
       }
-      if (!(ok = load(&map_v, sv, s.vfull, s.vempty, C::kNv, nv, cur))) break;
+      if (!(ok = load(map_v, sv, s.vfull, s.vempty, C::kNv, nv, cur))) break;
       ++nv;
       cur = nxt;
     }
@@ -811,7 +824,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         __syncwarp();
         const int chunk = lane & (chunks - 1), per = 32 / chunks;     // rows per instruction
         __nv_bfloat16* out = a.out + t.b * a.os.batch + t.l * a.os.layer + col0;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < chunks; ++i) {
           const int rr = i * per + lane / chunks, rt = quarter * 32 + rr;
           const int64_t at = __shfl_sync(0xffffffffu, own, rr);
