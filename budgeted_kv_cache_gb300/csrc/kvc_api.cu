@@ -1026,6 +1026,11 @@ kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_stri
     a.part_ml = reinterpret_cast<float2*>(ws + p.ws_docs);
     a.part_o = reinterpret_cast<float*>(ws + p.ws_docs + p.ws_ml);
   }
+  a.by_splits = FastDiv::of(a.splits);
+  a.by_units = FastDiv::of(a.U);
+  a.by_heads = FastDiv::of(a.Hkv);
+  a.by_layers = FastDiv::of(a.L);
+  a.by_group = FastDiv::of(a.G);
   a.q_tma = 128 % a.G == 0;
   CUtensorMap mq = {}, mk, mv;
   if (a.q_tma && (st = encode_rows(&mq, q, shape, shape->n_q_heads, n_q, a.qs, 128 / a.G, a.G, true)) != KVC_OK) return st;

@@ -208,6 +208,34 @@ struct Mods {
   const int32_t* prefix_len;   // optional [B]
 };
 
+// n / d for 32-bit n by a multiplication (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994): a division by a run-time
+// value is 30 to 40 instructions.
+struct FastDiv {
+  uint32_t d, mul, s1, s2;
+  static FastDiv of(uint32_t d) {
+    uint32_t l = 0;
+    while (l < 32 && (1ull << l) < d) ++l;
+    FastDiv f;
+    f.d = d;
+    f.mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+    f.s1 = l < 1 ? l : 1;
+    f.s2 = l < 1 ? 0 : l - 1;
+    return f;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    const uint32_t t = __umulhi(mul, n);
+    return (t + ((n - t) >> s1)) >> s2;
+  }
+  __device__ __forceinline__ uint32_t divmod(uint32_t n, uint32_t* rem) const {
+    const uint32_t q = div(n);
+    *rem = n - q * d;
+    return q;
+  }
+#endif
+};
+
 struct PromptArgs {
   int32_t U, L, Hkv, B, G, d, n_q;
   int64_t T;
@@ -230,6 +258,7 @@ struct PromptArgs {
   float* part_o;               // splits > 1: [U][n_q G][splits][d] unnormalised outputs
   float2* part_ml;             // [U][n_q G][splits] (log2-domain maximum, sum)
   int2* doc_tiles;             // with docs: [B][n_tiles] (min, max) document
+  FastDiv by_splits, by_units, by_heads, by_layers, by_group;   // divisors splits, U, Hkv, L, G
   bool q_tma;                  // G divides 128: a tile of rows is a box of whole queries
 };
 

@@ -191,11 +191,14 @@ struct Item {
 
 __device__ __forceinline__ Item make_item(const PromptArgs& a, int id) {
   Item t;
-  t.split = id % a.splits;
-  id /= a.splits;
-  t.u = id % a.U;
-  const int qb = a.n_blocks - 1 - id / a.U;      // long rows first: the causal tail fills the gaps
-  t.b = t.u / (a.L * a.Hkv), t.l = t.u / a.Hkv % a.L, t.g = t.u % a.Hkv;
+  uint32_t split, u, g, l;
+  const uint32_t qb_rev = a.by_units.divmod(a.by_splits.divmod(id, &split), &u);
+  t.split = static_cast<int>(split);
+  t.u = static_cast<int>(u);
+  const int qb = a.n_blocks - 1 - static_cast<int>(qb_rev);      // long rows first: the causal tail fills the gaps
+  t.b = static_cast<int>(a.by_layers.divmod(a.by_heads.divmod(u, &g), &l));
+  t.l = static_cast<int>(l);
+  t.g = static_cast<int>(g);
   t.nk = a.kv_len ? max(0, min(static_cast<int>(a.T), a.kv_len[t.b])) : static_cast<int>(a.T);
   const int nq = a.q_len ? clamp_count(a.q_len[t.b], a.n_q) : a.n_q;
   t.first = t.nk - nq;
@@ -206,7 +209,8 @@ __device__ __forceinline__ Item make_item(const PromptArgs& a, int id) {
     t.rows = t.lo = t.hi = t.n = t.skip = t.skip_at = t.i0 = t.i1 = 0;
     return t;
   }
-  const int p_min = t.first + t.row0 / a.G, p_max = t.first + (t.row0 + t.rows - 1) / a.G;
+  const int p_min = t.first + static_cast<int>(a.by_group.div(t.row0)),
+            p_max = t.first + static_cast<int>(a.by_group.div(t.row0 + t.rows - 1));
   t.hi = max(0, p_max + 1);
   t.lo = a.mods.window && p_min >= a.mods.window ? p_min - a.mods.window + 1 : 0;
   t.lo = min(t.lo, t.hi);
@@ -217,8 +221,8 @@ __device__ __forceinline__ Item make_item(const PromptArgs& a, int id) {
   t.skip = max(0, lo_tile - pre_tiles);
   t.n = max(pre_tiles, hi_tile) - t.skip;
   if (hi_tile <= lo_tile) t.n = pre_tiles, t.skip = 0;
-  t.i0 = static_cast<int>(static_cast<uint32_t>(t.n) * t.split / a.splits);     // tiles < 2^24, splits <= 256
-  t.i1 = t.split + 1 == a.splits ? t.n : static_cast<int>(static_cast<uint32_t>(t.n) * (t.split + 1) / a.splits);
+  t.i0 = static_cast<int>(a.by_splits.div(static_cast<uint32_t>(t.n) * split));      // tiles < 2^24, splits <= 256
+  t.i1 = t.split + 1 == a.splits ? t.n : static_cast<int>(a.by_splits.div(static_cast<uint32_t>(t.n) * (split + 1)));
   return t;
 }
 
@@ -292,7 +296,7 @@ __device__ __forceinline__ void load_queries(Bars& s, uint8_t* sq, const CUtenso
   mbar_arrive_expect_tx(smem_u32(&s.qfull[i]), Cfg<D>::kTile);
   for (int c = 0; c < Cfg<D>::kChunks; ++c)
     tma_load_5d(smem_u32(sq + i * Cfg<D>::kTile + c * kChunkBytes), &map, smem_u32(&s.qfull[i]), c * 64, t.g * a.G,
-                (t.row0 + i * kTileRows) / a.G, t.l, t.b);
+                static_cast<int>(a.by_group.div(t.row0 + i * kTileRows)), t.l, t.b);
 }
 
 // D: head dimension.  CAP, BIAS: the logits are capped, or get slopes.
@@ -551,7 +555,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const int r = quarter * 32 + lane;
     const int row = (share ? h * kTileRows : 0) + r;
     const bool valid = row < t.rows;
-    const int p = t.first + (t.row0 + (valid ? row : 0)) / a.G;
+    uint32_t in_group;                         // head of the group
+    const int p = t.first + static_cast<int>(a.by_group.divmod(t.row0 + (valid ? row : 0), &in_group));
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_col = tmem + lanes + h * 128, o_col = tmem + lanes + kOCol + h * 128;
     const bool warp_valid = __any_sync(0xffffffffu, valid);
@@ -575,7 +580,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       for (int k = 0; k < 5; ++k, f *= zs * zs) tc[k] = kTanh[k] * f;
     }
     // slope in units of y: base 2 behind a cap, raw scores otherwise
-    const float bias = BIAS ? a.mods.slopes[t.g * a.G + (t.row0 + (valid ? row : 0)) % a.G] * (CAP ? kLog2e : 1.f / a.scale) : 0.f;
+    const float bias = BIAS ? a.mods.slopes[t.g * a.G + static_cast<int>(in_group)] * (CAP ? kLog2e : 1.f / a.scale) : 0.f;
     const int all_pre_max = BIAS ? __reduce_max_sync(0xffffffffu, row_pre) : 0;
     float m = -INFINITY, l = 0.f;              // reference maximum (of y / cs) and sum of 2^(y - m cs)
     TileWalk walk(t, table, q_min, q_max);
@@ -775,7 +780,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     }
     if (!fail && warp_valid) {
       const int pr = t.row0 + (valid ? row : 0);
-      const int head = t.g * a.G + pr % a.G;
+      uint32_t in_group;
+      const int query = static_cast<int>(a.by_group.divmod(pr, &in_group)), head = t.g * a.G + static_cast<int>(in_group);
       const bool part = a.splits > 1;
       if (!part) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -783,7 +789,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         f1 *= inv;
       }
       const int64_t prow = static_cast<int64_t>(t.u) * a.n_q * a.G + pr;
-      const int64_t own = static_cast<int64_t>(head) * a.os.head + static_cast<int64_t>(pr / a.G) * a.os.token;
+      const int64_t own = static_cast<int64_t>(head) * a.os.head + static_cast<int64_t>(query) * a.os.token;
       // this stream's columns, staged in shared memory in 16-byte chunks (Q is not read any more)
       const int cols = share ? D : D / 2, col0 = share ? 0 : h * (D / 2);
       const int chunks = cols / 8, flip = min(chunks - 1, 7);
@@ -837,7 +843,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         if (part)
           a.part_ml[prow * a.splits + t.split] = make_float2(m2, l);
         else if (a.lse)
-          a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n_q + pr / a.G] =
+          a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n_q + query] =
               l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
       }
     }
