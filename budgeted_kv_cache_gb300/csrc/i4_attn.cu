@@ -131,7 +131,8 @@ struct Smem {
   float2 ml[NT * 8];                               // of the block
 };
 
-template <int D, int NT, bool ROW>
+// MODS: some change of the scores (cap, slopes, window, prefix) is asked for.
+template <int D, int NT, bool ROW, bool MODS>
 __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn_kernel(const I4AttnArgs a) {
   constexpr int NG = D / 32;                       // scale groups
   constexpr int CH = D / 32;                       // 16-byte chunks per row
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
   const Unit un(a, blockIdx.y + blockIdx.z * 65535);
   // what does not depend on the rows in use is on its way before anything waits for them
   const int32_t next = a.rows.next_pos[un.u];
-  const int prefix = a.mods.prefix_len ? a.mods.prefix_len[un.b] : INT32_MIN;
+  const int prefix = MODS && a.mods.prefix_len ? a.mods.prefix_len[un.b] : INT32_MIN;
   const int split = blockIdx.x % a.splits, r0 = blockIdx.x / a.splits * (NT * 8);
   uint32_t qf[NT][NG][4];                          // operand of both products' k-steps of a group
 #pragma unroll
@@ -219,26 +220,31 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
       const int r = min(r0 + nt * 8 + 2 * t + e, un.R - 1), i = r / a.G;
       const int64_t p = a.q_pos ? a.q_pos[un.b * a.n_q + i] : static_cast<int64_t>(next) - a.n_q + i;
       q_hi[nt][e] = static_cast<int>(max(p, static_cast<int64_t>(INT32_MIN)));
-      q_lo[nt][e] = a.mods.window ? static_cast<int>(max(p - a.mods.window + 1, static_cast<int64_t>(INT32_MIN))) : INT32_MIN;
-      slope[nt][e] = a.mods.slopes ? a.mods.slopes[un.g * a.G + r % a.G] * kLog2e : 0.f;
+      q_lo[nt][e] = MODS && a.mods.window ? static_cast<int>(max(p - a.mods.window + 1, static_cast<int64_t>(INT32_MIN))) : INT32_MIN;
+      slope[nt][e] = MODS && a.mods.slopes ? a.mods.slopes[un.g * a.G + r % a.G] * kLog2e : 0.f;
     }
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) copy_tile(t0 + warp + i * kWarps, i);
   fetch(t0 + warp);
 
-  const bool capped = a.mods.softcap > 0.f, biased = a.mods.slopes != nullptr;
-  const bool modified = capped || biased;
+  const bool capped = MODS && a.mods.softcap > 0.f, biased = MODS && a.mods.slopes;
+  const bool modified = capped || biased, windowed = MODS && a.mods.window;
   const float pre = capped ? a.scale : a.scale * kLog2e;      // goes into the key scales
   const float inv_cap = capped ? 1.f / a.mods.softcap : 0.f;
-  int hi_min = INT32_MAX, lo_max = INT32_MIN;
+  // limits over the block's query rows
+  int hi_min = INT32_MAX, lo_max = INT32_MIN, hi_max = INT32_MIN, lo_min = INT32_MAX;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       hi_min = min(hi_min, q_hi[nt][e]);
+      hi_max = max(hi_max, q_hi[nt][e]);
+      lo_min = min(lo_min, q_lo[nt][e]);
       lo_max = max(lo_max, q_lo[nt][e]);
     }
   hi_min = __reduce_min_sync(kFull, hi_min);
+  hi_max = __reduce_max_sync(kFull, hi_max);
+  lo_min = __reduce_min_sync(kFull, lo_min);
   lo_max = __reduce_max_sync(kFull, lo_max);
   float* const log_row = a.logits + (un.base + g) * a.logit_stride + r0 + 2 * t;      // [key][R rounded up to even]
   const uint32_t half_sel = (g >> 2) ? 0x7632u : 0x5410u;
@@ -262,10 +268,24 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
     put_scales(&s.scale[warp][1][lane][0], vs_next, 1.f);
     s.pos[warp][lane] = pos_next;
     // does every query row see every key of the tile?
-    const bool clear = __all_sync(kFull, i * kTile + lane < un.n && pos_next <= hi_min && pos_next >= lo_max);
+    const bool mine = i * kTile + lane < un.n;
+    const bool clear = __all_sync(kFull, mine && pos_next <= hi_min && (!MODS || pos_next >= lo_max));
+    // does none see any?  Known without the codes, but they are on their way
+    const bool none = !clear && windowed &&
+                      !__any_sync(kFull, mine && ((pos_next <= hi_max && pos_next >= lo_min) || pos_next < prefix));
     fetch(i + kWarps);
     cp_async_wait<kStages - 1>();
     __syncwarp();
+    if (none) {
+      if (a.logits && mine) {
+        float* dst = a.logits + (un.base + i * kTile + lane) * a.logit_stride + r0;
+        for (int c = 0; c < min(NT * 8, a.logit_stride - r0); c += 2)
+          *reinterpret_cast<float2*>(dst + c) = make_float2(-INFINITY, -INFINITY);
+      }
+      __syncwarp();
+      st = (st + 1) % kStages;
+      continue;
+    }
     const uint8_t* kc = &s.codes[warp][st][0][0][0];
     const uint8_t* vc = &s.codes[warp][st][1][0][0];
     auto scale_f = [&](int which, int key, float (&f)[NG]) {
@@ -322,31 +342,46 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
           for (int c = 0; c < 4; ++c) y[sub][nt][c] *= c < 2 ? f0[0] : f1[0];
       }
       if (modified || !clear) {
-        // cap tanh(x / cap): a polynomial while the warp's |x / cap| is small, else cap (1 - 2 / (1 + e^(2 x / cap)))
-        bool small = true;
+        const int pk[2] = {s.pos[warp][k0], s.pos[warp][k1]};
         if (capped) {
+          // cap tanh(x / cap): a polynomial while the warp's |x / cap| is small, else cap (1 - 2 / (1 + e^(2 x / cap)))
           float big = 0.f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c) big = fmaxf(big, fabsf(y[sub][nt][c]));
-          small = __all_sync(kFull, big * inv_cap <= kTanhRange);
-        }
-        const int pk[2] = {s.pos[warp][k0], s.pos[warp][k1]};
-        const bool in_use[2] = {i * kTile + k0 < un.n, i * kTile + k1 < un.n};
+          if (__all_sync(kFull, big * inv_cap <= kTanhRange)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int e = c & 1, k = c >> 1;
-            float x = y[sub][nt][c];
-            if (capped) x = small ? x * tanh_over_z(x * inv_cap) * kLog2e
-                                  : fmaf(-2.f * a.mods.softcap, rcp_approx(1.f + ex2_approx(x * (inv_cap * (2.f * kLog2e)))),
-                                         a.mods.softcap) * kLog2e;
-            if (biased) x = fmaf(-slope[nt][e], fabsf(static_cast<float>(q_hi[nt][e] - pk[k])), x);
-            const bool seen = in_use[k] && ((pk[k] <= q_hi[nt][e] && pk[k] >= q_lo[nt][e]) || pk[k] < prefix);
-            y[sub][nt][c] = seen ? x : -INFINITY;
+              for (int c = 0; c < 4; ++c) y[sub][nt][c] *= tanh_over_z(y[sub][nt][c] * inv_cap) * kLog2e;
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                y[sub][nt][c] = fmaf(-2.f * a.mods.softcap, rcp_approx(1.f + ex2_approx(y[sub][nt][c] * (inv_cap * (2.f * kLog2e)))),
+                                     a.mods.softcap) * kLog2e;
           }
+        }
+        if (biased) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              y[sub][nt][c] = fmaf(-slope[nt][c & 1], fabsf(static_cast<float>(q_hi[nt][c & 1] - pk[c >> 1])), y[sub][nt][c]);
+        }
+        if (!clear) {
+          const bool in_use[2] = {i * kTile + k0 < un.n, i * kTile + k1 < un.n};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int e = c & 1, k = c >> 1;
+              const bool seen = in_use[k] && ((pk[k] <= q_hi[nt][e] && (!MODS || pk[k] >= q_lo[nt][e])) || (MODS && pk[k] < prefix));
+              if (!seen) y[sub][nt][c] = -INFINITY;
+            }
+        }
       }
       if (a.logits) {
         float* dst = log_row + (static_cast<int64_t>(i) * kTile + sub * 16) * a.logit_stride;
@@ -658,7 +693,9 @@ __global__ void __launch_bounds__(kFinThreads, 4) i4_finish_kernel(const I4AttnA
 
 template <int D, int NT, bool ROW>
 cudaError_t launch_one(const I4AttnArgs& a, cudaStream_t stream) {
-  auto kernel = i4_attn_kernel<D, NT, ROW>;
+  // the plain scores' kernel is one of its own: with the branches of the others in its loop it takes 3-4 % longer
+  const bool mods = a.mods.softcap > 0.f || a.mods.slopes || a.mods.window || a.mods.prefix_len;
+  auto kernel = mods ? i4_attn_kernel<D, NT, ROW, true> : i4_attn_kernel<D, NT, ROW, false>;
   const int bytes = static_cast<int>(sizeof(Smem<D, NT, ROW>));
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
