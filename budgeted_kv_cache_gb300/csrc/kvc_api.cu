@@ -443,11 +443,13 @@ kvc_status plan_i4_attn(const kvc_shape* s, const kvc_i4_rows* r, int32_t n_q, u
   DevInfo info;
   if ((st = check_device(&info)) != KVC_OK) return st;
   // One round of the blocks (of four warps) that the SMs hold, not a block more, each warp with a tile of 32 keys at
-  // least; a second round, which evens out ragged lengths, where a block still gets 1,024 keys.  Measured (128 wide, 4
-  // heads): 32 units of 100K to 128K rows 153 us in two rounds, 159 in one; 8 units of 32K rows 40 and 32 us.
+  // least; two full rounds, which even out ragged lengths, where every block then still gets 1,024 keys.  Measured
+  // (128 wide, 4 heads): 32 units of 100K to 128K rows 153 us in two rounds, 159 in one; 8 units of 100K to 128K rows
+  // 54 in 1.7 rounds, 49 in one; (64 wide, 3 heads, 5 queries) 64 units of 8,000 to 9,000 rows 34 us in 1.1 rounds, 26 in
+  // one, of 300 to 9,000 rows 23 and 25.
   const int64_t blocks = U * ((rows + 31) / 32), slots = (rows <= 8 ? 4 : rows <= 16 ? 3 : 2) * info.sms;
-  const int64_t want = std::max(std::min<int64_t>(slots / blocks, r->capacity / 128),
-                                std::min<int64_t>(2 * slots / blocks, r->capacity / 1024));
+  const bool two = r->capacity / 1024 >= 2 * slots / blocks;
+  const int64_t want = two ? 2 * slots / blocks : std::min<int64_t>(slots / blocks, r->capacity / 128);
   p->splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(want, kMaxSplits)));
   p->logit_stride = static_cast<int32_t>((rows + 1) / 2 * 2);
   // mass: a key per thread for small caches, up to eight blocks of 256 threads per SM for long ones
