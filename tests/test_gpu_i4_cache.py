@@ -2,6 +2,7 @@
 scales, positions, counters, overflow), attention with accumulated mass, eviction in place, and a prompt and
 its tokens run through all of them."""
 import math
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -220,6 +221,7 @@ ATTN = {
     "window": dict(Hkv=2, G=4, n_q=4, cap=900, counts=[900], window=100, add=True),
     "window_nothing": dict(Hkv=1, G=2, n_q=2, cap=90, counts=[20], window=1, add=True),
     "prefix": dict(B=2, Hkv=1, G=2, n_q=4, cap=500, counts=[500, 400], window=30, prefix=[200, 0], add=True),
+    "window_many_rows": dict(Hkv=1, G=5, n_q=11, cap=2000, counts=[1900], window=40, add=True),
     "given_positions": dict(B=2, Hkv=2, G=2, n_q=3, cap=300, counts=[300, 200], q_pos=[[-1, 100, 5000], [0, 7, 200]], add=True),
     "everything": dict(B=2, L=2, Hkv=2, G=5, n_q=7, cap=1500, counts=[1500, 700], softcap=8.0, slopes=True, window=900,
                        prefix=[50, 0], add=True, token=True),
@@ -413,6 +415,68 @@ def test_evict(kvc, name):
         for t, t0 in zip(fields(r)[:6], before[:6]):
             assert torch.equal(t[u].contiguous().view(torch.uint8), t0[u][at].contiguous().view(torch.uint8))
         assert int(r.next_pos[u]) == int(before[7][u])
+
+
+# ---------------------------------------------------------------- large caches
+
+def test_more_units_than_a_grid_dimension_holds(kvc):
+    """2 x 32,800 units in one call: the bits of a call for each half."""
+    B, H, d, cap = 2, 32800, 64, 4
+    g = gen(9)
+    k, v, q = randn(g, B, 1, H, 3, d), randn(g, B, 1, H, 3, d), randn(g, B, 1, H, 1, d)
+
+    def run(b0, b1):
+        n = b1 - b0
+        shape = kvc.make_shape(n, 1, H, H, d, 1)
+        rows = kvc.I4Rows.allocate(shape, cap)
+        for t in fields(rows)[:6]:
+            t.zero_()
+        out, lse = torch.empty_like(q[b0:b1]), torch.empty(n, 1, H, 1, device="cuda")
+        k_out, v_out = torch.zeros_like(k[b0:b1]), torch.zeros_like(k[b0:b1])
+        kvc.kvc_i4_append(shape, rows, k[b0:b1], v[b0:b1])
+        ws = torch.empty(kvc.kvc_i4_attn_workspace_bytes(shape, rows, 1, True), dtype=torch.uint8, device="cuda")
+        kvc.kvc_i4_attn(shape, rows, q[b0:b1], out, add_mass=True, row_lse=lse, workspace=ws)
+        ws = torch.empty(max(1, kvc.kvc_i4_evict_workspace_bytes(shape, rows, 2)), dtype=torch.uint8, device="cuda")
+        kvc.kvc_i4_evict(shape, rows, 2, 0, 0, workspace=ws)
+        kvc.kvc_i4_read(shape, rows, k_out, v_out)
+        torch.cuda.synchronize()
+        assert bool((rows.count == 2).all()) and bool((rows.next_pos == 3).all())
+        return [out, lse, k_out, v_out] + fields(rows)
+
+    for whole, first, second in zip(run(0, 2), run(0, 1), run(1, 2)):
+        assert torch.equal(whole, torch.cat([first, second]))
+
+
+def test_rows_past_32_bit_offsets(kvc):
+    """Units of 70 million slots: the second one's rows lie past 2^31 bytes."""
+    small, n = Cache(kvc, 1, 1, 2, 64, 320, [300], ROW, n_q_heads=4), 320
+    big = kvc.I4Rows.allocate(small.shape, 70_000_000, ROW)
+    part = [t[:, :n] if t.dim() > 1 else t for t in fields(big)]
+    for t, t0 in zip(part, fields(small.rows)):
+        t.copy_(t0)
+    x, y, q = randn(small.g, 1, 1, 2, 10, 64), randn(small.g, 1, 1, 2, 10, 64), randn(small.g, 1, 1, 4, 2, 64)
+    for rows in (small.rows, big):
+        kvc.kvc_i4_append(small.shape, rows, x, y)
+    torch.cuda.synchronize()
+    for t, t0 in zip(part, fields(small.rows)):
+        assert torch.equal(t.contiguous().view(torch.uint8), t0.contiguous().view(torch.uint8))
+    out, lse, mass0 = torch.empty_like(q), torch.empty(q.shape[:-1], device="cuda"), part[5].clone()
+    ws = torch.empty(kvc.kvc_i4_attn_workspace_bytes(small.shape, big, 2, True), dtype=torch.uint8, device="cuda")
+    kvc.kvc_i4_attn(small.shape, big, q, out, add_mass=True, row_lse=lse, workspace=ws)
+    names = ["k", "v", "k_scale", "v_scale", "pos", "mass", "count", "next_pos"]
+    check_attention(SimpleNamespace(rows=SimpleNamespace(**dict(zip(names, part))), shape=small.shape, d=64), q, out, lse,
+                    mass0, add=True)
+    small.rows.mass.copy_(part[5])
+    outs = []
+    for rows in (small.rows, big):
+        ws = torch.empty(max(1, kvc.kvc_i4_evict_workspace_bytes(small.shape, rows, 305)), dtype=torch.uint8, device="cuda")
+        kvc.kvc_i4_evict(small.shape, rows, 305, 4, 16, workspace=ws)
+        outs.append([torch.zeros(1, 1, 2, n, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)])
+        kvc.kvc_i4_read(small.shape, rows, *outs[-1])
+    torch.cuda.synchronize()
+    assert big.count.tolist() == [305, 305]
+    for t, t0 in zip(part + outs[1], fields(small.rows) + outs[0]):
+        assert torch.equal(t.contiguous().view(torch.uint8), t0.contiguous().view(torch.uint8))
 
 
 # ---------------------------------------------------------------- together

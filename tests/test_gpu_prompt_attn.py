@@ -99,6 +99,8 @@ CASES = {
     "seven_heads": dict(n_q=301, T=333, G=7, Hkv=1, d=64),
     "wide_group": dict(n_q=3, T=700, G=33, Hkv=1),
     "very_wide_group": dict(n_q=2, T=140, G=150, Hkv=1, d=64),
+    "group_of_half_a_tile": dict(B=2, n_q=5, T=300, G=64, Hkv=2, q_len=[5, 2]),
+    "group_of_a_tile": dict(n_q=3, T=300, G=128, Hkv=2, d=64),
     "layers": dict(B=2, L=3, n_q=65, T=200, G=2),
     "square": dict(n_q=600, T=600, G=4, Hkv=1),
     "chunk_of_long": dict(n_q=100, T=3001, G=4, Hkv=2),
