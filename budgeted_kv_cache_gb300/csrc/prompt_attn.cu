@@ -299,6 +299,13 @@ __device__ __forceinline__ void load_queries(Bars& s, uint8_t* sq, const CUtenso
                 static_cast<int>(a.by_group.div(t.row0 + i * kTileRows)), t.l, t.b);
 }
 
+// The polynomial in x^2 with coefficients c, lowest first: of the odd function x p(x^2).
+__device__ __forceinline__ uint64_t odd_factor(uint64_t x, const float (&c)[5]) {
+  const uint64_t w = mul2(x, x);
+  return fma2(fma2(fma2(fma2(pair(c[4], c[4]), w, pair(c[3], c[3])), w, pair(c[2], c[2])), w, pair(c[1], c[1])), w,
+              pair(c[0], c[0]));
+}
+
 // D: head dimension.  CAP, BIAS: the logits are capped, or get slopes.
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -611,23 +618,28 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
       float (&y)[4][32] = reinterpret_cast<float (&)[4][32]>(sr);
       const int j0 = tile * kKeys;
+      // z = s scale / cap; cap tanh(z) log2 e = s times a polynomial in s^2 as long as the warp's |z| are small.  It
+      // grows with s, so without slopes the maximum is that of s, and the polynomial is evaluated between the
+      // exponentials (it fills the fp32 pipe while they wait for theirs).
+      bool late = false;
       if constexpr (CAP) {
-        // z = s scale / cap; cap tanh(z) log2 e = s times a polynomial in s^2 as long as the warp's |z| are small
         float big = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) big = fmaxf(big, fmaxf(fabsf(y[c][e]), fabsf(y[c][e + 1])));
         if (__all_sync(0xffffffffu, (big * zs <= kTanhRange && big < 1e18f) || !valid)) {
-          const uint64_t k4 = pair(tc[4], tc[4]), k3 = pair(tc[3], tc[3]), k2 = pair(tc[2], tc[2]), k1 = pair(tc[1], tc[1]),
-                         k0 = pair(tc[0], tc[0]);
+          if constexpr (BIAS) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const uint64_t x = pair(y[c][e], y[c][e + 1]), w = mul2(x, x);
-              unpair(mul2(x, fma2(fma2(fma2(fma2(k4, w, k3), w, k2), w, k1), w, k0)), &y[c][e], &y[c][e + 1]);
-            }
+              for (int e = 0; e < 32; e += 2) {
+                const uint64_t x = pair(y[c][e], y[c][e + 1]);
+                unpair(mul2(x, odd_factor(x, tc)), &y[c][e], &y[c][e + 1]);
+              }
+          } else {
+            late = true;
+          }
         } else {
           // cap tanh(z) = cap (1 - 2 / (1 + e^2z)): right at both infinities
 #pragma unroll
@@ -698,7 +710,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 #pragma unroll
         for (int e = 2; e < 32; e += 2) mx[c] = fmaxf(mx[c], fmaxf(y[c][e], y[c][e + 1]));
       }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if (late) {                              // -inf stays: the leading coefficient is positive
+        const float w = top * top;
+        top *= fmaf(fmaf(fmaf(fmaf(tc[4], w, tc[3]), w, tc[2]), w, tc[1]), w, tc[0]);
+      }
       const bool grow = (top - m) * cs > kGrow;          // also from -inf
       if (__any_sync(0xffffffffu, grow)) {
         float f = 1.f;
@@ -726,26 +742,30 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       const float sub = m == -INFINITY ? 0.f : m * cs;
       const uint64_t cs2 = pair(cs, cs), sub2 = pair(-sub, -sub);
       uint64_t sum[2] = {0, 0};
+      auto weights = [&](auto exponent) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float p0, p1;
-          unpair(fma2(pair(y[c][e], y[c][e + 1]), cs2, sub2), &p0, &p1);
-          p0 = ex2_approx(p0);
-          p1 = ex2_approx(p1);
-          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(p0, p1));
-          pk[e / 2] = pack_bf16x2(p0, p1);
+          for (int e = 0; e < 32; e += 2) {
+            float p0, p1;
+            unpair(exponent(pair(y[c][e], y[c][e + 1])), &p0, &p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(p0, p1));
+            pk[e / 2] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(s_col + c * 16, pk);
+          if (c == 1) {                        // the product may start on the first half of the keys
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.phalf[h]));
+          }
         }
-        tmem_st16(s_col + c * 16, pk);
-        if (c == 1) {                          // the product may start on the first half of the keys
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s.phalf[h]));
-        }
-      }
+      };
+      if (CAP && !BIAS && late) weights([&](uint64_t x) { return fma2(x, odd_factor(x, tc), sub2); });
+      else weights([&](uint64_t x) { return fma2(x, cs2, sub2); });
       float s0, s1;
       unpair(add2(sum[0], sum[1]), &s0, &s1);
       l += s0 + s1;
