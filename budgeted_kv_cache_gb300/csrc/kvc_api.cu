@@ -371,9 +371,30 @@ kvc_status check_queries(const kvc_shape* s, int64_t n_q) {
 }
 
 struct PromptPlan {
-  int32_t n_tiles = 0, block_rows = 0, n_blocks = 0, splits = 1;
+  int32_t n_tiles = 0, block_rows = 0, n_blocks = 0, splits = 1, sms = 0;
   size_t ws_docs = 0, ws_ml = 0, ws_total = 0;
 };
+
+// Fewer items than SMs: their keys are split as far as one round of the SMs
+// goes and a split keeps 4 tiles of keys.  Measured (8 KV heads of 4, d =
+// 128): a token over 8,192 keys 53 us whole, 15.5 in 16 splits, 17.7 in 19;
+// over 131,072 780 us whole, 87 in 19, 125 in 76; 256 tokens over 32,768 220
+// us whole, 122 in 2, 166 in 10.  Of 2,000 tokens, which fill the SMs: 35 us
+// whole, 84 in 2 splits (the partial outputs).
+// Sequences of a batch, which end at different lengths, are evened out by
+// splits over several whole rounds as long as each keeps 32 tiles and there
+// are few outputs: a token over 16 sequences of up to 32,768 keys 227 us
+// whole, 180 in 7 splits; over 16 of just 32,768 295 and 306.
+int32_t prompt_splits(int64_t sms, int32_t batch, int64_t items, int32_t n_blocks, int64_t tiles) {
+  const int64_t one = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(sms / items, tiles / 4), 256));
+  if (n_blocks == 1 && batch > 1) {
+    for (int64_t rounds = 6; rounds > 1; --rounds) {
+      const int64_t n = rounds * sms / items;
+      if (n > one && n <= 256 && tiles >= 32 * n) return static_cast<int32_t>(n);
+    }
+  }
+  return static_cast<int32_t>(one);
+}
 
 kvc_status plan_prompt(const kvc_shape* s, int32_t n_q, bool with_docs, PromptPlan* p) {
   kvc_status st = check_shape(s);
@@ -383,19 +404,17 @@ kvc_status plan_prompt(const kvc_shape* s, int32_t n_q, bool with_docs, PromptPl
   DevInfo info;
   if ((st = check_device(&info)) != KVC_OK) return st;
   const int64_t U = n_units(s), rows = static_cast<int64_t>(n_q) * (s->n_q_heads / s->n_kv_heads);
+  p->sms = info.sms;
   p->n_tiles = static_cast<int32_t>((s->n_tokens + kTileTokens - 1) / kTileTokens);
-  // two row tiles per item share the key tiles; one row tile per item where
-  // that is all there is or where pairs would leave SMs idle
-  p->block_rows = rows > 128 && U * ((rows + 255) / 256) >= info.sms ? 256 : 128;
+  // Two row tiles per item share the key tiles; one row tile per item while
+  // those fill one round of the SMs at most.  Measured (32 heads over 8, d =
+  // 128): 300 tokens 11.5 us in pairs, 9.9 one by one; 1,000 tokens 19.3 and
+  // 20.4; 800 tokens over 4,096 keys 53 and 60; 8,192 tokens 357 and 449.
+  p->block_rows = rows > 128 && U * ((rows + 127) / 128) > info.sms ? 256 : 128;
   p->n_blocks = static_cast<int32_t>((rows + p->block_rows - 1) / p->block_rows);
   const int64_t items = U * p->n_blocks;
   if (items > (1 << 28)) return KVC_ERR_UNSUPPORTED;
-  if (items < 2LL * info.sms) {
-    // several CTAs per SM's worth of items, so that ragged lengths even out;
-    // a split keeps at least 8 key tiles
-    const int64_t want = std::min<int64_t>((4LL * info.sms + items - 1) / items, p->n_tiles / 8);
-    p->splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(want, 256)));
-  }
+  p->splits = prompt_splits(info.sms, s->batch, items, p->n_blocks, p->n_tiles);
   if (with_docs) p->ws_docs = (static_cast<size_t>(s->batch) * p->n_tiles * sizeof(int2) + 255) / 256 * 256;
   p->ws_total = p->ws_docs;
   if (p->splits > 1) {
@@ -1018,9 +1037,10 @@ kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_stri
   a.n_blocks = p.n_blocks;
   a.splits = p.splits;
   if (a.mods.window > 0 && !a.mods.prefix_len) {
-    // no item walks more tiles than the window and its rows' queries touch
+    // no item walks more tiles than the window and its rows' queries touch: not more splits than the plan's
     const int64_t keys = static_cast<int64_t>(a.mods.window) + (p.block_rows + a.G - 1) / a.G;
-    a.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(p.splits, (keys / kTileTokens + 2) / 8)));
+    a.splits = prompt_splits(p.sms, a.B, static_cast<int64_t>(a.U) * p.n_blocks, p.n_blocks,
+                             std::min<int64_t>(p.n_tiles, keys / kTileTokens + 2));
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (docs) a.doc_tiles = reinterpret_cast<int2*>(ws);
