@@ -792,10 +792,21 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h]));
     }
-    // the last product of this stream
+    // statistics of the row, once they are those of all its keys in this item
+    const bool part = a.splits > 1;
+    const int query = p - t.first, head = t.g * a.G + static_cast<int>(in_group);
+    const int64_t prow = static_cast<int64_t>(t.u) * a.n_q * a.G + t.row0 + (valid ? row : 0);
+    auto write_stats = [&](float top, float sum) {
+      if (part)
+        a.part_ml[prow * a.splits + t.split] = make_float2(top, sum);
+      else if (a.lse)
+        a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n_q + query] =
+            sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    };
+    float m2 = m == -INFINITY ? -INFINITY : m * cs;
+    if (share && valid) write_stats(m2, l);      // while the last product of this stream runs
     if (!fail && n > 0 && !warp_wait(smem_u32(&s.odone[h]), (n - 1) & 1, abort_flag)) fail = true;
     tc_fence_after();
-    float m2 = m == -INFINITY ? -INFINITY : m * cs;
     // One row tile: both streams hold an output for the same rows, in the same lanes of tensor memory.  They exchange
     // (m, l) through the unused second Q tile, and each joins and writes one half of the columns.
     int n_other = 0;
@@ -815,18 +826,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       // the same order of the sum on both sides
       l = h == 0 ? fmaf(l, f0, o.y * f1) : fmaf(o.y, f1, l * f0);
       m2 = mm;
+      if (valid && h == 0) write_stats(m2, l);
     }
     if (!fail && warp_valid) {
-      const int pr = t.row0 + (valid ? row : 0);
-      uint32_t in_group;
-      const int query = static_cast<int>(a.by_group.divmod(pr, &in_group)), head = t.g * a.G + static_cast<int>(in_group);
-      const bool part = a.splits > 1;
       if (!part) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         f0 *= inv;
         f1 *= inv;
       }
-      const int64_t prow = static_cast<int64_t>(t.u) * a.n_q * a.G + pr;
       const int64_t own = static_cast<int64_t>(head) * a.os.head + static_cast<int64_t>(query) * a.os.token;
       // this stream's columns, staged in shared memory in 16-byte chunks (Q is not read any more)
       const int cols = share ? D : D / 2, col0 = share ? 0 : h * (D / 2);
@@ -834,23 +841,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       uint8_t* stage = sq + h * C::kTile + (share ? 0 : h * 4096);
       float* part_o = a.part_o + (prow * a.splits + t.split) * D + col0;
       const uint32_t mine = o_col + col0, other = tmem + lanes + kOCol + (h ^ 1) * 128 + col0;
-#pragma unroll 1
-      for (int c = 0; c < cols / 32; ++c) {
-        uint32_t o[32];
-        float x[32];
-        if (n > 0) {
-          tmem_ld32_issue(mine + c * 32, o);
-          tmem_ld_wait(o);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
-        if (n_other > 0) {
-          tmem_ld32_issue(other + c * 32, o);
-          tmem_ld_wait(o);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o[e]), f1, x[e]);
-        }
-        if (!valid) continue;
+      auto put = [&](int c, const float (&x)[32]) {
+        if (!valid) return;
         if (part) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
@@ -861,6 +853,42 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             *reinterpret_cast<uint4*>(stage + (r * chunks + ((c * 4 + e / 8) ^ (r & flip))) * 16) =
                 make_uint4(pack_bf16x2(x[e], x[e + 1]), pack_bf16x2(x[e + 2], x[e + 3]),
                            pack_bf16x2(x[e + 4], x[e + 5]), pack_bf16x2(x[e + 6], x[e + 7]));
+        }
+      };
+      // every column of this warp is on its way before the first is used; a stream without tiles holds nothing
+      constexpr int kOwn = D / 32, kHalf = D / 64;
+      uint32_t o[kOwn][32] = {};
+      float x[32];
+      if (share) {
+        if (n > 0) {
+#pragma unroll
+          for (int c = 0; c < kOwn; ++c) tmem_ld32_issue(mine + c * 32, o[c]);
+#pragma unroll
+          for (int c = 0; c < kOwn; ++c) tmem_ld_wait(o[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < kOwn; ++c) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(o[c][e]) * f0;
+          put(c, x);
+        }
+      } else {
+        if (n > 0) {
+#pragma unroll
+          for (int c = 0; c < kHalf; ++c) tmem_ld32_issue(mine + c * 32, o[c]);
+        }
+        if (n_other > 0) {
+#pragma unroll
+          for (int c = 0; c < kHalf; ++c) tmem_ld32_issue(other + c * 32, o[kHalf + c]);
+        }
+#pragma unroll
+        for (int c = 0; c < kOwn; ++c) tmem_ld_wait(o[c]);
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            x[e] = fmaf(__uint_as_float(o[kHalf + c][e]), f1, __uint_as_float(o[c][e]) * f0);
+          put(c, x);
         }
       }
       if (!part) {
@@ -876,13 +904,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             *(reinterpret_cast<uint4*>(out + at) + chunk) =
                 *reinterpret_cast<const uint4*>(stage + (rt * chunks + (chunk ^ (rt & flip))) * 16);
         }
-      }
-      if (valid && (share || h == 0)) {
-        if (part)
-          a.part_ml[prow * a.splits + t.split] = make_float2(m2, l);
-        else if (a.lse)
-          a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n_q + query] =
-              l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
       }
     }
     if (fail && lane == 0 && a.unit_status) a.unit_status[s.item.u] = KVC_UNIT_TIMEOUT;
