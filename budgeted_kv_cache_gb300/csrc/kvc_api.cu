@@ -1054,11 +1054,13 @@ kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_stri
   a.by_layers = FastDiv::of(a.L);
   a.by_group = FastDiv::of(a.G);
   a.q_tma = 128 % a.G == 0;
-  CUtensorMap mq = {}, mk, mv;
+  a.o_tma = 32 % a.G == 0;
+  CUtensorMap mq = {}, mk, mv, mo = {};
   if (a.q_tma && (st = encode_rows(&mq, q, shape, shape->n_q_heads, n_q, a.qs, 128 / a.G, a.G, true)) != KVC_OK) return st;
   if ((st = encode_rows(&mk, k, shape, shape->n_kv_heads, shape->n_tokens, a.kvs, kTileTokens, 1, false)) != KVC_OK) return st;
   if ((st = encode_rows(&mv, v, shape, shape->n_kv_heads, shape->n_tokens, a.kvs, kTileTokens, 1, false)) != KVC_OK) return st;
-  return launch_prompt(a, mq, mk, mv, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+  if (a.o_tma && (st = encode_rows(&mo, out, shape, shape->n_q_heads, n_q, a.os, 32 / a.G, a.G, true)) != KVC_OK) return st;
+  return launch_prompt(a, mq, mk, mv, mo, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
 kvc_status kvc_i4_append(const kvc_shape* shape, const kvc_i4_rows* rows, const void* k,

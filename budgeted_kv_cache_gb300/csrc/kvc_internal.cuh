@@ -260,6 +260,7 @@ struct PromptArgs {
   int2* doc_tiles;             // with docs: [B][n_tiles] (min, max) document
   FastDiv by_splits, by_units, by_heads, by_layers, by_group;   // divisors splits, U, Hkv, L, G
   bool q_tma;                  // G divides 128: a tile of rows is a box of whole queries
+  bool o_tma;                  // G divides 32: a warp's rows are
 };
 
 struct I4AppendArgs {
@@ -337,7 +338,7 @@ cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_engine(const DecodeArgs& a, cudaStream_t stream);
 size_t prompt_smem_bytes(int d);
 cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v,
-                          cudaStream_t stream);
+                          const CUtensorMap& map_o, cudaStream_t stream);
 cudaError_t launch_i4_append(const I4AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_read(const I4ReadArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream);

@@ -87,6 +87,19 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_5d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5, %6}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
+// Until the stores of this thread have read their sources.
+__device__ __forceinline__ void tma_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 // The MMA warp stays converged and lets one elected lane issue, by predicate:
 // under `if (lane == 0)` the compiler keeps descriptors in per-thread
 // registers and moves each to the uniform ones in front of every instruction
@@ -328,7 +341,7 @@ __device__ __forceinline__ uint64_t odd_factor(uint64_t x, const float (&c)[5]) 
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-              const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+              const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o, const PromptArgs a) {
   using C = Cfg<D>;
   let_next_kernel_start();
   extern __shared__ uint8_t smem_raw[];
@@ -370,6 +383,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       if (!a.docs && t.i0 < t.i1)
         load_tile<D>(sk, &s.kfull[0], map_k, t, t.i0 + (t.i0 >= t.skip_at ? t.skip : 0));
       if (a.q_tma && t.rows > kTileRows) load_queries<D>(s, sq, map_q, a, t, 1);
+      if (a.o_tma) tma_prefetch_desc(&map_o);
     }
   }
   if (warp == kMmaWarp) {
@@ -838,7 +852,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       // this stream's columns, staged in shared memory in 16-byte chunks (Q is not read any more)
       const int cols = share ? D : D / 2, col0 = share ? 0 : h * (D / 2);
       const int chunks = cols / 8, flip = min(chunks - 1, 7);
-      uint8_t* stage = sq + h * C::kTile + (share ? 0 : h * 4096);
+      // a warp's rows: 64 columns (or fewer) of all of them, then the next 64; chunks swizzled as a tensor copy takes them
+      uint8_t* stage = sq + h * C::kTile + (share ? 0 : h * 4096) + quarter * (32 * chunks * 16);
+      const int pitch = min(chunks, 8) * 16;
       float* part_o = a.part_o + (prow * a.splits + t.split) * D + col0;
       const uint32_t mine = o_col + col0, other = tmem + lanes + kOCol + (h ^ 1) * 128 + col0;
       auto put = [&](int c, const float (&x)[32]) {
@@ -850,7 +866,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         } else {
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(stage + (r * chunks + ((c * 4 + e / 8) ^ (r & flip))) * 16) =
+            *reinterpret_cast<uint4*>(stage + (c >> 1) * 4096 + lane * pitch + ((((c & 1) * 4 + e / 8) ^ (lane & flip)) << 4)) =
                 make_uint4(pack_bf16x2(x[e], x[e + 1]), pack_bf16x2(x[e + 2], x[e + 3]),
                            pack_bf16x2(x[e + 4], x[e + 5]), pack_bf16x2(x[e + 6], x[e + 7]));
         }
@@ -892,17 +908,30 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         }
       }
       if (!part) {
-        // the warp's rows from shared memory, whole rows (or halves) per store
-        __syncwarp();
-        const int chunk = lane & (chunks - 1), per = 32 / chunks;     // rows per instruction
-        __nv_bfloat16* out = a.out + t.b * a.os.batch + t.l * a.os.layer + col0;
-#pragma unroll 8
-        for (int i = 0; i < chunks; ++i) {
-          const int rr = i * per + lane / chunks, rt = quarter * 32 + rr;
-          const int64_t at = __shfl_sync(0xffffffffu, own, rr);
-          if ((share ? h * kTileRows : 0) + rt < t.rows)
-            *(reinterpret_cast<uint4*>(out + at) + chunk) =
-                *reinterpret_cast<const uint4*>(stage + (rt * chunks + (chunk ^ (rt & flip))) * 16);
+        const int row0 = (share ? h * kTileRows : 0) + quarter * 32;
+        if (a.o_tma && cols >= 64 && row0 + 32 <= t.rows) {
+          // whole queries, all of them rows: one copy per 64 columns
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int q0 = static_cast<int>(a.by_group.div(t.row0 + row0));
+            for (int c = 0; c < cols / 64; ++c)
+              tma_store_5d(&map_o, smem_u32(stage + c * 4096), col0 + c * 64, t.g * a.G, q0, t.l, t.b);
+            tma_store_wait();
+          }
+        } else {
+          // from shared memory, whole rows (or halves) per store
+          __syncwarp();
+          const int chunk = lane & (chunks - 1), per = 32 / chunks;     // rows per instruction
+          __nv_bfloat16* out = a.out + t.b * a.os.batch + t.l * a.os.layer + col0;
+#pragma unroll 4
+          for (int i = 0; i < chunks; ++i) {
+            const int rr = i * per + lane / chunks;
+            const int64_t at = __shfl_sync(0xffffffffu, own, rr);
+            if (row0 + rr < t.rows)
+              *(reinterpret_cast<uint4*>(out + at) + chunk) =
+                  *reinterpret_cast<const uint4*>(stage + (chunk >> 3) * 4096 + rr * pitch + (((chunk & 7) ^ (rr & flip)) << 4));
+          }
         }
       }
     }
@@ -985,7 +1014,7 @@ __global__ void __launch_bounds__(256) doc_tiles_kernel(const PromptArgs a) {
 size_t prompt_smem_bytes(int d) { return d == 128 ? Cfg<128>::kSmem : Cfg<64>::kSmem; }
 
 cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v,
-                          cudaStream_t stream) {
+                          const CUtensorMap& map_o, cudaStream_t stream) {
   if (a.docs)
     doc_tiles_kernel<<<dim3((a.n_tiles + 7) / 8, std::min(a.B, 65535)), 256, 0, stream>>>(a);
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.n_blocks) * a.U * a.splits);
@@ -993,8 +1022,8 @@ cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const C
     const int bytes = static_cast<int>(prompt_smem_bytes(a.d));
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    if (a.docs) return launch_after(kernel, dim3(grid), kThreads, bytes, stream, map_q, map_k, map_v, a);
-    kernel<<<grid, kThreads, bytes, stream>>>(map_q, map_k, map_v, a);
+    if (a.docs) return launch_after(kernel, dim3(grid), kThreads, bytes, stream, map_q, map_k, map_v, map_o, a);
+    kernel<<<grid, kThreads, bytes, stream>>>(map_q, map_k, map_v, map_o, a);
     return cudaGetLastError();
   };
   const bool cap = a.mods.softcap > 0.f, bias = a.mods.slopes != nullptr;
