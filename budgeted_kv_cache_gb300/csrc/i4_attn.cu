@@ -151,8 +151,9 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
   constexpr int kStages = S::kStages;
   S& s = *reinterpret_cast<S*>(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  let_next_kernel_start();
   if (static_cast<int>(blockIdx.y + blockIdx.z * 65535) >= a.U) return;
+  wait_for_previous_kernel();
+  let_next_kernel_start();                         // not before: it reads the counts while this kernel runs
   const Unit un(a, blockIdx.y + blockIdx.z * 65535);
   // what does not depend on the rows in use is on its way before anything waits for them
   const int32_t next = a.rows.next_pos[un.u];
@@ -711,8 +712,7 @@ cudaError_t launch_one(const I4AttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int R = a.n_q * a.G;
   const dim3 grid((R + NT * 8 - 1) / (NT * 8) * a.splits, std::min(a.U, 65535), (a.U + 65534) / 65535);
-  kernel<<<grid, kThreads, bytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(kernel, grid, kThreads, bytes, stream, a);
 }
 
 template <int D, bool ROW>

@@ -125,6 +125,7 @@ __device__ __forceinline__ void advance(const I4AppendArgs& a, int u, const Room
 // by the next kernel, after every block has read them.
 template <int D, bool ROW, int THREADS>
 __global__ void __launch_bounds__(THREADS) i4_append_kernel(const I4AppendArgs a) {
+  wait_for_previous_kernel();
   constexpr int LPR = D / 8, RPB = THREADS / LPR, NS = ROW ? 1 : D / 32;
   const int u = blockIdx.y + blockIdx.z * 65535;
   if (u >= a.U) return;
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(THREADS) i4_append_kernel(const I4AppendArgs a
 }
 
 __global__ void i4_advance_kernel(const I4AppendArgs a) {
+  wait_for_previous_kernel();
   const int u = blockIdx.x * blockDim.x + threadIdx.x;
   if (u < a.U) advance(a, u, room_of(a, u));
 }
@@ -222,6 +224,7 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t w, uint16_t scale, bool ro
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) i4_read_kernel(const I4ReadArgs a) {
+  wait_for_previous_kernel();
   constexpr int LPR = D / 8, RPB = kRowThreads / LPR;
   const int u = blockIdx.y + blockIdx.z * 65535;
   if (u >= a.U) return;
@@ -391,6 +394,7 @@ __device__ __forceinline__ void store_part(const I4EvictArgs& a, int64_t row, co
 }
 
 __global__ void __launch_bounds__(kEvictThreads, 2) i4_evict_kernel(const I4EvictArgs a) {
+  wait_for_previous_kernel();
   __shared__ EvictSmem s;
   const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cap = a.rows.capacity;
@@ -581,9 +585,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) i4_evict_kernel(const I4Evic
 namespace {
 
 template <int D, bool ROW>
-void append(const I4AppendArgs& a, dim3 grid, bool wide, cudaStream_t stream) {
-  if (wide) i4_append_kernel<D, ROW, 512><<<grid, 512, 0, stream>>>(a);
-  else i4_append_kernel<D, ROW, 256><<<grid, 256, 0, stream>>>(a);
+cudaError_t append(const I4AppendArgs& a, dim3 grid, bool wide, cudaStream_t stream) {
+  return wide ? launch_after(i4_append_kernel<D, ROW, 512>, grid, 512, 0, stream, a)
+              : launch_after(i4_append_kernel<D, ROW, 256>, grid, 256, 0, stream, a);
 }
 
 }  // namespace
@@ -592,14 +596,16 @@ cudaError_t launch_i4_append(const I4AppendArgs& a0, cudaStream_t stream) {
   I4AppendArgs a = a0;
   // up to 256 rows of a unit in one block, which advances the counters itself
   // (one launch), 512 threads from 64 rows on; longer ones in blocks of 128
-  // rows and a second launch
+  // rows and a second launch.  Measured (288 units, with the read): 200 rows
+  // 17.4 us, 19.0 with 256 threads, 20.1 in blocks of 128; one row 5.8 us, 6.9
+  // with 512 threads.
   a.rows_per_block = a.n <= 256 ? 256 : 128;
   const bool wide = a.n > 64 && a.n <= 256, row = a.rows.quant_mode == KVC_QUANT_ROW_FP16;
   const dim3 grid((a.n + a.rows_per_block - 1) / a.rows_per_block, std::min(a.U, 65535), (a.U + 65534) / 65535);
-  if (a.d == 128) row ? append<128, true>(a, grid, wide, stream) : append<128, false>(a, grid, wide, stream);
-  else row ? append<64, true>(a, grid, wide, stream) : append<64, false>(a, grid, wide, stream);
-  if (grid.x > 1) i4_advance_kernel<<<(a.U + 255) / 256, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  const cudaError_t e = a.d == 128 ? (row ? append<128, true>(a, grid, wide, stream) : append<128, false>(a, grid, wide, stream))
+                                   : (row ? append<64, true>(a, grid, wide, stream) : append<64, false>(a, grid, wide, stream));
+  if (e != cudaSuccess || grid.x == 1) return e;
+  return launch_after(i4_advance_kernel, dim3((a.U + 255) / 256), 256, 0, stream, a);
 }
 
 cudaError_t launch_i4_read(const I4ReadArgs& a0, cudaStream_t stream) {
@@ -607,14 +613,11 @@ cudaError_t launch_i4_read(const I4ReadArgs& a0, cudaStream_t stream) {
   // one batch of rows per thread: blocks of 64 rows (128 at d = 64)
   a.rows_per_block = kRowThreads / (a.d / 8) * kBatch;
   const dim3 grid((a.n + a.rows_per_block - 1) / a.rows_per_block, std::min(a.U, 65535), (a.U + 65534) / 65535);
-  if (a.d == 128) i4_read_kernel<128><<<grid, kRowThreads, 0, stream>>>(a);
-  else i4_read_kernel<64><<<grid, kRowThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(a.d == 128 ? i4_read_kernel<128> : i4_read_kernel<64>, grid, kRowThreads, 0, stream, a);
 }
 
 cudaError_t launch_i4_evict(const I4EvictArgs& a, cudaStream_t stream) {
-  i4_evict_kernel<<<a.U, kEvictThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(i4_evict_kernel, dim3(a.U), kEvictThreads, 0, stream, a);
 }
 
 }  // namespace kvc

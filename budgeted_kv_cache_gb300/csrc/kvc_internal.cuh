@@ -351,8 +351,9 @@ cudaError_t launch_protect(const ProtectArgs& a, cudaStream_t stream);
 cudaError_t launch_flags(const FlagArgs& a, cudaStream_t stream);
 
 // Launches a kernel that may begin while the one before it in the stream still
-// runs (it has to call wait_for_previous_kernel before it touches anything of
-// that one's): the launch costs no gap.
+// runs: the launch costs no gap.  It has to call wait_for_previous_kernel
+// before it touches any memory that a kernel before it may use, for reading or
+// for writing; that one may be anybody's.
 template <typename K, typename... A>
 cudaError_t launch_after(K kernel, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchAttribute attr = {};
@@ -373,7 +374,9 @@ cudaError_t launch_after(K kernel, dim3 grid, unsigned threads, size_t smem, cud
 // ----------------------------------------------------------------------------
 
 // The next kernel, launched with launch_after, may begin once every block has
-// called this; and it waits here until this one's results are there.
+// called this, and it waits here until this one's results are there.  A kernel
+// calls it behind its own wait, so whatever begins early finds the results of
+// everything before this kernel.
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

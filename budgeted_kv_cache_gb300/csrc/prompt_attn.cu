@@ -343,7 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
               const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o, const PromptArgs a) {
   using C = Cfg<D>;
-  let_next_kernel_start();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sq = base;                                  // two Q tiles
@@ -376,6 +375,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     s.q_min = INT32_MAX;
     s.q_max = -1;
     fence_barrier_init();
+    wait_for_previous_kernel();
     const Item t = make_item(a, blockIdx.x);
     s.item = t;
     if (t.rows > 0) {
@@ -390,7 +390,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     tmem_alloc(smem_u32(&s.tmem), kTmemCols);
     tmem_relinquish();
   }
-  if (a.docs) wait_for_previous_kernel();                // the documents of the key tiles
+  wait_for_previous_kernel();                            // its results, or the documents of the key tiles
+  let_next_kernel_start();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -991,6 +992,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
 
 // Smallest and largest document of each key tile: one warp per tile.
 __global__ void __launch_bounds__(256) doc_tiles_kernel(const PromptArgs a) {
+  wait_for_previous_kernel();
   let_next_kernel_start();
   const int tile = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (tile >= a.n_tiles) return;
@@ -1015,16 +1017,16 @@ size_t prompt_smem_bytes(int d) { return d == 128 ? Cfg<128>::kSmem : Cfg<64>::k
 
 cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v,
                           const CUtensorMap& map_o, cudaStream_t stream) {
-  if (a.docs)
-    doc_tiles_kernel<<<dim3((a.n_tiles + 7) / 8, std::min(a.B, 65535)), 256, 0, stream>>>(a);
+  if (a.docs) {
+    const cudaError_t e = launch_after(doc_tiles_kernel, dim3((a.n_tiles + 7) / 8, std::min(a.B, 65535)), 256, 0, stream, a);
+    if (e != cudaSuccess) return e;
+  }
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.n_blocks) * a.U * a.splits);
   auto go = [&](auto kernel) -> cudaError_t {
     const int bytes = static_cast<int>(prompt_smem_bytes(a.d));
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    if (a.docs) return launch_after(kernel, dim3(grid), kThreads, bytes, stream, map_q, map_k, map_v, map_o, a);
-    kernel<<<grid, kThreads, bytes, stream>>>(map_q, map_k, map_v, map_o, a);
-    return cudaGetLastError();
+    return launch_after(kernel, dim3(grid), kThreads, bytes, stream, map_q, map_k, map_v, map_o, a);
   };
   const bool cap = a.mods.softcap > 0.f, bias = a.mods.slopes != nullptr;
   cudaError_t e;

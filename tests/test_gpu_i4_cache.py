@@ -546,3 +546,47 @@ def test_prompt_then_tokens(kvc, graph):
             assert len(set(p.tolist())) == budget
             assert set(range(4)) <= set(p.tolist())
             assert set(range(int(rows.next_pos[u]) - 32, int(rows.next_pos[u]))) <= set(p.tolist())
+
+
+def test_calls_that_feed_each_other_without_a_pause(kvc):
+    """Each call's outputs are the next one's inputs, and torch overwrites them right behind: the bits of the same calls
+    with the device idle between them."""
+    T, H, d = 200, 2, 128
+    shape, g = kvc.make_shape(2, 1, H, H, d, T), gen(11)
+    q0, k0, v0 = randn(g, 2, 1, H, T, d), randn(g, 2, 1, H, T, d), randn(g, 2, 1, H, T, d)
+    space = lambda n: torch.empty(max(1, n), dtype=torch.uint8, device="cuda")
+    ws = space(kvc.kvc_prompt_attn_workspace_bytes(shape, T, True))
+    docs = i32([[0] * 90 + [1] * 110] * 2)
+    rows = kvc.I4Rows.allocate(shape, 2 * T)
+    for t in fields(rows)[:6]:
+        t.zero_()
+    ws4, wse = space(kvc.kvc_i4_attn_workspace_bytes(shape, rows, T, True)), space(kvc.kvc_i4_evict_workspace_bytes(shape, rows, 150))
+
+    def run(pause):
+        torch.cuda.synchronize()
+        rows.count.zero_(), rows.next_pos.zero_()
+        a, b, c = torch.empty_like(q0), torch.empty_like(q0), torch.empty_like(q0)
+        k_out, v_out = torch.zeros_like(k0), torch.zeros_like(v0)
+        steps = [lambda: kvc.kvc_prompt_attn(shape, q0, k0, v0, a, workspace=ws),
+                 lambda: kvc.kvc_prompt_attn(shape, a, k0, v0, b, docs=docs, workspace=ws),
+                 lambda: a.zero_(),
+                 lambda: kvc.kvc_prompt_attn(shape, b, b, v0, a, workspace=ws),
+                 lambda: kvc.kvc_i4_append(shape, rows, a, b),
+                 lambda: b.fill_(7.0),
+                 lambda: kvc.kvc_i4_attn(shape, rows, a, c, add_mass=True, workspace=ws4),
+                 lambda: kvc.kvc_i4_evict(shape, rows, 150, 4, 16, workspace=wse),
+                 lambda: kvc.kvc_i4_append(shape, rows, c, a, n_new=i32([30, 50])),
+                 lambda: kvc.kvc_i4_attn(shape, rows, c, a, workspace=ws4),
+                 lambda: kvc.kvc_i4_read(shape, rows, k_out, v_out),
+                 lambda: kvc.kvc_prompt_attn(shape, a, k_out, v_out, b, workspace=ws)]
+        for s in steps:
+            s()
+            if pause:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [t.clone() for t in (a, b, c, k_out, v_out, rows.mass[:, :180], rows.pos[:, :180], rows.count)]
+
+    want = run(True)
+    assert all(bool(torch.isfinite(t.float()).all()) for t in want)
+    for _ in range(20):
+        assert all(torch.equal(x, y) for x, y in zip(run(False), want))
