@@ -178,10 +178,11 @@ def _p(t) -> Optional[int]:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, dev: Optional[int] = None) -> Optional[int]:
+    """A stream's handle; None: the current one (of the current device, `dev` where the caller knows it)."""
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -654,7 +655,7 @@ def kvc_prompt_attn(shape, q, k, v, out, q_len=None, kv_len=None, docs=None, mod
         _dense(f, dev, q_len, i32, B), _dense(f, dev, kv_len, i32, B), _dense(f, dev, docs, i32, B * T),
         _mods(f, dev, mods, shape), softmax_scale, out.data_ptr(), _rows(f, dev, out, shape, Hq, n_q),
         _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n_q),
-        _dense(f, dev, unit_status, i32, _units(shape)), ws, ws_bytes, _stream(stream))
+        _dense(f, dev, unit_status, i32, _units(shape)), ws, ws_bytes, _stream(stream, dev))
     if code:
         raise KvcError(f, code)
 
@@ -666,7 +667,7 @@ def kvc_i4_append(shape, rows: I4Rows, k, v, n_new=None, unit_status=None, strea
     code = _load().kvc_i4_append(
         ctypes.byref(shape), _cache(f, dev, rows, shape), k.data_ptr(), v.data_ptr(), _pair(f, dev, k, v, shape),
         k.shape[3], _dense(f, dev, n_new, torch.int32, shape.batch),
-        _dense(f, dev, unit_status, torch.int32, _units(shape)), _stream(stream))
+        _dense(f, dev, unit_status, torch.int32, _units(shape)), _stream(stream, dev))
     if code:
         raise KvcError(f, code)
 
@@ -677,7 +678,7 @@ def kvc_i4_read(shape, rows: I4Rows, k_out, v_out, stream=None):
     dev = _device(f)
     strides = _pair(f, dev, k_out, v_out, shape)
     code = _load().kvc_i4_read(ctypes.byref(shape), _cache(f, dev, rows, shape), k_out.shape[3], k_out.data_ptr(),
-                               v_out.data_ptr(), strides, _stream(stream))
+                               v_out.data_ptr(), strides, _stream(stream, dev))
     if code:
         raise KvcError(f, code)
 
@@ -701,7 +702,7 @@ def kvc_i4_attn(shape, rows: I4Rows, q, out, q_pos=None, mods: Optional[ScoreMod
         ctypes.byref(shape), _cache(f, dev, rows, shape), q.data_ptr(), q_strides, n_q,
         _dense(f, dev, q_pos, torch.int32, B * n_q), _mods(f, dev, mods, shape), softmax_scale,
         ATTN_ADD_MASS if add_mass else 0, out.data_ptr(), _rows(f, dev, out, shape, Hq, n_q),
-        _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n_q), ws, ws_bytes, _stream(stream))
+        _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n_q), ws, ws_bytes, _stream(stream, dev))
     if code:
         raise KvcError(f, code)
 
@@ -718,6 +719,6 @@ def kvc_i4_evict(shape, rows: I4Rows, budget: int, n_sink: int, n_recent: int, u
     dev = _device(f)
     ws, ws_bytes = _space(f, dev, workspace)
     code = _load().kvc_i4_evict(ctypes.byref(shape), _cache(f, dev, rows, shape), budget, n_sink, n_recent,
-                                _dense(f, dev, unit_status, torch.int32, _units(shape)), ws, ws_bytes, _stream(stream))
+                                _dense(f, dev, unit_status, torch.int32, _units(shape)), ws, ws_bytes, _stream(stream, dev))
     if code:
         raise KvcError(f, code)
