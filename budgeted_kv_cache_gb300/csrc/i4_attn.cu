@@ -584,6 +584,10 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
 // Second kernel: blocks [0, a.merge_blocks) of a unit join the splits of its
 // rows, the others add the weights of their keys to the mass.
 constexpr int kFinThreads = 256;
+// Query rows up to which a thread adds a key's weights alone.  Measured: 4 rows of 32 units of 100K to 131K keys 142 us
+// alone, 172 by groups of lanes; 128 rows of 8 units of 8,192 keys 176 us alone (each lane's logits lie 512 bytes from
+// the next one's), 63 by groups.
+constexpr int kFewRows = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kFinThreads, 4) i4_finish_kernel(const I4AttnArgs a) {
@@ -644,8 +648,10 @@ __global__ void __launch_bounds__(kFinThreads, 4) i4_finish_kernel(const I4AttnA
     if (lane == 0 && a.lse) a.lse[un.lse_at(a, r)] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
     return;
   }
-  // Mass: four keys of a thread at once, two query rows per load; loads of keys past the rows in use stay inside the
-  // unit's logits (their values are not used).
+  // Mass.  Few query rows: four keys of a thread at once, two query rows per load.  More: a group of lanes per key, each
+  // with two query rows, so that a warp reads keys that follow each other as one piece.  Loads of keys past the rows in
+  // use stay inside the unit's logits (their values are not used).
+  const bool few = un.R <= kFewRows;
   const int j0 = (blockIdx.x - a.merge_blocks) * a.mass_keys, cap = a.rows.capacity;
   auto key_at = [&](int j, int k) { return un.base + min(j + k * kFinThreads, cap - 1); };
   float old[4];
@@ -660,26 +666,69 @@ __global__ void __launch_bounds__(kFinThreads, 4) i4_finish_kernel(const I4AttnA
     load(j, 0, y[0]);
     load(j, min(2, a.logit_stride - 2), y[1]);
   };
-  load_first(j0 + threadIdx.x);
-  for (int r = warp; r < un.R; r += kFinThreads / 32) {
-    // splits <= kMaxSplits: four per lane, read once
-    const float2* ml = a.part_ml + (static_cast<int64_t>(un.u) * un.R + r) * a.splits;
-    float2 v[kMaxSplits / 32];
-    float top = -INFINITY, sum = 0.f;
+  if (few) load_first(j0 + threadIdx.x);
+  // base-2 log-sum-exps; splits <= kMaxSplits: four per lane, read once, of `rows` rows together
+  auto statistics = [&](int r, auto rows_c) {
+    constexpr int rows = decltype(rows_c)::value, stride = kFinThreads / 32;
+    float2 v[rows][kMaxSplits / 32];
 #pragma unroll
-    for (int k = 0; k < kMaxSplits / 32; ++k) {
-      v[k] = k * 32 + lane < a.splits ? ml[k * 32 + lane] : make_float2(-INFINITY, 0.f);
-      top = fmaxf(top, v[k].x);
+    for (int i = 0; i < rows; ++i) {
+      const float2* ml = a.part_ml + (static_cast<int64_t>(un.u) * un.R + min(r + i * stride, un.R - 1)) * a.splits;
+#pragma unroll
+      for (int k = 0; k < kMaxSplits / 32; ++k)
+        v[i][k] = k * 32 + lane < a.splits ? ml[k * 32 + lane] : make_float2(-INFINITY, 0.f);
     }
-    for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
 #pragma unroll
-    for (int k = 0; k < kMaxSplits / 32; ++k)
-      if (v[k].x != -INFINITY) sum = fmaf(v[k].y, ex2_approx(v[k].x - top), sum);
-    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(kFull, sum, k);
-    if (lane == 0) lse2[r] = sum > 0.f ? top + log2f(sum) : 0.f;      // nothing seen: every logit is -inf
+    for (int i = 0; i < rows; ++i) {
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMaxSplits / 32; ++k) top = fmaxf(top, v[i][k].x);
+      for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
+#pragma unroll
+      for (int k = 0; k < kMaxSplits / 32; ++k)
+        if (v[i][k].x != -INFINITY) sum = fmaf(v[i][k].y, ex2_approx(v[i][k].x - top), sum);
+      for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(kFull, sum, k);
+      // nothing seen: every logit is -inf
+      if (lane == 0 && r + i * stride < un.R) lse2[r + i * stride] = sum > 0.f ? top + log2f(sum) : 0.f;
+    }
+  };
+  if (few) {
+    if (warp < un.R) statistics(warp, std::integral_constant<int, 1>{});
+  } else {
+#pragma unroll 1
+    for (int r = warp; r < un.R; r += kFinThreads / 32 * 4) statistics(r, std::integral_constant<int, 4>{});
   }
   const int j1 = min(un.n, j0 + a.mass_keys);
   __syncthreads();
+  if (!few) {
+    const int pairs = a.logit_stride / 2;
+    int group = 4;                                 // lanes of a key
+    while (group < pairs && group < 32) group *= 2;
+    const int keys = 32 / group, own = lane & (group - 1), step = kFinThreads / 32 * keys;
+    for (int jb = j0 + warp * keys; jb < j1; jb += 4 * step) {
+      const int j = jb + lane / group;
+      float was[4], sum[4] = {};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) was[k] = own == 0 ? a.rows.mass[un.base + min(j + k * step, cap - 1)] : 0.f;
+      for (int q = own; q < pairs; q += group) {
+        float2 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = *reinterpret_cast<const float2*>(a.logits + (un.base + min(j + k * step, cap - 1)) * a.logit_stride + 2 * q);
+        const bool two = 2 * q + 1 < un.R;         // a padding column adds nothing
+        const float l0 = lse2[2 * q], l1 = two ? lse2[2 * q + 1] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[k] += ex2_approx(v[k].x - l0) + (two ? ex2_approx(v[k].y - l1) : 0.f);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        for (int o = 1; o < group; o <<= 1) sum[k] += __shfl_xor_sync(kFull, sum[k], o);
+        if (own == 0 && j + k * step < j1) a.rows.mass[un.base + j + k * step] = was[k] + sum[k];
+      }
+    }
+    return;
+  }
   for (int j = j0 + threadIdx.x; j < j1; j += kFinThreads * 4) {
     if (j >= j0 + kFinThreads) load_first(j);
     float sum[4] = {};
