@@ -9,8 +9,8 @@
 //     own running maximum and sum, no barrier in the loop; the warps of a
 //     block and the blocks of a unit are joined at the end (PASK Eq. 15).
 //   * Plain causal scores have a kernel of their own; caps, slopes, windows
-//     and prefixes share the other.  With a window, tiles that no query row
-//     sees end after their masks (their copies are already under way).
+//     and prefixes share the other.  With a window, the codes of tiles that
+//     no query row sees are not read.
 //   * Both products put the codes in the 16-row operand and the packed query
 //     rows (row r = query r / G, head r % G of the unit) in the 8-column one:
 //     S^T = K Q^T and O^T = V^T P^T, so eight query rows cost one instruction.
@@ -175,8 +175,13 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
     }
   }
 
+  // this block's tiles: t0, t0 + 1, .. below t1, one warp after another; with a window every split takes each splits-th
+  // four, so that all of them have a part of what is seen
+  const bool windowed = MODS && a.mods.window;
   int t0, t1;
   split_range(a, un.n, split, &t0, &t1);
+  if (windowed) t0 = split * kWarps, t1 = (un.n + kTile - 1) / kTile;
+  const int stride = windowed ? kWarps * a.splits : kWarps;
 
   // one warp's copies of tile i: this lane's 16-byte chunk of every 32 / CH rows; rows past n filled with zeros
   auto swz = [](int row, int chunk) { return D == 128 ? chunk ^ ((row >> 1) & 3) : chunk ^ ((row >> 2) & 1); };
@@ -186,8 +191,8 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
   const int64_t c_src = (un.base + c_row) * (D / 2) + c_chunk * 16;
   const uint8_t* const c_k = static_cast<const uint8_t*>(a.rows.k) + c_src;
   const uint8_t* const c_v = static_cast<const uint8_t*>(a.rows.v) + c_src;
-  auto copy_tile = [&](int i, int st) {
-    if (i < t1) {
+  auto copy_tile = [&](int i, int st, bool wanted) {
+    if (i < t1 && wanted) {
       const int64_t at = static_cast<int64_t>(i) * (kTile * D / 2);
       const uint32_t dst = c_dst + st * (2 * kTile * D / 2);
       const int left = un.n - i * kTile - c_row;   // rows from this lane's first on
@@ -234,12 +239,14 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
       q_lo[nt][e] = MODS && a.mods.window ? static_cast<int>(max(p - a.mods.window + 1, static_cast<int64_t>(INT32_MIN))) : INT32_MIN;
       slope[nt][e] = MODS && a.mods.slopes ? a.mods.slopes[un.g * a.G + r % a.G] * kLog2e : 0.f;
     }
+  if (!MODS) {
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) copy_tile(t0 + warp + i * kWarps, i);
-  fetch(t0 + warp);
+    for (int i = 0; i < kStages - 1; ++i) copy_tile(t0 + warp + i * stride, i, true);
+    fetch(t0 + warp);
+  }
 
   const bool capped = MODS && a.mods.softcap > 0.f, biased = MODS && a.mods.slopes;
-  const bool modified = capped || biased, windowed = MODS && a.mods.window;
+  const bool modified = capped || biased;
   const float pre = capped ? a.scale : a.scale * kLog2e;      // goes into the key scales
   const float inv_cap = capped ? 1.f / a.mods.softcap : 0.f;
   // limits over the block's query rows
@@ -257,6 +264,25 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
   hi_max = __reduce_max_sync(kFull, hi_max);
   lo_min = __reduce_min_sync(kFull, lo_min);
   lo_max = __reduce_max_sync(kFull, lo_max);
+  // With a window the positions of a tile are looked at before its copies are sent for: what no query row sees is not read.
+  auto position = [&](int i) {
+    const int j = i * kTile + lane;
+    return i < t1 && j < un.n ? __ldg(a.rows.pos + un.base + j) : 0;
+  };
+  auto seen_by_any = [&](int i, int32_t p) {
+    return __any_sync(kFull, i < t1 && i * kTile + lane < un.n && ((p <= hi_max && p >= lo_min) || p < prefix)) != 0;
+  };
+  int32_t pos_far = 0;                             // of the tile that is copied next
+  if (MODS) {
+    int32_t p[kStages - 1];
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) p[i] = windowed ? position(t0 + warp + i * stride) : 0;
+    if (windowed) pos_far = position(t0 + warp + (kStages - 1) * stride);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+      copy_tile(t0 + warp + i * stride, i, !windowed || seen_by_any(t0 + warp + i * stride, p[i]));
+    fetch(t0 + warp);
+  }
   float* const log_row = a.logits + (un.base + g) * a.logit_stride + r0 + 2 * t;      // [key][R rounded up to even]
   const uint32_t half_sel = (g >> 2) ? 0x7632u : 0x5410u;
   float m[NT][2], l[NT][2], o[NG][2][NT][4];
@@ -272,8 +298,10 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
 
   int st = 0;
 #pragma unroll 1
-  for (int i = t0 + warp; i < t1; i += kWarps) {
-    copy_tile(i + (kStages - 1) * kWarps, (st + kStages - 1) % kStages);
+  for (int i = t0 + warp; i < t1; i += stride) {
+    const int far = i + (kStages - 1) * stride;
+    copy_tile(far, (st + kStages - 1) % kStages, !windowed || seen_by_any(far, pos_far));
+    if (windowed) pos_far = position(far + stride);
     // scales and positions of this tile: one lane per key, then to all
     put_scales(&s.scale[warp][0][lane][0], ks_next, pre);
     put_scales(&s.scale[warp][1][lane][0], vs_next, 1.f);
@@ -281,10 +309,8 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
     // does every query row see every key of the tile?
     const bool mine = i * kTile + lane < un.n;
     const bool clear = __all_sync(kFull, mine && pos_next <= hi_min && (!MODS || pos_next >= lo_max));
-    // does none see any?  Known without the codes, but they are on their way
-    const bool none = !clear && windowed &&
-                      !__any_sync(kFull, mine && ((pos_next <= hi_max && pos_next >= lo_min) || pos_next < prefix));
-    fetch(i + kWarps);
+    const bool none = !clear && windowed && !seen_by_any(i, pos_next);
+    fetch(i + stride);
     cp_async_wait<kStages - 1>();
     __syncwarp();
     if (none) {
