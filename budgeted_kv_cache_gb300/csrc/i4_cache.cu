@@ -10,7 +10,7 @@
 // flight together.  Measured (d = 128, g32 scales, 96 units of up to 30,011
 // rows): append 234 us and read 200 us, 438 us together = 6.0 TB/s, 89 % of the
 // measured bandwidth, the quantiser's instructions (59 % of the ALU cycles)
-// under the copies; one token's rows of 288 units appended and read back 5.9 us.
+// under the copies; one token's rows of 288 units appended and read back 5.4 us.
 #include <algorithm>
 
 #include "kvc_internal.cuh"

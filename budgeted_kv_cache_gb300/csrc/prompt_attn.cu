@@ -30,6 +30,10 @@
 // every row of a warp sees whole takes no mask.  Values of keys that no row of
 // the item sees are zeroed in shared memory (0 x NaN is NaN in a product).
 //
+// Outputs are staged in shared memory; a warp whose 32 rows are whole queries
+// sends them by tensor copies (documents 84.8 us, 86.6 by its own stores),
+// others store whole rows.
+//
 // Warp roles (12 warps): 0-3 and 4-7 softmax of stream 0 and 1 (a row of 128
 // scores per thread in registers: their warpgroups take 200 registers a
 // thread, the third gives them up and keeps 104; 2 x 200 + 104 = 3 x 168, what
@@ -43,10 +47,13 @@
 // cycles and its softmax 640 warp instructions a warp, 1,150 with a cap, which
 // two warps per scheduler cannot hide behind each other's latencies: about
 // 1,400 and 2,300 cycles a step.  Measured, replayed from a graph (32 query
-// heads over 8, d = 128): 8,192 causal tokens 358 us = 1,540 TFLOP/s, 82 % of
-// the measured bf16 peak, tensor pipe 67 % active; the same work capped runs at
-// 960 TFLOP/s.  One token over 16 sequences of up to 32,768: 182 us = 6.4 TB/s,
-// 95 % of the measured bandwidth; 206 us capped.  300 tokens: 9.8 us.
+// heads over 8, d = 128): 8,192 causal tokens 350 us = 1,570 TFLOP/s, 84 % of
+// the measured bf16 peak, tensor pipe 67 % active; capped 535 us = 1,030
+// TFLOP/s.  One token over 16 sequences of up to 32,768: 181 us = 6.5 TB/s, 96 %
+// of the measured bandwidth; 207 us capped.  300 tokens: 9.1 us.  Beside its
+// steps an item costs about 11,000 cycles: 1,400 to set up, 2,300 until the
+// first scores are there, 2,200 to read and stage its outputs, 1,200 until the
+// next block of the SM begins.
 // Tried and slower: one persistent CTA per SM with its outputs under the next
 // item's loads (407 us against 389: a value stage less, spills), scores read
 // from tensor memory in parts (422 against 365: spills).
