@@ -827,7 +827,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     };
     float m2 = m == -INFINITY ? -INFINITY : m * cs;
     if (share && valid) write_stats(m2, l);      // while the last product of this stream runs
-    if (!fail && n > 0 && !warp_wait(smem_u32(&s.odone[h]), (n - 1) & 1, abort_flag)) fail = true;
+    // Without a tile there is no product to wait for, but the queries are on their way all the same, into the shared
+    // memory that stages the outputs.
+    if (!fail && !warp_wait(smem_u32(n > 0 ? &s.odone[h] : &s.qfull[share ? h : 0]), n > 0 ? (n - 1) & 1 : 0, abort_flag))
+      fail = true;
     tc_fence_after();
     // One row tile: both streams hold an output for the same rows, in the same lanes of tensor memory.  They exchange
     // (m, l) through the unused second Q tile, and each joins and writes one half of the columns.

@@ -294,3 +294,21 @@ def test_workspace_too_small_is_refused(kvc):
     with pytest.raises(kvc.KvcError) as e:
         c.run()
     assert e.value.code == 3
+
+
+@pytest.mark.parametrize("empty", ["no_keys", "padding"])
+@pytest.mark.parametrize("G, n_q", [(4, 32), (4, 150), (3, 42), (3, 150)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_blocks_of_queries_that_walk_no_key(kvc, d, G, n_q, empty):
+    """Every query of many blocks (one or two row tiles, queries by tensor copies or by plain loads) sees nothing: the
+    outputs, staged where the queries land, are zeros whenever the queries land."""
+    B, T = 100, 300
+    c = Case(kvc, B=B, Hkv=2, G=G, d=d, n_q=n_q, T=T, q_norm=500.0, **(
+        dict(kv_len=[0] * B) if empty == "no_keys" else dict(docs=[0] * (T - n_q) + [-1] * n_q)))
+    for _ in range(20):
+        c.out.fill_(7.0)
+        c.lse.fill_(7.0)
+        c.run()
+        torch.cuda.synchronize()
+        assert int(c.status.abs().max()) == 0
+        assert int((c.out != 0).sum()) == 0 and bool((c.lse == -math.inf).all())
