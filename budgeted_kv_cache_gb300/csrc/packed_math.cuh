@@ -55,6 +55,18 @@ __device__ __forceinline__ float tanh_over_z(float z) {
   return r;
 }
 
+// Base-2 cap tanh(x / cap) of one score x, z = x / cap: the polynomial where z
+// is small, else cap (1 - 2 / (1 + e^2z)), which is off by about 2^-21 cap.
+// That is coarse beside scores far below a cap of more than kFineCap, so tiles
+// under such caps choose score by score and not as a whole.
+constexpr float kFineCap = 1024.f;
+
+__device__ __forceinline__ float capped_base2(float x, float z, float cap) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float far = fmaf(-2.f * cap, rcp_approx(1.f + ex2_approx(z * (2.f * kLog2e))), cap);
+  return (fabsf(z) <= kTanhRange ? x * tanh_over_z(z) : far) * kLog2e;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);

@@ -24,7 +24,11 @@
 //
 // A capped score is s times a polynomial in s^2 while |s scale / cap| stays
 // within 0.625 over a warp's tile (else cap (1 - 2 / (1 + e^2z))); slopes add
-// two packed operations an element pair.
+// two packed operations an element pair.  Where the polynomial's coefficients
+// for s leave fp32's range (caps far above or below the scale), and where caps
+// above 1,024 would make the second form coarse, another instance of the kernel
+// works in z = s scale / cap and chooses the form score by score (as a branch
+// of the first one it cost every capped call 2 to 6 %: spills).
 //
 // Masks.  An item walks only key tiles that some of its rows see; a tile that
 // every row of a warp sees whole takes no mask.  Values of keys that no row of
@@ -58,6 +62,8 @@
 // item's loads (407 us against 389: a value stage less, spills), scores read
 // from tensor memory in parts (422 against 365: spills).
 #include <algorithm>
+#include <cmath>
+#include <type_traits>
 
 #include "kvc_internal.cuh"
 #include "packed_math.cuh"
@@ -344,8 +350,9 @@ __device__ __forceinline__ uint64_t odd_factor(uint64_t x, const float (&c)[5]) 
               pair(c[0], c[0]));
 }
 
-// D: head dimension.  CAP, BIAS: the logits are capped, or get slopes.
-template <int D, bool CAP, bool BIAS>
+// D: head dimension.  CAP: the logits are capped; WIDE: by a cap that the
+// polynomial in s does not serve (cap_is_wide).  BIAS: they get slopes.
+template <int D, bool CAP, bool BIAS, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
               const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o, const PromptArgs a) {
@@ -619,10 +626,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const int all_pre = __reduce_min_sync(0xffffffffu, valid ? row_pre : INT32_MAX);
     const float cs = CAP ? 1.f : a.scale * kLog2e;
     const float cap = a.mods.softcap;
-    const float zs = CAP ? a.scale / cap : 0.f;
+    const float zs = !CAP ? 0.f : WIDE ? fminf(fmaxf(a.scale / cap, 0x1p-126f), 1e30f) : a.scale / cap;
     float tc[5];                               // the polynomial's coefficients for s
     if constexpr (CAP) {
-      float f = zs * cap * kLog2e;
+      float f = a.scale * kLog2e;
 #pragma unroll
       for (int k = 0; k < 5; ++k, f *= zs * zs) tc[k] = kTanh[k] * f;
     }
@@ -662,13 +669,30 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       // grows with s, so without slopes the maximum is that of s, and the polynomial is evaluated between the
       // exponentials (it fills the fp32 pipe while they wait for theirs).
       bool late = false;
-      if constexpr (CAP) {
+      if constexpr (CAP && WIDE) {
         float big = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) big = fmaxf(big, fmaxf(fabsf(y[c][e]), fabsf(y[c][e + 1])));
-        if (__all_sync(0xffffffffu, (big * zs <= kTanhRange && big < 1e18f) || !valid)) {
+        if (__all_sync(0xffffffffu, big * zs <= kTanhRange || !valid)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[c][e] *= tanh_over_z(y[c][e] * zs) * (a.scale * kLog2e);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[c][e] = capped_base2(y[c][e] * a.scale, y[c][e] * zs, cap);
+        }
+      } else if constexpr (CAP) {
+        float big = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) big = fmaxf(big, fmaxf(fabsf(y[c][e]), fabsf(y[c][e + 1])));
+        if (__all_sync(0xffffffffu, big * zs <= kTanhRange || !valid)) {
           if constexpr (BIAS) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -751,7 +775,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         for (int e = 2; e < 32; e += 2) mx[c] = fmaxf(mx[c], fmaxf(y[c][e], y[c][e + 1]));
       }
       float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (late) {                              // -inf stays: the leading coefficient is positive
+      if (late) {                              // -inf stays: the leading coefficient is positive, see cap_is_wide
         const float w = top * top;
         top *= fmaf(fmaf(fmaf(fmaf(tc[4], w, tc[3]), w, tc[2]), w, tc[1]), w, tc[0]);
       }
@@ -804,7 +828,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           }
         }
       };
-      if (CAP && !BIAS && late) weights([&](uint64_t x) { return fma2(x, odd_factor(x, tc), sub2); });
+      if (CAP && !WIDE && !BIAS && late) weights([&](uint64_t x) { return fma2(x, odd_factor(x, tc), sub2); });
       else weights([&](uint64_t x) { return fma2(x, cs2, sub2); });
       float s0, s1;
       unpair(add2(sum[0], sum[1]), &s0, &s1);
@@ -1021,6 +1045,13 @@ __global__ void __launch_bounds__(256) doc_tiles_kernel(const PromptArgs a) {
   }
 }
 
+// Caps beyond kFineCap, and those whose last coefficient kTanh[4] scale log2(e)
+// (scale / cap)^8 is no normal number: masked scores of -inf rely on its sign.
+bool cap_is_wide(const PromptArgs& a) {
+  const double z = static_cast<double>(a.scale) / a.mods.softcap, last = 0.015 * 1.44 * a.scale * std::pow(z, 8);
+  return a.mods.softcap > kFineCap || last < 0x1p-124 || last > 0x1p118;
+}
+
 }  // namespace
 
 size_t prompt_smem_bytes(int d) { return d == 128 ? Cfg<128>::kSmem : Cfg<64>::kSmem; }
@@ -1038,14 +1069,14 @@ cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const C
     if (e != cudaSuccess) return e;
     return launch_after(kernel, dim3(grid), kThreads, bytes, stream, map_q, map_k, map_v, map_o, a);
   };
-  const bool cap = a.mods.softcap > 0.f, bias = a.mods.slopes != nullptr;
-  cudaError_t e;
-  if (a.d == 128)
-    e = cap ? (bias ? go(prompt_kernel<128, true, true>) : go(prompt_kernel<128, true, false>))
-            : (bias ? go(prompt_kernel<128, false, true>) : go(prompt_kernel<128, false, false>));
-  else
-    e = cap ? (bias ? go(prompt_kernel<64, true, true>) : go(prompt_kernel<64, true, false>))
-            : (bias ? go(prompt_kernel<64, false, true>) : go(prompt_kernel<64, false, false>));
+  const bool bias = a.mods.slopes != nullptr;
+  auto go_capped = [&](auto d) -> cudaError_t {
+    constexpr int D = decltype(d)::value;
+    if (!(a.mods.softcap > 0.f)) return bias ? go(prompt_kernel<D, false, true, false>) : go(prompt_kernel<D, false, false, false>);
+    if (cap_is_wide(a)) return bias ? go(prompt_kernel<D, true, true, true>) : go(prompt_kernel<D, true, false, true>);
+    return bias ? go(prompt_kernel<D, true, true, false>) : go(prompt_kernel<D, true, false, false>);
+  };
+  const cudaError_t e = a.d == 128 ? go_capped(std::integral_constant<int, 128>{}) : go_capped(std::integral_constant<int, 64>{});
   if (e != cudaSuccess || a.splits == 1) return e;
   const int64_t rows = static_cast<int64_t>(a.U) * a.n_q * a.G;
   const unsigned blocks = static_cast<unsigned>((rows + 7) / 8);
