@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
   const bool capped = MODS && a.mods.softcap > 0.f, biased = MODS && a.mods.slopes;
   const bool modified = capped || biased;
   const float pre = capped ? a.scale : a.scale * kLog2e;      // goes into the key scales
-  const float inv_cap = capped ? 1.f / a.mods.softcap : 0.f;
+  const float inv_cap = capped ? fminf(1.f / a.mods.softcap, 1e30f) : 0.f;    // a smaller cap leaves no score either
   // limits over the block's query rows
   int hi_min = INT32_MAX, lo_max = INT32_MIN, hi_max = INT32_MIN, lo_min = INT32_MAX;
 #pragma unroll
@@ -395,6 +395,11 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int c = 0; c < 4; ++c) y[sub][nt][c] *= tanh_over_z(y[sub][nt][c] * inv_cap) * kLog2e;
+          } else if (a.mods.softcap > kFineCap) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) y[sub][nt][c] = capped_base2(y[sub][nt][c], y[sub][nt][c] * inv_cap, a.mods.softcap);
           } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)

@@ -1,4 +1,4 @@
-"""The tanh cap over its whole range of values, in kvc_prompt_attn: caps far above the scores (which
+"""The tanh cap over its whole range of values, in kvc_prompt_attn and kvc_i4_attn: caps far above the scores (which
 they leave nearly as they are), caps near zero (which make every score alike), small softmax scales, and rows whose
 scores pass the cap beside rows that stay far below it.
 
@@ -18,6 +18,7 @@ import pytest
 import torch
 
 from attn_reference import U, close, visible
+from test_gpu_i4_cache import G32, ROW, Cache, held, randn
 from test_gpu_prompt_attn import Case
 
 pytestmark = pytest.mark.gpu
@@ -127,3 +128,49 @@ def test_prompt_rows_past_the_cap_beside_rows_far_below(kvc, cap, form):
     c.q[:, :, :, ::16].mul_(cap)
     c.run()
     check_prompt(c)
+
+
+def i4_case(kvc, cap, mode, d, n_q, slopes, window, big, zeros):
+    c = Cache(kvc, 2, 1, 2, d, 300, [300, 77], mode, 5, 8)
+    q = randn(c.g, 2, 1, 8, n_q, d).mul_(2)
+    if big:
+        q[:, :, ::3].mul_(cap)
+    if zeros:
+        q[:, :, ::3] = 0
+    sl = torch.rand(8, generator=c.g, device="cuda") * 0.01 if slopes else None
+    out, lse = torch.full_like(q, 9.0), torch.full(q.shape[:-1], 9.0, device="cuda")
+    ws = torch.empty(max(1, kvc.kvc_i4_attn_workspace_bytes(c.shape, c.rows, n_q, True)), dtype=torch.uint8, device="cuda")
+    c.rows.mass.zero_()
+    kvc.kvc_i4_attn(c.shape, c.rows, q, out, mods=kvc.ScoreMods(cap, sl, window), add_mass=True, row_lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    cap = float(torch.tensor(cap, dtype=torch.float32))
+    for u in range(4):
+        b, g, n = u // 2, u % 2, int(c.rows.count[u])
+        k, v = held(c.rows.k[u, :n], c.rows.k_scale[u, :n], d), held(c.rows.v[u, :n], c.rows.v_scale[u, :n], d)
+        p_q = int(c.rows.next_pos[u]) - n_q + torch.arange(n_q, device="cuda")
+        p_k = c.rows.pos[u, :n].long()
+        seen = visible(p_q, p_k, window, -1)
+        mass, e_mass = (torch.zeros(n, dtype=torch.float64, device="cuda") for _ in range(2))
+        for h in range(g * 4, g * 4 + 4):
+            o, l, w, e_o, e_l, e_w = attend_capped(q[b, 0, h].double(), k, v, 1 / math.sqrt(d), seen,
+                                                   (p_q[:, None] - p_k[None]).double(), cap,
+                                                   None if sl is None else float(sl[h]))
+            close(out[b, 0, h], o, e_o, f"out u{u} h{h}")
+            close(lse[b, 0, h], l, e_l, f"lse u{u} h{h}")
+            mass += w.sum(0)
+            e_mass += e_w.sum(0) + 4 * n_q * U * w.sum(0)
+        close(c.rows.mass[u, :n], mass, e_mass + U * mass, f"mass u{u}")
+
+
+@pytest.mark.parametrize("cap", [1e3, 2e4, 1e6, 1e30, 3e38, 1e-2, 1e-12, 1e-30, 1e-42])
+@pytest.mark.parametrize("mode, d, n_q", [(G32, 128, 1), (ROW, 64, 3), (G32, 64, 9)])
+def test_4_bit_caps_far_from_the_scores(kvc, mode, d, n_q, cap):
+    for slopes, window in ((False, 0), (True, 120)):
+        i4_case(kvc, cap, mode, d, n_q, slopes, window, False, cap < 1)
+
+
+@pytest.mark.parametrize("cap", [30.0, 1e3, 5e3, 3e4])
+@pytest.mark.parametrize("mode, d, n_q", [(G32, 128, 1), (ROW, 64, 3), (G32, 64, 9)])
+def test_4_bit_rows_past_the_cap_beside_rows_far_below(kvc, mode, d, n_q, cap):
+    for slopes, window in ((False, 0), (True, 120)):
+        i4_case(kvc, cap, mode, d, n_q, slopes, window, True, False)
