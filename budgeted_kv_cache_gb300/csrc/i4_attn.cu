@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
     const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) + un.q_at(a, a.qs, min(r, un.R - 1)) + 8 * t;
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
-      const uint4 w = r < un.R ? __ldg(reinterpret_cast<const uint4*>(q + 32 * gr)) : make_uint4(0, 0, 0, 0);
+      const uint4 w = r < un.R ? *reinterpret_cast<const uint4*>(q + 32 * gr) : make_uint4(0, 0, 0, 0);
       // elements (0,4), (1,5), (2,6), (3,7) of the lane's eight
       qf[nt][gr][0] = __byte_perm(w.x, w.z, 0x5410);
       qf[nt][gr][1] = __byte_perm(w.x, w.z, 0x7632);
@@ -224,9 +224,9 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
     const int j = i * kTile + lane;
     ks_next = vs_next = Scales{};                  // rows behind those in use: no garbage meets a zero weight
     if (i < t1 && j < un.n) {
-      ks_next = __ldg(static_cast<const Scales*>(a.rows.k_scale) + un.base + j);
-      vs_next = __ldg(static_cast<const Scales*>(a.rows.v_scale) + un.base + j);
-      pos_next = __ldg(a.rows.pos + un.base + j);
+      ks_next = static_cast<const Scales*>(a.rows.k_scale)[un.base + j];
+      vs_next = static_cast<const Scales*>(a.rows.v_scale)[un.base + j];
+      pos_next = a.rows.pos[un.base + j];
     }
   };
   // query rows 2t, 2t + 1 of each column block: limits, slopes; and the query operand
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
   // With a window the positions of a tile are looked at before its copies are sent for: what no query row sees is not read.
   auto position = [&](int i) {
     const int j = i * kTile + lane;
-    return i < t1 && j < un.n ? __ldg(a.rows.pos + un.base + j) : 0;
+    return i < t1 && j < un.n ? a.rows.pos[un.base + j] : 0;
   };
   auto seen_by_any = [&](int i, int32_t p) {
     return __any_sync(kFull, i < t1 && i * kTile + lane < un.n && ((p <= hi_max && p >= lo_min) || p < prefix)) != 0;

@@ -243,9 +243,8 @@ __global__ void __launch_bounds__(kRowThreads) i4_read_kernel(const I4ReadArgs a
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         const int64_t row = row0 + min(i0 + k * RPB, i_end - 1);
-        pk[k][v] = __ldg(static_cast<const uint32_t*>(v ? a.rows.v : a.rows.k) + row * LPR + lane);
-        sb[k][v] = __ldg(static_cast<const uint16_t*>(v ? a.rows.v_scale : a.rows.k_scale) +
-                         (row_mode ? row : row * (D / 32) + lane / 4));
+        pk[k][v] = static_cast<const uint32_t*>(v ? a.rows.v : a.rows.k)[row * LPR + lane];
+        sb[k][v] = static_cast<const uint16_t*>(v ? a.rows.v_scale : a.rows.k_scale)[row_mode ? row : row * (D / 32) + lane / 4];
       }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {

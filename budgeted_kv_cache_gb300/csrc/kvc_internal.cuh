@@ -354,6 +354,9 @@ cudaError_t launch_flags(const FlagArgs& a, cudaStream_t stream);
 // runs: the launch costs no gap.  It has to call wait_for_previous_kernel
 // before it touches any memory that a kernel before it may use, for reading or
 // for writing; that one may be anybody's.
+// Its loads are coherent ones (no __ldg, no ld.global.nc): those are defined
+// for data that nobody writes while the kernel runs, and here the kernel before
+// it may still be writing after this one has begun.
 template <typename K, typename... A>
 cudaError_t launch_after(K kernel, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchAttribute attr = {};

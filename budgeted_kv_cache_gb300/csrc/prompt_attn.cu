@@ -302,7 +302,7 @@ struct TileWalk {
       const int i = at + (threadIdx.x & 31);
       bool ok = false;
       if (i < end) {
-        const int2 d = __ldg(table + tile(i));
+        const int2 d = table[tile(i)];
         ok = d.y >= q_min && d.x <= q_max;
       }
       mask = __ballot_sync(0xffffffffu, ok);
@@ -440,7 +440,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           for (int i = 0; i < 8; ++i) {
             const int r = (i0 + i) * (32 / LPR) + lane / LPR;
             const int64_t at = __shfl_sync(0xffffffffu, own, r);
-            w[i] = row - lane + r < t.rows ? __ldg(reinterpret_cast<const uint4*>(q + at) + chunk) : make_uint4(0, 0, 0, 0);
+            w[i] = row - lane + r < t.rows ? reinterpret_cast<const uint4*>(q + at)[chunk] : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -451,7 +451,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       }
       if (docs) {
         const int p = t.first + pr / a.G;
-        const int doc = ok && p >= 0 ? __ldg(docs + p) : -1;
+        const int doc = ok && p >= 0 ? docs[p] : -1;
         const int lo = __reduce_min_sync(0xffffffffu, doc >= 0 ? doc : INT32_MAX), hi = __reduce_max_sync(0xffffffffu, doc);
         if (lane == 0) {
           atomicMin(&s.q_min, lo);
@@ -550,7 +550,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         // values of keys that no row of the item sees become zeros
         bool live = j0 + kKeys <= t.nk && (j0 + kKeys <= t.pre || (j0 >= t.lo && j0 + kKeys <= t.hi));
         if (docs) {
-          const int2 d = __ldg(table + j0 / kKeys);
+          const int2 d = table[j0 / kKeys];
           live = live && d.x >= q_min && d.y <= q_max;
         }
         if (!live) {
@@ -559,7 +559,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             const int j = j0 + c;
             bool keep = j < t.nk && (j < t.pre || (j >= t.lo && j < t.hi));
             if (docs && keep) {
-              const int doc = __ldg(docs + j);
+              const int doc = docs[j];
               keep = doc >= q_min && doc <= q_max;         // 0 <= q_min
             }
             if (!keep) {
@@ -618,7 +618,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     int row_hi = min(p + 1, t.nk), row_lo = a.mods.window && p >= a.mods.window ? p - a.mods.window + 1 : 0;
     int row_pre = t.pre;
     int my_doc = 0;
-    if (docs) my_doc = p >= 0 && p < t.nk ? __ldg(docs + p) : -1;
+    if (docs) my_doc = p >= 0 && p < t.nk ? docs[p] : -1;
     if (p < 0 || my_doc < 0) row_hi = row_lo = row_pre = 0;
     // tiles that every row of the warp sees whole: keys [all_lo, all_hi) and [0, all_pre)
     const int all_lo = __reduce_max_sync(0xffffffffu, valid ? row_lo : 0);
@@ -736,7 +736,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       const bool whole = j0 + kKeys <= all_pre || (j0 >= all_lo && j0 + kKeys <= all_hi);
       bool same = true;
       if (docs) {
-        const int2 d = __ldg(table + tile);
+        const int2 d = table[tile];
         same = __all_sync(0xffffffffu, (d.x == d.y && d.x == my_doc) || !valid);
       }
       if (!whole || !same) {
@@ -745,7 +745,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           // the keys of each document that the warp's rows have, one document after another
           int kd[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) kd[c] = j0 + c * 32 + lane < t.nk ? __ldg(docs + j0 + c * 32 + lane) : -1;
+          for (int c = 0; c < 4; ++c) kd[c] = j0 + c * 32 + lane < t.nk ? docs[j0 + c * 32 + lane] : -1;
           uint32_t left = 0xffffffffu;
 #pragma unroll 1
           while (left) {
@@ -1035,7 +1035,7 @@ __global__ void __launch_bounds__(256) doc_tiles_kernel(const PromptArgs a) {
     for (int c = lane; c < kKeys; c += 32) {
       const int64_t j = static_cast<int64_t>(tile) * kKeys + c;
       if (j >= a.T) continue;
-      const int d = __ldg(a.docs + b * a.T + j);
+      const int d = a.docs[b * a.T + j];
       lo = min(lo, d);
       hi = max(hi, d);
     }

@@ -1,5 +1,7 @@
 """kvc_prompt_attn and the kvc_i4 calls refuse what they cannot do before they look for a device (CPU)."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -104,3 +106,15 @@ def test_binding_checks_tensors():
                 dict(mass=torch.zeros(8, 2).T), dict(quant_mode=kvc.QUANT_ROW_FP16)):
         with pytest.raises(kvc.KvcError):
             kvc.I4Rows(**dict(ok, **bad))
+
+
+def test_kernels_that_begin_early_load_coherently():
+    """A kernel that may begin while the one before it still writes uses no load that is defined for data nobody writes
+    during the kernel (read-only or non-coherent loads)."""
+    csrc = os.path.join(os.path.dirname(os.path.abspath(kvc.__file__)), "csrc")
+    sources = {f: open(os.path.join(csrc, f)).read() for f in os.listdir(csrc)}
+    early = [f for f, text in sources.items() if f.endswith(".cu") and "launch_after(" in text]
+    assert len(early) >= 3
+    for f in early + ["packed_math.cuh"]:
+        code = re.sub(r"//.*", "", sources[f])
+        assert not re.search(r"__ldg|ld\.global\.nc|__restrict__", code), f
