@@ -352,6 +352,10 @@ kvc_status check_mods(const kvc_score_mods* m, Mods* out) {
   return KVC_OK;
 }
 
+// Rows of a unit, and of one append: the kernels' slot numbers run past the last row by a block's step (a mass block's
+// 16,384 keys at most) and stay within 31 bits.
+constexpr int32_t kMaxRows = 0x7fff0000;
+
 kvc_status check_i4(const kvc_shape* s, const kvc_i4_rows* r) {
   kvc_status st = check_shape(s);
   if (st != KVC_OK) return st;
@@ -361,7 +365,7 @@ kvc_status check_i4(const kvc_shape* s, const kvc_i4_rows* r) {
     return KVC_ERR_INVALID_ARG;
   if (r->capacity < 1) return KVC_ERR_INVALID_ARG;
   if (r->quant_mode != KVC_QUANT_G32_BF16 && r->quant_mode != KVC_QUANT_ROW_FP16) return KVC_ERR_INVALID_ARG;
-  return KVC_OK;
+  return r->capacity > kMaxRows ? KVC_ERR_UNSUPPORTED : KVC_OK;
 }
 
 // Queries of one call: at least one, the packed rows of a unit within 31 bits.
@@ -1071,6 +1075,7 @@ kvc_status kvc_i4_append(const kvc_shape* shape, const kvc_i4_rows* rows, const 
   kvc_status st = check_i4(shape, rows);
   if (st != KVC_OK) return st;
   if (n < 0) return KVC_ERR_INVALID_ARG;
+  if (n > kMaxRows) return KVC_ERR_UNSUPPORTED;
   if (n == 0) return KVC_OK;
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return KVC_ERR_INVALID_ARG;
   I4AppendArgs a = {};

@@ -568,7 +568,7 @@ typedef struct {
   float* mass;        /* optional fp32 [U][capacity]: softmax weight it got  */
   int32_t* count;     /* int32 [U]: rows in use                              */
   int32_t* next_pos;  /* int32 [U]: position of the next appended row        */
-  int32_t capacity;   /* rows per unit                                       */
+  int32_t capacity;   /* rows per unit, below 2^31 - 65,535                  */
   int32_t quant_mode; /* KVC_QUANT_*                                         */
 } kvc_i4_rows;
 
@@ -580,7 +580,8 @@ typedef struct {
  * k, v       bf16 [B][L][H_kv][n][d] (keys rotated at their positions), with
  *            strides as in kvc_strides.  Rows are finite.
  * n_new      optional int32 [B], limited to [0, n]: rows of each sequence
- *            (NULL: n).
+ *            (NULL: n).  n is below 2^31 - 65,535, and next_pos[u] + n below
+ *            2^31.
  * unit_status  optional int32 [U], only errors are written: KVC_UNIT_FULL if
  *            the rows do not fit, KVC_UNIT_BAD_INDEX if count[u] is outside
  *            [0, capacity]; such a unit is left as it was.

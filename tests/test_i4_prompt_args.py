@@ -118,3 +118,19 @@ def test_kernels_that_begin_early_load_coherently():
     for f in early + ["packed_math.cuh"]:
         code = re.sub(r"//.*", "", sources[f])
         assert not re.search(r"__ldg|ld\.global\.nc|__restrict__", code), f
+
+
+def test_slot_numbers_stay_within_31_bits(lib):
+    """Capacities and appends so near 2^31 that a block's step past the last row would leave 31 bits are refused."""
+    most = 0x7fff0000
+    assert lib.kvc_i4_append(shape(), rows(), A, A, None, most + 1, None, None, None) == UNSUPPORTED
+    for capacity in (most + 1, 2 ** 31 - 1):
+        r = rows(capacity=capacity)
+        assert lib.kvc_i4_append(shape(), r, A, A, None, 1, None, None, None) == UNSUPPORTED
+        assert lib.kvc_i4_read(shape(), r, 1, A, A, None, None) == UNSUPPORTED
+        assert lib.kvc_i4_attn(shape(), r, A, None, 1, None, None, 0.0, 1, A, None, None, None, 0, None) == UNSUPPORTED
+        assert lib.kvc_i4_evict(shape(), r, 10, 0, 0, None, None, 0, None) == UNSUPPORTED
+        assert lib.kvc_i4_evict_workspace_bytes(shape(), r, 10) == 0
+    # the largest that is allowed: every index that the kernels form (per unit) fits
+    step = 16384 + 8 * 1024
+    assert most + step < 2 ** 31 and kvc.library().kvc_i4_evict_workspace_bytes(shape(), rows(capacity=most), 10) > 0
