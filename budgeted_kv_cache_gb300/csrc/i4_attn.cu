@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              y[sub][nt][c] = fmaf(-slope[nt][c & 1], fabsf(static_cast<float>(q_hi[nt][c & 1] - pk[c >> 1])), y[sub][nt][c]);
+              y[sub][nt][c] = fmaf(-slope[nt][c & 1], static_cast<float>(__sad(q_hi[nt][c & 1], pk[c >> 1], 0u)), y[sub][nt][c]);
         }
         if (!clear) {
           const bool in_use[2] = {i * kTile + k0 < un.n, i * kTile + k1 < un.n};
