@@ -597,7 +597,9 @@ def _pair(fn: str, dev: int, k: torch.Tensor, v: torch.Tensor, s: kvc_shape, n: 
         _refuse(fn)
     strides = _rows(fn, dev, k, s, s.n_kv_heads, n)
     if not v.is_contiguous() if strides is None else v.stride() != k.stride():
-        _refuse(fn)
+        # those of dimensions of size 1 are not looked at
+        if any(m > 1 and a != b for m, a, b in zip(k.shape, k.stride(), v.stride())):
+            _refuse(fn)
     return strides
 
 

@@ -1,0 +1,53 @@
+"""Tensors that the binding of the prompt attention and the 4-bit cache takes and refuses (CPU: helpers with the host's
+device number, -1; GPU: the calls)."""
+import pytest
+import torch
+
+import budgeted_kv_cache_gb300 as kvc
+
+
+def bf16(*s):
+    return torch.zeros(*s, dtype=torch.bfloat16)
+
+
+def views(make):
+    """Keys and values of one sequence and layer that lie alike but for the strides of the dimensions of size 1."""
+    k = make(3, 1, 4, 20, 64)[1:2, :, :, :8]                   # one sequence of three
+    v = make(1, 2, 4, 20, 64)[:, 1:2, :, :8]                   # one layer of two
+    return k, v
+
+
+def test_strides_of_single_dimensions_are_not_compared():
+    s = kvc.make_shape(1, 1, 8, 4, 64, 8)
+    k, v = views(bf16)
+    assert k.stride() != v.stride()
+    assert kvc._pair("f", -1, k, v, s, 8) is not None
+    assert kvc._pair("f", -1, v, k, s, 8) is not None
+    for other in (bf16(1, 1, 4, 8, 64), bf16(1, 1, 4, 21, 64)[:, :, :, :8], bf16(1, 1, 20, 4, 64).transpose(2, 3)[:, :, :, :8]):
+        for pair in ((k, other), (other, k)):
+            with pytest.raises(kvc.KvcError):
+                kvc._pair("f", -1, *pair, s, 8)
+
+
+@pytest.mark.gpu
+def test_calls_with_views_that_differ_in_single_dimensions():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from budgeted_kv_cache_gb300 import build
+    build.build()
+    make = lambda *s: torch.randn(*s, device="cuda").to(torch.bfloat16)
+    s = kvc.make_shape(1, 1, 8, 4, 64, 8)
+    k, v = views(make)
+    q, got, want = make(1, 1, 8, 8, 64), bf16(1, 1, 8, 8, 64).cuda(), bf16(1, 1, 8, 8, 64).cuda()
+    ws = torch.empty(max(256, kvc.kvc_prompt_attn_workspace_bytes(s, 8)), dtype=torch.uint8, device="cuda")
+    kvc.kvc_prompt_attn(s, q, k, v, got, workspace=ws)
+    kvc.kvc_prompt_attn(s, q, k.contiguous(), v.contiguous(), want, workspace=ws)
+    assert torch.equal(got, want)
+    rows = [kvc.I4Rows.allocate(s, 8) for _ in range(2)]
+    kvc.kvc_i4_append(s, rows[0], k, v)
+    kvc.kvc_i4_append(s, rows[1], k.contiguous(), v.contiguous())
+    assert torch.equal(rows[0].k, rows[1].k) and torch.equal(rows[0].v, rows[1].v)
+    outs = [views(make), (bf16(1, 1, 4, 8, 64).cuda(), bf16(1, 1, 4, 8, 64).cuda())]
+    for o in outs:
+        kvc.kvc_i4_read(s, rows[0], *o)
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
