@@ -519,6 +519,11 @@ class I4Rows:
     mass: Optional[torch.Tensor] = None
     quant_mode: int = QUANT_G32_BF16
 
+    def __setattr__(self, name, value):
+        """A tensor put in another's place is checked by the next call."""
+        self.__dict__[name] = value
+        self.__dict__["_checked"] = False
+
     def __post_init__(self):
         """Shapes and types that belong together: codes [U][capacity][d/2], the scales of the mode,
         positions and mass [U][capacity], counters [U]; contiguous, on one device."""
@@ -533,6 +538,7 @@ class I4Rows:
         for t, n, dtype in want:
             if t is not None and (t.numel() != n or t.dtype != dtype or not t.is_contiguous() or t.device != self.k.device):
                 raise KvcError("I4Rows", 1)
+        self.__dict__["_checked"] = True
 
     def c(self) -> kvc_i4_rows:
         pos, mass = self.pos, self.mass
@@ -617,6 +623,8 @@ def _units(s: kvc_shape) -> int:
 
 
 def _cache(fn: str, dev: int, rows: I4Rows, s: kvc_shape):
+    if not rows._checked:
+        rows.__post_init__()
     size = rows.k.shape
     if size[0] != s.batch * s.n_layers * s.n_kv_heads or size[2] * 2 != s.head_dim or rows.k.get_device() != dev:
         _refuse(fn)

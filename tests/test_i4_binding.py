@@ -29,6 +29,37 @@ def test_strides_of_single_dimensions_are_not_compared():
                 kvc._pair("f", -1, *pair, s, 8)
 
 
+def rows_on_the_host():
+    s = kvc.make_shape(1, 1, 2, 2, 64, 1)
+    return s, kvc.I4Rows.allocate(s, 8, device="cpu")
+
+
+def test_replaced_tensors_of_a_cache_are_checked():
+    """What takes a tensor's place later has to fit as well: kernels index it by the codes' capacity."""
+    i32 = torch.int32
+    for name, bad in (("mass", torch.zeros(2, 7)), ("mass", torch.zeros(2, 8, dtype=torch.float64)),
+                      ("pos", torch.zeros(2, 9, dtype=i32)), ("count", torch.zeros(1, dtype=i32)),
+                      ("next_pos", torch.zeros(2, dtype=torch.int64)), ("v", torch.zeros(2, 8, 16, dtype=torch.uint8)),
+                      ("k_scale", torch.zeros(2, 8, 1, dtype=torch.bfloat16)), ("quant_mode", kvc.QUANT_ROW_FP16),
+                      ("pos", torch.zeros(8, 2, dtype=i32).T)):
+        s, rows = rows_on_the_host()
+        kvc._cache("f", -1, rows, s)
+        setattr(rows, name, bad)
+        for _ in range(2):                                     # still refused the second time
+            with pytest.raises(kvc.KvcError):
+                kvc._cache("f", -1, rows, s)
+    # one that fits, none, and all of them in turn for a larger cache
+    s, rows = rows_on_the_host()
+    for mass in (torch.zeros(2, 8), None):
+        rows.mass = mass
+        kvc._cache("f", -1, rows, s)
+    larger = kvc.I4Rows.allocate(s, 16, device="cpu")
+    for name in ("k", "v", "k_scale", "v_scale", "pos", "mass", "count", "next_pos"):
+        setattr(rows, name, getattr(larger, name))
+    kvc._cache("f", -1, rows, s)
+    assert rows.c().capacity == 16
+
+
 @pytest.mark.gpu
 def test_calls_with_views_that_differ_in_single_dimensions():
     if not torch.cuda.is_available():
