@@ -1038,6 +1038,7 @@ kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_stri
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = row_lse;
   a.unit_status = unit_status;
+  a.stall_unit = g_score_stall_unit.load(std::memory_order_relaxed);   // failure test hook (-1: none)
   a.n_tiles = p.n_tiles;
   a.block_rows = p.block_rows;
   a.n_blocks = p.n_blocks;

@@ -251,6 +251,7 @@ struct PromptArgs {
   __nv_bfloat16* out;
   float* lse;                  // optional [B][L][H_q][n_q]
   int32_t* unit_status;        // optional [U]
+  int32_t stall_unit;          // test hook (-1 = none): this unit's waits for their first key tile never complete
   int32_t n_tiles;             // key tiles of T
   int32_t block_rows;          // packed rows per item: 128 or 256
   int32_t n_blocks;            // items per unit

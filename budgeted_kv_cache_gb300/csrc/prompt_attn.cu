@@ -108,6 +108,10 @@ __device__ __forceinline__ void tma_store_5d(const CUtensorMap* map, uint32_t sr
       : "memory");
 }
 
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // Until the stores of this thread have read their sources.
 __device__ __forceinline__ void tma_store_wait() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -393,6 +397,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const Item t = make_item(a, blockIdx.x);
     s.item = t;
     if (t.rows > 0) {
+      // (a.stall_unit: a test makes the first key tile's wait expect 16 bytes more than its copies bring)
+      if (t.u == a.stall_unit) mbar_expect_tx(smem_u32(&s.kfull[0]), 16);
       if (a.q_tma) load_queries<D>(s, sq, map_q, a, t, 0);
       if (!a.docs && t.i0 < t.i1)
         load_tile<D>(sk, &s.kfull[0], map_k, t, t.i0 + (t.i0 >= t.skip_at ? t.skip : 0));

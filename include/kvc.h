@@ -796,6 +796,10 @@ kvc_status kvc_commit_flags(int32_t batch, int64_t n_tokens, int32_t n_pages,
  *                       of this unit never completes, so after the bounded
  *                       wait (2 s) that unit and every unit its CTA leaves
  *                       unscored report KVC_UNIT_TIMEOUT.
+ *                       kvc_prompt_attn: the waits for this unit's first key
+ *                       tiles never complete, and the unit reports
+ *                       KVC_UNIT_TIMEOUT after the bounded wait (2 s, then 2 s
+ *                       more for the copies).
  *   select_stall_unit   -1 = off.  Test hook: in kvc_select (token and page
  *                       mode, units of at most 32,768 items whose scores
  *                       are copied to shared memory in bulk) this unit waits
