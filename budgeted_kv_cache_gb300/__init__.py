@@ -618,6 +618,20 @@ def _dense(fn: str, dev: int, t: Optional[torch.Tensor], dtype, n: int) -> Optio
     return t.data_ptr()
 
 
+def _i32(fn: str, v: int) -> int:
+    """A number that ctypes would cut to 32 bits."""
+    if not -0x80000000 <= v <= 0x7fffffff:
+        _refuse(fn)
+    return v
+
+
+def _f32(fn: str, v: float) -> float:
+    """A positive number that fp32 would turn into 0, which means something else."""
+    if 0.0 < v < 2.0 ** -149:
+        _refuse(fn)
+    return v
+
+
 def _units(s: kvc_shape) -> int:
     return s.batch * s.n_layers * s.n_kv_heads
 
@@ -634,7 +648,8 @@ def _cache(fn: str, dev: int, rows: I4Rows, s: kvc_shape):
 def _mods(fn: str, dev: int, m: Optional[ScoreMods], s: kvc_shape):
     if m is None:
         return None
-    return ctypes.byref(kvc_score_mods(m.softcap, _dense(fn, dev, m.slopes, torch.float32, s.n_q_heads), m.window,
+    return ctypes.byref(kvc_score_mods(_f32(fn, m.softcap), _dense(fn, dev, m.slopes, torch.float32, s.n_q_heads),
+                                       _i32(fn, m.window),
                                        _dense(fn, dev, m.prefix_len, torch.int32, s.batch)))
 
 
@@ -648,7 +663,7 @@ def _space(fn: str, dev: int, workspace: Optional[torch.Tensor]):
 
 
 def kvc_prompt_attn_workspace_bytes(shape, n_q: int, with_docs: bool = False) -> int:
-    return _load().kvc_prompt_attn_workspace_bytes(ctypes.byref(shape), int(n_q), int(with_docs))
+    return _load().kvc_prompt_attn_workspace_bytes(ctypes.byref(shape), _i32("kvc_prompt_attn", int(n_q)), int(with_docs))
 
 
 def kvc_prompt_attn(shape, q, k, v, out, q_len=None, kv_len=None, docs=None, mods: Optional[ScoreMods] = None,
@@ -663,7 +678,7 @@ def kvc_prompt_attn(shape, q, k, v, out, q_len=None, kv_len=None, docs=None, mod
     code = _load().kvc_prompt_attn(
         ctypes.byref(shape), q.data_ptr(), q_strides, n_q, k.data_ptr(), v.data_ptr(), _pair(f, dev, k, v, shape, T),
         _dense(f, dev, q_len, i32, B), _dense(f, dev, kv_len, i32, B), _dense(f, dev, docs, i32, B * T),
-        _mods(f, dev, mods, shape), softmax_scale, out.data_ptr(), _rows(f, dev, out, shape, Hq, n_q),
+        _mods(f, dev, mods, shape), _f32(f, softmax_scale), out.data_ptr(), _rows(f, dev, out, shape, Hq, n_q),
         _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n_q),
         _dense(f, dev, unit_status, i32, _units(shape)), ws, ws_bytes, _stream(stream, dev))
     if code:
@@ -695,7 +710,7 @@ def kvc_i4_read(shape, rows: I4Rows, k_out, v_out, stream=None):
 
 def kvc_i4_attn_workspace_bytes(shape, rows: I4Rows, n_q: int, add_mass: bool = False) -> int:
     r = rows.c()
-    return _load().kvc_i4_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(r), int(n_q),
+    return _load().kvc_i4_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(r), _i32("kvc_i4_attn", int(n_q)),
                                                ATTN_ADD_MASS if add_mass else 0)
 
 
@@ -710,7 +725,7 @@ def kvc_i4_attn(shape, rows: I4Rows, q, out, q_pos=None, mods: Optional[ScoreMod
     ws, ws_bytes = _space(f, dev, workspace)
     code = _load().kvc_i4_attn(
         ctypes.byref(shape), _cache(f, dev, rows, shape), q.data_ptr(), q_strides, n_q,
-        _dense(f, dev, q_pos, torch.int32, B * n_q), _mods(f, dev, mods, shape), softmax_scale,
+        _dense(f, dev, q_pos, torch.int32, B * n_q), _mods(f, dev, mods, shape), _f32(f, softmax_scale),
         ATTN_ADD_MASS if add_mass else 0, out.data_ptr(), _rows(f, dev, out, shape, Hq, n_q),
         _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n_q), ws, ws_bytes, _stream(stream, dev))
     if code:
@@ -719,7 +734,7 @@ def kvc_i4_attn(shape, rows: I4Rows, q, out, q_pos=None, mods: Optional[ScoreMod
 
 def kvc_i4_evict_workspace_bytes(shape, rows: I4Rows, budget: int) -> int:
     r = rows.c()
-    return _load().kvc_i4_evict_workspace_bytes(ctypes.byref(shape), ctypes.byref(r), int(budget))
+    return _load().kvc_i4_evict_workspace_bytes(ctypes.byref(shape), ctypes.byref(r), _i32("kvc_i4_evict", int(budget)))
 
 
 def kvc_i4_evict(shape, rows: I4Rows, budget: int, n_sink: int, n_recent: int, unit_status=None, workspace=None,
@@ -728,7 +743,8 @@ def kvc_i4_evict(shape, rows: I4Rows, budget: int, n_sink: int, n_recent: int, u
     f = "kvc_i4_evict"
     dev = _device(f)
     ws, ws_bytes = _space(f, dev, workspace)
-    code = _load().kvc_i4_evict(ctypes.byref(shape), _cache(f, dev, rows, shape), budget, n_sink, n_recent,
-                                _dense(f, dev, unit_status, torch.int32, _units(shape)), ws, ws_bytes, _stream(stream, dev))
+    code = _load().kvc_i4_evict(ctypes.byref(shape), _cache(f, dev, rows, shape), _i32(f, budget), _i32(f, n_sink),
+                                _i32(f, n_recent), _dense(f, dev, unit_status, torch.int32, _units(shape)), ws, ws_bytes,
+                                _stream(stream, dev))
     if code:
         raise KvcError(f, code)

@@ -60,6 +60,37 @@ def test_replaced_tensors_of_a_cache_are_checked():
     assert rows.c().capacity == 16
 
 
+def test_numbers_that_the_c_types_would_change_are_refused():
+    """2^32 + 5 as a window of 5, 2^32 recent rows as none, a cap of 1e-50 as no cap."""
+    s, rows = rows_on_the_host()
+    for mods in (kvc.ScoreMods(window=2 ** 32 + 5), kvc.ScoreMods(window=2 ** 31), kvc.ScoreMods(softcap=1e-50)):
+        with pytest.raises(kvc.KvcError):
+            kvc._mods("f", -1, mods, s)
+    for mods in (kvc.ScoreMods(window=2 ** 31 - 1), kvc.ScoreMods(softcap=1e-42), kvc.ScoreMods(softcap=0.0)):
+        assert kvc._mods("f", -1, mods, s) is not None
+    with pytest.raises(kvc.KvcError):
+        kvc.kvc_prompt_attn_workspace_bytes(s, 2 ** 32 + 1)
+    with pytest.raises(kvc.KvcError):
+        kvc.kvc_i4_attn_workspace_bytes(s, rows, 2 ** 32 + 1)
+    with pytest.raises(kvc.KvcError):
+        kvc.kvc_i4_evict_workspace_bytes(s, rows, 2 ** 32 + 1)
+
+
+@pytest.mark.gpu
+def test_eviction_numbers_past_32_bits_are_refused():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    s = kvc.make_shape(1, 1, 2, 2, 64, 1)
+    rows = kvc.I4Rows.allocate(s, 8)
+    x = torch.randn(1, 1, 2, 8, 64, device="cuda").to(torch.bfloat16)
+    kvc.kvc_i4_append(s, rows, x, x)
+    ws = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    for bad in ((2 ** 32 + 4, 0, 0), (4, 2 ** 32, 0), (4, 0, 2 ** 32)):
+        with pytest.raises(kvc.KvcError):
+            kvc.kvc_i4_evict(s, rows, *bad, workspace=ws)
+    assert rows.count.tolist() == [8, 8]
+
+
 @pytest.mark.gpu
 def test_calls_with_views_that_differ_in_single_dimensions():
     if not torch.cuda.is_available():
