@@ -12,7 +12,7 @@
 //     and prefixes share the other.  With a window, the codes of tiles that
 //     no query row sees are not read, and a unit's splits take its tiles in
 //     turn, so that all of them have a part of what is seen (32 units of 100K
-//     to 131K rows, window 8,192: 45 us without mass, 107 when every split
+//     to 131K rows, window 8,192: 47 us without mass, 107 when every split
 //     read a run of tiles).
 //   * Both products put the codes in the 16-row operand and the packed query
 //     rows (row r = query r / G, head r % G of the unit) in the 8-column one:
@@ -22,7 +22,10 @@
 //     exact; the scales never touch the codes:
 //   * the key scale of a group multiplies that group's partial sum in fp32;
 //     the value scale multiplies the weight, which is rounded to bf16 once
-//     after it, per group of 32 columns.
+//     after it, per group of 32 columns (mma.sync takes operands of one type,
+//     and the codes are exact in bf16: half a step, 2^-8 of a weight, as much
+//     as the output's own rounding; the row's sum and the mass take the
+//     unrounded weight).
 //   * The order of d inside a product is free: a lane takes the eight codes of
 //     one 32-bit word as they lie, and the queries are laid out to match.  For
 //     the values a byte permutation pairs the words of two rows.
@@ -38,9 +41,9 @@
 // Measured, replayed from a graph (d = 128, four heads a unit, g32 scales, one
 // query): 32 units of 100K to 131K rows 120 us without mass = 4.7 TB/s (the
 // copies alone take 104 us; 62 % of the ALU cycles turn codes into operands),
-// 142 us with it (the logits' round trip); 8 units of 2,304 rows 7.1 us with
+// 142 us with it (the logits' round trip), 172 with a cap, whatever the scores; 8 units of 2,304 rows 7.1 us with
 // mass, two launches' latencies.  64 units of 300 to 9,000 rows, d = 64, 15
-// query rows, capped, slopes and a window of 4,096: 16 us.
+// query rows, capped, slopes and a window of 4,096: 16.6 us.
 #include <algorithm>
 #include <type_traits>
 

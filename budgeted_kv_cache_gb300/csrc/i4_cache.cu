@@ -8,9 +8,9 @@
 // piece of bf16 on the one side and four bytes of codes on the other, so a
 // warp's accesses are whole rows on both sides.  Four rows of a thread are in
 // flight together.  Measured (d = 128, g32 scales, 96 units of up to 30,011
-// rows): append 234 us and read 200 us, 438 us together = 6.0 TB/s, 89 % of the
+// rows): append 235 us and read 192 us, 428 us together = 6.1 TB/s, 91 % of the
 // measured bandwidth, the quantiser's instructions (59 % of the ALU cycles)
-// under the copies; one token's rows of 288 units appended and read back 5.4 us.
+// under the copies; one token's rows of 288 units appended and read back 5.8 us.
 #include <algorithm>
 
 #include "kvc_internal.cuh"

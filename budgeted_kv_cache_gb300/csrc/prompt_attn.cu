@@ -18,7 +18,10 @@
 //                  when the maximum grew by more than 2^8 (P then stays below
 //                  2^8 and every sum in fp32), which a row does a few times
 //   O += P V       tcgen05, P from tensor memory, V read as an MN-major
-//                  operand straight from its TMA tile
+//                  operand straight from its TMA tile.  P is rounded to bf16
+//                  because the product wants the values' own type: half a step,
+//                  2^-8 of a weight, as much as the output's own rounding; the
+//                  row's sum is that of the unrounded weights
 // Few rows: the keys of an item are split over CTAs and the partial (m, l, O)
 // joined by PASK Eq. 15 in a second kernel.
 //
@@ -52,9 +55,10 @@
 // two warps per scheduler cannot hide behind each other's latencies: about
 // 1,400 and 2,300 cycles a step.  Measured, replayed from a graph (32 query
 // heads over 8, d = 128): 8,192 causal tokens 350 us = 1,570 TFLOP/s, 84 % of
-// the measured bf16 peak, tensor pipe 67 % active; capped 535 us = 1,030
-// TFLOP/s.  One token over 16 sequences of up to 32,768: 181 us = 6.5 TB/s, 96 %
-// of the measured bandwidth; 207 us capped.  300 tokens: 9.1 us.  Beside its
+// the measured bf16 peak, tensor pipe 67 % active; capped 523 us = 1,050
+// TFLOP/s, 751 us with scores past 0.625 of the cap in every tile.  One token over
+// 16 sequences of up to 32,768: 180 us = 6.5 TB/s, 96 % of the measured
+// bandwidth; 208 us capped, 268 past 0.625.  300 tokens: 9.3 us.  Beside its
 // steps an item costs about 11,000 cycles: 1,400 to set up, 2,300 until the
 // first scores are there, 2,200 to read and stage its outputs, 1,200 until the
 // next block of the SM begins.

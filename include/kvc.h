@@ -491,6 +491,10 @@ kvc_status kvc_engine_attn(const kvc_shape* shape, const kvc_policy* policy, con
  * and sees it iff  p_k < prefix_len[b]  or
  *                  p_k <= p_q and (window == 0 or p_q - p_k < window).
  *
+ * Under any finite cap, scores below 0.6 of it are as exact as fp32 sums; those
+ * beyond, and under caps of at most 1,024 those of the same tile, are off by
+ * 2^-21 of the cap at most.
+ *
  * A NULL kvc_score_mods is all zeros: causal attention.  With prefix_len at
  * the sequence's length every query sees every key.
  * ---------------------------------------------------------------------- */
@@ -538,7 +542,8 @@ typedef struct {
  *          nothing.
  * Rows of k and v at or past kv_len[b] and of negative documents may hold
  * any bits.  Every other row is finite: a NaN or infinity in it may also
- * reach queries that do not see it.
+ * reach queries that do not see it.  Values are below 2^119 / T in magnitude
+ * (weights of up to 2^8 are summed before the division).
  * row_lse  optional fp32 [B][L][H_q][n_q], dense.
  * unit_status  optional int32 [U]; KVC_UNIT_TIMEOUT if a device wait gave up
  *          (its rows are then undefined); untouched otherwise.
@@ -616,7 +621,9 @@ kvc_status kvc_i4_read(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t 
  * row_lse  optional fp32 [B][L][H_q][n_q], dense: natural-log log-sum-exps.
  * fp32 scores, statistics and accumulation; the weights (times the value
  * scales) are rounded to bf16 for the value product, not for the mass; bf16
- * output.  A query that sees no row outputs 0 and row_lse -inf.
+ * output (kvc_decode_attn and kvc_engine_attn keep the weights in fp32).
+ * A query that sees no row outputs 0 and row_lse -inf.  Rows in use hold finite
+ * scales, values below 2^119 / capacity in magnitude.
  * workspace >= kvc_i4_attn_workspace_bytes(...), 256-byte aligned, contents
  *          need not be initialised (may be 0 bytes: then NULL is accepted).
  * ---------------------------------------------------------------------- */
