@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 from typing import Optional
 
@@ -89,6 +90,12 @@ class kvc_i4_rows(ctypes.Structure):
         [("capacity", ctypes.c_int32), ("quant_mode", ctypes.c_int32)]
 
 
+class kvc_rope_scaling(ctypes.Structure):
+    """Scaling of kvc_rope_tables."""
+    _fields_ = [("kind", ctypes.c_int32)] + [(n, ctypes.c_double) for n in ("factor", "original_len", "low", "high")] + \
+        [("magnitude", ctypes.c_float)]
+
+
 class kvc_effect_record(ctypes.Structure):
     """Window record of kvc_deletion_effect (device pointers: o, lse, s, u)."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("o", "lse", "s", "u")]
@@ -145,6 +152,8 @@ def _load():
             "kvc_commit_flags": (ctypes.c_int, [I32, I64, I32, P, P, P, P, P, P]),
             "kvc_prompt_attn_workspace_bytes": (SZ, [SH, I32, I32]),
             "kvc_prompt_attn": (ctypes.c_int, [SH, P, ST, I32, P, P, ST, P, P, P, SM, F32, P, ST, P, P, P, SZ, P]),
+            "kvc_rope_tables": (ctypes.c_int, [I64, I32, ctypes.c_double, ctypes.POINTER(kvc_rope_scaling), P, P, P]),
+            "kvc_rope": (ctypes.c_int, [SH, P, ST, P, ST, I32, P, P, P, P, I64, I32, I32, U32, P, ST, P, ST, P, P]),
             "kvc_i4_append": (ctypes.c_int, [SH, RW, P, P, ST, I32, P, P, P]),
             "kvc_i4_read": (ctypes.c_int, [SH, RW, I32, P, P, ST, P]),
             "kvc_i4_attn_workspace_bytes": (SZ, [SH, RW, I32, U32]),
@@ -681,6 +690,71 @@ def kvc_prompt_attn(shape, q, k, v, out, q_len=None, kv_len=None, docs=None, mod
         _mods(f, dev, mods, shape), _f32(f, softmax_scale), out.data_ptr(), _rows(f, dev, out, shape, Hq, n_q),
         _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n_q),
         _dense(f, dev, unit_status, i32, _units(shape)), ws, ws_bytes, _stream(stream, dev))
+    if code:
+        raise KvcError(f, code)
+
+
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_BASE, ROPE_SCALE_TURNS, ROPE_SCALE_DIMS = 0, 1, 2, 3, 4
+ROPE_INVERSE = 1
+
+
+@dataclasses.dataclass
+class RopeScaling:
+    """How kvc_rope_tables scales its angles for long contexts (see include/kvc.h)."""
+    kind: int = ROPE_SCALE_NONE
+    factor: float = 1.0
+    original_len: float = 0.0
+    low: float = 1.0
+    high: float = 32.0
+    magnitude: float = 1.0
+
+
+def kvc_rope_tables(rope_cos, rope_sin, base: float = 10000.0, scaling: Optional[RopeScaling] = None, stream=None):
+    """Fills fp32 tables [max_pos][rotary_dim / 2] of cosines and sines (see include/kvc.h)."""
+    f = "kvc_rope_tables"
+    dev = _device(f)
+    if rope_cos.dim() != 2:
+        _refuse(f)
+    n, half = rope_cos.shape
+    c = None
+    if scaling is not None:
+        # a magnitude that fp32 would turn into 0 or infinity means something else, and one of 0 is not 1
+        m = ctypes.c_float(scaling.magnitude).value
+        if m == 0.0 or m in (math.inf, -math.inf):
+            _refuse(f)
+        c = ctypes.byref(kvc_rope_scaling(_i32(f, scaling.kind), scaling.factor, scaling.original_len, scaling.low, scaling.high, m))
+    f32 = torch.float32
+    code = _load().kvc_rope_tables(n, _i32(f, 2 * half), base, c, _dense(f, dev, rope_cos, f32, n * half),
+                                   _dense(f, dev, rope_sin, f32, n * half), _stream(stream, dev))
+    if code:
+        raise KvcError(f, code)
+
+
+def kvc_rope(shape, q, k, pos, rope_cos, rope_sin, q_out=None, k_out=None, n_rows=None,
+             rope_layout: int = ROPE_SPLIT_HALF, rotary_dim: int = 0, inverse: bool = False, unit_status=None, stream=None):
+    """q [B][L][H_q][n][d] and k [B][L][H_kv][n][d] (either may be None) rotated to positions pos [B][n] into q_out, k_out
+    (None: in place) by tables [max_pos][rotary_dim / 2] (see include/kvc.h)."""
+    f = "kvc_rope"
+    dev = _device(f)
+    x = q if q is not None else k
+    if x is None or x.dim() != 5 or rope_cos.dim() != 2 or (q is None and q_out is not None) or (k is None and k_out is not None):
+        _refuse(f)
+    n, f32, i32 = x.shape[3], torch.float32, torch.int32
+    rot = rotary_dim or shape.head_dim
+    if rope_cos.shape[1] * 2 != rot:
+        _refuse(f)
+
+    def place(t, heads):
+        return (None, None) if t is None else (t.data_ptr(), _rows(f, dev, t, shape, heads, n))
+    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+    (qp, qs), (qop, qos) = place(q, shape.n_q_heads), place(q_out, shape.n_q_heads)
+    (kp, ks), (kop, kos) = place(k, shape.n_kv_heads), place(k_out, shape.n_kv_heads)
+    code = _load().kvc_rope(
+        ctypes.byref(shape), qp, qs, kp, ks, n, _dense(f, dev, pos, i32, shape.batch * n),
+        _dense(f, dev, n_rows, i32, shape.batch), _dense(f, dev, rope_cos, f32, rope_cos.numel()),
+        _dense(f, dev, rope_sin, f32, rope_cos.numel()), rope_cos.shape[0], _i32(f, rope_layout), _i32(f, rot),
+        ROPE_INVERSE if inverse else 0, qop, qos, kop, kos, _dense(f, dev, unit_status, i32, _units(shape)),
+        _stream(stream, dev))
     if code:
         raise KvcError(f, code)
 

@@ -492,6 +492,44 @@ kvc_status plan_i4_attn(const kvc_shape* s, const kvc_i4_rows* r, int32_t n_q, u
   return KVC_OK;
 }
 
+// Turns per position of every pair, in 2^-64 (whole turns dropped), and the tables' magnitude; false: not a valid scaling.
+bool rope_turns(int rotary_dim, double base, const kvc_rope_scaling* s, uint64_t* turns, float* magnitude) {
+  constexpr double kTau = 6.283185307179586;
+  if (!(base >= 1.0) || isinf(base)) return false;
+  const int kind = s ? s->kind : KVC_ROPE_SCALE_NONE;
+  *magnitude = s && s->magnitude != 0.f ? s->magnitude : 1.f;
+  if (!isfinite(*magnitude) || kind < KVC_ROPE_SCALE_NONE || kind > KVC_ROPE_SCALE_DIMS) return false;
+  double factor = 1.0, first = 0.0, last = 0.0;
+  if (kind != KVC_ROPE_SCALE_NONE) {
+    factor = s->factor;
+    if (!(factor > 0.0) || isinf(factor)) return false;
+  }
+  if (kind == KVC_ROPE_SCALE_BASE) {
+    base *= pow(factor, rotary_dim / (rotary_dim - 2.0));
+    if (!(base >= 1.0) || isinf(base)) return false;
+  }
+  if (kind == KVC_ROPE_SCALE_TURNS || kind == KVC_ROPE_SCALE_DIMS) {
+    if (!(s->original_len > 0.0) || isinf(s->original_len) || !(s->low >= 0.0) || !(s->high > s->low) || isinf(s->high)) return false;
+    if (kind == KVC_ROPE_SCALE_DIMS) {
+      if (!(s->low > 0.0) || !(base > 1.0)) return false;
+      auto at = [&](double n) { return rotary_dim * log(s->original_len / (n * kTau)) / (2.0 * log(base)); };
+      first = fmax(floor(at(s->high)), 0.0);
+      last = fmin(ceil(at(s->low)), rotary_dim - 1.0);
+    }
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double theta = pow(base, -2.0 * i / rotary_dim), keep = 0.0;
+    if (kind == KVC_ROPE_SCALE_NONE || kind == KVC_ROPE_SCALE_BASE) keep = 1.0;
+    if (kind == KVC_ROPE_SCALE_TURNS) keep = (s->original_len * theta / kTau - s->low) / (s->high - s->low);
+    if (kind == KVC_ROPE_SCALE_DIMS) keep = 1.0 - (i - first) / fmax(last - first, 0.001);
+    keep = fmin(fmax(keep, 0.0), 1.0);
+    theta *= keep + (1.0 - keep) / factor;
+    const double t = fmod(theta / kTau, 1.0) * 0x1p64;
+    turns[i] = t < 0x1p64 ? static_cast<uint64_t>(t) : 0;
+  }
+  return true;
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------- CommitKV plans
@@ -1165,6 +1203,85 @@ kvc_status kvc_i4_attn(const kvc_shape* shape, const kvc_i4_rows* rows, const vo
   if (p.ws_o) a.part_o = reinterpret_cast<float*>(ws + p.ws_ml);
   if (a.add_mass) a.logits = reinterpret_cast<float*>(ws + p.ws_ml + p.ws_o);
   return launch_i4_attn(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+kvc_status kvc_rope_tables(int64_t max_pos, int32_t rotary_dim, double base, const kvc_rope_scaling* scaling,
+                           float* rope_cos, float* rope_sin, kvc_stream stream) {
+  if (max_pos < 0 || max_pos > 0x7fffffffLL || rotary_dim < 16 || rotary_dim > 128 || rotary_dim % 16) return KVC_ERR_INVALID_ARG;
+  RopeTableArgs a = {};
+  if (!rope_turns(rotary_dim, base, scaling, a.turns, &a.magnitude)) return KVC_ERR_INVALID_ARG;
+  if (max_pos == 0) return KVC_OK;
+  if (!rope_cos || !rope_sin || !aligned(rope_cos, 16) || !aligned(rope_sin, 16)) return KVC_ERR_INVALID_ARG;
+  DevInfo info;
+  const kvc_status st = check_device(&info);
+  if (st != KVC_OK) return st;
+  a.max_pos = max_pos;
+  a.half = rotary_dim / 2;
+  a.cos = rope_cos;
+  a.sin = rope_sin;
+  return launch_rope_tables(a, info.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+kvc_status kvc_rope(const kvc_shape* shape, const void* q, const kvc_strides* q_strides, const void* k,
+                    const kvc_strides* k_strides, int32_t n, const int32_t* pos, const int32_t* n_rows,
+                    const float* rope_cos, const float* rope_sin, int64_t rope_max_pos, int32_t rope_layout,
+                    int32_t rotary_dim, uint32_t flags, void* q_out, const kvc_strides* q_out_strides, void* k_out,
+                    const kvc_strides* k_out_strides, int32_t* unit_status, kvc_stream stream) {
+  kvc_status st = check_shape(shape);
+  if (st != KVC_OK) return st;
+  if (rotary_dim == 0) rotary_dim = shape->head_dim;
+  if (n < 0 || rotary_dim < 16 || rotary_dim > shape->head_dim || rotary_dim % 16) return KVC_ERR_INVALID_ARG;
+  if (rope_layout != KVC_ROPE_SPLIT_HALF && rope_layout != KVC_ROPE_INTERLEAVED) return KVC_ERR_INVALID_ARG;
+  if (rope_max_pos < 1 || (flags & ~static_cast<uint32_t>(KVC_ROPE_INVERSE))) return KVC_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr)) return KVC_ERR_INVALID_ARG;
+  if (n == 0 || (!q && !k)) return KVC_OK;
+  if (!pos || !rope_cos || !rope_sin || !aligned(rope_cos, 16) || !aligned(rope_sin, 16)) return KVC_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16)) return KVC_ERR_INVALID_ARG;
+  RopeArgs a = {};
+  if (q && (st = tensor_strides(shape, shape->n_q_heads, n, q_strides, &a.qs)) != KVC_OK) return st;
+  if (q && (st = tensor_strides(shape, shape->n_q_heads, n, q_out_strides, &a.qos)) != KVC_OK) return st;
+  if (k && (st = tensor_strides(shape, shape->n_kv_heads, n, k_strides, &a.ks)) != KVC_OK) return st;
+  if (k && (st = tensor_strides(shape, shape->n_kv_heads, n, k_out_strides, &a.kos)) != KVC_OK) return st;
+  auto same = [](const kvc_strides& x, const kvc_strides& y) {
+    return x.batch == y.batch && x.layer == y.layer && x.head == y.head && x.token == y.token;
+  };
+  // in place: every element where it was
+  if ((q && q == q_out && !same(a.qs, a.qos)) || (k && k == k_out && !same(a.ks, a.kos))) return KVC_ERR_INVALID_ARG;
+  DevInfo info;
+  if ((st = check_device(&info)) != KVC_OK) return st;
+  a.B = shape->batch;
+  a.L = shape->n_layers;
+  a.Hq = q ? shape->n_q_heads : 0;
+  a.Hkv = k ? shape->n_kv_heads : 0;
+  a.units = shape->n_kv_heads;
+  a.d = shape->head_dim;
+  a.n = n;
+  a.max_pos = rope_max_pos;
+  a.rotary_dim = rotary_dim;
+  a.layout = rope_layout;
+  a.inverse = (flags & KVC_ROPE_INVERSE) != 0;
+  a.in_place = q == q_out && k == k_out;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.pos = pos;
+  a.n_rows = n_rows;
+  a.cos = rope_cos;
+  a.sin = rope_sin;
+  a.unit_status = unit_status;
+  // A block takes up to 32 (64 at d = 64) tokens, and the heads of as many as fit beside each other; where that leaves
+  // SMs idle, several blocks share the heads of their tokens.
+  const int rows = kRopeThreads / (a.d / 16);
+  while ((2 << a.token_bits) <= rows && (1 << a.token_bits) < n) ++a.token_bits;
+  const int64_t blocks = (static_cast<int64_t>(n) + (1 << a.token_bits) - 1) >> a.token_bits;
+  const int64_t all = blocks * a.B * a.L;
+  if (all > 0x7fffffffLL) return KVC_ERR_UNSUPPORTED;
+  const int side = rows >> a.token_bits;
+  a.split = static_cast<int32_t>(std::max<int64_t>(
+      1, std::min<int64_t>((16LL * info.sms + all - 1) / all, (a.Hq + a.Hkv + side - 1) / side)));
+  a.by_blocks = FastDiv::of(static_cast<uint32_t>(blocks));
+  return launch_rope(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
 size_t kvc_i4_evict_workspace_bytes(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t budget) {

@@ -316,6 +316,37 @@ struct I4EvictArgs {
   int32_t* unit_status;        // optional [U]
 };
 
+constexpr int kRopeThreads = 256;
+
+struct RopeTableArgs {
+  int64_t max_pos;
+  int32_t half;                // rotary_dim / 2
+  float magnitude;
+  float* cos;
+  float* sin;
+  uint64_t turns[64];          // turns per position of each pair, in 2^-64
+};
+
+struct RopeArgs {
+  int32_t B, L, Hq, Hkv, d, n; // Hq, Hkv: heads of q and of k (0: not given)
+  int64_t max_pos;
+  int32_t rotary_dim, layout;
+  bool inverse, in_place;      // in_place: what does not turn need not be copied
+  kvc_strides qs, ks, qos, kos;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;
+  const int32_t* pos;          // [B][n]
+  const int32_t* n_rows;       // optional [B]
+  const float* cos;
+  const float* sin;
+  int32_t* unit_status;        // optional [U]
+  int32_t units;               // KV heads of the shape
+  int32_t token_bits, split;   // log2 of a block's tokens; blocks that share the heads of a token
+  FastDiv by_blocks;           // divisor: blocks of a sequence and layer
+};
+
 // host launchers (each returns a cudaError_t from the launch)
 cudaError_t launch_bonus(const BonusArgs& a, cudaStream_t stream);
 cudaError_t launch_pool(const float* in, float* out, int64_t rows, int64_t n, int kernel, int mode,
@@ -344,6 +375,8 @@ cudaError_t launch_i4_append(const I4AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_read(const I4ReadArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_evict(const I4EvictArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_tables(const RopeTableArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 size_t effect_smem_bytes(int Rp, int n_stages);
 cudaError_t launch_effect(const EffectArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                           const CUtensorMap& tmap_q, int grid, size_t smem_bytes, cudaStream_t stream);

@@ -20,6 +20,8 @@
  *   kvc_i4_attn                 attention over the 4-bit cache, which may add
  *                               the softmax weights to its rows' mass
  *   kvc_i4_evict                in-place eviction of the rows of least mass
+ *   kvc_rope_tables, kvc_rope   rotary tables, and fresh queries and keys
+ *                               rotated by them
  *
  * Sources, cited by page title and section:
  *   PASK     "Parser Transitions Already Reveal Structural Responsibility:
@@ -558,6 +560,84 @@ kvc_status kvc_prompt_attn(const kvc_shape* shape, const void* q, const kvc_stri
                            const kvc_score_mods* mods, float softmax_scale, void* out,
                            const kvc_strides* out_strides, float* row_lse, int32_t* unit_status,
                            void* workspace, size_t workspace_bytes, kvc_stream stream);
+
+/* ------------------------------------------------------------------------
+ * kvc_rope_tables -- the rotary tables of kvc_rope and
+ * kvc_compact_rerotate_quant: cosines and sines of p theta_i, i < rotary_dim / 2.
+ *
+ *   theta_i = base^(-2 i / rotary_dim), scaled for contexts longer than the
+ *   trained one (kvc_rope_scaling; NULL = as trained):
+ *     KVC_ROPE_SCALE_LINEAR  theta_i / factor
+ *     KVC_ROPE_SCALE_BASE    with base factor^(rotary_dim / (rotary_dim - 2))
+ *     KVC_ROPE_SCALE_TURNS   theta_i (g + (1 - g) / factor), g = (r - low) / (high - low)
+ *                            limited to [0, 1], r = original_len theta_i / (2 pi) the
+ *                            pair's turns over the trained length (YaRN, arXiv
+ *                            2309.00071, Sec. 3.2)
+ *     KVC_ROPE_SCALE_DIMS    the same with g = 1 - (i - a) / max(b - a, 0.001)
+ *                            limited to [0, 1], a = max(floor(at(high)), 0),
+ *                            b = min(ceil(at(low)), rotary_dim - 1), at(n) =
+ *                            rotary_dim ln(original_len / (2 pi n)) / (2 ln base),
+ *                            the pair that turns n times
+ *   and both tables times `magnitude` (0 = 1; YaRN: 0.1 ln(factor) + 1).
+ *
+ * max_pos    rows of the tables, >= 0, below 2^31: positions 0 .. max_pos - 1.
+ * rotary_dim a multiple of 16, 16 .. 128.  base >= 1.
+ * rope_cos, rope_sin  fp32 [max_pos][rotary_dim / 2], 16-byte aligned; within
+ *            2^-22 (times the magnitude) of the cosine and sine of the exact
+ *            product, at any position.
+ * ---------------------------------------------------------------------- */
+enum {
+  KVC_ROPE_SCALE_NONE = 0,
+  KVC_ROPE_SCALE_LINEAR = 1,
+  KVC_ROPE_SCALE_BASE = 2,
+  KVC_ROPE_SCALE_TURNS = 3,
+  KVC_ROPE_SCALE_DIMS = 4
+};
+
+typedef struct {
+  int32_t kind;          /* KVC_ROPE_SCALE_*                                  */
+  double factor;         /* > 0: length served / length trained; NONE: unread */
+  double original_len;   /* TURNS, DIMS: trained length, > 0                  */
+  double low, high;      /* TURNS, DIMS: turns, 0 <= low < high (DIMS: 0 < low) */
+  float magnitude;       /* finite; 0 = 1                                     */
+} kvc_rope_scaling;
+
+kvc_status kvc_rope_tables(int64_t max_pos, int32_t rotary_dim, double base,
+                           const kvc_rope_scaling* scaling, float* rope_cos, float* rope_sin,
+                           kvc_stream stream);
+
+/* ------------------------------------------------------------------------
+ * kvc_rope -- queries and keys rotated to their positions, ready for the
+ * attention calls and the caches (PACE Sec. 3.2's rotation R_p).
+ *
+ *   x' = x C - y S,  y' = y C + x S   for every pair (x, y) of a row,
+ *
+ * C, S the tables' row of its position; fp32, no fused multiply-add, rounded
+ * once to bf16 (nearest even).  rope_layout and rotary_dim (0 = head_dim) as
+ * in kvc_policy: elements past rotary_dim are copied.
+ *
+ * q, k     bf16 [B][L][H_q][n][d] and [B][L][H_kv][n][d], strides as in
+ *          kvc_strides; either may be NULL, with its output.
+ * q_out, k_out  alike, with strides of their own; may be q and k themselves,
+ *          with the same strides, and must not overlap the inputs otherwise.
+ * pos      int32 [B][n]: position of each token, the same in every layer.
+ * n_rows   optional int32 [B], limited to [0, n] (NULL: n).  Rows at or past
+ *          n_rows[b] are left as they were, and their positions not read.
+ * flags    KVC_ROPE_INVERSE: turned back by R_-p (S negated), which is also
+ *          the gradient's way through the rotation.
+ * unit_status  optional int32 [U]; a token whose position is outside
+ *          [0, rope_max_pos) is left as it was and marks every unit of its
+ *          sequence KVC_UNIT_BAD_INDEX; untouched otherwise.
+ * shape->n_tokens is not read.
+ * ---------------------------------------------------------------------- */
+enum { KVC_ROPE_INVERSE = 1 };
+
+kvc_status kvc_rope(const kvc_shape* shape, const void* q, const kvc_strides* q_strides,
+                    const void* k, const kvc_strides* k_strides, int32_t n, const int32_t* pos,
+                    const int32_t* n_rows, const float* rope_cos, const float* rope_sin,
+                    int64_t rope_max_pos, int32_t rope_layout, int32_t rotary_dim, uint32_t flags,
+                    void* q_out, const kvc_strides* q_out_strides, void* k_out,
+                    const kvc_strides* k_out_strides, int32_t* unit_status, kvc_stream stream);
 
 /* ------------------------------------------------------------------------
  * A growing cache held in 4 bits.  Row storage is that of the int4 pool of
