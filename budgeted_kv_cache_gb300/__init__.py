@@ -152,6 +152,8 @@ def _load():
             "kvc_commit_flags": (ctypes.c_int, [I32, I64, I32, P, P, P, P, P, P]),
             "kvc_prompt_attn_workspace_bytes": (SZ, [SH, I32, I32]),
             "kvc_prompt_attn": (ctypes.c_int, [SH, P, ST, I32, P, P, ST, P, P, P, SM, F32, P, ST, P, P, P, SZ, P]),
+            "kvc_i4_tree_attn_workspace_bytes": (SZ, [SH, RW, I32]),
+            "kvc_i4_tree_attn": (ctypes.c_int, [SH, RW, P, ST, I32, P, P, ST, P, P, SM, F32, P, ST, P, P, P, SZ, P]),
             "kvc_rope_tables": (ctypes.c_int, [I64, I32, ctypes.c_double, ctypes.POINTER(kvc_rope_scaling), P, P, P]),
             "kvc_rope": (ctypes.c_int, [SH, P, ST, P, ST, I32, P, P, P, P, I64, I32, I32, U32, P, ST, P, ST, P, P]),
             "kvc_i4_append": (ctypes.c_int, [SH, RW, P, P, ST, I32, P, P, P]),
@@ -802,6 +804,35 @@ def kvc_i4_attn(shape, rows: I4Rows, q, out, q_pos=None, mods: Optional[ScoreMod
         _dense(f, dev, q_pos, torch.int32, B * n_q), _mods(f, dev, mods, shape), _f32(f, softmax_scale),
         ATTN_ADD_MASS if add_mass else 0, out.data_ptr(), _rows(f, dev, out, shape, Hq, n_q),
         _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n_q), ws, ws_bytes, _stream(stream, dev))
+    if code:
+        raise KvcError(f, code)
+
+
+TREE_MAX_NODES = 1024
+
+
+def kvc_i4_tree_attn_workspace_bytes(shape, rows: I4Rows, n: int) -> int:
+    r = rows.c()
+    return _load().kvc_i4_tree_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(r), _i32("kvc_i4_tree_attn", int(n)))
+
+
+def kvc_i4_tree_attn(shape, rows: I4Rows, q, k_new, v_new, parent, out, n_nodes=None, mods: Optional[ScoreMods] = None,
+                     softmax_scale=0.0, row_lse=None, unit_status=None, workspace=None, stream=None):
+    """Attention of a tree of drafted tokens, q [B][L][H_q][n][d] with parents [B][n], over a 4-bit cache and over the
+    tree's own k_new, v_new [B][L][H_kv][n][d] (see include/kvc.h)."""
+    f = "kvc_i4_tree_attn"
+    dev = _device(f)
+    B, Hq, i32 = shape.batch, shape.n_q_heads, torch.int32
+    q_strides, n = _rows(f, dev, q, shape, Hq), q.shape[3]
+    ws, ws_bytes = _space(f, dev, workspace)
+    if parent is None:
+        _refuse(f)
+    code = _load().kvc_i4_tree_attn(
+        ctypes.byref(shape), _cache(f, dev, rows, shape), q.data_ptr(), q_strides, n, k_new.data_ptr(), v_new.data_ptr(),
+        _pair(f, dev, k_new, v_new, shape, n), _dense(f, dev, parent, i32, B * n), _dense(f, dev, n_nodes, i32, B),
+        _mods(f, dev, mods, shape), _f32(f, softmax_scale), out.data_ptr(), _rows(f, dev, out, shape, Hq, n),
+        _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n), _dense(f, dev, unit_status, i32, _units(shape)),
+        ws, ws_bytes, _stream(stream, dev))
     if code:
         raise KvcError(f, code)
 

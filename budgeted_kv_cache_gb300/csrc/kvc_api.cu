@@ -492,6 +492,25 @@ kvc_status plan_i4_attn(const kvc_shape* s, const kvc_i4_rows* r, int32_t n_q, u
   return KVC_OK;
 }
 
+// A tree's calls: its nodes (KVC_TREE_MAX_NODES at most) over a 4-bit cache.
+kvc_status check_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n) {
+  const kvc_status st = check_i4(s, r);
+  if (st != KVC_OK) return st;
+  if (n < 1) return KVC_ERR_INVALID_ARG;
+  return n > KVC_TREE_MAX_NODES || s->n_q_heads / s->n_kv_heads > (1 << 16) ? KVC_ERR_UNSUPPORTED : KVC_OK;
+}
+
+struct TreePlan {
+  size_t ws_total = 0;
+};
+
+kvc_status plan_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n, TreePlan* p) {
+  const kvc_status st = check_tree(s, r, n);
+  if (st != KVC_OK) return st;
+  DevInfo info;
+  return check_device(&info);
+}
+
 // Turns per position of every pair, in 2^-64 (whole turns dropped), and the tables' magnitude; false: not a valid scaling.
 bool rope_turns(int rotary_dim, double base, const kvc_rope_scaling* s, uint64_t* turns, float* magnitude) {
   constexpr double kTau = 6.283185307179586;
@@ -1203,6 +1222,49 @@ kvc_status kvc_i4_attn(const kvc_shape* shape, const kvc_i4_rows* rows, const vo
   if (p.ws_o) a.part_o = reinterpret_cast<float*>(ws + p.ws_ml);
   if (a.add_mass) a.logits = reinterpret_cast<float*>(ws + p.ws_ml + p.ws_o);
   return launch_i4_attn(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+size_t kvc_i4_tree_attn_workspace_bytes(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t n) {
+  TreePlan p;
+  return plan_tree(shape, rows, n, &p) == KVC_OK ? p.ws_total : 0;
+}
+
+kvc_status kvc_i4_tree_attn(const kvc_shape* shape, const kvc_i4_rows* rows, const void* q, const kvc_strides* q_strides,
+                            int32_t n, const void* k_new, const void* v_new, const kvc_strides* new_strides,
+                            const int32_t* parent, const int32_t* n_nodes, const kvc_score_mods* mods,
+                            float softmax_scale, void* out, const kvc_strides* out_strides, float* row_lse,
+                            int32_t* unit_status, void* workspace, size_t workspace_bytes, kvc_stream stream) {
+  kvc_status st = check_tree(shape, rows, n);
+  if (st != KVC_OK) return st;
+  if (!q || !k_new || !v_new || !parent || !out) return KVC_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(out, 16)) return KVC_ERR_INVALID_ARG;
+  TreeArgs a = {};
+  if ((st = tensor_strides(shape, shape->n_q_heads, n, q_strides, &a.qs)) != KVC_OK) return st;
+  if ((st = tensor_strides(shape, shape->n_kv_heads, n, new_strides, &a.news)) != KVC_OK) return st;
+  if ((st = tensor_strides(shape, shape->n_q_heads, n, out_strides, &a.os)) != KVC_OK) return st;
+  if ((st = check_mods(mods, &a.mods)) != KVC_OK) return st;
+  TreePlan p;
+  if ((st = plan_tree(shape, rows, n, &p)) != KVC_OK) return st;
+  if (p.ws_total > 0 && (!workspace || workspace_bytes < p.ws_total || !aligned(workspace, 256))) return KVC_ERR_WORKSPACE;
+  if (!(softmax_scale > 0.f)) softmax_scale = 1.0f / sqrtf(static_cast<float>(shape->head_dim));
+  a.U = static_cast<int32_t>(n_units(shape));
+  a.L = shape->n_layers;
+  a.Hkv = shape->n_kv_heads;
+  a.B = shape->batch;
+  a.G = shape->n_q_heads / shape->n_kv_heads;
+  a.d = shape->head_dim;
+  a.n = n;
+  a.scale = softmax_scale;
+  a.rows = *rows;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  a.parent = parent;
+  a.n_nodes = n_nodes;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = row_lse;
+  a.unit_status = unit_status;
+  return launch_tree(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
 kvc_status kvc_rope_tables(int64_t max_pos, int32_t rotary_dim, double base, const kvc_rope_scaling* scaling,

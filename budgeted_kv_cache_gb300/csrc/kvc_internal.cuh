@@ -306,6 +306,23 @@ struct I4AttnArgs {
 
 constexpr int kMaxSplits = 128;      // blocks that share a unit's keys in the 4-bit attention
 
+// A tree of drafted tokens over a 4-bit cache.
+struct TreeArgs {
+  int32_t U, L, Hkv, B, G, d, n;
+  float scale;
+  kvc_i4_rows rows;
+  kvc_strides qs, news, os;    // element strides
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  const int32_t* parent;       // [B][n]
+  const int32_t* n_nodes;      // optional [B]
+  Mods mods;
+  __nv_bfloat16* out;
+  float* lse;                  // optional [B][L][H_q][n]
+  int32_t* unit_status;        // optional [U]
+};
+
 struct I4EvictArgs {
   int32_t U, d, budget, n_sink, n_recent;
   int32_t max_moves;           // entries of each list
@@ -375,6 +392,7 @@ cudaError_t launch_i4_append(const I4AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_read(const I4ReadArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_evict(const I4EvictArgs& a, cudaStream_t stream);
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_rope_tables(const RopeTableArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 size_t effect_smem_bytes(int Rp, int n_stages);

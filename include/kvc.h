@@ -20,6 +20,8 @@
  *   kvc_i4_attn                 attention over the 4-bit cache, which may add
  *                               the softmax weights to its rows' mass
  *   kvc_i4_evict                in-place eviction of the rows of least mass
+ *   kvc_i4_tree_attn            attention of a tree of drafted tokens over the
+ *                               4-bit cache
  *   kvc_rope_tables, kvc_rope   rotary tables, and fresh queries and keys
  *                               rotated by them
  *
@@ -743,6 +745,50 @@ size_t kvc_i4_evict_workspace_bytes(const kvc_shape* shape, const kvc_i4_rows* r
 kvc_status kvc_i4_evict(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t budget,
                         int32_t n_sink, int32_t n_recent, int32_t* unit_status, void* workspace,
                         size_t workspace_bytes, kvc_stream stream);
+
+/* ------------------------------------------------------------------------
+ * kvc_i4_tree_attn -- attention of a tree of drafted tokens over a 4-bit
+ * cache: what a model needs to check the whole tree in one step.  The tree's
+ * keys and values stay in bf16 beside the cache; kvc_i4_tree_commit puts those
+ * of the accepted path into it.
+ *
+ * Node i of unit u stands at position p_i = next_pos[u] + depth(i), a node
+ * without a parent at depth 0.  It sees the rows in use, its ancestors and
+ * itself, of them with a window those with p_i - p_k < window or p_k <
+ * prefix_len[b]; scores are capped and sloped as above, and one softmax goes
+ * over all of them:
+ *   out[h][i] = sum_j softmax_j(x_hij) v_j,  row_lse[h][i] = ln sum_j exp(x_hij).
+ *
+ * rows     as for kvc_i4_attn (mass is not touched: see kvc_i4_tree_commit);
+ *          positions of the rows in use lie below next_pos[u], and
+ *          next_pos[u] + n below 2^31.
+ * q, out   bf16 [B][L][H_q][n][d], strides as in kvc_strides; 1 <= n <=
+ *          KVC_TREE_MAX_NODES.
+ * k_new, v_new  bf16 [B][L][H_kv][n][d] (keys rotated at the nodes' positions),
+ *          which share their strides.  Rows of nodes are finite, others not read.
+ * parent   int32 [B][n]: each node's parent, an earlier node, or -1.  A node
+ *          with another value counts as one without a parent, and marks the
+ *          units of its sequence KVC_UNIT_BAD_INDEX in unit_status.
+ * n_nodes  optional int32 [B], limited to [0, n] (NULL: n).  Rows of out and
+ *          row_lse at or past n_nodes[b] are left as they were.
+ * row_lse  optional fp32 [B][L][H_q][n], dense.
+ * unit_status  optional int32 [U], only errors are written.
+ * Keys and values are used as they are stored (code * scale; fp32 scores,
+ * statistics and accumulation); bf16 output.
+ * workspace >= kvc_i4_tree_attn_workspace_bytes(...), 256-byte aligned,
+ *          contents need not be initialised (may be 0 bytes: then NULL is
+ *          accepted).
+ * ---------------------------------------------------------------------- */
+enum { KVC_TREE_MAX_NODES = 1024 };
+
+size_t kvc_i4_tree_attn_workspace_bytes(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t n);
+kvc_status kvc_i4_tree_attn(const kvc_shape* shape, const kvc_i4_rows* rows, const void* q,
+                            const kvc_strides* q_strides, int32_t n, const void* k_new,
+                            const void* v_new, const kvc_strides* new_strides,
+                            const int32_t* parent, const int32_t* n_nodes,
+                            const kvc_score_mods* mods, float softmax_scale, void* out,
+                            const kvc_strides* out_strides, float* row_lse, int32_t* unit_status,
+                            void* workspace, size_t workspace_bytes, kvc_stream stream);
 
 /* ------------------------------------------------------------------------
  * CommitKV lifecycle-aware retirement ("CommitKV: Lifecycle-Aware KV Cache
