@@ -154,6 +154,7 @@ def _load():
             "kvc_prompt_attn": (ctypes.c_int, [SH, P, ST, I32, P, P, ST, P, P, P, SM, F32, P, ST, P, P, P, SZ, P]),
             "kvc_i4_tree_attn_workspace_bytes": (SZ, [SH, RW, I32]),
             "kvc_i4_tree_attn": (ctypes.c_int, [SH, RW, P, ST, I32, P, P, ST, P, P, SM, F32, P, ST, P, P, P, SZ, P]),
+            "kvc_i4_tree_commit": (ctypes.c_int, [SH, RW, P, P, ST, I32, P, P, I32, P, ST, P, SM, F32, P, P, ST, P, P]),
             "kvc_rope_tables": (ctypes.c_int, [I64, I32, ctypes.c_double, ctypes.POINTER(kvc_rope_scaling), P, P, P]),
             "kvc_rope": (ctypes.c_int, [SH, P, ST, P, ST, I32, P, P, P, P, I64, I32, I32, U32, P, ST, P, ST, P, P]),
             "kvc_i4_append": (ctypes.c_int, [SH, RW, P, P, ST, I32, P, P, P]),
@@ -808,7 +809,7 @@ def kvc_i4_attn(shape, rows: I4Rows, q, out, q_pos=None, mods: Optional[ScoreMod
         raise KvcError(f, code)
 
 
-TREE_MAX_NODES = 1024
+TREE_MAX_NODES, TREE_MAX_PATH = 1024, 64
 
 
 def kvc_i4_tree_attn_workspace_bytes(shape, rows: I4Rows, n: int) -> int:
@@ -833,6 +834,30 @@ def kvc_i4_tree_attn(shape, rows: I4Rows, q, k_new, v_new, parent, out, n_nodes=
         _mods(f, dev, mods, shape), _f32(f, softmax_scale), out.data_ptr(), _rows(f, dev, out, shape, Hq, n),
         _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n), _dense(f, dev, unit_status, i32, _units(shape)),
         ws, ws_bytes, _stream(stream, dev))
+    if code:
+        raise KvcError(f, code)
+
+
+def kvc_i4_tree_commit(shape, rows: I4Rows, k_new, v_new, path, path_len, q=None, row_lse=None,
+                       mods: Optional[ScoreMods] = None, softmax_scale=0.0, k_out=None, v_out=None, unit_status=None,
+                       stream=None):
+    """The rows of the accepted path [B][max_path] of a tree's k_new, v_new [B][L][H_kv][n][d] into a 4-bit cache; with q
+    and row_lse its softmax weights into the mass (see include/kvc.h)."""
+    f = "kvc_i4_tree_commit"
+    dev = _device(f)
+    B, Hq, i32 = shape.batch, shape.n_q_heads, torch.int32
+    strides, n = _pair(f, dev, k_new, v_new, shape), k_new.shape[3]
+    if path is None or path_len is None or path.dim() != 2 or (q is None) != (row_lse is None) or (k_out is None) != (v_out is None):
+        _refuse(f)
+    steps = path.shape[1]
+    code = _load().kvc_i4_tree_commit(
+        ctypes.byref(shape), _cache(f, dev, rows, shape), k_new.data_ptr(), v_new.data_ptr(), strides, n,
+        _dense(f, dev, path, i32, B * steps), _dense(f, dev, path_len, i32, B), steps,
+        None if q is None else q.data_ptr(), None if q is None else _rows(f, dev, q, shape, Hq, n),
+        _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n), _mods(f, dev, mods, shape), _f32(f, softmax_scale),
+        None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
+        None if k_out is None else _pair(f, dev, k_out, v_out, shape, steps),
+        _dense(f, dev, unit_status, i32, _units(shape)), _stream(stream, dev))
     if code:
         raise KvcError(f, code)
 

@@ -47,6 +47,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "i4_codes.cuh"
 #include "kvc_internal.cuh"
 #include "packed_math.cuh"
 
@@ -54,54 +55,11 @@ namespace kvc {
 
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTile = 32;                        // keys per warp tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;                     // log2 growth of the maximum that forces a rescale
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// D (16 x 8) += A (16 x 16) B (16 x 8), bf16 in, fp32 out.
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
-// The codes in bits 0..3 and 16..19 of w as a bf16 pair.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x43084308, 0x6a;" : "=r"(r) : "r"(w));      // (w & mask) ^ magic
-  asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0x43084308u));
-  return r;
-}
-
-// Scales of one key times `by`, as fp32.
-__device__ __forceinline__ void put_scales(float* to, uint2 s, float by) {
-  *reinterpret_cast<float4*>(to) =
-      make_float4(__uint_as_float(s.x << 16) * by, __uint_as_float(s.x & 0xffff0000u) * by, __uint_as_float(s.y << 16) * by,
-                  __uint_as_float(s.y & 0xffff0000u) * by);
-}
-__device__ __forceinline__ void put_scales(float* to, uint32_t s, float by) {
-  *reinterpret_cast<float2*>(to) = make_float2(__uint_as_float(s << 16) * by, __uint_as_float(s & 0xffff0000u) * by);
-}
-__device__ __forceinline__ void put_scales(float* to, uint16_t s, float by) { *to = __half2float(__ushort_as_half(s)) * by; }
 
 struct Unit {
   int u, b, l, g, n, R;

@@ -13,6 +13,7 @@
 // under the copies; one token's rows of 288 units appended and read back 5.8 us.
 #include <algorithm>
 
+#include "i4_codes.cuh"
 #include "kvc_internal.cuh"
 #include "packed_math.cuh"
 
@@ -20,78 +21,8 @@ namespace kvc {
 
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRowThreads = 256;
 constexpr int kBatch = 4;                        // rows of a thread whose loads are in flight together
-
-// Quantises the 8 elements of this lane (`LANES` adjacent lanes share a
-// scale): packed codes, and the scale's bits.
-//   scale = max / 7 rounded to the scale's format, code = rint(x / scale).
-// Both quotients are q0 = x y, q = q0 + (x - q0 b) y (Markstein) with y within
-// one ulp of 1 / b.  The codes equal those of IEEE division: checked for every
-// bf16 mantissa against every bf16 and fp16 scale mantissa with y one ulp off
-// either way; and so does the rounded scale, because a / 7 for a bf16 a is
-// never within an ulp of a tie of either format (checked for every a).  rint
-// is an addition of 1.5 x 2^23 (a conversion to integer runs at a quarter of
-// the rate); the eight sums, 8 larger than their codes, are packed by shifted
-// additions and the offset is taken out at the end.  Everything but the
-// packing works on two elements per instruction.
-// Scales that are subnormal or clipped (where the quotient may exceed 7.5)
-// take the slow way.
-template <bool ROW, int LANES>
-__device__ __forceinline__ uint32_t quantise8(const uint4& w, uint16_t* bits) {
-  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-  __nv_bfloat162 mx = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&r[0]));
-#pragma unroll
-  for (int i = 1; i < 4; ++i) mx = __hmax2(mx, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&r[i])));
-  float amax = fmaxf(__low2float(mx), __high2float(mx));
-#pragma unroll
-  for (int o = 1; o < LANES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-  float sc = div_by_recip(amax, 7.f, 0x1.24924ap-3f);       // the reciprocal of 7, rounded
-  uint16_t sb;
-  if (ROW) {
-    sb = __half_as_ushort(__float2half_rn(sc));
-    sc = __half2float(__ushort_as_half(sb));
-  } else {
-    sb = float_to_bf16_bits(sc);
-    sc = bf16_bits_to_float(sb);
-  }
-  if (!(amax > 0.f)) {                           // a group of zeros: codes 0, scale 1
-    sc = 1.f;
-    sb = ROW ? 0x3c00 : 0x3f80;
-  }
-  const bool fast = ROW ? sc >= 0x1p-14f && sc < 65504.f : recip_div_ok(sc);
-  if (__all_sync(kFull, fast)) {
-    const float y = rcp_approx(sc);
-    const uint64_t y2 = pair(y, y), nb2 = pair(-sc, -sc), round2 = pair(12582920.f, 12582920.f);
-    uint32_t pk = 0u - 0x3f400000u;                          // the exponents' part of the sum below
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t x2 = pair(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xffff0000u));
-      const uint64_t q0 = mul2(x2, y2);
-      float lo, hi;
-      unpair(add2(fma2(fma2(q0, nb2, x2), y2, q0), round2), &lo, &hi);
-      pk += (__float_as_uint(lo) << (8 * i)) + (__float_as_uint(hi) << (8 * i + 4));
-    }
-    *bits = sb;
-    return pk ^ 0x88888888u;
-  }
-  sc = 1.f;
-  if (amax > 0.f) {
-    const float s = __fdiv_rn(amax, 7.f);
-    if (ROW) sc = fmaxf(fminf(__half2float(__float2half_rn(s)), 65504.f), 0x1p-24f);
-    else sc = fmaxf(bf16_bits_to_float(float_to_bf16_bits(s)), __uint_as_float(0x00010000u));   // 2^-133
-  }
-  *bits = ROW ? __half_as_ushort(__float2half_rn(sc)) : float_to_bf16_bits(sc);
-  uint32_t pk = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = __uint_as_float(i & 1 ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
-    const int q = max(-7, min(7, amax > 0.f ? __float2int_rn(__fdiv_rn(x, sc)) : 0));
-    pk |= static_cast<uint32_t>(q & 0xf) << (4 * i);
-  }
-  return pk;
-}
 
 // The first free slot and number of new rows of unit u; n = 0 with `status`
 // set if they cannot be appended.
@@ -194,32 +125,6 @@ __global__ void i4_advance_kernel(const I4AppendArgs a) {
   wait_for_previous_kernel();
   const int u = blockIdx.x * blockDim.x + threadIdx.x;
   if (u < a.U) advance(a, u, room_of(a, u));
-}
-
-// The 8 codes of a word times their scale, as bf16 in element order, each
-// rounded once: codes are exact in bf16 (136 + code - 136), a bf16 scale
-// multiplies them in bf16, an fp16 scale in fp32.
-__device__ __forceinline__ uint4 dequantise8(uint32_t w, uint16_t scale, bool row_mode) {
-  uint32_t c[4];                                 // elements (0,4), (1,5), (2,6), (3,7)
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t x = ((w >> (4 * k)) & 0x000f000fu) ^ 0x43084308u;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c[k]) : "r"(x), "r"(0x43084308u));
-  }
-  if (row_mode) {
-    const float s = __half2float(__ushort_as_half(scale));
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(c[k] << 16) * s, __uint_as_float(c[k] & 0xffff0000u) * s);
-      c[k] = *reinterpret_cast<const uint32_t*>(&p);
-    }
-  } else {
-    const uint32_t s2 = scale * 0x10001u;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(c[k]) : "r"(s2));
-  }
-  return make_uint4(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410), __byte_perm(c[0], c[1], 0x7632),
-                    __byte_perm(c[2], c[3], 0x7632));
 }
 
 template <int D>

@@ -1267,6 +1267,52 @@ kvc_status kvc_i4_tree_attn(const kvc_shape* shape, const kvc_i4_rows* rows, con
   return launch_tree(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
+kvc_status kvc_i4_tree_commit(const kvc_shape* shape, const kvc_i4_rows* rows, const void* k_new, const void* v_new,
+                              const kvc_strides* new_strides, int32_t n, const int32_t* path, const int32_t* path_len,
+                              int32_t max_path, const void* q, const kvc_strides* q_strides, const float* row_lse,
+                              const kvc_score_mods* mods, float softmax_scale, void* k_out, void* v_out,
+                              const kvc_strides* out_strides, int32_t* unit_status, kvc_stream stream) {
+  kvc_status st = check_tree(shape, rows, n);
+  if (st != KVC_OK) return st;
+  if (max_path < 1 || max_path > n) return KVC_ERR_INVALID_ARG;
+  if (max_path > KVC_TREE_MAX_PATH) return KVC_ERR_UNSUPPORTED;
+  if (!k_new || !v_new || !path || !path_len || (k_out == nullptr) != (v_out == nullptr)) return KVC_ERR_INVALID_ARG;
+  if (q && (!row_lse || !rows->mass)) return KVC_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(q, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return KVC_ERR_INVALID_ARG;
+  TreeCommitArgs a = {};
+  if ((st = tensor_strides(shape, shape->n_kv_heads, n, new_strides, &a.news)) != KVC_OK) return st;
+  if (q && (st = tensor_strides(shape, shape->n_q_heads, n, q_strides, &a.qs)) != KVC_OK) return st;
+  if (k_out && (st = tensor_strides(shape, shape->n_kv_heads, max_path, out_strides, &a.outs)) != KVC_OK) return st;
+  if ((st = check_mods(mods, &a.mods)) != KVC_OK) return st;
+  DevInfo info;
+  if ((st = check_device(&info)) != KVC_OK) return st;
+  if (!(softmax_scale > 0.f)) softmax_scale = 1.0f / sqrtf(static_cast<float>(shape->head_dim));
+  a.U = static_cast<int32_t>(n_units(shape));
+  a.L = shape->n_layers;
+  a.Hkv = shape->n_kv_heads;
+  a.B = shape->batch;
+  a.G = shape->n_q_heads / shape->n_kv_heads;
+  a.d = shape->head_dim;
+  a.n = n;
+  a.max_path = max_path;
+  a.scale = softmax_scale;
+  a.rows = *rows;
+  a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  a.path = path;
+  a.path_len = path_len;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.row_lse = row_lse;
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  a.unit_status = unit_status;
+  // one round of the blocks that the SMs hold, each warp of four with a tile of 32 keys at least
+  const int64_t want = std::min<int64_t>(4LL * info.sms / a.U, (static_cast<int64_t>(rows->capacity) + 127) / 128);
+  a.splits = static_cast<int32_t>(std::max<int64_t>(1, want));
+  return launch_tree_commit(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
 kvc_status kvc_rope_tables(int64_t max_pos, int32_t rotary_dim, double base, const kvc_rope_scaling* scaling,
                            float* rope_cos, float* rope_sin, kvc_stream stream) {
   if (max_pos < 0 || max_pos > 0x7fffffffLL || rotary_dim < 16 || rotary_dim > 128 || rotary_dim % 16) return KVC_ERR_INVALID_ARG;

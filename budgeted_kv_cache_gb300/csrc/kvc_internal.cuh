@@ -323,6 +323,25 @@ struct TreeArgs {
   int32_t* unit_status;        // optional [U]
 };
 
+// The accepted path of such a tree.
+struct TreeCommitArgs {
+  int32_t U, L, Hkv, B, G, d, n, max_path;
+  float scale;
+  kvc_i4_rows rows;
+  kvc_strides qs, news, outs;  // element strides
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  const int32_t* path;         // [B][max_path]
+  const int32_t* path_len;     // [B]
+  const __nv_bfloat16* q;      // optional: mass is added
+  const float* row_lse;        // [B][L][H_q][n]
+  Mods mods;
+  __nv_bfloat16* k_out;        // optional
+  __nv_bfloat16* v_out;
+  int32_t* unit_status;        // optional [U]
+  int32_t splits;              // blocks that share a unit's cached rows
+};
+
 struct I4EvictArgs {
   int32_t U, d, budget, n_sink, n_recent;
   int32_t max_moves;           // entries of each list
@@ -393,6 +412,7 @@ cudaError_t launch_i4_read(const I4ReadArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_evict(const I4EvictArgs& a, cudaStream_t stream);
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t stream);
 cudaError_t launch_rope_tables(const RopeTableArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 size_t effect_smem_bytes(int Rp, int n_stages);

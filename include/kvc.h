@@ -22,6 +22,7 @@
  *   kvc_i4_evict                in-place eviction of the rows of least mass
  *   kvc_i4_tree_attn            attention of a tree of drafted tokens over the
  *                               4-bit cache
+ *   kvc_i4_tree_commit          the accepted path's rows and mass into it
  *   kvc_rope_tables, kvc_rope   rotary tables, and fresh queries and keys
  *                               rotated by them
  *
@@ -789,6 +790,47 @@ kvc_status kvc_i4_tree_attn(const kvc_shape* shape, const kvc_i4_rows* rows, con
                             const kvc_score_mods* mods, float softmax_scale, void* out,
                             const kvc_strides* out_strides, float* row_lse, int32_t* unit_status,
                             void* workspace, size_t workspace_bytes, kvc_stream stream);
+
+/* ------------------------------------------------------------------------
+ * kvc_i4_tree_commit -- puts the accepted path of a drafted tree into the
+ * 4-bit cache: the rows of its nodes are quantised (as kvc_i4_append does)
+ * into slots count[u].. of every unit, at positions next_pos[u].., and count
+ * and next_pos advance.  With q, the softmax weights of the path's queries,
+ * and of no other node, are added to the mass (PACE Sec. 2: H2O's cumulative
+ * score): the rows in use get
+ *
+ *   mass[u][r] += sum over the path's nodes i and the G heads of
+ *                 exp(x_hir - row_lse[h][i]),
+ *
+ * and the new rows start with what they get from the path's nodes from their
+ * own on (over the bf16 keys that the attention used).
+ *
+ * k_new, v_new, n  as in kvc_i4_tree_attn.  Rows of the path are finite.
+ * path     int32 [B][max_path]: the accepted nodes, one without a parent
+ *          first, then each a child of the one before it (that is not
+ *          checked).  1 <= max_path <= n, KVC_TREE_MAX_PATH at most.
+ * path_len int32 [B], limited to [0, max_path]; 0 leaves a sequence as it was.
+ * q, row_lse, mods, softmax_scale  as given to kvc_i4_tree_attn, and its
+ *          row_lse; q NULL: no mass is added, the new rows start with 0.
+ *          With q, rows->mass is required.
+ * k_out, v_out  optional (both or none) bf16 [B][L][H_kv][max_path][d], strides
+ *          as in kvc_strides: the new rows as the cache holds them (code *
+ *          scale, rounded once), for a bf16 store of recent rows beside it.
+ *          Rows at or past path_len[b] are left as they were.
+ * unit_status  optional int32 [U], only errors are written: KVC_UNIT_FULL if
+ *          the rows do not fit, KVC_UNIT_BAD_INDEX if a node of the path is
+ *          outside [0, n) or count[u] outside [0, capacity]; such a unit is
+ *          left as it was.
+ * ---------------------------------------------------------------------- */
+enum { KVC_TREE_MAX_PATH = 64 };
+
+kvc_status kvc_i4_tree_commit(const kvc_shape* shape, const kvc_i4_rows* rows, const void* k_new,
+                              const void* v_new, const kvc_strides* new_strides, int32_t n,
+                              const int32_t* path, const int32_t* path_len, int32_t max_path,
+                              const void* q, const kvc_strides* q_strides, const float* row_lse,
+                              const kvc_score_mods* mods, float softmax_scale, void* k_out,
+                              void* v_out, const kvc_strides* out_strides, int32_t* unit_status,
+                              kvc_stream stream);
 
 /* ------------------------------------------------------------------------
  * CommitKV lifecycle-aware retirement ("CommitKV: Lifecycle-Aware KV Cache

@@ -91,7 +91,7 @@ class Problem:
                         continue
                     want = tree_attention(self.rows, u, self.q[b, l, here, :m].double(), self.k[b, l, h, :m].double(),
                                           self.v[b, l, h, :m].double(), self.parents[b][:m], scale or 1 / math.sqrt(self.d),
-                                          self.d, slopes=None if slopes is None else slopes[here], prefix=prefix[b], **mods)
+                                          slopes=None if slopes is None else slopes[here], prefix=prefix[b], **mods)
                     close(out[:, :m], want[0], want[3], f"out of unit {u}")
                     close(lse[:, :m], want[1], want[4], f"lse of unit {u}")
         assert self.status.tolist() == [status] * self.status.numel()

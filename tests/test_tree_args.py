@@ -1,4 +1,4 @@
-"""kvc_i4_tree_attn refuses what it cannot do before it looks for a device (CPU)."""
+"""kvc_i4_tree_attn and kvc_i4_tree_commit refuse what they cannot do before they look for a device (CPU)."""
 import ctypes
 
 import pytest
@@ -66,6 +66,35 @@ def test_attention(lib):
     assert lib.kvc_i4_tree_attn_workspace_bytes(shape(), rows(), kvc.TREE_MAX_NODES + 1) == 0
 
 
+def commit(lib, sh=None, r=None, k=A, v=A, ks=None, n=8, path=A, size=A, steps=4, q=A, qs=None, lse=A, mods=None, ko=A, vo=A,
+           os=None):
+    return lib.kvc_i4_tree_commit(sh or shape(), r or rows(), k, v, ks, n, path, size, steps, q, qs, lse,
+                                  ctypes.byref(mods) if mods else None, 0.0, ko, vo, os, None, None)
+
+
+@pytest.mark.parametrize("bad", BAD_ROWS, ids=lambda b: "_".join(b))
+def test_rows_of_a_commit(lib, bad):
+    assert commit(lib, r=rows(**bad)) == INVALID
+
+
+def test_commit(lib):
+    assert commit(lib, sh=shape(d=96)) == UNSUPPORTED and commit(lib, sh=shape(Hq=3)) == INVALID
+    assert commit(lib, n=0) == INVALID and commit(lib, n=kvc.TREE_MAX_NODES + 1) == UNSUPPORTED
+    assert commit(lib, steps=0) == INVALID and commit(lib, steps=9) == INVALID and commit(lib, steps=-1) == INVALID
+    assert commit(lib, n=100, steps=kvc.TREE_MAX_PATH + 1) == UNSUPPORTED
+    assert commit(lib, r=rows(capacity=0x7fff0001)) == UNSUPPORTED
+    for bad in ("k", "v", "path", "size", "lse", "ko", "vo"):
+        assert commit(lib, **{bad: None}) == INVALID
+    for bad in ("k", "v", "q", "ko", "vo"):
+        assert commit(lib, **{bad: A + 8}) == INVALID
+    assert commit(lib, r=rows(mass=None)) == INVALID             # weights with nowhere to go
+    for bad in ("ks", "qs", "os"):
+        assert commit(lib, **{bad: st(800, 0, 801, 64)}) == INVALID
+        assert commit(lib, **{bad: st(0, 0, 6400, 64)}) == INVALID
+    for bad in (kvc.kvc_score_mods(-1.0, None, 0, None), kvc.kvc_score_mods(0.0, None, -1, None)):
+        assert commit(lib, mods=bad) == INVALID
+
+
 def test_binding_refuses_tensors_on_the_host():
     s = kvc.make_shape(1, 1, 2, 2, 64, 1)
     x, parent = torch.zeros(1, 1, 2, 8, 64, dtype=torch.bfloat16), torch.zeros(1, 8, dtype=torch.int32)
@@ -74,3 +103,6 @@ def test_binding_refuses_tensors_on_the_host():
         kvc.kvc_i4_tree_attn(s, r, x, x, x, parent, x.clone())
     with pytest.raises(kvc.KvcError):
         kvc.kvc_i4_tree_attn_workspace_bytes(s, r, 2 ** 32 + 1)
+    path, size = torch.zeros(1, 2, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    with pytest.raises(kvc.KvcError):
+        kvc.kvc_i4_tree_commit(s, r, x, x, path, size)

@@ -9,7 +9,7 @@ import numpy as np
 import torch
 
 import oracle as o
-from attn_reference import attend
+from attn_reference import U, attend
 
 
 def held(codes, scale, d):
@@ -38,8 +38,8 @@ def trees(kind, n, seed=0):
     return [int(r.randint(max(-1, i - 9), i)) if i else -1 for i in range(n)]
 
 
-def tree_attention(rows, u, q, k_new, v_new, parent, scale, mode_d, softcap=0.0, slopes=None, window=0, prefix=0):
-    """One unit: q [G][n][d], k_new, v_new [n][d] (64 bits, nodes only).  out, lse and their bounds, [G][n]."""
+def heads_of(rows, u, q, k_new, v_new, parent, scale, softcap=0.0, slopes=None, window=0, prefix=0):
+    """One unit: q [G][n][d], k_new, v_new [n][d] (64 bits, nodes only): what attend gives for each head, and the values."""
     G, n, d = q.shape
     count, nxt = int(rows.count[u]), int(rows.next_pos[u])
     way = lines(parent)
@@ -52,9 +52,23 @@ def tree_attention(rows, u, q, k_new, v_new, parent, scale, mode_d, softcap=0.0,
     dist = at[:, None] - pos
     if window:
         seen = seen & ((dist < window) | (pos < prefix))
-    k = torch.cat((held(rows.k[u, :count], rows.k_scale[u, :count], mode_d), k_new))
-    v = torch.cat((held(rows.v[u, :count], rows.v_scale[u, :count], mode_d), v_new))
-    got = [attend(q[h], k, v, scale, seen, dist, softcap, None if slopes is None else float(slopes[h])) for h in range(G)]
+    k = torch.cat((held(rows.k[u, :count], rows.k_scale[u, :count], d), k_new))
+    v = torch.cat((held(rows.v[u, :count], rows.v_scale[u, :count], d), v_new))
+    return [attend(q[h], k, v, scale, seen, dist, softcap, None if slopes is None else float(slopes[h])) for h in range(G)], v
+
+
+def tree_attention(rows, u, q, k_new, v_new, parent, scale, **mods):
+    """out, lse and their bounds, [G][n]."""
+    got, v = heads_of(rows, u, q, k_new, v_new, parent, scale, **mods)
     got = [torch.stack([x[i] for x in got]) for i in range(5)]
-    got[3] = got[3] + k.shape[0] * 2.0 ** -25 * v.abs().max()
+    got[3] = got[3] + v.shape[0] * 2.0 ** -25 * v.abs().max()
     return got
+
+
+def path_mass(rows, u, q, k_new, scale, **mods):
+    """Of a path (q [G][m][d], k_new [m][d]): log-sum-exps [G][m], the weight that every cached and path row gets from
+    its queries, and how far a sum of fp32 weights may be from it (in any order)."""
+    m = q.shape[1]
+    got, _ = heads_of(rows, u, q, k_new, k_new, list(range(-1, m - 1)), scale, **mods)
+    w = sum(x[2].sum(0) for x in got)
+    return torch.stack([x[1] for x in got]), w, sum(x[5].sum(0) for x in got) + (len(got) * m + 8) * U * w
