@@ -501,14 +501,28 @@ kvc_status check_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n) {
 }
 
 struct TreePlan {
-  size_t ws_total = 0;
+  int32_t block_rows = 0, n_blocks = 0, splits = 1;
+  size_t ws_ml = 0, ws_total = 0;
 };
 
 kvc_status plan_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n, TreePlan* p) {
-  const kvc_status st = check_tree(s, r, n);
+  kvc_status st = check_tree(s, r, n);
   if (st != KVC_OK) return st;
   DevInfo info;
-  return check_device(&info);
+  if ((st = check_device(&info)) != KVC_OK) return st;
+  const int64_t U = n_units(s), rows = static_cast<int64_t>(n) * (s->n_q_heads / s->n_kv_heads);
+  const int64_t tiles = (static_cast<int64_t>(r->capacity) + kTileTokens - 1) / kTileTokens + (n + kTileTokens - 1) / kTileTokens;
+  p->block_rows = rows > 128 ? 256 : 128;
+  p->n_blocks = static_cast<int32_t>((rows + p->block_rows - 1) / p->block_rows);
+  const int64_t items = U * p->n_blocks;
+  if (items > (1 << 28)) return KVC_ERR_UNSUPPORTED;
+  p->splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(info.sms / items, tiles), 256)));
+  if (p->splits > 1) {
+    const size_t parts = static_cast<size_t>(U) * rows * p->splits;
+    p->ws_ml = (parts * sizeof(float2) + 255) / 256 * 256;
+    p->ws_total = p->ws_ml + parts * s->head_dim * sizeof(float);
+  }
+  return KVC_OK;
 }
 
 // Turns per position of every pair, in 2^-64 (whole turns dropped), and the tables' magnitude; false: not a valid scaling.
@@ -1264,6 +1278,19 @@ kvc_status kvc_i4_tree_attn(const kvc_shape* shape, const kvc_i4_rows* rows, con
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = row_lse;
   a.unit_status = unit_status;
+  a.stall_unit = g_score_stall_unit.load(std::memory_order_relaxed);   // failure test hook (-1: none)
+  a.block_rows = p.block_rows;
+  a.n_blocks = p.n_blocks;
+  a.splits = p.splits;
+  if (p.splits > 1) {
+    a.part_ml = static_cast<float2*>(workspace);
+    a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.ws_ml);
+  }
+  a.by_splits = FastDiv::of(a.splits);
+  a.by_units = FastDiv::of(a.U);
+  a.by_heads = FastDiv::of(a.Hkv);
+  a.by_layers = FastDiv::of(a.L);
+  a.by_group = FastDiv::of(a.G);
   return launch_tree(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 

@@ -71,6 +71,7 @@
 
 #include "kvc_internal.cuh"
 #include "packed_math.cuh"
+#include "tc_attn.cuh"
 
 namespace kvc {
 
@@ -79,7 +80,6 @@ namespace {
 constexpr int kThreads = 384;                    // three warpgroups of 168 registers a thread at launch
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;                       // keys per tile
-constexpr int kChunkBytes = 128 * 128;           // 128 rows x 64 bf16, 128-byte swizzle
 constexpr uint32_t kTmemCols = 512;              // S0, S1, O0, O1 of 128 columns each
 constexpr uint32_t kOCol = 256;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
@@ -112,123 +112,9 @@ __device__ __forceinline__ void tma_store_5d(const CUtensorMap* map, uint32_t sr
       : "memory");
 }
 
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
 // Until the stores of this thread have read their sources.
 __device__ __forceinline__ void tma_store_wait() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-
-// The MMA warp stays converged and lets one elected lane issue, by predicate:
-// under `if (lane == 0)` the compiler keeps descriptors in per-thread
-// registers and moves each to the uniform ones in front of every instruction
-// (58 cycles an MMA measured, 118 in this kernel, whatever its size; 30 for
-// 128 x 64 x 16 this way, which is the tensor core's own time).
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, e;\n\t}"
-      : "=r"(p));
-  return p;
-}
-
-// D[tmem] (+)= A[smem] * B[smem]^T.
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate, uint32_t elected) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
-      : "memory");
-}
-
-// D[tmem] (+)= A[tmem] * B[smem]: A bf16, two elements of K per column.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate, uint32_t elected) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
-      : "memory");
-}
-
-__device__ __forceinline__ void commit(uint32_t bar, uint32_t elected) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "setp.ne.b32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-      "r"(elected)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ bool try_once(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Bounded wait by a whole warp, with one answer for all lanes (what follows is
-// executed by the warp together).
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (__all_sync(0xffffffffu, try_once(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
-}
-
-// Bounded wait that goes on after an abort: for copies and products in flight.
-__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return;
-  }
-}
-
-// Descriptor of an MN-major operand in 128-byte swizzle: 64 elements along N
-// per 128-byte row, rows along K, 8 rows 1024 bytes, the next 64 elements
-// along N kChunkBytes further.
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(kChunkBytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
-// Bits [lo, hi) of a 32-bit word, either end outside it allowed.
-__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
-  lo = max(lo, 0);
-  hi = min(hi, 32);
-  if (lo >= hi) return 0u;
-  return (0xffffffffu >> (32 - (hi - lo))) << lo;
 }
 
 // What an item covers.
@@ -277,10 +163,6 @@ __device__ __forceinline__ Item make_item(const PromptArgs& a, int id) {
   t.i1 = t.split + 1 == a.splits ? t.n : static_cast<int>(a.by_splits.div(static_cast<uint32_t>(t.n) * (split + 1)));
   return t;
 }
-
-// The same value in every lane, known as such to the compiler (uniform
-// registers, and no divergence after a branch on it).
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ Item uniform_item(const Item& from) {
   static_assert(sizeof(Item) % 4 == 0, "an Item is ints");
@@ -1087,7 +969,10 @@ cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const C
     return bias ? go(prompt_kernel<D, true, true, false>) : go(prompt_kernel<D, true, false, false>);
   };
   const cudaError_t e = a.d == 128 ? go_capped(std::integral_constant<int, 128>{}) : go_capped(std::integral_constant<int, 64>{});
-  if (e != cudaSuccess || a.splits == 1) return e;
+  return e != cudaSuccess || a.splits == 1 ? e : launch_prompt_merge(a, stream);
+}
+
+cudaError_t launch_prompt_merge(const PromptArgs& a, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.U) * a.n_q * a.G;
   const unsigned blocks = static_cast<unsigned>((rows + 7) / 8);
   return launch_after(a.d == 128 ? prompt_merge_kernel<128> : prompt_merge_kernel<64>, blocks, 256, 0, stream, a);
