@@ -516,7 +516,7 @@ kvc_status plan_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n, TreePl
   p->n_blocks = static_cast<int32_t>((rows + p->block_rows - 1) / p->block_rows);
   const int64_t items = U * p->n_blocks;
   if (items > (1 << 28)) return KVC_ERR_UNSUPPORTED;
-  p->splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(info.sms / items, tiles), 256)));
+  p->splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(info.sms / items, tiles), 128)));
   if (p->splits > 1) {
     const size_t parts = static_cast<size_t>(U) * rows * p->splits;
     p->ws_ml = (parts * sizeof(float2) + 255) / 256 * 256;

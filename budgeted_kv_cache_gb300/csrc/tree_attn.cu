@@ -10,10 +10,10 @@
 //
 // Both products run on the tensor cores from operands that are exact: code *
 // scale has 3 + 8 bits and an fp16 number 11, so the rows are turned into fp16,
-// scaled by a power of two per tile that keeps them within its range (2^-ek for
+// scaled by a power of two per 32 rows that keeps them within its range (2^-ek for
 // keys, 2^-ev for values; it is taken back in fp32: 2^ek goes into the softmax
 // scale, 2^ev into the running maximum).  Elements more than 2^24 below the
-// tile's largest lose bits to the format's end.  A scale per row in fp16 has 11
+// largest of their 32 rows lose bits to the format's end.  A scale per row in fp16 has 11
 // bits itself: there the operands are the plain codes, and the scales multiply
 // the scores and the weights in fp32.  Queries are scaled to fp16 per row alike;
 // they, and the tree's rows, come in 8 bits.
@@ -35,15 +35,15 @@
 // walk up.  With a window, tiles that no row sees are not read: the warps that
 // turn rows into operands decide, and say so to the others tile by tile.
 //
-// Warp roles (16 warps): 0-3 and 4-7 softmax of stream 0 and 1 (176 registers),
-// 8-11 operands (104; a tile's codes on their way in registers while the one
-// before is turned, tiles behind them prefetched to L2), 12 tensor memory and
-// MMA issuer (56): 176 + 176 + 104 + 56 = 4 x 128, what the block was launched
-// with.  Every wait is bounded; one that gives up raises a shared abort flag, the
-// unit is marked KVC_UNIT_TIMEOUT and the block ends.
+// Warp roles (20 warps): 0-3 and 4-7 softmax of stream 0 and 1 (160 registers),
+// 8-11 make the keys' operands and 12-15 the values' (56; a quarter of every tile
+// each), 16 tensor memory and MMA issuer (48): 2 x 160 + 2 x 56 + 48 = 5 x 96, what
+// the block was launched with.  Every wait is bounded; one that gives up raises a
+// shared abort flag, the unit is marked KVC_UNIT_TIMEOUT and the block ends.
 #include <algorithm>
 #include <type_traits>
 
+#include "i4_codes.cuh"
 #include "kvc_internal.cuh"
 #include "packed_math.cuh"
 #include "tc_attn.cuh"
@@ -52,38 +52,30 @@ namespace kvc {
 
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;                       // keys per tile
 constexpr uint32_t kTmemCols = 512;              // S0, S1, O0, O1 of 128 columns each
 constexpr uint32_t kOCol = 256;
-constexpr int kOperandWarp = 8, kMmaWarp = 12;   // the first of four; the only one
+constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16;        // four, four, one
 constexpr int kStages = 2;                       // key tiles, and value tiles, in shared memory
 constexpr int kSlots = 4;                        // tiles whose description is held
-constexpr int kAhead = 4;                        // tiles prefetched to L2 in front of the registers' own
+constexpr int kAhead = 4;                        // tiles prefetched to L2 behind the one on its way
+constexpr int kNoValues = -40;                   // exponent of 32 rows whose values are all zero: below any that matter
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;                     // log2 growth of the maximum that forces a rescale
 
-// What the operand warps say about a tile.
-struct Tile {
-  int j0;                      // its first key: a cached row's slot, or a node
-  int tree;                    // the tree's own rows
-  int ek, ev;                  // operands are rows times 2^-ek, 2^-ev
-  int p_min;                   // smallest position
-};
-
 struct Bars {
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-  uint64_t sfull[2], phalf[2], pfull[2], odone[2], qfull[2], done;
+  uint64_t efull[kStages], sfull[2], phalf[2], pfull[2], odone[2], qfull[2], done;
   uint32_t tmem;
   int abort_flag;
   int total;                   // tiles of this item, once that is known
-  int e_ref;                   // ev of the first of them
+  int e_ref;                   // ev of the first 32 rows of the first of them
   int tiles[2];                // of each stream
-  uint32_t top[kSlots][4][2];  // largest key and value scale that each operand warp met
-  Tile tile[kSlots];
+  int j0[kSlots];              // a tile's first slot, or -1 - its first node
+  alignas(16) int ek[kSlots][4], ev[kSlots][4];      // operands are keys times 2^-ek and values times 2^-ev, per 32 rows
   int8_t q_exp[256];           // queries are rows times 2^-q_exp
   alignas(16) int32_t pos[kSlots][kKeys];
   alignas(16) float ks[kSlots][kKeys], vs[kSlots][kKeys];    // scale per row: of keys; of values times 2^-ev
@@ -92,7 +84,8 @@ struct Bars {
 template <int D>
 struct Cfg {
   static constexpr int kTile = D / 64 * kChunkBytes;         // a Q, K or V tile
-  static constexpr int kSmem = (2 + 2 * kStages) * kTile + 1024 /* alignment */ + sizeof(Bars);
+  static constexpr int kRaw = 32 * (D / 2) + 32 * (D / 16);  // codes and scales of 32 rows
+  static constexpr int kSmem = (2 + 2 * kStages) * kTile + 8 * kRaw + 1024 /* alignment */ + sizeof(Bars);
 };
 static_assert(Cfg<128>::kSmem <= 232448, "shared memory of a block");
 
@@ -120,11 +113,11 @@ __device__ __forceinline__ Item make_item(const TreeArgs& a, int id) {
   const int n = a.n_nodes ? clamp_count(a.n_nodes[t.b], a.n) : a.n;
   t.row0 = qb * a.block_rows;
   t.rows = max(0, min(a.block_rows, n * a.G - t.row0));
-  t.nodes = t.rows > 0 ? (t.row0 + t.rows - 1) / a.G + 1 : 0;
+  t.nodes = t.rows > 0 ? static_cast<int>(a.by_group.div(t.row0 + t.rows - 1)) + 1 : 0;
   t.cached = (t.count + kKeys - 1) / kKeys;
-  const int64_t all = t.cached + (t.nodes + kKeys - 1) / kKeys;
-  t.i0 = static_cast<int>(all * split / a.splits);
-  t.i1 = static_cast<int>(all * (split + 1) / a.splits);
+  const uint32_t all = t.cached + (t.nodes + kKeys - 1) / kKeys;
+  t.i0 = static_cast<int>(a.by_splits.div(all * split));             // tiles < 2^24 + 8, splits < 256
+  t.i1 = static_cast<int>(a.by_splits.div(all * (split + 1)));
   return t;
 }
 
@@ -137,9 +130,6 @@ __device__ __forceinline__ int parent_of(const int32_t* parent, int i, bool* bad
 }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(max(-126, min(127, e)) + 127) << 23); }
-
-// x 2^e for |e| up to 252, in two exact steps.
-__device__ __forceinline__ float times_pow2(float x, int e) { return x * pow2(e >> 1) * pow2(e - (e >> 1)); }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
@@ -159,10 +149,10 @@ __device__ __forceinline__ uint4 codes_to_half(uint32_t w, uint32_t s, uint32_t 
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// Eight bf16 elements times 2^-e in the same order.
-__device__ __forceinline__ uint4 bf16_to_half(const uint4& w, int e) {
+// Eight bf16 elements in the same order, times two powers of two.
+__device__ __forceinline__ uint4 bf16_to_half(const uint4& w, float by0, float by1) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-  auto at = [&](int i) { return times_pow2(__uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16), -e); };
+  auto at = [&](int i) { return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16) * by0 * by1; };
   return make_uint4(pack_half2(at(0), at(4)), pack_half2(at(1), at(5)), pack_half2(at(2), at(6)), pack_half2(at(3), at(7)));
 }
 
@@ -185,228 +175,201 @@ __device__ __forceinline__ uint4* piece(uint8_t* tile, int r, int c) {
 
 // ---------------------------------------------------------------- operand warps
 
-// Turns the item's rows into operand tiles, keys one tile ahead of values.
+// One warp turns a quarter (32 rows) of every tile of the item's keys (v = false) or values into operands; nothing but
+// the tiles' barriers joins it with others.  The next tile's codes are on their way to the warp's own shared memory
+// while those in registers are turned, and tiles behind that one to L2.
 template <int D, bool ROW, bool MODS>
-__device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, Bars& s, uint8_t* sk, uint8_t* sv) {
+__device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, Bars& s, uint8_t* ring, uint8_t* raw, bool v) {
   using C = Cfg<D>;
-  constexpr int CH = D / 32;                     // 16-byte pieces of codes per row
-  constexpr int N = CH;                          // pieces of a thread per tile (128 threads, 128 rows)
-  const int tid = threadIdx.x - kOperandWarp * 32, warp = tid >> 5, lane = tid & 31;
+  constexpr int CH = D / 32;                     // 16-byte pieces of codes per row, one to a lane in turn
+  using Scales = typename std::conditional<ROW, uint16_t, typename std::conditional<D == 128, uint2, uint32_t>::type>::type;
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, first = quarter * 32;
   volatile int* abort_flag = &s.abort_flag;
+  uint64_t* const full = v ? s.vfull : s.kfull;
+  uint64_t* const empty = v ? s.vempty : s.kempty;
   const int64_t base = static_cast<int64_t>(t.u) * a.rows.capacity;
-  const uint8_t* codes[2] = {static_cast<const uint8_t*>(a.rows.k) + base * (D / 2), static_cast<const uint8_t*>(a.rows.v) + base * (D / 2)};
-  const uint16_t* scales[2] = {static_cast<const uint16_t*>(a.rows.k_scale) + base * (ROW ? 1 : CH),
-                               static_cast<const uint16_t*>(a.rows.v_scale) + base * (ROW ? 1 : CH)};
-  const int64_t new_at = t.b * a.news.batch + t.l * a.news.layer + t.g * a.news.head;
+  const uint8_t* const codes = static_cast<const uint8_t*>(v ? a.rows.v : a.rows.k) + (base + first) * (D / 2);
+  const Scales* const scales = static_cast<const Scales*>(v ? a.rows.v_scale : a.rows.k_scale) + base + first;
+  const uint16_t* const piece_scale = reinterpret_cast<const uint16_t*>(raw + 32 * (D / 2));
   const bool windowed = MODS && a.mods.window;
-  struct Raw {
-    uint4 w[N];
-    uint16_t sc[N];
-  };
-  // codes and scales of this thread's pieces of cached tile i; nothing behind the rows in use is read
-  auto load = [&](int which, int i, Raw& raw) {
-    const int left = t.count - i * kKeys;
-    const uint4* src = reinterpret_cast<const uint4*>(codes[which] + static_cast<int64_t>(i) * (kKeys * D / 2)) + tid;
-    const uint16_t* sc = scales[which] + static_cast<int64_t>(i) * (ROW ? kKeys : kKeys * CH);
+  // Copies of the quarter's codes of cached tile i, and its scales to a register: a row a lane.  Nothing behind the rows
+  // in use is read.
+  Scales sc = {};
+  auto load = [&](int i) {
+    const int left = t.count - i * kKeys - first;
+    const uint8_t* src = codes + static_cast<int64_t>(i) * (kKeys * D / 2);
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int p = k * 128 + tid;
+    for (int k = 0; k < CH; ++k) {
+      const int p = k * 32 + lane;
       const bool ok = p / CH < left;
-      raw.w[k] = ok ? src[k * 128] : make_uint4(0, 0, 0, 0);
-      raw.sc[k] = ok ? sc[ROW ? p / CH : p] : static_cast<uint16_t>(0);
-      // a piece of zeros tells nothing about the sizes of the others, whatever its scale
-      if ((raw.w[k].x | raw.w[k].y | raw.w[k].z | raw.w[k].w) == 0) raw.sc[k] = 0;
+      cp_async16(smem_u32(raw + p * 16), ok ? src + p * 16 : codes - first * (D / 2), ok);
     }
+    cp_async_commit();
+    sc = Scales{};
+    if (lane < left) sc = scales[static_cast<int64_t>(i) * kKeys + lane];
   };
   auto prefetch = [&](int i) {
-    if (i >= min(t.cached, t.i1)) return;
-    const int left = min(kKeys, t.count - i * kKeys);
-    // a line of codes per thread (64 lines of keys, 64 of values at d = 128), and the scales' lines
-    const int line = tid & 63, which = tid >> 6;
-    if (line * 128 < left * (D / 2)) prefetch_l2(codes[which] + static_cast<int64_t>(i) * (kKeys * D / 2) + line * 128);
-    if (line * 64 < left * (ROW ? 1 : CH)) prefetch_l2(scales[which] + static_cast<int64_t>(i) * (ROW ? kKeys : kKeys * CH) + line * 64);
+    const int left = min(32, t.count - i * kKeys - first);
+    if (i >= min(t.cached, t.i1) || left <= 0) return;
+    if (lane * 128 < left * (D / 2)) prefetch_l2(codes + static_cast<int64_t>(i) * (kKeys * D / 2) + lane * 128);
+    if (lane >= 30 && (lane - 30) * 128 < left * static_cast<int>(sizeof(Scales)))
+      prefetch_l2(reinterpret_cast<const uint8_t*>(scales + static_cast<int64_t>(i) * kKeys) + (lane - 30) * 128);
   };
-  auto store = [&](uint8_t* tile, const Raw& raw, int e) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int p = k * 128 + tid, key = p / CH, chunk = p % CH;
-      uint32_t sc = 0x3c003c00u;                 // a scale per row: the codes alone
-      if (!ROW) {
-        const float f = times_pow2(bf16_bits_to_float(raw.sc[k]), -e);
-        sc = pack_half2(f, f);
-      }
-      uint32_t m;
-      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(m) : "r"(sc), "r"(0xce00ce00u));          // -24
-      // lanes of the second 64 columns take their words in another order: eight lanes then meet every bank once
-      const bool far = D == 128 && (chunk & 2);
-      const uint32_t w[4] = {far ? raw.w[k].z : raw.w[k].x, far ? raw.w[k].w : raw.w[k].y, far ? raw.w[k].x : raw.w[k].z,
-                             far ? raw.w[k].y : raw.w[k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) *piece(tile, key, chunk * 4 + (far ? j ^ 2 : j)) = codes_to_half(w[j], sc, m);
-    }
-  };
-  // a tile of the tree: 16-byte pieces of bf16, each thread those of one column
-  constexpr int BP = D / 8;
-  auto tree_piece = [&](const __nv_bfloat16* x, int j0, int k) -> uint4 {
-    const int p = k * 128 + tid, key = j0 + p / BP;
-    if (key >= t.nodes) return make_uint4(0, 0, 0, 0);
-    return *reinterpret_cast<const uint4*>(x + new_at + static_cast<int64_t>(key) * a.news.token + (p % BP) * 8);
-  };
-  auto tree_top = [&](const __nv_bfloat16* x, int j0) {
-    uint32_t top = 0;
-#pragma unroll 8
-    for (int k = 0; k < BP; ++k) top = max(top, max_bits(tree_piece(x, j0, k)));
-    return top;
-  };
-  auto tree_store = [&](uint8_t* tile, const __nv_bfloat16* x, int j0, int e) {
-#pragma unroll 4
-    for (int k = 0; k < BP; ++k) {
-      const int p = k * 128 + tid;
-      *piece(tile, p / BP, p % BP) = bf16_to_half(tree_piece(x, j0, k), e);
-    }
-  };
-  // the walk over the item's tiles: cached ones in order, then the tree's from the last to the first
-  int at = t.i0, pos_here = 0;
+  // The walk over the item's tiles: cached ones in order (with a window those that some node sees), then the tree's from
+  // the last to the first.  Every warp walks alike.
+  int at = t.i0;
   auto next = [&]() -> int {
     for (; at < t.i1; ++at) {
-      if (!MODS || at >= t.cached) return at++;
-      const int j = at * kKeys + tid;
-      const bool mine = j < t.count;
-      const int p = mine ? a.rows.pos[base + j] : INT32_MAX;
-      if (windowed) {
-        // every warp looks at every position: four of them are four keys of a lane
-        bool seen = false;
+      if (!windowed || at >= t.cached) return at++;
+      bool seen = false;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int jj = at * kKeys + k * 32 + lane;
-          if (jj < t.count) {
-            const int q = a.rows.pos[base + jj];
-            seen |= t.next - q < a.mods.window || q < t.prefix;
-          }
+      for (int k = 0; k < 4; ++k) {
+        const int j = at * kKeys + k * 32 + lane;
+        if (j < t.count) {
+          const int p = a.rows.pos[base + j];
+          seen |= t.next - p < a.mods.window || p < t.prefix;
         }
-        if (!__any_sync(kFull, seen)) continue;
       }
-      pos_here = p;
-      return at++;
+      if (__any_sync(kFull, seen)) return at++;
     }
     return -1;
   };
-  // distance of the prefetches: without a window the tiles that follow each other
+  int cur = next();
+  if (cur >= 0 && cur < t.cached) load(cur);
+  // without a window the tiles follow each other
   if (!windowed)
-    for (int i = 0; i < kAhead; ++i) prefetch(t.i0 + 1 + i);
+    for (int i = 1; i <= kAhead; ++i) prefetch(t.i0 + i);
 
-  Raw rk, rv[2];
-  int cur = next();                              // the tile whose codes are in rk and rv[0]
-  int cur_pos = pos_here;
-  if (cur >= 0 && cur < t.cached) load(0, cur, rk), load(1, cur, rv[0]);
-  bool fail = false;
-  int e_v[2] = {0, 0}, id[2] = {-1, -1};         // of the tiles in flight between keys and values
-  // tile n's keys are made, then the values of tile n - 1
 #pragma unroll 1
-  for (int n0 = 0;; n0 += 2) {
-    bool end = false;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int n = n0 + h, slot = n & (kSlots - 1), st = n & 1;
-      const bool more = cur >= 0, tree = more && cur >= t.cached;
-      const int j0 = !more ? 0 : tree ? ((t.nodes + kKeys - 1) / kKeys - 1 - (cur - t.cached)) * kKeys : cur * kKeys;
-      // the largest scales of the tile, and with modifiers its smallest position
-      uint32_t tk = 0, tv = 0;
-      if (tree) {
-        tk = tree_top(a.k_new, j0);
-        tv = tree_top(a.v_new, j0);
-      } else if (more) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) tk = max(tk, static_cast<uint32_t>(rk.sc[k])), tv = max(tv, static_cast<uint32_t>(rv[h].sc[k]));
-      }
-      tk = __reduce_max_sync(kFull, tk);
-      tv = __reduce_max_sync(kFull, tv);
-      if (lane == 0) s.top[slot][warp][0] = tk, s.top[slot][warp][1] = tv;
-      fail = named_bar_or(2, 128, fail);         // one answer for the four warps
-      if (fail) return;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) tk = max(tk, s.top[slot][w][0]), tv = max(tv, s.top[slot][w][1]);
-      int ek = 0, ev = 0;
-      if (tree) {
-        ek = tk ? exponent_of(tk) - 13 : 0;      // the largest element below 2^14
-        ev = tv ? exponent_of(tv) - 13 : 0;
-      } else if (ROW) {
-        // 2^ev above the largest row scale
-        ev = tv ? static_cast<int>(max(1u, tv >> 10)) - 14 : 0;
-      } else {
-        ek = tk ? exponent_of(tk) - 10 : 0;      // the largest scale below 2^11: 24 of it and 7 of it fit
-        ev = tv ? exponent_of(tv) - 10 : 0;
-      }
-      if (more) {
-        if (!warp_wait(smem_u32(&s.kempty[st]), ((n >> 1) & 1) ^ 1, abort_flag)) fail = true;
-        if (!fail) {
-          if (tid == 0) {
-            s.tile[slot] = {j0, tree ? 1 : 0, ek, ev, 0};
-            if (n == 0) s.e_ref = ev;
-          }
-          if (MODS) {
-            int p = cur_pos;
-            if (tree) {
-              bool bad = false;
-              p = t.next;
-              if (j0 + tid < t.nodes)
-                for (int i = parent_of(a.parent + static_cast<int64_t>(t.b) * a.n, j0 + tid, &bad); i >= 0;
-                     i = parent_of(a.parent + static_cast<int64_t>(t.b) * a.n, i, &bad))
-                  ++p;
-            }
-            s.pos[slot][tid] = p;
-          }
-          if (ROW && !tree) {
-            const int j = j0 + tid;
-            s.ks[slot][tid] = j < t.count ? __half2float(__ushort_as_half(scales[0][j])) : 0.f;
-            // a row of zeros may have a scale above the others'
-            s.vs[slot][tid] = j < t.count ? fminf(__half2float(__ushort_as_half(scales[1][j])) * pow2(-ev), 2.f) : 0.f;
-          }
-          if (tree) tree_store(sk + st * C::kTile, a.k_new, j0, ek);
-          else store(sk + st * C::kTile, rk, ek);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s.kfull[st]));
-        }
-        id[h] = tree ? -2 - j0 : cur;
-        e_v[h] = ev;
-        if (!windowed && !tree) prefetch(cur + 1 + kAhead);
-        cur = next();
-        cur_pos = pos_here;
-        if (cur >= 0 && cur < t.cached) load(0, cur, rk);
-      } else {
-        id[h] = -1;
-        if (tid == 0) s.total = n;
-        // one more phase, without keys: the end
-        if (!warp_wait(smem_u32(&s.kempty[st]), ((n >> 1) & 1) ^ 1, abort_flag)) fail = true;
-        __syncwarp();
-        if (!fail && lane == 0) mbar_arrive(smem_u32(&s.kfull[st]));
-        end = true;
-      }
-      // values of the tile before
-      const int was = id[h ^ 1];
-      if (n > 0 && was != -1 && !fail) {
-        const int vst = (n - 1) & 1;
-        if (!warp_wait(smem_u32(&s.vempty[vst]), (((n - 1) >> 1) & 1) ^ 1, abort_flag)) {
-          fail = true;
-        } else {
-          if (was < -1) tree_store(sv + vst * C::kTile, a.v_new, -2 - was, e_v[h ^ 1]);
-          else store(sv + vst * C::kTile, rv[h ^ 1], e_v[h ^ 1]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s.vfull[vst]));
-        }
-      }
-      if (cur >= 0 && cur < t.cached) load(1, cur, rv[h ^ 1]);
-      if (end) return;
+  for (int n = 0;; ++n) {
+    const int slot = n & (kSlots - 1), st = n & 1;
+    const bool tree = cur >= t.cached;
+    auto wait_empty = [&] { return warp_wait(smem_u32(&empty[st]), ((n >> 1) & 1) ^ 1, abort_flag); };
+    if (cur < 0) {                               // the end: one more phase of the keys, without any
+      if (v || !wait_empty()) break;
+      if (threadIdx.x == kKeyWarp * 32) s.total = n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.kfull[st]));
+      break;
     }
+    uint8_t* const to = ring + st * C::kTile;
+    const int j0 = tree ? ((t.nodes + kKeys - 1) / kKeys - 1 - (cur - t.cached)) * kKeys : cur * kKeys;
+    auto publish = [&](int e, Scales own) {      // what the softmax needs of this quarter
+      if (v) {
+        if (ROW && !tree) {
+          const float f = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(&own)));
+          s.vs[slot][first + lane] = fminf(f * pow2(-e), 2.f);       // a row of zeros may have a scale above the others'
+        }
+        if (lane == 0) {
+          s.ev[slot][quarter] = e;
+          if (n == 0 && quarter == 0) s.e_ref = e;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.efull[st]));
+        return;
+      }
+      if (lane == 0) {
+        s.ek[slot][quarter] = e;
+        if (quarter == 0) s.j0[slot] = tree ? -1 - j0 : j0;
+      }
+      const int j = j0 + first + lane;
+      if (MODS) {
+        int p = 0;
+        if (!tree) {
+          if (j < t.count) p = a.rows.pos[base + j];
+        } else if (j < t.nodes) {
+          const int32_t* parent = a.parent + static_cast<int64_t>(t.b) * a.n;
+          bool bad = false;
+          p = t.next;
+          for (int i = parent_of(parent, j, &bad); i >= 0; i = parent_of(parent, i, &bad)) ++p;
+        }
+        s.pos[slot][first + lane] = p;
+      }
+      if (ROW && !tree) s.ks[slot][first + lane] = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(&own)));
+    };
+    if (!tree) {
+      // this tile's codes to registers, the next one's on their way
+      cp_async_wait<0>();
+      const Scales own = sc;
+      if (!ROW) *reinterpret_cast<Scales*>(raw + 32 * (D / 2) + lane * sizeof(Scales)) = own;
+      __syncwarp();
+      uint4 w[CH];
+      uint32_t scale[CH], top = 0;
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int p = k * 32 + lane;
+        w[k] = *reinterpret_cast<const uint4*>(raw + p * 16);
+        scale[k] = ROW ? __shfl_sync(kFull, static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&own)), p / CH) : piece_scale[p];
+        // A piece of zeros tells nothing about the sizes of the others, whatever its scale (the quantiser writes 1)
+        if ((w[k].x | w[k].y | w[k].z | w[k].w) == 0) scale[k] = 0;
+        top = max(top, scale[k]);
+      }
+      __syncwarp();
+      if (!windowed) prefetch(cur + 1 + kAhead);
+      cur = next();
+      if (cur >= 0 && cur < t.cached) load(cur);
+      top = __reduce_max_sync(kFull, top);
+      int e = v ? kNoValues : 0;                 // rows times 2^-e:
+      if (top && !ROW) e = exponent_of(top) - 10;                              // the largest scale below 2^11
+      else if (top && v) e = static_cast<int>(max(1u, top >> 10)) - 14;        // the largest row scale below 1
+      if (!wait_empty()) break;
+      publish(e, own);
+      const float by0 = pow2((-e) >> 1), by1 = pow2(-e - ((-e) >> 1));
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int p = k * 32 + lane, key = first + p / CH, chunk = p % CH;
+        uint32_t f = 0x3c003c00u, m;             // a scale per row: the codes alone
+        if (!ROW) {
+          const float x = __uint_as_float(scale[k] << 16) * by0 * by1;
+          f = pack_half2(x, x);
+        }
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(m) : "r"(f), "r"(0xce00ce00u));         // -24
+        // lanes of the second 64 columns take their words in another order: eight lanes then meet every bank once
+        const bool far = D == 128 && (chunk & 2);
+        const uint32_t x[4] = {far ? w[k].z : w[k].x, far ? w[k].w : w[k].y, far ? w[k].x : w[k].z, far ? w[k].y : w[k].w};
+        uint8_t* const row = to + (chunk >> 1) * kChunkBytes + key * 128;
+        const int place = ((chunk & 1) * 4 + (far ? 2 : 0)) ^ (key & 7);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(row + ((place ^ j) << 4)) = codes_to_half(x[j], f, m);
+      }
+    } else {
+      // the tree's rows, bf16, straight to their places; then turned there, each lane its own pieces
+      if (!wait_empty()) break;
+      const __nv_bfloat16* src = (v ? a.v_new : a.k_new) + t.b * a.news.batch + t.l * a.news.layer + t.g * a.news.head;
+      constexpr int BP = D / 8;
+      const int c = lane % BP, r0 = first + lane / BP;
+#pragma unroll 4
+      for (int r = 0; r < 32; r += 32 / BP) {
+        const bool ok = j0 + r0 + r < t.nodes;
+        cp_async16(smem_u32(piece(to, r0 + r, c)), ok ? src + static_cast<int64_t>(j0 + r0 + r) * a.news.token + c * 8 : src, ok);
+      }
+      cp_async_commit();
+      cur = next();
+      cp_async_wait<0>();
+      uint32_t top = 0;
+#pragma unroll 4
+      for (int r = 0; r < 32; r += 32 / BP) top = max(top, max_bits(*piece(to, r0 + r, c)));
+      top = __reduce_max_sync(kFull, top);
+      const int e = top ? exponent_of(top) - 13 : v ? kNoValues : 0;         // the largest element below 2^14
+      publish(e, Scales{});
+      const float by0 = pow2((-e) >> 1), by1 = pow2(-e - ((-e) >> 1));
+#pragma unroll 2
+      for (int r = 0; r < 32; r += 32 / BP) {
+        uint4* x = piece(to, r0 + r, c);
+        *x = bf16_to_half(*x, by0, by1);
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&full[st]));
   }
+  cp_async_wait<0>();                            // of a tile that an abort left
 }
 
 // ---------------------------------------------------------------- MMA issuer
 
 template <int D>
-__device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8_t* sk, uint8_t* sv, uint32_t tmem, bool share) {
+__device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8_t* sk, uint8_t* sv, uint32_t tmem, bool share, bool stall) {
   using C = Cfg<D>;
   volatile int* abort_flag = &s.abort_flag;
   constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(128 >> 4) << 24);           // fp16 x fp16 -> fp32, M = 128
@@ -423,7 +386,7 @@ __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8
     const int h = x & 1;
     if (!k_more) return false;
     if (!share || h == 0) {
-      if (!warp_wait(smem_u32(&s.kfull[n_k & 1]), (n_k >> 1) & 1, abort_flag)) return ok = k_more = false;
+      if (!warp_wait(smem_u32(stall ? &s.done : &s.kfull[n_k & 1]), (n_k >> 1) & 1, abort_flag)) return ok = k_more = false;
       if (n_k >= uniform(*reinterpret_cast<volatile int*>(&s.total))) return k_more = false;
       ++n_k;
     }
@@ -503,27 +466,23 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
     const __nv_bfloat16* q = a.q + t.b * a.qs.batch + t.l * a.qs.layer;
     const int64_t own = static_cast<int64_t>(head) * a.qs.head + static_cast<int64_t>(node) * a.qs.token;
     const int chunk = lane % LPR;
-#pragma unroll 1
-    for (int i0 = 0; i0 < LPR; i0 += 8) {
-      uint4 w[8];
+    uint4 w[LPR];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = (i0 + i) * PER + lane / LPR;
-        const int64_t at = __shfl_sync(kFull, own, rr);
-        w[i] = row - lane + rr < t.rows ? reinterpret_cast<const uint4*>(q + at)[chunk] : make_uint4(0, 0, 0, 0);
-      }
+    for (int i = 0; i < LPR; ++i) {
+      const int rr = i * PER + lane / LPR;
+      const int64_t at = __shfl_sync(kFull, own, rr);
+      w[i] = row - lane + rr < t.rows ? reinterpret_cast<const uint4*>(q + at)[chunk] : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = (i0 + i) * PER + lane / LPR;
-        uint32_t top = max_bits(w[i]);
+    for (int i = 0; i < LPR; ++i) {
+      const int rr = i * PER + lane / LPR;
+      uint32_t top = max_bits(w[i]);
 #pragma unroll
-        for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-        const int e = top ? exponent_of(top) - 14 : 0;       // the largest element below 2^15
-        // (bounded so that it fits a byte: queries below 2^-100 lose bits, and no score)
-        const int eb = max(-114, min(113, e));
-        *piece(sq + (share ? h : 0) * C::kTile, quarter * 32 + rr, chunk) = bf16_to_half(w[i], eb);
-        if (chunk == 0) s.q_exp[(share ? h * kTileRows : 0) + quarter * 32 + rr] = static_cast<int8_t>(eb);
-      }
+      for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+      // the largest element below 2^15 (bounded: queries below 2^-100 lose bits, and no score)
+      const int e = top ? max(-112, min(113, exponent_of(top) - 14)) : 0;
+      *piece(sq + (share ? h : 0) * C::kTile, quarter * 32 + rr, chunk) = bf16_to_half(w[i], pow2(-e), 1.f);
+      if (chunk == 0) s.q_exp[(share ? h * kTileRows : 0) + quarter * 32 + rr] = static_cast<int8_t>(e);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -569,28 +528,30 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
 #pragma unroll
     for (int c = 0; c < 4; ++c) tmem_ld32_issue(s_col + c * 32, sr[c]);
     const int slot = i & (kSlots - 1);
-    const Tile tile = s.tile[slot];
-    e_ref = s.e_ref;
+    const int j0_or = s.j0[slot];
     // keys of the tile that this row sees
-    const bool tree = tile.tree != 0;
+    const bool tree = j0_or < 0;
+    const int j0 = tree ? -1 - j0_or : j0_or;
     uint32_t bits[4] = {0, 0, 0, 0};
     bool whole = false;
     if (tree) {
-      while (up >= tile.j0 + kKeys) up = parent_of(parent, up, &bad);
-      while (up >= tile.j0) {
-        const int j = up - tile.j0;
+      while (up >= j0 + kKeys) up = parent_of(parent, up, &bad);
+      while (up >= j0) {
+        const int j = up - j0;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           if (j >> 5 == c) bits[c] |= 1u << (j & 31);
         up = parent_of(parent, up, &bad);
       }
     } else {
-      whole = tile.j0 + kKeys <= t.count;
+      whole = j0 + kKeys <= t.count;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) bits[c] = bit_range(0, t.count - tile.j0 - c * 32);
+      for (int c = 0; c < 4; ++c) bits[c] = bit_range(0, t.count - j0 - c * 32);
     }
     // y = scores in base 2 = acc f (scores themselves with a cap)
-    float f = fmaxf(scale * pow2(min(120, q_exp + tile.ek)), 0x1p-126f);
+    const int4 ek = *reinterpret_cast<const int4*>(s.ek[slot]);
+    auto factor = [&](int e) { return fmaxf(scale * pow2(min(120, q_exp + e)), 0x1p-126f); };
+    float f[4] = {factor(ek.x), factor(ek.y), factor(ek.z), factor(ek.w)};
 #pragma unroll
     for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
     float (&y)[4][32] = reinterpret_cast<float (&)[4][32]>(sr);
@@ -610,32 +571,25 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) big = fmaxf(big, fabsf(y[c][e]));
-        if (__all_sync(kFull, big * f * inv_cap <= kTanhRange || !valid)) {
+          for (int e = 0; e < 32; ++e) big = fmaxf(big, fabsf(y[c][e] *= f[c]));
+        if (__all_sync(kFull, big * inv_cap <= kTanhRange || !valid)) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float x = y[c][e] * f;
-              y[c][e] = x * tanh_over_z(x * inv_cap) * kLog2e;
-            }
+            for (int e = 0; e < 32; ++e) y[c][e] *= tanh_over_z(y[c][e] * inv_cap) * kLog2e;
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float x = y[c][e] * f;
-              y[c][e] = capped_base2(x, x * inv_cap, cap);
-            }
+            for (int e = 0; e < 32; ++e) y[c][e] = capped_base2(y[c][e], y[c][e] * inv_cap, cap);
         }
-        f = 1.f;
       } else if (biased) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[c][e] *= f;
-        f = 1.f;
+          for (int e = 0; e < 32; ++e) y[c][e] *= f[c];
       }
+      if (capped || biased) f[0] = f[1] = f[2] = f[3] = 1.f;
       if (biased || windowed) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -661,8 +615,16 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
 #pragma unroll
       for (int e = 2; e < 32; e += 2) mx[c] = fmaxf(mx[c], fmaxf(y[c][e], y[c][e + 1]));
     }
-    const float ev = static_cast<float>(tile.ev);
-    const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), f, ev);
+    if (!warp_wait(smem_u32(&s.efull[i & 1]), (i >> 1) & 1, abort_flag)) {       // how far the values were scaled
+      fail = true;
+      break;
+    }
+    e_ref = s.e_ref;
+    const int4 e_here = *reinterpret_cast<const int4*>(s.ev[slot]);
+    const float ev[4] = {static_cast<float>(e_here.x), static_cast<float>(e_here.y), static_cast<float>(e_here.z),
+                         static_cast<float>(e_here.w)};
+    const float top = fmaxf(fmaxf(fmaf(mx[0], f[0], ev[0]), fmaf(mx[1], f[1], ev[1])),
+                            fmaxf(fmaf(mx[2], f[2], ev[2]), fmaf(mx[3], f[3], ev[3])));
     const bool grow = top - m > kGrow;           // also from -inf
     if (__any_sync(kFull, grow)) {
       float by = 1.f;
@@ -687,11 +649,12 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
         }
       }
     }
-    const float sub = m == -INFINITY ? 0.f : m - ev;
-    const uint64_t f2 = pair(f, f), sub2 = pair(-sub, -sub);
-    uint64_t sum[2] = {0, 0};
+    const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
+      const float sub = ev[c] - ref;
+      const uint64_t f2 = pair(f[c], f[c]), sub2 = pair(sub, sub);
+      uint64_t sum[2] = {0, 0};
       uint32_t pk[16];
 #pragma unroll
       for (int e = 0; e < 32; e += 2) {
@@ -707,6 +670,9 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
         }
         pk[e / 2] = pack_half2(p0, p1);
       }
+      float s0, s1;
+      unpair(add2(sum[0], sum[1]), &s0, &s1);
+      l = fmaf(s0 + s1, pow2(e_ref - (c == 0 ? e_here.x : c == 1 ? e_here.y : c == 2 ? e_here.z : e_here.w)), l);
       tmem_st16(s_col + c * 16, pk);
       if (c == 1) {                              // the product may start on the first half of the keys
         tmem_st_wait();
@@ -715,9 +681,6 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
         if (lane == 0) mbar_arrive(smem_u32(&s.phalf[h]));
       }
     }
-    float s0, s1;
-    unpair(add2(sum[0], sum[1]), &s0, &s1);
-    l = fmaf(s0 + s1, pow2(e_ref - tile.ev), l);
     tmem_st_wait();
     tc_fence_before();
     __syncwarp();
@@ -829,20 +792,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   uint8_t* sq = base;                                  // two Q tiles
   uint8_t* sk = sq + 2 * C::kTile;
   uint8_t* sv = sk + kStages * C::kTile;
-  Bars& s = *reinterpret_cast<Bars*>(sv + kStages * C::kTile);
+  uint8_t* raw = sv + kStages * C::kTile;              // the operand warps' own
+  Bars& s = *reinterpret_cast<Bars*>(raw + 8 * C::kRaw);
   const int warp = uniform(threadIdx.x >> 5);
-  wait_for_previous_kernel();
-  let_next_kernel_start();
-  const Item t = make_item(a, blockIdx.x);
-  if (t.rows == 0) return;                             // rows past the tree's nodes
-  const bool share = t.rows > kTileRows;               // two Q tiles, or two streams over one
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      // (a.stall_unit: a test makes the first key tile's wait expect an arrival that never comes)
-      mbar_init(smem_u32(&s.kfull[i]), i == 0 && t.u == a.stall_unit ? 5 : 4);
+      mbar_init(smem_u32(&s.kfull[i]), 4);
       mbar_init(smem_u32(&s.kempty[i]), 1);
       mbar_init(smem_u32(&s.vfull[i]), 4);
       mbar_init(smem_u32(&s.vempty[i]), 1);
+      mbar_init(smem_u32(&s.efull[i]), 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.sfull[i]), 1);
@@ -861,18 +820,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     tmem_alloc(smem_u32(&s.tmem), kTmemCols);
     tmem_relinquish();
   }
+  wait_for_previous_kernel();
+  let_next_kernel_start();
+  const Item t = make_item(a, blockIdx.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(s.tmem);
+  if (t.rows == 0) {                                   // rows past the tree's nodes
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
+  const bool share = t.rows > kTileRows;               // two Q tiles, or two streams over one
   if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    // (a.stall_unit: a test makes the MMA warp wait for key tiles that never come)
+    if (warp == kMmaWarp) issue<D>(t, s, sq, sk, sv, tmem, share, t.u == a.stall_unit);
+  } else if (warp >= kKeyWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == kMmaWarp) issue<D>(t, s, sq, sk, sv, tmem, share);
-  } else if (warp >= kOperandWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    make_operands<D, ROW, MODS>(a, t, s, sk, sv);
+    const bool v = warp >= kValueWarp;
+    make_operands<D, ROW, MODS>(a, t, s, v ? sv : sk, raw + (warp - kKeyWarp) * C::kRaw, v);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     softmax<D, ROW, MODS>(a, t, s, sq, tmem, share);
   }
   tc_fence_before();
