@@ -76,15 +76,17 @@ struct Bars {
   int tiles[2];                // of each stream
   int j0[kSlots];              // a tile's first slot, or -1 - its first node
   alignas(16) int ek[kSlots][4], ev[kSlots][4];      // operands are keys times 2^-ek and values times 2^-ev, per 32 rows
-  int8_t q_exp[256];           // queries are rows times 2^-q_exp
-  alignas(16) int32_t pos[kSlots][kKeys];
+  int8_t q_exp[128];           // queries are rows times 2^-q_exp (one row tile)
+  // with modifiers: smallest position of 32 rows; positions, and how far they lie behind the first nodes
+  alignas(16) int32_t p_min[kSlots][4], pos[kSlots][kKeys];
+  alignas(16) float behind[kSlots][kKeys];
   alignas(16) float ks[kSlots][kKeys], vs[kSlots][kKeys];    // scale per row: of keys; of values times 2^-ev
 };
 
 template <int D>
 struct Cfg {
   static constexpr int kTile = D / 64 * kChunkBytes;         // a Q, K or V tile
-  static constexpr int kRaw = 32 * (D / 2) + 32 * (D / 16);  // codes and scales of 32 rows
+  static constexpr int kRaw = 32 * (D / 2);                  // codes of 32 rows
   static constexpr int kSmem = (2 + 2 * kStages) * kTile + 8 * kRaw + 1024 /* alignment */ + sizeof(Bars);
 };
 static_assert(Cfg<128>::kSmem <= 232448, "shared memory of a block");
@@ -94,7 +96,8 @@ struct Item {
   int u, b, l, g, split;
   int row0, rows;              // first packed row, packed rows of the item (<= 256)
   int count, next, prefix;     // cached rows, position of the first nodes, visible prefix
-  int cached, i0, i1;          // tiles of cached rows; tiles [i0, i1) of them and the tree's are this split's
+  int cached;                  // tiles of cached rows
+  int i0, i1, step;            // of those and the tree's this split takes i0, i0 + step, .. below i1
   int nodes;                   // of the tree, as far as this item's rows see
 };
 
@@ -118,6 +121,8 @@ __device__ __forceinline__ Item make_item(const TreeArgs& a, int id) {
   const uint32_t all = t.cached + (t.nodes + kKeys - 1) / kKeys;
   t.i0 = static_cast<int>(a.by_splits.div(all * split));             // tiles < 2^24 + 8, splits < 256
   t.i1 = static_cast<int>(a.by_splits.div(all * (split + 1)));
+  t.step = 1;
+  if (a.mods.window) t.i0 = split, t.i1 = all, t.step = a.splits;    // every split has a part of what is seen
   return t;
 }
 
@@ -149,10 +154,10 @@ __device__ __forceinline__ uint4 codes_to_half(uint32_t w, uint32_t s, uint32_t 
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// Eight bf16 elements in the same order, times two powers of two.
-__device__ __forceinline__ uint4 bf16_to_half(const uint4& w, float by0, float by1) {
+// Eight bf16 elements in the same order, times a power of two.
+__device__ __forceinline__ uint4 bf16_to_half(const uint4& w, float by) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-  auto at = [&](int i) { return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16) * by0 * by1; };
+  auto at = [&](int i) { return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16) * by; };
   return make_uint4(pack_half2(at(0), at(4)), pack_half2(at(1), at(5)), pack_half2(at(2), at(6)), pack_half2(at(3), at(7)));
 }
 
@@ -181,7 +186,7 @@ __device__ __forceinline__ uint4* piece(uint8_t* tile, int r, int c) {
 template <int D, bool ROW, bool MODS>
 __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, Bars& s, uint8_t* ring, uint8_t* raw, bool v) {
   using C = Cfg<D>;
-  constexpr int CH = D / 32;                     // 16-byte pieces of codes per row, one to a lane in turn
+  constexpr int CH = D / 32;                     // 16-byte pieces of codes per row; a lane turns one row
   using Scales = typename std::conditional<ROW, uint16_t, typename std::conditional<D == 128, uint2, uint32_t>::type>::type;
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, first = quarter * 32;
   volatile int* abort_flag = &s.abort_flag;
@@ -190,11 +195,11 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
   const int64_t base = static_cast<int64_t>(t.u) * a.rows.capacity;
   const uint8_t* const codes = static_cast<const uint8_t*>(v ? a.rows.v : a.rows.k) + (base + first) * (D / 2);
   const Scales* const scales = static_cast<const Scales*>(v ? a.rows.v_scale : a.rows.k_scale) + base + first;
-  const uint16_t* const piece_scale = reinterpret_cast<const uint16_t*>(raw + 32 * (D / 2));
   const bool windowed = MODS && a.mods.window;
   // Copies of the quarter's codes of cached tile i, and its scales to a register: a row a lane.  Nothing behind the rows
   // in use is read.
   Scales sc = {};
+  auto spot = [&](int r, int c) { return raw + r * (D / 2) + ((c ^ (D == 128 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4); };
   auto load = [&](int i) {
     const int left = t.count - i * kKeys - first;
     const uint8_t* src = codes + static_cast<int64_t>(i) * (kKeys * D / 2);
@@ -202,7 +207,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
     for (int k = 0; k < CH; ++k) {
       const int p = k * 32 + lane;
       const bool ok = p / CH < left;
-      cp_async16(smem_u32(raw + p * 16), ok ? src + p * 16 : codes - first * (D / 2), ok);
+      cp_async16(smem_u32(spot(p / CH, p % CH)), ok ? src + p * 16 : codes - first * (D / 2), ok);
     }
     cp_async_commit();
     sc = Scales{};
@@ -219,8 +224,11 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
   // the last to the first.  Every warp walks alike.
   int at = t.i0;
   auto next = [&]() -> int {
-    for (; at < t.i1; ++at) {
-      if (!windowed || at >= t.cached) return at++;
+    for (; at < t.i1; at += t.step) {
+      if (!windowed || at >= t.cached) {
+        at += t.step;
+        return at - t.step;
+      }
       bool seen = false;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -230,7 +238,10 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
           seen |= t.next - p < a.mods.window || p < t.prefix;
         }
       }
-      if (__any_sync(kFull, seen)) return at++;
+      if (__any_sync(kFull, seen)) {
+        at += t.step;
+        return at - t.step;
+      }
     }
     return -1;
   };
@@ -284,6 +295,9 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
           for (int i = parent_of(parent, j, &bad); i >= 0; i = parent_of(parent, i, &bad)) ++p;
         }
         s.pos[slot][first + lane] = p;
+        s.behind[slot][first + lane] = static_cast<float>(t.next - p);
+        const int low = __reduce_min_sync(kFull, j < (tree ? t.nodes : t.count) ? p : INT32_MAX);
+        if (lane == 0) s.p_min[slot][quarter] = low;
       }
       if (ROW && !tree) s.ks[slot][first + lane] = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(&own)));
     };
@@ -291,72 +305,77 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
       // this tile's codes to registers, the next one's on their way
       cp_async_wait<0>();
       const Scales own = sc;
-      if (!ROW) *reinterpret_cast<Scales*>(raw + 32 * (D / 2) + lane * sizeof(Scales)) = own;
       __syncwarp();
       uint4 w[CH];
-      uint32_t scale[CH], top = 0;
+      uint32_t top = 0;
+      auto scale = [&](int k) -> uint32_t {
+        if constexpr (ROW) return own;
+        else if constexpr (D == 128) return k == 0 ? own.x & 0xffffu : k == 1 ? own.x >> 16 : k == 2 ? own.y & 0xffffu : own.y >> 16;
+        else return k == 0 ? own & 0xffffu : own >> 16;
+      };
+      // A group of zeros tells nothing about the sizes of the others, whatever its scale (the quantiser writes 1)
+      auto zeros = [](const uint4& x) { return (x.x | x.y | x.z | x.w) == 0; };
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        const int p = k * 32 + lane;
-        w[k] = *reinterpret_cast<const uint4*>(raw + p * 16);
-        scale[k] = ROW ? __shfl_sync(kFull, static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&own)), p / CH) : piece_scale[p];
-        // A piece of zeros tells nothing about the sizes of the others, whatever its scale (the quantiser writes 1)
-        if ((w[k].x | w[k].y | w[k].z | w[k].w) == 0) scale[k] = 0;
-        top = max(top, scale[k]);
+        w[k] = *reinterpret_cast<const uint4*>(spot(lane, k));
+        if (v || !ROW) top = max(top, zeros(w[k]) ? 0u : scale(k));
       }
       __syncwarp();
       if (!windowed) prefetch(cur + 1 + kAhead);
       cur = next();
       if (cur >= 0 && cur < t.cached) load(cur);
-      top = __reduce_max_sync(kFull, top);
       int e = v ? kNoValues : 0;                 // rows times 2^-e:
-      if (top && !ROW) e = exponent_of(top) - 10;                              // the largest scale below 2^11
-      else if (top && v) e = static_cast<int>(max(1u, top >> 10)) - 14;        // the largest row scale below 1
+      if (v || !ROW) {
+        top = __reduce_max_sync(kFull, top);
+        if (top && !ROW) e = max(exponent_of(top) - 10, -126);                 // the largest scale below 2^11
+        else if (top) e = static_cast<int>(max(1u, top >> 10)) - 14;           // the largest row scale below 1
+      }
       if (!wait_empty()) break;
       publish(e, own);
-      const float by0 = pow2((-e) >> 1), by1 = pow2(-e - ((-e) >> 1));
+      const float by = pow2(-e);
+      const int key = first + lane, x = key & 7;
+      uint8_t* const row = to + key * 128;
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        const int p = k * 32 + lane, key = first + p / CH, chunk = p % CH;
         uint32_t f = 0x3c003c00u, m;             // a scale per row: the codes alone
         if (!ROW) {
-          const float x = __uint_as_float(scale[k] << 16) * by0 * by1;
-          f = pack_half2(x, x);
+          const float g = zeros(w[k]) ? 0.f : __uint_as_float(scale(k) << 16) * by;
+          f = pack_half2(g, g);
         }
         asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(m) : "r"(f), "r"(0xce00ce00u));         // -24
-        // lanes of the second 64 columns take their words in another order: eight lanes then meet every bank once
-        const bool far = D == 128 && (chunk & 2);
-        const uint32_t x[4] = {far ? w[k].z : w[k].x, far ? w[k].w : w[k].y, far ? w[k].x : w[k].z, far ? w[k].y : w[k].w};
-        uint8_t* const row = to + (chunk >> 1) * kChunkBytes + key * 128;
-        const int place = ((chunk & 1) * 4 + (far ? 2 : 0)) ^ (key & 7);
+        const uint32_t word[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(row + ((place ^ j) << 4)) = codes_to_half(x[j], f, m);
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(row + (k >> 1) * kChunkBytes + ((((k & 1) * 4 + j) ^ x) << 4)) = codes_to_half(word[j], f, m);
       }
     } else {
       // the tree's rows, bf16, straight to their places; then turned there, each lane its own pieces
       if (!wait_empty()) break;
       const __nv_bfloat16* src = (v ? a.v_new : a.k_new) + t.b * a.news.batch + t.l * a.news.layer + t.g * a.news.head;
       constexpr int BP = D / 8;
-      const int c = lane % BP, r0 = first + lane / BP;
+      {
+        const int c = lane % BP, r0 = first + lane / BP;
 #pragma unroll 4
-      for (int r = 0; r < 32; r += 32 / BP) {
-        const bool ok = j0 + r0 + r < t.nodes;
-        cp_async16(smem_u32(piece(to, r0 + r, c)), ok ? src + static_cast<int64_t>(j0 + r0 + r) * a.news.token + c * 8 : src, ok);
+        for (int r = 0; r < 32; r += 32 / BP) {
+          const bool ok = j0 + r0 + r < t.nodes;
+          cp_async16(smem_u32(piece(to, r0 + r, c)), ok ? src + static_cast<int64_t>(j0 + r0 + r) * a.news.token + c * 8 : src, ok);
+        }
       }
       cp_async_commit();
       cur = next();
       cp_async_wait<0>();
+      __syncwarp();
       uint32_t top = 0;
 #pragma unroll 4
-      for (int r = 0; r < 32; r += 32 / BP) top = max(top, max_bits(*piece(to, r0 + r, c)));
+      for (int c = 0; c < BP; ++c) top = max(top, max_bits(*piece(to, first + lane, c)));
       top = __reduce_max_sync(kFull, top);
-      const int e = top ? exponent_of(top) - 13 : v ? kNoValues : 0;         // the largest element below 2^14
+      const int e = top ? max(exponent_of(top) - 13, -126) : v ? kNoValues : 0;        // the largest element below 2^14
       publish(e, Scales{});
-      const float by0 = pow2((-e) >> 1), by1 = pow2(-e - ((-e) >> 1));
+      const float by = pow2(-e);
 #pragma unroll 2
-      for (int r = 0; r < 32; r += 32 / BP) {
-        uint4* x = piece(to, r0 + r, c);
-        *x = bf16_to_half(*x, by0, by1);
+      for (int c = 0; c < BP; ++c) {
+        uint4* x = piece(to, first + lane, c);
+        *x = bf16_to_half(*x, by);
       }
     }
     fence_proxy_async_smem();
@@ -459,47 +478,55 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
   const int node = static_cast<int>(a.by_group.divmod(t.row0 + (valid ? row : 0), &in_group));
   const int head = t.g * a.G + static_cast<int>(in_group);
 
-  // Queries of this warp's 32 rows: 16 lanes a row (8 at d = 64), scaled to fp16 by a power of two per row.  One row tile
-  // is loaded by the first stream's warps.
+  // Queries of this warp's 32 rows, straight to their places in whole rows; then each lane scales its own to fp16 by a
+  // power of two.  One row tile is made by the first stream's warps.
+  int q_exp = 0;
   if (share || h == 0) {
     constexpr int LPR = D / 8, PER = 32 / LPR;
+    uint8_t* const tile = sq + (share ? h : 0) * C::kTile;
     const __nv_bfloat16* q = a.q + t.b * a.qs.batch + t.l * a.qs.layer;
     const int64_t own = static_cast<int64_t>(head) * a.qs.head + static_cast<int64_t>(node) * a.qs.token;
-    const int chunk = lane % LPR;
-    uint4 w[LPR];
-#pragma unroll
-    for (int i = 0; i < LPR; ++i) {
-      const int rr = i * PER + lane / LPR;
+#pragma unroll 4
+    for (int i = 0; i < 32; i += PER) {
+      const int rr = i + lane / LPR;
       const int64_t at = __shfl_sync(kFull, own, rr);
-      w[i] = row - lane + rr < t.rows ? reinterpret_cast<const uint4*>(q + at)[chunk] : make_uint4(0, 0, 0, 0);
+      const bool ok = row - lane + rr < t.rows;
+      cp_async16(smem_u32(piece(tile, quarter * 32 + rr, lane % LPR)), ok ? q + at + (lane % LPR) * 8 : q, ok);
     }
-#pragma unroll
-    for (int i = 0; i < LPR; ++i) {
-      const int rr = i * PER + lane / LPR;
-      uint32_t top = max_bits(w[i]);
-#pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-      // the largest element below 2^15 (bounded: queries below 2^-100 lose bits, and no score)
-      const int e = top ? max(-112, min(113, exponent_of(top) - 14)) : 0;
-      *piece(sq + (share ? h : 0) * C::kTile, quarter * 32 + rr, chunk) = bf16_to_half(w[i], pow2(-e), 1.f);
-      if (chunk == 0) s.q_exp[(share ? h * kTileRows : 0) + quarter * 32 + rr] = static_cast<int8_t>(e);
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncwarp();
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int c = 0; c < LPR; ++c) top = max(top, max_bits(*piece(tile, r, c)));
+    // the largest element below 2^15 (bounded: queries below 2^-100 lose bits, and no score)
+    q_exp = top ? max(-112, min(113, exponent_of(top) - 14)) : 0;
+    const float by = pow2(-q_exp);
+#pragma unroll 2
+    for (int c = 0; c < LPR; ++c) {
+      uint4* x = piece(tile, r, c);
+      *x = bf16_to_half(*x, by);
     }
+    if (!share) s.q_exp[r] = static_cast<int8_t>(q_exp);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s.qfull[share ? h : 0]));
   }
   bool fail = false;
-  if (!share && h == 1 && !warp_wait(smem_u32(&s.qfull[0]), 0, abort_flag)) fail = true;
-  const int q_exp = s.q_exp[row];
+  if (!share && h == 1) {
+    if (!warp_wait(smem_u32(&s.qfull[0]), 0, abort_flag)) fail = true;
+    q_exp = s.q_exp[r];
+  }
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
   const uint32_t s_col = tmem + lanes + h * 128, o_col = tmem + lanes + kOCol + h * 128;
   const bool warp_valid = __any_sync(kFull, valid);
   const int32_t* parent = a.parent + static_cast<int64_t>(t.b) * a.n;
   bool bad = false;
-  int p_q = t.next;
+  int depth = 0;
   const bool capped = MODS && a.mods.softcap > 0.f, biased = MODS && a.mods.slopes, windowed = MODS && a.mods.window;
   if (MODS && (biased || windowed) && valid)
-    for (int i = parent_of(parent, node, &bad); i >= 0; i = parent_of(parent, i, &bad)) ++p_q;
+    for (int i = parent_of(parent, node, &bad); i >= 0; i = parent_of(parent, i, &bad)) ++depth;
+  const int p_q = t.next + depth;
   const float slope = biased ? a.mods.slopes[head] * kLog2e : 0.f;
   const float cap = MODS ? a.mods.softcap : 0.f, inv_cap = capped ? fminf(1.f / cap, 1e30f) : 0.f;
   const float scale = capped ? a.scale : a.scale * kLog2e;
@@ -556,15 +583,15 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
     for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
     float (&y)[4][32] = reinterpret_cast<float (&)[4][32]>(sr);
     const bool rows = ROW && !tree;              // a scale per key
-    if (rows) {
+    // every pair of scores through one function of packed operations
+    auto each = [&](auto change) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 k = *reinterpret_cast<const float4*>(&s.ks[slot][c * 32 + e]);
-          y[c][e] *= k.x, y[c][e + 1] *= k.y, y[c][e + 2] *= k.z, y[c][e + 3] *= k.w;
-        }
-    }
+        for (int e = 0; e < 32; e += 2) unpair(change(pair(y[c][e], y[c][e + 1]), c, e), &y[c][e], &y[c][e + 1]);
+    };
+    if (rows)
+      each([&](uint64_t x, int c, int e) { return mul2(x, *reinterpret_cast<const uint64_t*>(&s.ks[slot][c * 32 + e])); });
     if (MODS) {
       if (capped) {
         float big = 0.f;
@@ -573,32 +600,44 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
 #pragma unroll
           for (int e = 0; e < 32; ++e) big = fmaxf(big, fabsf(y[c][e] *= f[c]));
         if (__all_sync(kFull, big * inv_cap <= kTanhRange || !valid)) {
+          const uint64_t z2 = pair(inv_cap, inv_cap);
+          each([&](uint64_t x, int, int) {
+            const uint64_t z = mul2(x, z2), w = mul2(z, z);
+            uint64_t p = pair(kTanh[4] * kLog2e, kTanh[4] * kLog2e);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) y[c][e] *= tanh_over_z(y[c][e] * inv_cap) * kLog2e;
+            for (int k = 3; k >= 0; --k) p = fma2(p, w, pair(kTanh[k] * kLog2e, kTanh[k] * kLog2e));
+            return mul2(x, p);
+          });
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[c][e] = capped_base2(y[c][e], y[c][e] * inv_cap, cap);
         }
-      } else if (biased) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) y[c][e] *= f[c];
+        f[0] = f[1] = f[2] = f[3] = 1.f;
       }
-      if (capped || biased) f[0] = f[1] = f[2] = f[3] = 1.f;
-      if (biased || windowed) {
+      if (biased) {
+        // whoever is seen lies behind the row: -slope (p_q - p) = -slope (next - p) - slope depth
+        const float at = -slope * static_cast<float>(depth);
+        const uint64_t at2 = pair(at, at), slope2 = pair(-slope, -slope);
+        each([&](uint64_t x, int c, int e) {
+          return fma2(slope2, *reinterpret_cast<const uint64_t*>(&s.behind[slot][c * 32 + e]), fma2(x, pair(f[c], f[c]), at2));
+        });
+        f[0] = f[1] = f[2] = f[3] = 1.f;
+      }
+      if (windowed) {
+        const int4 low = *reinterpret_cast<const int4*>(s.p_min[slot]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          // (the first node's window is the shortest reach back; the smallest position is the furthest)
+          const int p = c == 0 ? low.x : c == 1 ? low.y : c == 2 ? low.z : low.w;
+          if (__all_sync(kFull, p == INT32_MAX || p_q - p < a.mods.window)) continue;
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const int p = s.pos[slot][c * 32 + e], far = p_q - p;
-            if (biased) y[c][e] = fmaf(-slope, fabsf(static_cast<float>(far)), y[c][e]);
-            if (windowed && far >= a.mods.window && p >= t.prefix) y[c][e] = -INFINITY;
+            const int k = s.pos[slot][c * 32 + e];
+            if (p_q - k >= a.mods.window && k >= t.prefix) y[c][e] = -INFINITY;
           }
+        }
       }
     }
     if (!whole) {
@@ -613,7 +652,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
     for (int c = 0; c < 4; ++c) {
       mx[c] = fmaxf(y[c][0], y[c][1]);
 #pragma unroll
-      for (int e = 2; e < 32; e += 2) mx[c] = fmaxf(mx[c], fmaxf(y[c][e], y[c][e + 1]));
+      for (int e = 2; e < 32; e += 2) mx[c] = fmax3(mx[c], y[c][e], y[c][e + 1]);
     }
     if (!warp_wait(smem_u32(&s.efull[i & 1]), (i >> 1) & 1, abort_flag)) {       // how far the values were scaled
       fail = true;
@@ -663,11 +702,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
         p0 = ex2_approx(p0);
         p1 = ex2_approx(p1);
         sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(p0, p1));
-        if (rows) {
-          const float2 v = *reinterpret_cast<const float2*>(&s.vs[slot][c * 32 + e]);
-          p0 *= v.x;
-          p1 *= v.y;
-        }
+        if (rows) unpair(mul2(pair(p0, p1), *reinterpret_cast<const uint64_t*>(&s.vs[slot][c * 32 + e])), &p0, &p1);
         pk[e / 2] = pack_half2(p0, p1);
       }
       float s0, s1;
