@@ -35,9 +35,9 @@
 // walk up.  With a window, tiles that no row sees are not read: the warps that
 // turn rows into operands decide, and say so to the others tile by tile.
 //
-// Warp roles (20 warps): 0-3 and 4-7 softmax of stream 0 and 1 (160 registers),
-// 8-11 make the keys' operands and 12-15 the values' (56; a quarter of every tile
-// each), 16 tensor memory and MMA issuer (48): 2 x 160 + 2 x 56 + 48 = 5 x 96, what
+// Warp roles (20 warps): 0-3 and 4-7 softmax of stream 0 and 1 (128 registers),
+// 8-11 make the keys' operands and 12-15 the values' (88; a quarter of every tile
+// each), 16 tensor memory and MMA issuer (48): 2 x 128 + 2 x 88 + 48 = 5 x 96, what
 // the block was launched with.  Every wait is bounded; one that gives up raises a
 // shared abort flag, the unit is marked KVC_UNIT_TIMEOUT and the block ends.
 #include <algorithm>
@@ -68,7 +68,7 @@ constexpr float kGrow = 8.f;                     // log2 growth of the maximum t
 
 struct Bars {
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-  uint64_t efull[kStages], sfull[2], phalf[2], pfull[2], odone[2], qfull[2], done;
+  uint64_t efull[kStages], sfull[2][2], pfull[2][2], odone[2], qfull[2], done;      // [stream][half of a tile's keys]
   uint32_t tmem;
   int abort_flag;
   int total;                   // tiles of this item, once that is known
@@ -199,6 +199,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
   // Copies of the quarter's codes of cached tile i, and its scales to a register: a row a lane.  Nothing behind the rows
   // in use is read.
   Scales sc = {};
+  int32_t pos = 0;
   auto spot = [&](int r, int c) { return raw + r * (D / 2) + ((c ^ (D == 128 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4); };
   auto load = [&](int i) {
     const int left = t.count - i * kKeys - first;
@@ -211,7 +212,10 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
     }
     cp_async_commit();
     sc = Scales{};
-    if (lane < left) sc = scales[static_cast<int64_t>(i) * kKeys + lane];
+    if (lane < left) {
+      sc = scales[static_cast<int64_t>(i) * kKeys + lane];
+      if (MODS) pos = a.rows.pos[base + static_cast<int64_t>(i) * kKeys + first + lane];
+    }
   };
   auto prefetch = [&](int i) {
     const int left = min(32, t.count - i * kKeys - first);
@@ -265,7 +269,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
     }
     uint8_t* const to = ring + st * C::kTile;
     const int j0 = tree ? ((t.nodes + kKeys - 1) / kKeys - 1 - (cur - t.cached)) * kKeys : cur * kKeys;
-    auto publish = [&](int e, Scales own) {      // what the softmax needs of this quarter
+    auto publish = [&](int e, Scales own, int32_t p) {      // what the softmax needs of this quarter
       if (v) {
         if (ROW && !tree) {
           const float f = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(&own)));
@@ -285,10 +289,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
       }
       const int j = j0 + first + lane;
       if (MODS) {
-        int p = 0;
-        if (!tree) {
-          if (j < t.count) p = a.rows.pos[base + j];
-        } else if (j < t.nodes) {
+        if (tree && j < t.nodes) {
           const int32_t* parent = a.parent + static_cast<int64_t>(t.b) * a.n;
           bool bad = false;
           p = t.next;
@@ -305,6 +306,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
       // this tile's codes to registers, the next one's on their way
       cp_async_wait<0>();
       const Scales own = sc;
+      const int32_t own_pos = pos;
       __syncwarp();
       uint4 w[CH];
       uint32_t top = 0;
@@ -331,7 +333,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
         else if (top) e = static_cast<int>(max(1u, top >> 10)) - 14;           // the largest row scale below 1
       }
       if (!wait_empty()) break;
-      publish(e, own);
+      publish(e, own, own_pos);
       const float by = pow2(-e);
       const int key = first + lane, x = key & 7;
       uint8_t* const row = to + key * 128;
@@ -370,7 +372,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
       for (int c = 0; c < BP; ++c) top = max(top, max_bits(*piece(to, first + lane, c)));
       top = __reduce_max_sync(kFull, top);
       const int e = top ? max(exponent_of(top) - 13, -126) : v ? kNoValues : 0;        // the largest element below 2^14
-      publish(e, Scales{});
+      publish(e, Scales{}, 0);
       const float by = pow2(-e);
 #pragma unroll 2
       for (int c = 0; c < BP; ++c) {
@@ -387,75 +389,84 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
 
 // ---------------------------------------------------------------- MMA issuer
 
+// A stream's scores of 64 keys are in the making while its softmax works on the 64 before: S of half b lies in columns
+// 64 b of the stream's 128, its weights over the first 32 of them.
 template <int D>
 __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8_t* sk, uint8_t* sv, uint32_t tmem, bool share, bool stall) {
   using C = Cfg<D>;
   volatile int* abort_flag = &s.abort_flag;
   constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(128 >> 4) << 24);           // fp16 x fp16 -> fp32, M = 128
-  const uint32_t idesc_s = kIdesc | (static_cast<uint32_t>(kKeys >> 3) << 17);
+  constexpr uint32_t kHalf = kKeys / 2 * 128 >> 4;                 // half of a tile's rows
+  const uint32_t idesc_s = kIdesc | (static_cast<uint32_t>(kKeys / 2 >> 3) << 17);
   const uint32_t idesc_o = kIdesc | (static_cast<uint32_t>(D >> 3) << 17) | (1u << 16);     // B (values) MN-major
   bool ok = warp_wait(smem_u32(&s.qfull[0]), 0, abort_flag);
   if (ok && share) ok = warp_wait(smem_u32(&s.qfull[1]), 0, abort_flag);
   const uint32_t elected = elect_one();
   const uint64_t q_desc = sw128_desc(smem_u32(sq)), k_desc = sw128_desc(smem_u32(sk)), val_desc = v_desc(smem_u32(sv));
-  int n_k = 0, n_v = 0;                // K and V tiles taken up
-  bool k_more = true;
-  // the scores of step x (stream x & 1); false when there is no such step
-  auto scores = [&](int x) -> bool {
-    const int h = x & 1;
-    if (!k_more) return false;
-    if (!share || h == 0) {
-      if (!warp_wait(smem_u32(stall ? &s.done : &s.kfull[n_k & 1]), (n_k >> 1) & 1, abort_flag)) return ok = k_more = false;
-      if (n_k >= uniform(*reinterpret_cast<volatile int*>(&s.total))) return k_more = false;
-      ++n_k;
-    }
+  // stream h's tile of round j
+  auto tile_of = [&](int j, int h) { return share ? j : 2 * j + h; };
+  bool over = false;
+  // waits for the keys of that tile; false: there is none, or the wait gave up
+  auto has = [&](int j, int h) -> bool {
+    if (over || !ok) return false;
+    const int n = tile_of(j, h);
+    if (!warp_wait(smem_u32(stall ? &s.done : &s.kfull[n & 1]), (n >> 1) & 1, abort_flag)) return ok = false;
+    over = n >= uniform(*reinterpret_cast<volatile int*>(&s.total));
+    return !over;
+  };
+  auto scores = [&](int j, int h, int b) {
+    const uint32_t st = tile_of(j, h) & 1;
+    const uint64_t qd = q_desc + (share ? h : 0) * (C::kTile >> 4), kd = k_desc + st * (C::kTile >> 4) + b * kHalf;
     tc_fence_after();
-    const uint32_t st = (n_k - 1) & 1;
-    const uint64_t qd = q_desc + (share ? h : 0) * (C::kTile >> 4), kd = k_desc + st * (C::kTile >> 4);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       const uint32_t off = (ks >> 2) * (kChunkBytes >> 4) + (ks & 3) * 2;
-      mma_ss(tmem + h * 128, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u, elected);
+      mma_ss(tmem + h * 128 + b * 64, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u, elected);
     }
-    commit(smem_u32(&s.sfull[h]), elected);
-    if (!share || h == 1) commit(smem_u32(&s.kempty[st]), elected);
-    return true;
+    commit(smem_u32(&s.sfull[h][b]), elected);
+    if (b == 1 && (!share || h == 1)) commit(smem_u32(&s.kempty[st]), elected);
   };
-  auto values = [&](int x) -> bool {
-    const int h = x & 1;
-    if (!share || h == 0) {
-      if (!warp_wait(smem_u32(&s.vfull[n_v & 1]), (n_v >> 1) & 1, abort_flag)) return false;
-      ++n_v;
-    }
-    if (!warp_wait(smem_u32(&s.phalf[h]), (x >> 1) & 1, abort_flag)) return false;
+  auto values = [&](int j, int h, int b) -> bool {
+    const int n = tile_of(j, h);
+    const uint32_t st = n & 1;
+    if (b == 0 && (!share || h == 0) && !warp_wait(smem_u32(&s.vfull[st]), (n >> 1) & 1, abort_flag)) return false;
+    if (!warp_wait(smem_u32(&s.pfull[h][b]), j & 1, abort_flag)) return false;
     tc_fence_after();
-    const uint32_t st = (n_v - 1) & 1;
-    const uint64_t vd = val_desc + st * (C::kTile >> 4);
-    const uint32_t more = x > 1 ? 1u : 0u;
+    const uint64_t vd = val_desc + st * (C::kTile >> 4) + b * kHalf;
+    const uint32_t more = j + b > 0 ? 1u : 0u;
 #pragma unroll
     for (int ks = 0; ks < kKeys / 32; ++ks)
-      mma_ts(tmem + kOCol + h * 128, tmem + h * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o, ks > 0 ? 1u : more, elected);
-    if (!warp_wait(smem_u32(&s.pfull[h]), (x >> 1) & 1, abort_flag)) return false;
-    tc_fence_after();
-#pragma unroll
-    for (int ks = kKeys / 32; ks < kKeys / 16; ++ks)
-      mma_ts(tmem + kOCol + h * 128, tmem + h * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o, 1u, elected);
+      mma_ts(tmem + kOCol + h * 128, tmem + h * 128 + b * 64 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o, ks > 0 ? 1u : more, elected);
     commit(smem_u32(&s.odone[h]), elected);
-    if (!share || h == 1) commit(smem_u32(&s.vempty[st]), elected);
+    if (b == 1 && (!share || h == 1)) commit(smem_u32(&s.vempty[st]), elected);
     return true;
   };
-  if (ok) {
-    int issued = 0;
-    while (issued < 2 && scores(issued)) ++issued;
-    for (int x = 0; ok && x < issued; ++x) {
-      if (!(ok = values(x))) break;
-      if (issued == x + 2 && scores(issued)) ++issued;
+  bool live0 = has(0, 0), live1 = false;
+  if (live0) scores(0, 0, 0);
+  if (live0) live1 = share || has(0, 1);
+  if (live1) scores(0, 1, 0);
+  if (live0) scores(0, 0, 1);
+  if (live1) scores(0, 1, 1);
+#pragma unroll 1
+  for (int j = 0; ok && live0; ++j) {
+    bool next0 = false, next1 = false;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (!(ok = ok && values(j, 0, b))) break;
+      if (b == 0) next0 = has(j + 1, 0);
+      if (next0) scores(j + 1, 0, b);
+      if (!live1) continue;
+      if (!(ok = ok && values(j, 1, b))) break;
+      if (b == 0) next1 = next0 && (share || has(j + 1, 1));
+      if (next1) scores(j + 1, 1, b);
     }
+    live0 = next0;
+    live1 = next1;
   }
   // the streams' next scores are none (after an abort they find that by themselves)
   if (ok && elected) {
-    mbar_arrive(smem_u32(&s.sfull[0]));
-    mbar_arrive(smem_u32(&s.sfull[1]));
+    mbar_arrive(smem_u32(&s.sfull[0][0]));
+    mbar_arrive(smem_u32(&s.sfull[1][0]));
   }
   __syncwarp();
   // all MMAs issued above complete before tensor memory is freed
@@ -535,191 +546,198 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
   int n = 0;                                     // tiles of this stream
   int e_ref = 0;
 #pragma unroll 1
-  for (int i = share ? 0 : h; !fail; i += share ? 1 : 2) {
-    if (!warp_wait(smem_u32(&s.sfull[h]), n & 1, abort_flag)) {
+  for (; !fail; ++n) {
+    if (!warp_wait(smem_u32(&s.sfull[h][0]), n & 1, abort_flag)) {
       fail = true;
       break;
     }
+    const int i = share ? n : 2 * n + h, slot = i & (kSlots - 1);
     if (i >= uniform(*reinterpret_cast<volatile int*>(&s.total))) break;
-    ++n;
-    tc_fence_after();
-    if (!warp_valid) {                           // nothing of this warp is a row: the product's result is not read
+    if (!warp_valid) {                           // nothing of this warp is a row: the products' results are not read
+      tc_fence_after();
       tc_fence_before();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&s.phalf[h]));
-        mbar_arrive(smem_u32(&s.pfull[h]));
+      if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h][0]));
+      if (!warp_wait(smem_u32(&s.sfull[h][1]), n & 1, abort_flag)) {
+        fail = true;
+        break;
       }
+      tc_fence_after();
+      tc_fence_before();
+      if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h][1]));
       continue;
     }
-    uint32_t sr[4][32];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32_issue(s_col + c * 32, sr[c]);
-    const int slot = i & (kSlots - 1);
     const int j0_or = s.j0[slot];
-    // keys of the tile that this row sees
-    const bool tree = j0_or < 0;
+    const bool tree = j0_or < 0, rows = ROW && !tree;        // rows: a scale per key
     const int j0 = tree ? -1 - j0_or : j0_or;
-    uint32_t bits[4] = {0, 0, 0, 0};
-    bool whole = false;
+    uint32_t met[4] = {0, 0, 0, 0};              // keys of a tree's tile that this row sees
     if (tree) {
       while (up >= j0 + kKeys) up = parent_of(parent, up, &bad);
       while (up >= j0) {
         const int j = up - j0;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (j >> 5 == c) bits[c] |= 1u << (j & 31);
+          if (j >> 5 == c) met[c] |= 1u << (j & 31);
         up = parent_of(parent, up, &bad);
       }
-    } else {
-      whole = j0 + kKeys <= t.count;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) bits[c] = bit_range(0, t.count - j0 - c * 32);
     }
-    // y = scores in base 2 = acc f (scores themselves with a cap)
-    const int4 ek = *reinterpret_cast<const int4*>(s.ek[slot]);
-    auto factor = [&](int e) { return fmaxf(scale * pow2(min(120, q_exp + e)), 0x1p-126f); };
-    float f[4] = {factor(ek.x), factor(ek.y), factor(ek.z), factor(ek.w)};
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+      if (b == 1 && !warp_wait(smem_u32(&s.sfull[h][1]), n & 1, abort_flag)) {
+        fail = true;
+        break;
+      }
+      tc_fence_after();
+      uint32_t sr[2][32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
-    float (&y)[4][32] = reinterpret_cast<float (&)[4][32]>(sr);
-    const bool rows = ROW && !tree;              // a scale per key
-    // every pair of scores through one function of packed operations
-    auto each = [&](auto change) {
+      for (int c = 0; c < 2; ++c) tmem_ld32_issue(s_col + b * 64 + c * 32, sr[c]);
+      // y = scores in base 2 = acc f (scores themselves with a cap)
+      const int2 ek = *reinterpret_cast<const int2*>(&s.ek[slot][2 * b]);
+      auto factor = [&](int e) { return fmaxf(scale * pow2(min(120, q_exp + e)), 0x1p-126f); };
+      float f[2] = {factor(ek.x), factor(ek.y)};
+      const int left = t.count - j0 - b * 64;
+      const bool whole = !tree && left >= 64;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 2; ++c) tmem_ld_wait(sr[c]);
+      float (&y)[2][32] = reinterpret_cast<float (&)[2][32]>(sr);
+      // every four scores through one function of packed operations on pairs, with what lies at their keys' places
+      auto each = [&](const float* at, auto change) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) unpair(change(pair(y[c][e], y[c][e + 1]), c, e), &y[c][e], &y[c][e + 1]);
-    };
-    if (rows)
-      each([&](uint64_t x, int c, int e) { return mul2(x, *reinterpret_cast<const uint64_t*>(&s.ks[slot][c * 32 + e])); });
-    if (MODS) {
-      if (capped) {
-        float big = 0.f;
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int e = 0; e < 32; e += 4) {
+            const ulonglong2 x = at ? *reinterpret_cast<const ulonglong2*>(at + c * 32 + e) : make_ulonglong2(0, 0);
+            unpair(change(pair(y[c][e], y[c][e + 1]), x.x, c), &y[c][e], &y[c][e + 1]);
+            unpair(change(pair(y[c][e + 2], y[c][e + 3]), x.y, c), &y[c][e + 2], &y[c][e + 3]);
+          }
+      };
+      if (rows) each(&s.ks[slot][b * 64], [&](uint64_t x, uint64_t k, int) { return mul2(x, k); });
+      if (MODS) {
+        if (capped) {
+          float big = 0.f;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) big = fmaxf(big, fabsf(y[c][e] *= f[c]));
-        if (__all_sync(kFull, big * inv_cap <= kTanhRange || !valid)) {
-          const uint64_t z2 = pair(inv_cap, inv_cap);
-          each([&](uint64_t x, int, int) {
-            const uint64_t z = mul2(x, z2), w = mul2(z, z);
-            uint64_t p = pair(kTanh[4] * kLog2e, kTanh[4] * kLog2e);
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int k = 3; k >= 0; --k) p = fma2(p, w, pair(kTanh[k] * kLog2e, kTanh[k] * kLog2e));
-            return mul2(x, p);
-          });
-        } else {
+            for (int e = 0; e < 32; ++e) big = fmaxf(big, fabsf(y[c][e] *= f[c]));
+          if (__all_sync(kFull, big * inv_cap <= kTanhRange || !valid)) {
+            const uint64_t z2 = pair(inv_cap, inv_cap);
+            each(nullptr, [&](uint64_t x, uint64_t, int) {
+              const uint64_t z = mul2(x, z2), w = mul2(z, z);
+              uint64_t p = pair(kTanh[4] * kLog2e, kTanh[4] * kLog2e);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+              for (int k = 3; k >= 0; --k) p = fma2(p, w, pair(kTanh[k] * kLog2e, kTanh[k] * kLog2e));
+              return mul2(x, p);
+            });
+          } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[c][e] = capped_base2(y[c][e], y[c][e] * inv_cap, cap);
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) y[c][e] = capped_base2(y[c][e], y[c][e] * inv_cap, cap);
+          }
+          f[0] = f[1] = 1.f;
         }
-        f[0] = f[1] = f[2] = f[3] = 1.f;
-      }
-      if (biased) {
-        // whoever is seen lies behind the row: -slope (p_q - p) = -slope (next - p) - slope depth
-        const float at = -slope * static_cast<float>(depth);
-        const uint64_t at2 = pair(at, at), slope2 = pair(-slope, -slope);
-        each([&](uint64_t x, int c, int e) {
-          return fma2(slope2, *reinterpret_cast<const uint64_t*>(&s.behind[slot][c * 32 + e]), fma2(x, pair(f[c], f[c]), at2));
-        });
-        f[0] = f[1] = f[2] = f[3] = 1.f;
-      }
-      if (windowed) {
-        const int4 low = *reinterpret_cast<const int4*>(s.p_min[slot]);
+        if (biased) {
+          // whoever is seen lies behind the row: -slope (p_q - p) = -slope (next - p) - slope depth
+          const float at = -slope * static_cast<float>(depth);
+          const uint64_t at2 = pair(at, at), slope2 = pair(-slope, -slope);
+          each(&s.behind[slot][b * 64],
+               [&](uint64_t x, uint64_t behind, int c) { return fma2(slope2, behind, fma2(x, pair(f[c], f[c]), at2)); });
+          f[0] = f[1] = 1.f;
+        }
+        if (windowed) {
+          const int2 low = *reinterpret_cast<const int2*>(&s.p_min[slot][2 * b]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          // (the first node's window is the shortest reach back; the smallest position is the furthest)
-          const int p = c == 0 ? low.x : c == 1 ? low.y : c == 2 ? low.z : low.w;
-          if (__all_sync(kFull, p == INT32_MAX || p_q - p < a.mods.window)) continue;
+          for (int c = 0; c < 2; ++c) {
+            const int p = c == 0 ? low.x : low.y;          // what lies furthest back
+            if (__all_sync(kFull, p == INT32_MAX || p_q - p < a.mods.window)) continue;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int k = s.pos[slot][c * 32 + e];
-            if (p_q - k >= a.mods.window && k >= t.prefix) y[c][e] = -INFINITY;
+            for (int e = 0; e < 32; ++e) {
+              const int k = s.pos[slot][b * 64 + c * 32 + e];
+              if (p_q - k >= a.mods.window && k >= t.prefix) y[c][e] = -INFINITY;
+            }
           }
         }
       }
-    }
-    if (!whole) {
+      if (!whole) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t bits = tree ? (b ? met[2 + c] : met[c]) : bit_range(0, left - c * 32);
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (!(bits[c] & (1u << e))) y[c][e] = -INFINITY;
-    }
-    float mx[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      mx[c] = fmaxf(y[c][0], y[c][1]);
-#pragma unroll
-      for (int e = 2; e < 32; e += 2) mx[c] = fmax3(mx[c], y[c][e], y[c][e + 1]);
-    }
-    if (!warp_wait(smem_u32(&s.efull[i & 1]), (i >> 1) & 1, abort_flag)) {       // how far the values were scaled
-      fail = true;
-      break;
-    }
-    e_ref = s.e_ref;
-    const int4 e_here = *reinterpret_cast<const int4*>(s.ev[slot]);
-    const float ev[4] = {static_cast<float>(e_here.x), static_cast<float>(e_here.y), static_cast<float>(e_here.z),
-                         static_cast<float>(e_here.w)};
-    const float top = fmaxf(fmaxf(fmaf(mx[0], f[0], ev[0]), fmaf(mx[1], f[1], ev[1])),
-                            fmaxf(fmaf(mx[2], f[2], ev[2]), fmaf(mx[3], f[3], ev[3])));
-    const bool grow = top - m > kGrow;           // also from -inf
-    if (__any_sync(kFull, grow)) {
-      float by = 1.f;
-      if (grow) {
-        by = m == -INFINITY ? 0.f : ex2_approx(m - top);
-        m = top;
-        l *= by;
+          for (int e = 0; e < 32; ++e)
+            if (!(bits & (1u << e))) y[c][e] = -INFINITY;
+        }
       }
-      if (n > 1) {
-        if (!warp_wait(smem_u32(&s.odone[h]), n & 1, abort_flag)) {       // the product of tile n - 2
+      float mx[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        mx[c] = fmaxf(y[c][0], y[c][1]);
+#pragma unroll
+        for (int e = 2; e < 32; e += 2) mx[c] = fmax3(mx[c], y[c][e], y[c][e + 1]);
+      }
+      if (b == 0) {                              // how far the values were scaled
+        if (!warp_wait(smem_u32(&s.efull[i & 1]), (i >> 1) & 1, abort_flag)) {
           fail = true;
           break;
         }
-        tc_fence_after();
+        e_ref = s.e_ref;
+      }
+      const int2 e_here = *reinterpret_cast<const int2*>(&s.ev[slot][2 * b]);
+      const float ev[2] = {static_cast<float>(e_here.x), static_cast<float>(e_here.y)};
+      const float top = fmaxf(fmaf(mx[0], f[0], ev[0]), fmaf(mx[1], f[1], ev[1]));
+      const bool grow = top - m > kGrow;         // also from -inf
+      if (__any_sync(kFull, grow)) {
+        float by = 1.f;
+        if (grow) {
+          by = m == -INFINITY ? 0.f : ex2_approx(m - top);
+          m = top;
+          l *= by;
+        }
+        if (n + b > 0) {
+          if (!warp_wait(smem_u32(&s.odone[h]), (b ^ 1) & 1, abort_flag)) {       // the product of the 64 keys before
+            fail = true;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t o[16];
-          tmem_ld16(o_col + c * 16, o);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o_col + c * 16, o);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
-          tmem_st16(o_col + c * 16, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+            tmem_st16(o_col + c * 16, o);
+          }
         }
       }
-    }
-    const float ref = m == -INFINITY ? 0.f : m;
+      const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float sub = ev[c] - ref;
-      const uint64_t f2 = pair(f[c], f[c]), sub2 = pair(sub, sub);
-      uint64_t sum[2] = {0, 0};
-      uint32_t pk[16];
+      for (int c = 0; c < 2; ++c) {
+        const float sub = ev[c] - ref;
+        const uint64_t f2 = pair(f[c], f[c]), sub2 = pair(sub, sub);
+        uint64_t sum[2] = {0, 0};
+        uint32_t pk[16];
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float p0, p1;
-        unpair(fma2(pair(y[c][e], y[c][e + 1]), f2, sub2), &p0, &p1);
-        p0 = ex2_approx(p0);
-        p1 = ex2_approx(p1);
-        sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(p0, p1));
-        if (rows) unpair(mul2(pair(p0, p1), *reinterpret_cast<const uint64_t*>(&s.vs[slot][c * 32 + e])), &p0, &p1);
-        pk[e / 2] = pack_half2(p0, p1);
+        for (int e = 0; e < 32; e += 4) {
+          const ulonglong2 v = rows ? *reinterpret_cast<const ulonglong2*>(&s.vs[slot][b * 64 + c * 32 + e]) : make_ulonglong2(0, 0);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float p0, p1;
+            unpair(fma2(pair(y[c][e + 2 * k], y[c][e + 2 * k + 1]), f2, sub2), &p0, &p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum[k] = add2(sum[k], pair(p0, p1));
+            if (rows) unpair(mul2(pair(p0, p1), k ? v.y : v.x), &p0, &p1);
+            pk[e / 2 + k] = pack_half2(p0, p1);
+          }
+        }
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), &s0, &s1);
+        l = fmaf(s0 + s1, pow2(e_ref - (c == 0 ? e_here.x : e_here.y)), l);
+        tmem_st16(s_col + b * 64 + c * 16, pk);
       }
-      float s0, s1;
-      unpair(add2(sum[0], sum[1]), &s0, &s1);
-      l = fmaf(s0 + s1, pow2(e_ref - (c == 0 ? e_here.x : c == 1 ? e_here.y : c == 2 ? e_here.z : e_here.w)), l);
-      tmem_st16(s_col + c * 16, pk);
-      if (c == 1) {                              // the product may start on the first half of the keys
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.phalf[h]));
-      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h][b]));
     }
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h]));
   }
   if (bad && valid && a.unit_status) a.unit_status[t.u] = KVC_UNIT_BAD_INDEX;
   // statistics of the row, once they are those of all its keys in this item
@@ -734,7 +752,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
   };
   float m2 = m == -INFINITY ? -INFINITY : m - static_cast<float>(e_ref);
   if (share && valid) write_stats(m2, l);        // while the last product of this stream runs
-  if (!fail && n > 0 && !warp_wait(smem_u32(&s.odone[h]), (n - 1) & 1, abort_flag)) fail = true;
+  if (!fail && n > 0 && !warp_wait(smem_u32(&s.odone[h]), 1, abort_flag)) fail = true;         // the last of 2 n products
   tc_fence_after();
   // One row tile: both streams hold an output for the same rows, in the same lanes of tensor memory.  They exchange
   // (m, l) through the unused second Q tile, and each joins and writes one half of the columns.
@@ -839,9 +857,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       mbar_init(smem_u32(&s.efull[i]), 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&s.sfull[i]), 1);
-      mbar_init(smem_u32(&s.phalf[i]), 4);
-      mbar_init(smem_u32(&s.pfull[i]), 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_u32(&s.sfull[i][b]), 1);
+        mbar_init(smem_u32(&s.pfull[i][b]), 4);
+      }
       mbar_init(smem_u32(&s.odone[i]), 1);
       mbar_init(smem_u32(&s.qfull[i]), 4);
     }
@@ -872,11 +891,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     // (a.stall_unit: a test makes the MMA warp wait for key tiles that never come)
     if (warp == kMmaWarp) issue<D>(t, s, sq, sk, sv, tmem, share, t.u == a.stall_unit);
   } else if (warp >= kKeyWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     const bool v = warp >= kValueWarp;
     make_operands<D, ROW, MODS>(a, t, s, v ? sv : sk, raw + (warp - kKeyWarp) * C::kRaw, v);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     softmax<D, ROW, MODS>(a, t, s, sq, tmem, share);
   }
   tc_fence_before();
