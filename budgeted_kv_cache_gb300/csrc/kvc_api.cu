@@ -505,6 +505,23 @@ struct TreePlan {
   size_t ws_ml = 0, ws_total = 0;
 };
 
+// Blocks that share an item's keys: of as many as fill one to six rounds of the SMs those of least cost, in tiles' times (2
+// us for two row tiles): rounds x (tiles of a split + what an item costs beside them) + the partial outputs' way to memory
+// and back.  Measured (64 units of 20K to 32K rows, 256 query rows): 292 us in 2 (128 items for 152 SMs), 358 in 3, 317 in
+// 4, 270 in 7 (three rounds).  One row tile's two streams take a tile each.
+int32_t tree_splits(int64_t sms, int64_t items, int64_t tiles, bool two_row_tiles, double part_bytes) {
+  const int64_t most = std::min<int64_t>(two_row_tiles ? tiles : (tiles + 1) / 2, 128);
+  int64_t best = 1;
+  double least = 1e300;
+  for (int64_t rounds = 0; rounds <= 6; ++rounds) {
+    const int64_t n = std::max<int64_t>(1, std::min(most, rounds * sms / items));
+    const double cost = static_cast<double>((items * n + sms - 1) / sms) * ((tiles + n - 1) / n + (two_row_tiles ? 3.0 : 5.0)) +
+                        (n > 1 ? 0.5 + n * part_bytes / 26e6 : 0.0);
+    if (cost < least) least = cost, best = n;
+  }
+  return static_cast<int32_t>(best);
+}
+
 kvc_status plan_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n, TreePlan* p) {
   kvc_status st = check_tree(s, r, n);
   if (st != KVC_OK) return st;
@@ -516,7 +533,7 @@ kvc_status plan_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n, TreePl
   p->n_blocks = static_cast<int32_t>((rows + p->block_rows - 1) / p->block_rows);
   const int64_t items = U * p->n_blocks;
   if (items > (1 << 28)) return KVC_ERR_UNSUPPORTED;
-  p->splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(info.sms / items, tiles), 128)));
+  p->splits = tree_splits(info.sms, items, tiles, rows > 128, 8.0 * U * rows * s->head_dim);
   if (p->splits > 1) {
     const size_t parts = static_cast<size_t>(U) * rows * p->splits;
     p->ws_ml = (parts * sizeof(float2) + 255) / 256 * 256;
@@ -1291,6 +1308,7 @@ kvc_status kvc_i4_tree_attn(const kvc_shape* shape, const kvc_i4_rows* rows, con
   a.by_heads = FastDiv::of(a.Hkv);
   a.by_layers = FastDiv::of(a.L);
   a.by_group = FastDiv::of(a.G);
+  a.by_rows = FastDiv::of(static_cast<uint32_t>(a.n) * a.G);
   return launch_tree(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 

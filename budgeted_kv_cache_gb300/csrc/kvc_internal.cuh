@@ -327,7 +327,7 @@ struct TreeArgs {
   int32_t splits;              // blocks that share an item's keys
   float* part_o;               // splits > 1: [U][n G][splits][d] unnormalised outputs
   float2* part_ml;             // [U][n G][splits] (log2-domain maximum, sum)
-  FastDiv by_splits, by_units, by_heads, by_layers, by_group;   // divisors splits, U, Hkv, L, G
+  FastDiv by_splits, by_units, by_heads, by_layers, by_group, by_rows;   // divisors splits, U, Hkv, L, G, n G
 };
 
 // The accepted path of such a tree.
@@ -414,7 +414,6 @@ cudaError_t launch_engine(const DecodeArgs& a, cudaStream_t stream);
 size_t prompt_smem_bytes(int d);
 cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v,
                           const CUtensorMap& map_o, cudaStream_t stream);
-cudaError_t launch_prompt_merge(const PromptArgs& a, cudaStream_t stream);    // joins the splits of every row
 cudaError_t launch_i4_append(const I4AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_read(const I4ReadArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream);

@@ -969,10 +969,7 @@ cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const C
     return bias ? go(prompt_kernel<D, true, true, false>) : go(prompt_kernel<D, true, false, false>);
   };
   const cudaError_t e = a.d == 128 ? go_capped(std::integral_constant<int, 128>{}) : go_capped(std::integral_constant<int, 64>{});
-  return e != cudaSuccess || a.splits == 1 ? e : launch_prompt_merge(a, stream);
-}
-
-cudaError_t launch_prompt_merge(const PromptArgs& a, cudaStream_t stream) {
+  if (e != cudaSuccess || a.splits == 1) return e;
   const int64_t rows = static_cast<int64_t>(a.U) * a.n_q * a.G;
   const unsigned blocks = static_cast<unsigned>((rows + 7) / 8);
   return launch_after(a.d == 128 ? prompt_merge_kernel<128> : prompt_merge_kernel<64>, blocks, 256, 0, stream, a);

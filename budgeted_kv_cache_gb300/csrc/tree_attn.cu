@@ -61,6 +61,7 @@ constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16;        // four, four
 constexpr int kStages = 2;                       // key tiles, and value tiles, in shared memory
 constexpr int kSlots = 4;                        // tiles whose description is held
 constexpr int kAhead = 4;                        // tiles prefetched to L2 behind the one on its way
+constexpr int kLeast = -100;                     // least exponent: rows below 2^-90 lose bits, and 2^-ev stays in range
 constexpr int kNoValues = -40;                   // exponent of 32 rows whose values are all zero: below any that matter
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -72,10 +73,13 @@ struct Bars {
   uint32_t tmem;
   int abort_flag;
   int total;                   // tiles of this item, once that is known
-  int e_ref;                   // ev of the first 32 rows of the first of them
   int tiles[2];                // of each stream
   int j0[kSlots];              // a tile's first slot, or -1 - its first node
-  alignas(16) int ek[kSlots][4], ev[kSlots][4];      // operands are keys times 2^-ek and values times 2^-ev, per 32 rows
+  // operands are keys times 2^-ek and values times 2^-ev, per 32 rows: 2^ek; ev and 2^-ev
+  alignas(16) float k_by[kSlots][4];
+  alignas(16) float2 v_by[kSlots][4];
+  int16_t parent[KVC_TREE_MAX_NODES], depth[KVC_TREE_MAX_NODES];      // of the nodes that the item's rows see
+  float2 ml[2][kTileRows];     // of each stream's rows
   int8_t q_exp[128];           // queries are rows times 2^-q_exp (one row tile)
   // with modifiers: smallest position of 32 rows; positions, and how far they lie behind the first nodes
   alignas(16) int32_t p_min[kSlots][4], pos[kSlots][kKeys];
@@ -126,14 +130,6 @@ __device__ __forceinline__ Item make_item(const TreeArgs& a, int id) {
   return t;
 }
 
-// The parent of node i, -1: none (also for what is no earlier node).
-__device__ __forceinline__ int parent_of(const int32_t* parent, int i, bool* bad) {
-  const int p = parent[i];
-  if (p >= -1 && p < i) return p;
-  *bad = true;
-  return -1;
-}
-
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(max(-126, min(127, e)) + 127) << 23); }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -173,6 +169,15 @@ __device__ __forceinline__ int exponent_of(uint32_t bits) { return static_cast<i
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
+__device__ __forceinline__ uint4 load_shared(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void store_shared(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // 16-byte piece c of row r of an operand tile of 64-element chunks in 128-byte swizzle.
 __device__ __forceinline__ uint4* piece(uint8_t* tile, int r, int c) {
   return reinterpret_cast<uint4*>(tile + (c >> 3) * kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -201,21 +206,31 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
   Scales sc = {};
   int32_t pos = 0;
   auto spot = [&](int r, int c) { return raw + r * (D / 2) + ((c ^ (D == 128 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4); };
+  const uint32_t spot0 = smem_u32(spot(lane / CH, lane % CH)), own_raw = smem_u32(raw) + lane * (D / 2);
+  const int flip = D == 128 ? (lane >> 1) & 3 : (lane >> 2) & 1;
+  constexpr int kStep = 32 / CH;                 // rows of one copy of the warp; the swizzle repeats with them
   auto load = [&](int i) {
     const int left = t.count - i * kKeys - first;
-    const uint8_t* src = codes + static_cast<int64_t>(i) * (kKeys * D / 2);
+    const uint8_t* src = codes + static_cast<int64_t>(i) * (kKeys * D / 2) + lane * 16;
+    const int64_t j = static_cast<int64_t>(i) * kKeys + lane;
+    if (left >= 32) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int p = k * 32 + lane;
-      const bool ok = p / CH < left;
-      cp_async16(smem_u32(spot(p / CH, p % CH)), ok ? src + p * 16 : codes - first * (D / 2), ok);
+      for (int k = 0; k < CH; ++k) cp_async16(spot0 + k * 512, src + k * 512, true);
+      sc = scales[j];
+      if (MODS) pos = a.rows.pos[base + first + j];
+    } else {
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const bool ok = k * kStep + lane / CH < left;
+        cp_async16(spot0 + k * 512, ok ? src + k * 512 : codes - first * (D / 2), ok);
+      }
+      sc = Scales{};
+      if (lane < left) {
+        sc = scales[j];
+        if (MODS) pos = a.rows.pos[base + first + j];
+      }
     }
     cp_async_commit();
-    sc = Scales{};
-    if (lane < left) {
-      sc = scales[static_cast<int64_t>(i) * kKeys + lane];
-      if (MODS) pos = a.rows.pos[base + static_cast<int64_t>(i) * kKeys + first + lane];
-    }
   };
   auto prefetch = [&](int i) {
     const int left = min(32, t.count - i * kKeys - first);
@@ -275,26 +290,18 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
           const float f = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(&own)));
           s.vs[slot][first + lane] = fminf(f * pow2(-e), 2.f);       // a row of zeros may have a scale above the others'
         }
-        if (lane == 0) {
-          s.ev[slot][quarter] = e;
-          if (n == 0 && quarter == 0) s.e_ref = e;
-        }
+        if (lane == 0) s.v_by[slot][quarter] = make_float2(static_cast<float>(e), pow2(-e));
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.efull[st]));
         return;
       }
       if (lane == 0) {
-        s.ek[slot][quarter] = e;
+        s.k_by[slot][quarter] = pow2(e);
         if (quarter == 0) s.j0[slot] = tree ? -1 - j0 : j0;
       }
       const int j = j0 + first + lane;
       if (MODS) {
-        if (tree && j < t.nodes) {
-          const int32_t* parent = a.parent + static_cast<int64_t>(t.b) * a.n;
-          bool bad = false;
-          p = t.next;
-          for (int i = parent_of(parent, j, &bad); i >= 0; i = parent_of(parent, i, &bad)) ++p;
-        }
+        if (tree && j < t.nodes) p = t.next + s.depth[j];
         s.pos[slot][first + lane] = p;
         s.behind[slot][first + lane] = static_cast<float>(t.next - p);
         const int low = __reduce_min_sync(kFull, j < (tree ? t.nodes : t.count) ? p : INT32_MAX);
@@ -319,7 +326,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
       auto zeros = [](const uint4& x) { return (x.x | x.y | x.z | x.w) == 0; };
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        w[k] = *reinterpret_cast<const uint4*>(spot(lane, k));
+        w[k] = load_shared(own_raw + ((k ^ flip) << 4));
         if (v || !ROW) top = max(top, zeros(w[k]) ? 0u : scale(k));
       }
       __syncwarp();
@@ -329,14 +336,14 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
       int e = v ? kNoValues : 0;                 // rows times 2^-e:
       if (v || !ROW) {
         top = __reduce_max_sync(kFull, top);
-        if (top && !ROW) e = max(exponent_of(top) - 10, -126);                 // the largest scale below 2^11
+        if (top && !ROW) e = max(exponent_of(top) - 10, kLeast);               // the largest scale below 2^11
         else if (top) e = static_cast<int>(max(1u, top >> 10)) - 14;           // the largest row scale below 1
       }
       if (!wait_empty()) break;
       publish(e, own, own_pos);
       const float by = pow2(-e);
       const int key = first + lane, x = key & 7;
-      uint8_t* const row = to + key * 128;
+      const uint32_t row = smem_u32(to) + key * 128;
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         uint32_t f = 0x3c003c00u, m;             // a scale per row: the codes alone
@@ -348,7 +355,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
         const uint32_t word[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(row + (k >> 1) * kChunkBytes + ((((k & 1) * 4 + j) ^ x) << 4)) = codes_to_half(word[j], f, m);
+          store_shared(row + (k >> 1) * kChunkBytes + ((((k & 1) * 4 + j) ^ x) << 4), codes_to_half(word[j], f, m));
       }
     } else {
       // the tree's rows, bf16, straight to their places; then turned there, each lane its own pieces
@@ -371,7 +378,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
 #pragma unroll 4
       for (int c = 0; c < BP; ++c) top = max(top, max_bits(*piece(to, first + lane, c)));
       top = __reduce_max_sync(kFull, top);
-      const int e = top ? max(exponent_of(top) - 13, -126) : v ? kNoValues : 0;        // the largest element below 2^14
+      const int e = top ? max(exponent_of(top) - 13, kLeast) : v ? kNoValues : 0;        // the largest element below 2^14
       publish(e, Scales{}, 0);
       const float by = pow2(-e);
 #pragma unroll 2
@@ -497,7 +504,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
     uint8_t* const tile = sq + (share ? h : 0) * C::kTile;
     const __nv_bfloat16* q = a.q + t.b * a.qs.batch + t.l * a.qs.layer;
     const int64_t own = static_cast<int64_t>(head) * a.qs.head + static_cast<int64_t>(node) * a.qs.token;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < 32; i += PER) {
       const int rr = i + lane / LPR;
       const int64_t at = __shfl_sync(kFull, own, rr);
@@ -508,12 +515,12 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
     cp_async_wait<0>();
     __syncwarp();
     uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int c = 0; c < LPR; ++c) top = max(top, max_bits(*piece(tile, r, c)));
     // the largest element below 2^15 (bounded: queries below 2^-100 lose bits, and no score)
     q_exp = top ? max(-112, min(113, exponent_of(top) - 14)) : 0;
     const float by = pow2(-q_exp);
-#pragma unroll 2
+#pragma unroll 4
     for (int c = 0; c < LPR; ++c) {
       uint4* x = piece(tile, r, c);
       *x = bf16_to_half(*x, by);
@@ -531,20 +538,14 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
   const uint32_t s_col = tmem + lanes + h * 128, o_col = tmem + lanes + kOCol + h * 128;
   const bool warp_valid = __any_sync(kFull, valid);
-  const int32_t* parent = a.parent + static_cast<int64_t>(t.b) * a.n;
-  bool bad = false;
-  int depth = 0;
   const bool capped = MODS && a.mods.softcap > 0.f, biased = MODS && a.mods.slopes, windowed = MODS && a.mods.window;
-  if (MODS && (biased || windowed) && valid)
-    for (int i = parent_of(parent, node, &bad); i >= 0; i = parent_of(parent, i, &bad)) ++depth;
-  const int p_q = t.next + depth;
+  const int depth = biased || windowed ? s.depth[node] : 0, p_q = t.next + depth;
   const float slope = biased ? a.mods.slopes[head] * kLog2e : 0.f;
   const float cap = MODS ? a.mods.softcap : 0.f, inv_cap = capped ? fminf(1.f / cap, 1e30f) : 0.f;
-  const float scale = capped ? a.scale : a.scale * kLog2e;
+  const float scale = (capped ? a.scale : a.scale * kLog2e) * pow2(q_exp);
   int up = node;                                 // the lowest ancestor (or the node) that no tile has shown yet
-  float m = -INFINITY, l = 0.f;                  // reference of y + ev (base 2), and sum of 2^(y + e_ref - m)
+  float m = -INFINITY, l = 0.f;                  // reference of y + ev (base 2), and sum of 2^(y - m)
   int n = 0;                                     // tiles of this stream
-  int e_ref = 0;
 #pragma unroll 1
   for (; !fail; ++n) {
     if (!warp_wait(smem_u32(&s.sfull[h][0]), n & 1, abort_flag)) {
@@ -571,13 +572,13 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
     const int j0 = tree ? -1 - j0_or : j0_or;
     uint32_t met[4] = {0, 0, 0, 0};              // keys of a tree's tile that this row sees
     if (tree) {
-      while (up >= j0 + kKeys) up = parent_of(parent, up, &bad);
+      while (up >= j0 + kKeys) up = s.parent[up];
       while (up >= j0) {
         const int j = up - j0;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           if (j >> 5 == c) met[c] |= 1u << (j & 31);
-        up = parent_of(parent, up, &bad);
+        up = s.parent[up];
       }
     }
 #pragma unroll 1
@@ -591,9 +592,9 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
 #pragma unroll
       for (int c = 0; c < 2; ++c) tmem_ld32_issue(s_col + b * 64 + c * 32, sr[c]);
       // y = scores in base 2 = acc f (scores themselves with a cap)
-      const int2 ek = *reinterpret_cast<const int2*>(&s.ek[slot][2 * b]);
-      auto factor = [&](int e) { return fmaxf(scale * pow2(min(120, q_exp + e)), 0x1p-126f); };
-      float f[2] = {factor(ek.x), factor(ek.y)};
+      const float2 k_by = *reinterpret_cast<const float2*>(&s.k_by[slot][2 * b]);
+      auto factor = [&](float by) { return fminf(fmaxf(scale * by, 0x1p-126f), 0x1p120f); };
+      float f[2] = {factor(k_by.x), factor(k_by.y)};
       const int left = t.count - j0 - b * 64;
       const bool whole = !tree && left >= 64;
 #pragma unroll
@@ -602,13 +603,16 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
       // every four scores through one function of packed operations on pairs, with what lies at their keys' places
       auto each = [&](const float* at, auto change) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          ulonglong2 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = at ? *reinterpret_cast<const ulonglong2*>(at + c * 32 + 4 * k) : make_ulonglong2(0, 0);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const ulonglong2 x = at ? *reinterpret_cast<const ulonglong2*>(at + c * 32 + e) : make_ulonglong2(0, 0);
-            unpair(change(pair(y[c][e], y[c][e + 1]), x.x, c), &y[c][e], &y[c][e + 1]);
-            unpair(change(pair(y[c][e + 2], y[c][e + 3]), x.y, c), &y[c][e + 2], &y[c][e + 3]);
+            unpair(change(pair(y[c][e], y[c][e + 1]), x[e / 4].x, c), &y[c][e], &y[c][e + 1]);
+            unpair(change(pair(y[c][e + 2], y[c][e + 3]), x[e / 4].y, c), &y[c][e + 2], &y[c][e + 3]);
           }
+        }
       };
       if (rows) each(&s.ks[slot][b * 64], [&](uint64_t x, uint64_t k, int) { return mul2(x, k); });
       if (MODS) {
@@ -673,15 +677,12 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
 #pragma unroll
         for (int e = 2; e < 32; e += 2) mx[c] = fmax3(mx[c], y[c][e], y[c][e + 1]);
       }
-      if (b == 0) {                              // how far the values were scaled
-        if (!warp_wait(smem_u32(&s.efull[i & 1]), (i >> 1) & 1, abort_flag)) {
-          fail = true;
-          break;
-        }
-        e_ref = s.e_ref;
+      if (b == 0 && !warp_wait(smem_u32(&s.efull[i & 1]), (i >> 1) & 1, abort_flag)) {       // how far the values were scaled
+        fail = true;
+        break;
       }
-      const int2 e_here = *reinterpret_cast<const int2*>(&s.ev[slot][2 * b]);
-      const float ev[2] = {static_cast<float>(e_here.x), static_cast<float>(e_here.y)};
+      const float4 v_by = *reinterpret_cast<const float4*>(&s.v_by[slot][2 * b]);
+      const float ev[2] = {v_by.x, v_by.z};
       const float top = fmaxf(fmaf(mx[0], f[0], ev[0]), fmaf(mx[1], f[1], ev[1]));
       const bool grow = top - m > kGrow;         // also from -inf
       if (__any_sync(kFull, grow)) {
@@ -714,9 +715,12 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
         const uint64_t f2 = pair(f[c], f[c]), sub2 = pair(sub, sub);
         uint64_t sum[2] = {0, 0};
         uint32_t pk[16];
+        ulonglong2 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          v[k] = rows ? *reinterpret_cast<const ulonglong2*>(&s.vs[slot][b * 64 + c * 32 + 4 * k]) : make_ulonglong2(0, 0);
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const ulonglong2 v = rows ? *reinterpret_cast<const ulonglong2*>(&s.vs[slot][b * 64 + c * 32 + e]) : make_ulonglong2(0, 0);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float p0, p1;
@@ -724,13 +728,13 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
             p0 = ex2_approx(p0);
             p1 = ex2_approx(p1);
             sum[k] = add2(sum[k], pair(p0, p1));
-            if (rows) unpair(mul2(pair(p0, p1), k ? v.y : v.x), &p0, &p1);
+            if (rows) unpair(mul2(pair(p0, p1), k ? v[e / 4].y : v[e / 4].x), &p0, &p1);
             pk[e / 2 + k] = pack_half2(p0, p1);
           }
         }
         float s0, s1;
         unpair(add2(sum[0], sum[1]), &s0, &s1);
-        l = fmaf(s0 + s1, pow2(e_ref - (c == 0 ? e_here.x : e_here.y)), l);
+        l = fmaf(s0 + s1, c == 0 ? v_by.y : v_by.w, l);
         tmem_st16(s_col + b * 64 + c * 16, pk);
       }
       tmem_st_wait();
@@ -739,7 +743,6 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
       if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h][b]));
     }
   }
-  if (bad && valid && a.unit_status) a.unit_status[t.u] = KVC_UNIT_BAD_INDEX;
   // statistics of the row, once they are those of all its keys in this item
   const bool part = a.splits > 1;
   const int64_t prow = static_cast<int64_t>(t.u) * a.n * a.G + t.row0 + (valid ? row : 0);
@@ -750,24 +753,22 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
       a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n + node] =
           sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
   };
-  float m2 = m == -INFINITY ? -INFINITY : m - static_cast<float>(e_ref);
+  float m2 = m;
   if (share && valid) write_stats(m2, l);        // while the last product of this stream runs
   if (!fail && n > 0 && !warp_wait(smem_u32(&s.odone[h]), 1, abort_flag)) fail = true;         // the last of 2 n products
   tc_fence_after();
   // One row tile: both streams hold an output for the same rows, in the same lanes of tensor memory.  They exchange
-  // (m, l) through the unused second Q tile, and each joins and writes one half of the columns.
+  // (m, l), and each joins and writes one half of the columns.
   int n_other = 0;
   float f0 = 1.f, f1 = 0.f;
   if (!share) {
-    float2* ml = reinterpret_cast<float2*>(sq + C::kTile);
-    ml[h * kTileRows + r] = make_float2(m2, l);
+    s.ml[h][r] = make_float2(m2, l);
     if (r == 0) s.tiles[h] = n;
     tc_fence_before();
     fail = named_bar_or(1, 256, fail);                       // both streams' products are done
     tc_fence_after();
     n_other = uniform(s.tiles[h ^ 1]);
-    e_ref = s.e_ref;                                         // (a stream without tiles has not read it)
-    const float2 o = ml[(h ^ 1) * kTileRows + r];
+    const float2 o = s.ml[h ^ 1][r];
     const float mm = fmaxf(m2, o.x);
     f0 = m2 == -INFINITY ? 0.f : ex2_approx(m2 - mm);
     f1 = o.x == -INFINITY ? 0.f : ex2_approx(o.x - mm);
@@ -778,16 +779,14 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
   }
   if (!fail && warp_valid) {
     const float inv = part ? 1.f : l > 0.f ? 1.f / l : 0.f;
-    const float back = pow2(e_ref);                          // outputs are 2^e_ref times what is accumulated
-    f0 = f0 * inv * back;
-    f1 = f1 * inv * back;
+    f0 *= inv;
+    f1 *= inv;
     const int64_t own = static_cast<int64_t>(head) * a.os.head + static_cast<int64_t>(node) * a.os.token;
     // this stream's columns, staged in shared memory in 16-byte chunks (Q is not read any more)
     const int cols = share ? D : D / 2, col0 = share ? 0 : h * (D / 2);
     const int chunks = cols / 8, flip = min(chunks - 1, 7);
-    uint8_t* stage = sq + h * C::kTile + (share ? 0 : h * 4096) + quarter * (32 * chunks * 16);
+    uint8_t* stage = sq + h * C::kTile + quarter * (part ? 4096 : 32 * chunks * 16);
     const int pitch = min(chunks, 8) * 16;
-    float* part_o = a.part_o + (prow * a.splits + t.split) * D + col0;
     const uint32_t mine = o_col + col0, other = tmem + lanes + kOCol + (h ^ 1) * 128 + col0;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
@@ -805,12 +804,23 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
         x[e] = __uint_as_float(o0[at]) * f0;
         if (!share) x[e] = fmaf(__uint_as_float(o1[at]), f1, x[e]);
       }
-      if (!valid) continue;
       if (part) {
+        // 32 rows x 32 columns through shared memory, four whole rows per store
+        __syncwarp();
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(part_o + c * 32 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-      } else {
+          *reinterpret_cast<float4*>(stage + lane * 128 + (((e >> 2) ^ (lane & 7)) << 4)) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        __syncwarp();
+        const int row0 = (share ? h * kTileRows : 0) + quarter * 32, at = lane & 7;
+        float* dst = a.part_o + (static_cast<int64_t>(t.u) * a.n * a.G + t.row0 + row0) * a.splits * D + t.split * D + col0 + c * 32 + at * 4;
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          const int rr = k + (lane >> 3);
+          if (row0 + rr < t.rows)
+            *reinterpret_cast<float4*>(dst + static_cast<int64_t>(rr) * a.splits * D) =
+                *reinterpret_cast<const float4*>(stage + rr * 128 + ((at ^ (rr & 7)) << 4));
+        }
+      } else if (valid) {
 #pragma unroll
         for (int e = 0; e < 32; e += 8)
           *reinterpret_cast<uint4*>(stage + (c >> 1) * 4096 + lane * pitch + ((((c & 1) * 4 + e / 8) ^ (lane & flip)) << 4)) =
@@ -867,7 +877,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     mbar_init(smem_u32(&s.done), 1);
     s.abort_flag = 0;
     s.total = INT32_MAX;
-    s.e_ref = 0;
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -877,9 +886,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   wait_for_previous_kernel();
   let_next_kernel_start();
   const Item t = make_item(a, blockIdx.x);
+  bool bad = false;
+  for (int i = threadIdx.x; i < t.nodes; i += kThreads) {
+    const int p = a.parent[static_cast<int64_t>(t.b) * a.n + i];
+    const bool fine = p >= -1 && p < i;
+    s.parent[i] = static_cast<int16_t>(fine ? p : -1);
+    bad |= !fine;
+  }
+  if (bad && a.unit_status) a.unit_status[t.u] = KVC_UNIT_BAD_INDEX;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (MODS && (a.mods.slopes || a.mods.window)) {
+    for (int i = threadIdx.x; i < t.nodes; i += kThreads) {
+      int n = 0;
+      for (int p = s.parent[i]; p >= 0; p = s.parent[p]) ++n;
+      s.depth[i] = static_cast<int16_t>(n);
+    }
+    __syncthreads();
+  }
   const uint32_t tmem = uniform(s.tmem);
   if (t.rows == 0) {                                   // rows past the tree's nodes
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
@@ -906,6 +931,93 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   }
 }
 
+// Joins the splits of every row (PASK Eq. 15): W warps a row, each every W-th split, eight splits' outputs on their way
+// together and with the statistics.  One warp a row up to eight splits, else four.
+constexpr int kMergeThreads = 256;
+
+template <int D, int W>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a) {
+  using Vec = typename std::conditional<D == 128, float4, float2>::type;
+  constexpr int kRows = kMergeThreads / 32 / W;
+  __shared__ float part[W > 1 ? kMergeThreads / 32 : 1][D];
+  __shared__ float2 part_ml[kMergeThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, own = warp % W;
+  const uint32_t R = a.n * a.G, at = blockIdx.x * kRows + warp / W;
+  const bool there = at < a.U * R;                 // (the last block may have fewer rows)
+  uint32_t r, g, l, in_group;
+  const uint32_t u = a.by_rows.divmod(there ? at : 0, &r);
+  const uint32_t b = a.by_layers.divmod(a.by_heads.divmod(u, &g), &l), node = a.by_group.divmod(r, &in_group);
+  const int64_t row = static_cast<int64_t>(u) * R + r;
+  const float2* ml = a.part_ml + row * a.splits;
+  const float* src = a.part_o + row * a.splits * D + lane * (D / 32);
+  wait_for_previous_kernel();
+  let_next_kernel_start();
+  const bool live = there && (!a.n_nodes || static_cast<int>(node) < clamp_count(a.n_nodes[b], a.n));
+  float x[D / 32] = {}, top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+  for (int i0 = live ? own : a.splits; i0 < a.splits; i0 += 8 * W) {
+    Vec o[8] = {};
+    float2 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + W * k;
+      v[k] = make_float2(-INFINITY, 0.f);
+      if (i < a.splits) {
+        o[k] = *reinterpret_cast<const Vec*>(src + static_cast<int64_t>(i) * D);
+        v[k] = ml[i];
+      }
+    }
+    float most = top;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) most = fmaxf(most, v[k].x);
+    const float f = top == -INFINITY ? 0.f : ex2_approx(top - most);
+    top = most;
+    sum *= f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) x[c] *= f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float w = v[k].x == -INFINITY ? 0.f : ex2_approx(v[k].x - top);
+      sum = fmaf(v[k].y, w, sum);
+      const float* e = reinterpret_cast<const float*>(&o[k]);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) x[c] = fmaf(e[c], w, x[c]);
+    }
+  }
+  if (W > 1) {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) part[warp][lane * (D / 32) + c] = x[c];
+    if (lane == 0) part_ml[warp] = make_float2(top, sum);
+    __syncthreads();
+    if (own != 0) return;
+    float2 v[W];
+    top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      v[k] = part_ml[warp + k];
+      top = fmaxf(top, v[k].x);
+    }
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) x[c] = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const float w = v[k].x == -INFINITY ? 0.f : ex2_approx(v[k].x - top);
+      sum = fmaf(v[k].y, w, sum);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) x[c] = fmaf(part[warp + k][lane * (D / 32) + c], w, x[c]);
+    }
+  }
+  if (!live) return;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int64_t head = g * a.G + in_group;
+  __nv_bfloat16* out = a.out + b * a.os.batch + l * a.os.layer + head * a.os.head + node * a.os.token + lane * (D / 32);
+#pragma unroll
+  for (int c = 0; c < D / 32; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(x[c] * inv, x[c + 1] * inv);
+  if (lane == 0 && a.lse)
+    a.lse[((static_cast<int64_t>(b) * a.L + l) * (a.Hkv * a.G) + head) * a.n + node] =
+        sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+}
+
 }  // namespace
 
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
@@ -926,16 +1038,12 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
   };
   const cudaError_t e = a.d == 128 ? go_row(std::integral_constant<int, 128>{}) : go_row(std::integral_constant<int, 64>{});
   if (e != cudaSuccess || a.splits == 1) return e;
-  PromptArgs m = {};                               // what joining the splits of a row needs
-  m.U = a.U, m.L = a.L, m.Hkv = a.Hkv, m.B = a.B, m.G = a.G, m.d = a.d, m.n_q = a.n;
-  m.q_len = a.n_nodes;
-  m.os = a.os;
-  m.out = a.out;
-  m.lse = a.lse;
-  m.splits = a.splits;
-  m.part_o = a.part_o;
-  m.part_ml = a.part_ml;
-  return launch_prompt_merge(m, stream);
+  const int64_t rows = static_cast<int64_t>(a.U) * a.n * a.G;
+  auto join = [&](auto kernel, int per_block) {
+    return launch_after(kernel, dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)), kMergeThreads, 0, stream, a);
+  };
+  if (a.splits <= 8) return a.d == 128 ? join(tree_merge_kernel<128, 1>, 8) : join(tree_merge_kernel<64, 1>, 8);
+  return a.d == 128 ? join(tree_merge_kernel<128, 4>, 2) : join(tree_merge_kernel<64, 4>, 2);
 }
 
 }  // namespace kvc
