@@ -61,6 +61,7 @@ constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16;        // four, four
 constexpr int kStages = 2;                       // key tiles, and value tiles, in shared memory
 constexpr int kSlots = 4;                        // tiles whose description is held
 constexpr int kAhead = 4;                        // tiles prefetched to L2 behind the one on its way
+constexpr int kEnd = INT32_MIN;
 constexpr int kLeast = -100;                     // least exponent: rows below 2^-90 lose bits, and 2^-ev stays in range
 constexpr int kNoValues = -40;                   // exponent of 32 rows whose values are all zero: below any that matter
 constexpr float kLog2e = 1.4426950408889634f;
@@ -72,9 +73,8 @@ struct Bars {
   uint64_t efull[kStages], sfull[2][2], pfull[2][2], odone[2], qfull[2], done;      // [stream][half of a tile's keys]
   uint32_t tmem;
   int abort_flag;
-  int total;                   // tiles of this item, once that is known
   int tiles[2];                // of each stream
-  int j0[kSlots];              // a tile's first slot, or -1 - its first node
+  int j0[2 * kSlots];          // a tile's first slot, or -1 - its first node; kEnd: no more tiles (for either stream)
   // operands are keys times 2^-ek and values times 2^-ev, per 32 rows: 2^ek; ev and 2^-ev
   alignas(16) float k_by[kSlots][4];
   alignas(16) float2 v_by[kSlots][4];
@@ -167,6 +167,17 @@ __device__ __forceinline__ uint32_t max_bits(const uint4& w) {
 // Exponent of a bf16 number's bits (subnormals count as the smallest normal).
 __device__ __forceinline__ int exponent_of(uint32_t bits) { return static_cast<int>(max(1u, bits >> 7)) - 127; }
 
+// What seldom happens is told to the compiler, which puts it out of the way: the roles' loops are long, and a jump over
+// code that is not there yet costs more than what it skips.
+#define SELDOM(x) (__builtin_expect(static_cast<bool>(x), 0))
+
+// warp_wait, its first test in line.
+__device__ __forceinline__ bool wait_for(const uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t at = smem_u32(bar);
+  if (SELDOM(!__all_sync(kFull, try_once(at, parity)))) return warp_wait(at, parity, abort);
+  return true;
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ uint4 load_shared(uint32_t at) {
@@ -213,7 +224,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
     const int left = t.count - i * kKeys - first;
     const uint8_t* src = codes + static_cast<int64_t>(i) * (kKeys * D / 2) + lane * 16;
     const int64_t j = static_cast<int64_t>(i) * kKeys + lane;
-    if (left >= 32) {
+    if (__builtin_expect(left >= 32, 1)) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) cp_async16(spot0 + k * 512, src + k * 512, true);
       sc = scales[j];
@@ -274,10 +285,10 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
   for (int n = 0;; ++n) {
     const int slot = n & (kSlots - 1), st = n & 1;
     const bool tree = cur >= t.cached;
-    auto wait_empty = [&] { return warp_wait(smem_u32(&empty[st]), ((n >> 1) & 1) ^ 1, abort_flag); };
-    if (cur < 0) {                               // the end: one more phase of the keys, without any
+    auto wait_empty = [&] { return wait_for(&empty[st], ((n >> 1) & 1) ^ 1, abort_flag); };
+    if (SELDOM(cur < 0)) {                               // the end: one more phase of the keys, without any
       if (v || !wait_empty()) break;
-      if (threadIdx.x == kKeyWarp * 32) s.total = n;
+      if (threadIdx.x == kKeyWarp * 32) s.j0[n & (2 * kSlots - 1)] = s.j0[(n + 1) & (2 * kSlots - 1)] = kEnd;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s.kfull[st]));
       break;
@@ -297,7 +308,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
       }
       if (lane == 0) {
         s.k_by[slot][quarter] = pow2(e);
-        if (quarter == 0) s.j0[slot] = tree ? -1 - j0 : j0;
+        if (quarter == 0) s.j0[n & (2 * kSlots - 1)] = tree ? -1 - j0 : j0;
       }
       const int j = j0 + first + lane;
       if (MODS) {
@@ -309,7 +320,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
       }
       if (ROW && !tree) s.ks[slot][first + lane] = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(&own)));
     };
-    if (!tree) {
+    if (__builtin_expect(!tree, 1)) {
       // this tile's codes to registers, the next one's on their way
       cp_async_wait<0>();
       const Scales own = sc;
@@ -406,8 +417,8 @@ __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8
   constexpr uint32_t kHalf = kKeys / 2 * 128 >> 4;                 // half of a tile's rows
   const uint32_t idesc_s = kIdesc | (static_cast<uint32_t>(kKeys / 2 >> 3) << 17);
   const uint32_t idesc_o = kIdesc | (static_cast<uint32_t>(D >> 3) << 17) | (1u << 16);     // B (values) MN-major
-  bool ok = warp_wait(smem_u32(&s.qfull[0]), 0, abort_flag);
-  if (ok && share) ok = warp_wait(smem_u32(&s.qfull[1]), 0, abort_flag);
+  bool ok = wait_for(&s.qfull[0], 0, abort_flag);
+  if (ok && share) ok = wait_for(&s.qfull[1], 0, abort_flag);
   const uint32_t elected = elect_one();
   const uint64_t q_desc = sw128_desc(smem_u32(sq)), k_desc = sw128_desc(smem_u32(sk)), val_desc = v_desc(smem_u32(sv));
   // stream h's tile of round j
@@ -417,8 +428,8 @@ __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8
   auto has = [&](int j, int h) -> bool {
     if (over || !ok) return false;
     const int n = tile_of(j, h);
-    if (!warp_wait(smem_u32(stall ? &s.done : &s.kfull[n & 1]), (n >> 1) & 1, abort_flag)) return ok = false;
-    over = n >= uniform(*reinterpret_cast<volatile int*>(&s.total));
+    if (SELDOM(!wait_for(stall ? &s.done : &s.kfull[n & 1], (n >> 1) & 1, abort_flag))) return ok = false;
+    over = uniform(*reinterpret_cast<volatile int*>(&s.j0[n & (2 * kSlots - 1)])) == kEnd;
     return !over;
   };
   auto scores = [&](int j, int h, int b) {
@@ -436,8 +447,8 @@ __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8
   auto values = [&](int j, int h, int b) -> bool {
     const int n = tile_of(j, h);
     const uint32_t st = n & 1;
-    if (b == 0 && (!share || h == 0) && !warp_wait(smem_u32(&s.vfull[st]), (n >> 1) & 1, abort_flag)) return false;
-    if (!warp_wait(smem_u32(&s.pfull[h][b]), j & 1, abort_flag)) return false;
+    if (b == 0 && (!share || h == 0) && SELDOM(!wait_for(&s.vfull[st], (n >> 1) & 1, abort_flag))) return false;
+    if (SELDOM(!wait_for(&s.pfull[h][b], j & 1, abort_flag))) return false;
     tc_fence_after();
     const uint64_t vd = val_desc + st * (C::kTile >> 4) + b * kHalf;
     const uint32_t more = j + b > 0 ? 1u : 0u;
@@ -532,7 +543,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
   }
   bool fail = false;
   if (!share && h == 1) {
-    if (!warp_wait(smem_u32(&s.qfull[0]), 0, abort_flag)) fail = true;
+    if (SELDOM(!wait_for(&s.qfull[0], 0, abort_flag))) fail = true;
     q_exp = s.q_exp[r];
   }
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -548,17 +559,18 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
   int n = 0;                                     // tiles of this stream
 #pragma unroll 1
   for (; !fail; ++n) {
-    if (!warp_wait(smem_u32(&s.sfull[h][0]), n & 1, abort_flag)) {
+    if (SELDOM(!wait_for(&s.sfull[h][0], n & 1, abort_flag))) {
       fail = true;
       break;
     }
     const int i = share ? n : 2 * n + h, slot = i & (kSlots - 1);
-    if (i >= uniform(*reinterpret_cast<volatile int*>(&s.total))) break;
-    if (!warp_valid) {                           // nothing of this warp is a row: the products' results are not read
+    const int j0_or = *reinterpret_cast<volatile int*>(&s.j0[i & (2 * kSlots - 1)]);
+    if (SELDOM(j0_or == kEnd)) break;
+    if (SELDOM(!warp_valid)) {                           // nothing of this warp is a row: the products' results are not read
       tc_fence_after();
       tc_fence_before();
       if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h][0]));
-      if (!warp_wait(smem_u32(&s.sfull[h][1]), n & 1, abort_flag)) {
+      if (SELDOM(!wait_for(&s.sfull[h][1], n & 1, abort_flag))) {
         fail = true;
         break;
       }
@@ -567,11 +579,10 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
       if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h][1]));
       continue;
     }
-    const int j0_or = s.j0[slot];
     const bool tree = j0_or < 0, rows = ROW && !tree;        // rows: a scale per key
     const int j0 = tree ? -1 - j0_or : j0_or;
     uint32_t met[4] = {0, 0, 0, 0};              // keys of a tree's tile that this row sees
-    if (tree) {
+    if (SELDOM(tree)) {
       while (up >= j0 + kKeys) up = s.parent[up];
       while (up >= j0) {
         const int j = up - j0;
@@ -583,7 +594,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
     }
 #pragma unroll 1
     for (int b = 0; b < 2; ++b) {
-      if (b == 1 && !warp_wait(smem_u32(&s.sfull[h][1]), n & 1, abort_flag)) {
+      if (b == 1 && SELDOM(!wait_for(&s.sfull[h][1], n & 1, abort_flag))) {
         fail = true;
         break;
       }
@@ -661,7 +672,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
           }
         }
       }
-      if (!whole) {
+      if (SELDOM(!whole)) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const uint32_t bits = tree ? (b ? met[2 + c] : met[c]) : bit_range(0, left - c * 32);
@@ -677,7 +688,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
 #pragma unroll
         for (int e = 2; e < 32; e += 2) mx[c] = fmax3(mx[c], y[c][e], y[c][e + 1]);
       }
-      if (b == 0 && !warp_wait(smem_u32(&s.efull[i & 1]), (i >> 1) & 1, abort_flag)) {       // how far the values were scaled
+      if (b == 0 && SELDOM(!wait_for(&s.efull[i & 1], (i >> 1) & 1, abort_flag))) {       // how far the values were scaled
         fail = true;
         break;
       }
@@ -685,7 +696,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
       const float ev[2] = {v_by.x, v_by.z};
       const float top = fmaxf(fmaf(mx[0], f[0], ev[0]), fmaf(mx[1], f[1], ev[1]));
       const bool grow = top - m > kGrow;         // also from -inf
-      if (__any_sync(kFull, grow)) {
+      if (SELDOM(__any_sync(kFull, grow))) {
         float by = 1.f;
         if (grow) {
           by = m == -INFINITY ? 0.f : ex2_approx(m - top);
@@ -693,7 +704,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
           l *= by;
         }
         if (n + b > 0) {
-          if (!warp_wait(smem_u32(&s.odone[h]), (b ^ 1) & 1, abort_flag)) {       // the product of the 64 keys before
+          if (SELDOM(!wait_for(&s.odone[h], (b ^ 1) & 1, abort_flag))) {       // the product of the 64 keys before
             fail = true;
             break;
           }
@@ -755,7 +766,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
   };
   float m2 = m;
   if (share && valid) write_stats(m2, l);        // while the last product of this stream runs
-  if (!fail && n > 0 && !warp_wait(smem_u32(&s.odone[h]), 1, abort_flag)) fail = true;         // the last of 2 n products
+  if (!fail && n > 0 && SELDOM(!wait_for(&s.odone[h], 1, abort_flag))) fail = true;         // the last of 2 n products
   tc_fence_after();
   // One row tile: both streams hold an output for the same rows, in the same lanes of tensor memory.  They exchange
   // (m, l), and each joins and writes one half of the columns.
@@ -876,7 +887,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     }
     mbar_init(smem_u32(&s.done), 1);
     s.abort_flag = 0;
-    s.total = INT32_MAX;
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {

@@ -110,6 +110,14 @@ def test_lengths(counts, mode):
     Problem(B=len(counts), G=4, H=1, n=7, counts=counts, mode=mode).call().check()
 
 
+@pytest.mark.parametrize("mode", [G32, ROW], ids=["g32", "row"])
+@pytest.mark.parametrize("n,window", [(9, 0), (40, 0), (40, 500), (9, 500)])
+def test_units_that_fill_the_gpu(n, window, mode):
+    """Every block walks many tiles: one row tile's two streams take them in turn, two row tiles share them."""
+    p = Problem(B=20, G=4, H=8, d=64, n=n, counts=[1500 - 61 * b for b in range(20)], mode=mode, seed=9)
+    p.call(mods=kvc.ScoreMods(window=window)).check(window=window)
+
+
 @pytest.mark.parametrize("G", [1, 2, 3, 5, 7, 8, 33])
 @pytest.mark.parametrize("n", [1, 9, 51])
 def test_groups(G, n):
