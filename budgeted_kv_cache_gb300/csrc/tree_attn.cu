@@ -297,9 +297,9 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
     const int j0 = tree ? ((t.nodes + kKeys - 1) / kKeys - 1 - (cur - t.cached)) * kKeys : cur * kKeys;
     auto publish = [&](int e, Scales own, int32_t p) {      // what the softmax needs of this quarter
       if (v) {
-        if (ROW && !tree) {
+        if (ROW) {
           const float f = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(&own)));
-          s.vs[slot][first + lane] = fminf(f * pow2(-e), 2.f);       // a row of zeros may have a scale above the others'
+          s.vs[slot][first + lane] = tree ? 1.f : fminf(f * pow2(-e), 2.f);      // a row of zeros may have a scale above the others'
         }
         if (lane == 0) s.v_by[slot][quarter] = make_float2(static_cast<float>(e), pow2(-e));
         __syncwarp();
@@ -318,7 +318,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
         const int low = __reduce_min_sync(kFull, j < (tree ? t.nodes : t.count) ? p : INT32_MAX);
         if (lane == 0) s.p_min[slot][quarter] = low;
       }
-      if (ROW && !tree) s.ks[slot][first + lane] = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(&own)));
+      if (ROW) s.ks[slot][first + lane] = tree ? 1.f : __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(&own)));
     };
     if (__builtin_expect(!tree, 1)) {
       // this tile's codes to registers, the next one's on their way
@@ -579,7 +579,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
       if (lane == 0) mbar_arrive(smem_u32(&s.pfull[h][1]));
       continue;
     }
-    const bool tree = j0_or < 0, rows = ROW && !tree;        // rows: a scale per key
+    const bool tree = j0_or < 0;
     const int j0 = tree ? -1 - j0_or : j0_or;
     uint32_t met[4] = {0, 0, 0, 0};              // keys of a tree's tile that this row sees
     if (SELDOM(tree)) {
@@ -625,7 +625,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
           }
         }
       };
-      if (rows) each(&s.ks[slot][b * 64], [&](uint64_t x, uint64_t k, int) { return mul2(x, k); });
+      if (ROW) each(&s.ks[slot][b * 64], [&](uint64_t x, uint64_t k, int) { return mul2(x, k); });
       if (MODS) {
         if (capped) {
           float big = 0.f;
@@ -729,7 +729,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
         ulonglong2 v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          v[k] = rows ? *reinterpret_cast<const ulonglong2*>(&s.vs[slot][b * 64 + c * 32 + 4 * k]) : make_ulonglong2(0, 0);
+          v[k] = ROW ? *reinterpret_cast<const ulonglong2*>(&s.vs[slot][b * 64 + c * 32 + 4 * k]) : make_ulonglong2(0, 0);
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
 #pragma unroll
@@ -739,7 +739,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
             p0 = ex2_approx(p0);
             p1 = ex2_approx(p1);
             sum[k] = add2(sum[k], pair(p0, p1));
-            if (rows) unpair(mul2(pair(p0, p1), k ? v[e / 4].y : v[e / 4].x), &p0, &p1);
+            if (ROW) unpair(mul2(pair(p0, p1), k ? v[e / 4].y : v[e / 4].x), &p0, &p1);
             pk[e / 2 + k] = pack_half2(p0, p1);
           }
         }
