@@ -522,6 +522,19 @@ int32_t tree_splits(int64_t sms, int64_t items, int64_t tiles, bool two_row_tile
   return static_cast<int32_t>(best);
 }
 
+// Blocks that share a unit's cached rows in the mass of a path: as many as fill one to six rounds of the blocks that the
+// SMs hold, by the tiles of 32 keys that a warp (of four) then takes, and three more for its start.
+int32_t tree_mass_splits(int64_t sms, int64_t units, int64_t capacity, int32_t rows) {
+  const int64_t slots = (rows > 16 ? 3 : 4) * sms, tiles = (capacity + 31) / 32, most = (tiles + 3) / 4;
+  int64_t best = 1, least = INT64_MAX;
+  for (int64_t rounds = 0; rounds <= 6; ++rounds) {
+    const int64_t n = std::max<int64_t>(1, std::min(most, rounds * slots / units));
+    const int64_t cost = (units * n + slots - 1) / slots * ((tiles + 4 * n - 1) / (4 * n) + 3);
+    if (cost < least) least = cost, best = n;
+  }
+  return static_cast<int32_t>(best);
+}
+
 kvc_status plan_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n, TreePlan* p) {
   kvc_status st = check_tree(s, r, n);
   if (st != KVC_OK) return st;
@@ -1352,9 +1365,7 @@ kvc_status kvc_i4_tree_commit(const kvc_shape* shape, const kvc_i4_rows* rows, c
   a.k_out = static_cast<__nv_bfloat16*>(k_out);
   a.v_out = static_cast<__nv_bfloat16*>(v_out);
   a.unit_status = unit_status;
-  // one round of the blocks that the SMs hold, each warp of four with a tile of 32 keys at least
-  const int64_t want = std::min<int64_t>(4LL * info.sms / a.U, (static_cast<int64_t>(rows->capacity) + 127) / 128);
-  a.splits = static_cast<int32_t>(std::max<int64_t>(1, want));
+  a.splits = tree_mass_splits(info.sms, a.U, rows->capacity, max_path * a.G);
   return launch_tree_commit(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 

@@ -10,8 +10,8 @@
 // bf16, in the 16-row operand, the key scales applied to the groups' partial
 // sums in fp32.  More than 32 query rows take another pass over the codes each.
 //
-// Rows.  One block per unit, behind the mass (it advances the counters that the
-// other kernel reads): d / 8 lanes a row, as kvc_i4_append.  A row's own mass is
+// Rows.  One block per unit, launched with the mass (only the counters, which
+// the other kernel reads, wait for it): d / 8 lanes a row, as kvc_i4_append.  A row's own mass is
 // the weight that it got from the path behind it: few products, a lane each.
 #include <algorithm>
 #include <type_traits>
@@ -39,12 +39,16 @@ struct Path {
   __device__ __forceinline__ Path(const TreeCommitArgs& a, int u_) : u(u_) {
     b = u / (a.L * a.Hkv), l = u / a.Hkv % a.L, g = u % a.Hkv;
     node = a.path + static_cast<int64_t>(b) * a.max_path;
+    // every load at once: nodes behind the path are not looked at
+    static_assert(KVC_TREE_MAX_PATH <= 64, "two nodes a lane");
+    const int lane = threadIdx.x & 31;
+    const int first = lane < a.max_path ? node[lane] : 0, second = lane + 32 < a.max_path ? node[lane + 32] : 0;
     n = clamp_count(a.path_len[b], a.max_path);
     count = a.rows.count[u];
     base = static_cast<int64_t>(u) * a.rows.capacity;
     status = KVC_UNIT_OK;
-    bool bad = count < 0 || count > a.rows.capacity;
-    for (int i = threadIdx.x & 31; i < n; i += 32) bad |= node[i] < 0 || node[i] >= a.n;
+    const bool bad = count < 0 || count > a.rows.capacity || (lane < n && (first < 0 || first >= a.n)) ||
+                     (lane + 32 < n && (second < 0 || second >= a.n));
     if (__any_sync(kFull, bad)) status = KVC_UNIT_BAD_INDEX;
     else if (n > a.rows.capacity - count) status = KVC_UNIT_FULL;
     if (status != KVC_UNIT_OK) n = 0;
@@ -69,7 +73,7 @@ struct Smem {
 
 // NT: query rows of a pass / 8.  MODS: some change of the scores is asked for.
 template <int D, int NT, bool ROW, bool MODS>
-__global__ void __launch_bounds__(kThreads) tree_mass_kernel(const TreeCommitArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4) tree_mass_kernel(const TreeCommitArgs a) {
   constexpr int NG = D / 32, CH = D / 32;          // scale groups; 16-byte chunks per row
   __shared__ Smem<D, ROW> s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -228,10 +232,17 @@ __global__ void __launch_bounds__(kThreads) tree_mass_kernel(const TreeCommitArg
 #pragma unroll
                 for (int c = 0; c < 4; ++c) big = fmaxf(big, fabsf(y[nt][c]));
               if (__all_sync(kFull, big * inv_cap <= kTanhRange)) {
+                const uint64_t z2 = pair(inv_cap, inv_cap);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                  for (int c = 0; c < 4; ++c) y[nt][c] *= tanh_over_z(y[nt][c] * inv_cap) * kLog2e;
+                  for (int c = 0; c < 4; c += 2) {
+                    const uint64_t x = pair(y[nt][c], y[nt][c + 1]), z = mul2(x, z2), w = mul2(z, z);
+                    uint64_t p = pair(kTanh[4] * kLog2e, kTanh[4] * kLog2e);
+#pragma unroll
+                    for (int k = 3; k >= 0; --k) p = fma2(p, w, pair(kTanh[k] * kLog2e, kTanh[k] * kLog2e));
+                    unpair(mul2(x, p), &y[nt][c], &y[nt][c + 1]);
+                  }
               } else {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -239,14 +250,20 @@ __global__ void __launch_bounds__(kThreads) tree_mass_kernel(const TreeCommitArg
                   for (int c = 0; c < 4; ++c) y[nt][c] = capped_base2(y[nt][c], y[nt][c] * inv_cap, a.mods.softcap);
               }
             }
+            if (biased) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const int dist = p_q[nt][c & 1] - pk[c >> 1];
-                if (biased) y[nt][c] = fmaf(-slope[nt][c & 1], fabsf(static_cast<float>(dist)), y[nt][c]);
-                if (windowed && dist >= a.mods.window && pk[c >> 1] >= prefix) y[nt][c] = -INFINITY;
-              }
+                for (int c = 0; c < 4; ++c)
+                  y[nt][c] = fmaf(-slope[nt][c & 1], fabsf(static_cast<float>(p_q[nt][c & 1] - pk[c >> 1])), y[nt][c]);
+            }
+            if (windowed) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  if (p_q[nt][c & 1] - pk[c >> 1] >= a.mods.window && pk[c >> 1] >= prefix) y[nt][c] = -INFINITY;
+            }
           }
           sum[2 * sub] = sum[2 * sub + 1] = 0.f;
 #pragma unroll
@@ -276,7 +293,9 @@ template <int D, bool ROW>
 __global__ void __launch_bounds__(kRowThreads) tree_rows_commit_kernel(const TreeCommitArgs a) {
   constexpr int LPR = D / 8, RPB = kRowThreads / LPR, NS = ROW ? 1 : D / 32;
   __shared__ float sk[kRowThreads / 32][D];
-  wait_for_previous_kernel();
+  // With q the kernel in front is the one that adds the mass: it touches rows in use alone, and nothing began before
+  // everything in front of it was done.  Only the counters, which it reads, wait for it.
+  if (!a.q) wait_for_previous_kernel();
   const Path un(a, blockIdx.x);
   if (un.status != KVC_UNIT_OK && threadIdx.x == 0 && a.unit_status) a.unit_status[un.u] = un.status;
   if (un.n == 0) return;
@@ -337,6 +356,7 @@ __global__ void __launch_bounds__(kRowThreads) tree_rows_commit_kernel(const Tre
   }
   __syncthreads();
   if (threadIdx.x == 0) {
+    if (a.q) wait_for_previous_kernel();
     a.rows.count[un.u] = un.count + un.n;
     a.rows.next_pos[un.u] = next + un.n;
   }
