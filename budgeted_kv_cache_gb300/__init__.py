@@ -621,6 +621,29 @@ def _pair(fn: str, dev: int, k: torch.Tensor, v: torch.Tensor, s: kvc_shape, n: 
     return strides
 
 
+def _place(fn: str, dev: int, t: torch.Tensor, size: tuple):
+    """Strides of a bf16 tensor of five dimensions (None: dense)."""
+    if t.shape != size or t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        _refuse(fn)
+    if t.is_contiguous():
+        return None
+    st = t.stride()
+    if st[4] != 1:
+        _refuse(fn)
+    return ctypes.byref(kvc_strides(st[0], st[1], st[2], st[3]))
+
+
+def _places(fn: str, dev: int, k: torch.Tensor, v: torch.Tensor, size: tuple):
+    """Strides that keys and values share (those of dimensions of size 1 are not looked at)."""
+    strides = _place(fn, dev, k, size)
+    if v.shape != size or v.dtype is not torch.bfloat16 or v.get_device() != dev:
+        _refuse(fn)
+    if not v.is_contiguous() if strides is None else v.stride() != k.stride():
+        if any(m > 1 and a != b for m, a, b in zip(size, k.stride(), v.stride())):
+            _refuse(fn)
+    return strides
+
+
 def _dense(fn: str, dev: int, t: Optional[torch.Tensor], dtype, n: int) -> Optional[int]:
     """Address of an optional contiguous tensor of n elements."""
     if t is None:
@@ -739,24 +762,31 @@ def kvc_rope(shape, q, k, pos, rope_cos, rope_sin, q_out=None, k_out=None, n_row
     (None: in place) by tables [max_pos][rotary_dim / 2] (see include/kvc.h)."""
     f = "kvc_rope"
     dev = _device(f)
-    x = q if q is not None else k
-    if x is None or x.dim() != 5 or rope_cos.dim() != 2 or (q is None and q_out is not None) or (k is None and k_out is not None):
+    B, L, Hkv, d, i32 = shape.batch, shape.n_layers, shape.n_kv_heads, shape.head_dim, torch.int32
+    x = k if q is None else q
+    if x is None or x.dim() != 5 or rope_cos.dim() != 2:
         _refuse(f)
-    n, f32, i32 = x.shape[3], torch.float32, torch.int32
-    rot = rotary_dim or shape.head_dim
-    if rope_cos.shape[1] * 2 != rot:
+    n, (top, half) = x.shape[3], rope_cos.shape
+    if half * 2 != (rotary_dim or d):
         _refuse(f)
-
-    def place(t, heads):
-        return (None, None) if t is None else (t.data_ptr(), _rows(f, dev, t, shape, heads, n))
-    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
-    (qp, qs), (qop, qos) = place(q, shape.n_q_heads), place(q_out, shape.n_q_heads)
-    (kp, ks), (kop, kos) = place(k, shape.n_kv_heads), place(k_out, shape.n_kv_heads)
+    qp = qs = qop = qos = kp = ks = kop = kos = None
+    if q is not None:
+        size = (B, L, shape.n_q_heads, n, d)
+        qp, qs = q.data_ptr(), _place(f, dev, q, size)
+        qop, qos = (qp, qs) if q_out is None else (q_out.data_ptr(), _place(f, dev, q_out, size))
+    elif q_out is not None:
+        _refuse(f)
+    if k is not None:
+        size = (B, L, Hkv, n, d)
+        kp, ks = k.data_ptr(), _place(f, dev, k, size)
+        kop, kos = (kp, ks) if k_out is None else (k_out.data_ptr(), _place(f, dev, k_out, size))
+    elif k_out is not None:
+        _refuse(f)
     code = _load().kvc_rope(
-        ctypes.byref(shape), qp, qs, kp, ks, n, _dense(f, dev, pos, i32, shape.batch * n),
-        _dense(f, dev, n_rows, i32, shape.batch), _dense(f, dev, rope_cos, f32, rope_cos.numel()),
-        _dense(f, dev, rope_sin, f32, rope_cos.numel()), rope_cos.shape[0], _i32(f, rope_layout), _i32(f, rot),
-        ROPE_INVERSE if inverse else 0, qop, qos, kop, kos, _dense(f, dev, unit_status, i32, _units(shape)),
+        ctypes.byref(shape), qp, qs, kp, ks, n, _dense(f, dev, pos, i32, B * n),
+        None if n_rows is None else _dense(f, dev, n_rows, i32, B), _dense(f, dev, rope_cos, torch.float32, top * half),
+        _dense(f, dev, rope_sin, torch.float32, top * half), top, _i32(f, rope_layout), 2 * half, ROPE_INVERSE if inverse else 0,
+        qop, qos, kop, kos, None if unit_status is None else _dense(f, dev, unit_status, i32, B * L * Hkv),
         _stream(stream, dev))
     if code:
         raise KvcError(f, code)
@@ -823,17 +853,18 @@ def kvc_i4_tree_attn(shape, rows: I4Rows, q, k_new, v_new, parent, out, n_nodes=
     tree's own k_new, v_new [B][L][H_kv][n][d] (see include/kvc.h)."""
     f = "kvc_i4_tree_attn"
     dev = _device(f)
-    B, Hq, i32 = shape.batch, shape.n_q_heads, torch.int32
-    q_strides, n = _rows(f, dev, q, shape, Hq), q.shape[3]
-    ws, ws_bytes = _space(f, dev, workspace)
-    if parent is None:
+    B, L, Hq, Hkv, d, i32 = shape.batch, shape.n_layers, shape.n_q_heads, shape.n_kv_heads, shape.head_dim, torch.int32
+    if q.dim() != 5 or parent is None:
         _refuse(f)
+    n = q.shape[3]
+    size = (B, L, Hq, n, d)
+    ws, ws_bytes = _space(f, dev, workspace)
     code = _load().kvc_i4_tree_attn(
-        ctypes.byref(shape), _cache(f, dev, rows, shape), q.data_ptr(), q_strides, n, k_new.data_ptr(), v_new.data_ptr(),
-        _pair(f, dev, k_new, v_new, shape, n), _dense(f, dev, parent, i32, B * n), _dense(f, dev, n_nodes, i32, B),
-        _mods(f, dev, mods, shape), _f32(f, softmax_scale), out.data_ptr(), _rows(f, dev, out, shape, Hq, n),
-        _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n), _dense(f, dev, unit_status, i32, _units(shape)),
-        ws, ws_bytes, _stream(stream, dev))
+        ctypes.byref(shape), _cache(f, dev, rows, shape), q.data_ptr(), _place(f, dev, q, size), n, k_new.data_ptr(),
+        v_new.data_ptr(), _places(f, dev, k_new, v_new, (B, L, Hkv, n, d)), _dense(f, dev, parent, i32, B * n),
+        None if n_nodes is None else _dense(f, dev, n_nodes, i32, B), _mods(f, dev, mods, shape), _f32(f, softmax_scale),
+        out.data_ptr(), _place(f, dev, out, size), None if row_lse is None else _dense(f, dev, row_lse, torch.float32, B * L * Hq * n),
+        None if unit_status is None else _dense(f, dev, unit_status, i32, B * L * Hkv), ws, ws_bytes, _stream(stream, dev))
     if code:
         raise KvcError(f, code)
 
@@ -845,19 +876,21 @@ def kvc_i4_tree_commit(shape, rows: I4Rows, k_new, v_new, path, path_len, q=None
     and row_lse its softmax weights into the mass (see include/kvc.h)."""
     f = "kvc_i4_tree_commit"
     dev = _device(f)
-    B, Hq, i32 = shape.batch, shape.n_q_heads, torch.int32
-    strides, n = _pair(f, dev, k_new, v_new, shape), k_new.shape[3]
-    if path is None or path_len is None or path.dim() != 2 or (q is None) != (row_lse is None) or (k_out is None) != (v_out is None):
+    B, L, Hq, Hkv, d, i32 = shape.batch, shape.n_layers, shape.n_q_heads, shape.n_kv_heads, shape.head_dim, torch.int32
+    if k_new.dim() != 5 or path is None or path_len is None or path.dim() != 2 or (q is None) != (row_lse is None) or \
+            (k_out is None) != (v_out is None):
         _refuse(f)
-    steps = path.shape[1]
+    n, steps = k_new.shape[3], path.shape[1]
+    qp = qs = lse = ko = vo = os = None
+    if q is not None:
+        qp, qs, lse = q.data_ptr(), _place(f, dev, q, (B, L, Hq, n, d)), _dense(f, dev, row_lse, torch.float32, B * L * Hq * n)
+    if k_out is not None:
+        ko, vo, os = k_out.data_ptr(), v_out.data_ptr(), _places(f, dev, k_out, v_out, (B, L, Hkv, steps, d))
     code = _load().kvc_i4_tree_commit(
-        ctypes.byref(shape), _cache(f, dev, rows, shape), k_new.data_ptr(), v_new.data_ptr(), strides, n,
-        _dense(f, dev, path, i32, B * steps), _dense(f, dev, path_len, i32, B), steps,
-        None if q is None else q.data_ptr(), None if q is None else _rows(f, dev, q, shape, Hq, n),
-        _dense(f, dev, row_lse, torch.float32, B * shape.n_layers * Hq * n), _mods(f, dev, mods, shape), _f32(f, softmax_scale),
-        None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
-        None if k_out is None else _pair(f, dev, k_out, v_out, shape, steps),
-        _dense(f, dev, unit_status, i32, _units(shape)), _stream(stream, dev))
+        ctypes.byref(shape), _cache(f, dev, rows, shape), k_new.data_ptr(), v_new.data_ptr(),
+        _places(f, dev, k_new, v_new, (B, L, Hkv, n, d)), n, _dense(f, dev, path, i32, B * steps),
+        _dense(f, dev, path_len, i32, B), steps, qp, qs, lse, _mods(f, dev, mods, shape), _f32(f, softmax_scale), ko, vo, os,
+        None if unit_status is None else _dense(f, dev, unit_status, i32, B * L * Hkv), _stream(stream, dev))
     if code:
         raise KvcError(f, code)
 
