@@ -773,9 +773,14 @@ kvc_status kvc_i4_evict(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t
  * n_nodes  optional int32 [B], limited to [0, n] (NULL: n).  Rows of out and
  *          row_lse at or past n_nodes[b] are left as they were.
  * row_lse  optional fp32 [B][L][H_q][n], dense.
- * unit_status  optional int32 [U], only errors are written.
- * Keys and values are used as they are stored (code * scale; fp32 scores,
- * statistics and accumulation); bf16 output.
+ * unit_status  optional int32 [U], only errors are written (KVC_UNIT_TIMEOUT if
+ *          a device wait gave up: its rows are then undefined).
+ * Keys and values are used as they are stored (code * scale), but for those
+ * more than 2^24 below the largest of their 32 rows, or below 2^-100; fp32
+ * scores, statistics and accumulation; the weights of the value product are
+ * rounded to fp16 (off by 2^-11 of a weight, and by 2^-25 of the row's largest
+ * product of a weight and a value); bf16 output.
+ * Rows in use hold finite scales, values below 2^119 / capacity in magnitude.
  * workspace >= kvc_i4_tree_attn_workspace_bytes(...), 256-byte aligned,
  *          contents need not be initialised (may be 0 bytes: then NULL is
  *          accepted).
@@ -971,8 +976,8 @@ kvc_status kvc_commit_flags(int32_t batch, int64_t n_tokens, int32_t n_pages,
  *                       of this unit never completes, so after the bounded
  *                       wait (2 s) that unit and every unit its CTA leaves
  *                       unscored report KVC_UNIT_TIMEOUT.
- *                       kvc_prompt_attn: the waits for this unit's first key
- *                       tiles never complete, and the unit reports
+ *                       kvc_prompt_attn, kvc_i4_tree_attn: the waits for this
+ *                       unit's first key tiles never complete, and it reports
  *                       KVC_UNIT_TIMEOUT after the bounded wait (2 s, then 2 s
  *                       more for the copies).
  *   select_stall_unit   -1 = off.  Test hook: in kvc_select (token and page
