@@ -106,7 +106,10 @@ struct Smem {
 };
 
 // MODS: some change of the scores (cap, slopes, window, prefix) is asked for.
-template <int D, int NT, bool ROW, bool MODS>
+// TREE: the queries are the nodes of a drafted tree (a.tree, at most 32 query
+// rows): at next_pos + depth, over the cached rows and over the tree's own bf16
+// rows, which the last warp of the last split takes behind its tiles.
+template <int D, int NT, bool ROW, bool MODS, bool TREE>
 __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn_kernel(const I4AttnArgs a) {
   constexpr int NG = D / 32;                       // scale groups
   constexpr int CH = D / 32;                       // 16-byte chunks per row
@@ -123,6 +126,23 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
   const int32_t next = a.rows.next_pos[un.u];
   const int prefix = MODS && a.mods.prefix_len ? a.mods.prefix_len[un.b] : INT32_MIN;
   const int split = blockIdx.x % a.splits, r0 = blockIdx.x / a.splits * (NT * 8);
+  // a tree's nodes, one a lane: ancestors (and the node itself) as bits, depth
+  uint32_t above = 0;
+  int depth = 0, nodes = 0;
+  if constexpr (TREE) {
+    nodes = a.tree.n_nodes ? clamp_count(a.tree.n_nodes[un.b], a.n_q) : a.n_q;
+    const int32_t* parent = a.tree.parent + static_cast<int64_t>(un.b) * a.n_q;
+    const int up = lane < nodes ? parent[lane] : -1;
+    const bool fine = up >= -1 && up < lane;       // parents come before their children
+    if (lane < nodes && !fine && a.tree.unit_status) a.tree.unit_status[un.u] = KVC_UNIT_BAD_INDEX;
+    above = 1u << lane;
+    int at = fine ? up : -1;
+    for (int i = 1; i < a.n_q; ++i) {              // all lanes together: every step up is another lane's parent
+      if (at >= 0) above |= 1u << at, ++depth;
+      const int p = __shfl_sync(kFull, fine ? up : -1, max(at, 0));
+      at = at >= 0 ? p : -1;
+    }
+  }
   uint32_t qf[NT][NG][4];                          // operand of both products' k-steps of a group
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -198,7 +218,9 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = min(r0 + nt * 8 + 2 * t + e, un.R - 1), i = r / a.G;
-      const int64_t p = a.q_pos ? a.q_pos[un.b * a.n_q + i] : static_cast<int64_t>(next) - a.n_q + i;
+      const int64_t p = TREE      ? static_cast<int64_t>(next) + __shfl_sync(kFull, depth, i)
+                        : a.q_pos ? a.q_pos[un.b * a.n_q + i]
+                                  : static_cast<int64_t>(next) - a.n_q + i;
       q_hi[nt][e] = static_cast<int>(max(p, static_cast<int64_t>(INT32_MIN)));
       q_lo[nt][e] = MODS && a.mods.window ? static_cast<int>(max(p - a.mods.window + 1, static_cast<int64_t>(INT32_MIN))) : INT32_MIN;
       slope[nt][e] = MODS && a.mods.slopes ? a.mods.slopes[un.g * a.G + r % a.G] * kLog2e : 0.f;
@@ -259,6 +281,52 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
 #pragma unroll
       for (int k = 0; k < 8; ++k) o[gr][k >> 2][nt][k & 3] = 0.f;
   }
+
+  // ---- running maximum per query row over the warp's keys; logits y become weights
+  auto take = [&](float (&y)[2][NT][4]) {
+    bool grow = false;
+    float top[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(fmaxf(y[0][nt][e], y[0][nt][e + 2]), fmaxf(y[1][nt][e], y[1][nt][e + 2]));
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, k));
+        top[nt][e] = x;
+        grow |= x - m[nt][e] > kGrow;
+      }
+    if (__any_sync(kFull, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (!(top[nt][e] > m[nt][e])) continue;
+          const float f = m[nt][e] == -INFINITY ? 0.f : ex2_approx(m[nt][e] - top[nt][e]);
+          m[nt][e] = top[nt][e];
+          l[nt][e] *= f;
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              o[gr][mt][nt][e] *= f;
+              o[gr][mt][nt][e + 2] *= f;
+            }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float& x = y[k >> 1][nt][(k & 1) * 2 + e];
+          x = ex2_approx(x - ref);
+          l[nt][e] += x;
+        }
+      }
+  };
 
   int st = 0;
 #pragma unroll 1
@@ -406,49 +474,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
       }
     }
 
-    // ---- running maximum per query row over the warp's keys
-    bool grow = false;
-    float top[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(fmaxf(y[0][nt][e], y[0][nt][e + 2]), fmaxf(y[1][nt][e], y[1][nt][e + 2]));
-#pragma unroll
-        for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, k));
-        top[nt][e] = x;
-        grow |= x - m[nt][e] > kGrow;
-      }
-    if (__any_sync(kFull, grow)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (!(top[nt][e] > m[nt][e])) continue;
-          const float f = m[nt][e] == -INFINITY ? 0.f : ex2_approx(m[nt][e] - top[nt][e]);
-          m[nt][e] = top[nt][e];
-          l[nt][e] *= f;
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              o[gr][mt][nt][e] *= f;
-              o[gr][mt][nt][e + 2] *= f;
-            }
-        }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float& x = y[k >> 1][nt][(k & 1) * 2 + e];
-          x = ex2_approx(x - ref);
-          l[nt][e] += x;
-        }
-      }
+    take(y);
 
     // ---- O^T += V^T P^T
 #pragma unroll
@@ -487,6 +513,80 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
     st = (st + 1) % kStages;
   }
   cp_async_wait<0>();
+
+  if constexpr (TREE) {
+    if (split == a.splits - 1 && warp == kWarps - 1 && nodes > 0) {
+      const int64_t base = un.b * a.tree.news.batch + un.l * a.tree.news.layer + un.g * a.tree.news.head;
+      float y[2][NT][4] = {};
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        const int k0 = sub * 16 + g, k1 = k0 + 8;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          auto piece = [&](int k) {
+            return k < nodes ? *reinterpret_cast<const uint4*>(a.tree.k_new + base + k * a.tree.news.token + 32 * gr + 8 * t)
+                             : make_uint4(0, 0, 0, 0);
+          };
+          const uint4 w0 = piece(k0), w1 = piece(k1);
+          const uint32_t lo[4] = {__byte_perm(w0.x, w0.z, 0x5410), __byte_perm(w1.x, w1.z, 0x5410),
+                                  __byte_perm(w0.x, w0.z, 0x7632), __byte_perm(w1.x, w1.z, 0x7632)};
+          const uint32_t hi[4] = {__byte_perm(w0.y, w0.w, 0x5410), __byte_perm(w1.y, w1.w, 0x5410),
+                                  __byte_perm(w0.y, w0.w, 0x7632), __byte_perm(w1.y, w1.w, 0x7632)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(y[sub][nt], lo, qf[nt][gr][0], qf[nt][gr][1]);
+            mma16816(y[sub][nt], hi, qf[nt][gr][2], qf[nt][gr][3]);
+          }
+        }
+        const int pk[2] = {next + __shfl_sync(kFull, depth, k0), next + __shfl_sync(kFull, depth, k1)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t mine = __shfl_sync(kFull, above, min(r0 + nt * 8 + 2 * t + e, un.R - 1) / a.G);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float& x = y[sub][nt][2 * k + e];
+              x *= pre;
+              if (capped) x = capped_base2(x, x * inv_cap, a.mods.softcap);
+              if (biased) x = fmaf(-slope[nt][e], static_cast<float>(__sad(q_hi[nt][e], pk[k], 0u)), x);
+              const int j = k ? k1 : k0;
+              if (j >= nodes || !((mine >> j) & 1) || (MODS && pk[k] < q_lo[nt][e] && pk[k] >= prefix)) x = -INFINITY;
+            }
+          }
+      }
+      take(y);
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          pb[nt][0] = transpose8x8(pack_bf16x2(y[sub][nt][0], y[sub][nt][1]));
+          pb[nt][1] = transpose8x8(pack_bf16x2(y[sub][nt][2], y[sub][nt][3]));
+        }
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          uint2 w[4];                              // four columns of rows 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int key = sub * 16 + 2 * t + (k & 1) + (k >> 1) * 8;
+            w[k] = key < nodes ? *reinterpret_cast<const uint2*>(a.tree.v_new + base + key * a.tree.news.token + 32 * gr +
+                                                                 8 * (g & 3) + 4 * (g >> 2))
+                               : make_uint2(0, 0);
+          }
+          const uint32_t a0[4] = {__byte_perm(w[0].x, w[1].x, 0x5410), __byte_perm(w[0].x, w[1].x, 0x7632),
+                                  __byte_perm(w[2].x, w[3].x, 0x5410), __byte_perm(w[2].x, w[3].x, 0x7632)};
+          const uint32_t a1[4] = {__byte_perm(w[0].y, w[1].y, 0x5410), __byte_perm(w[0].y, w[1].y, 0x7632),
+                                  __byte_perm(w[2].y, w[3].y, 0x5410), __byte_perm(w[2].y, w[3].y, 0x7632)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(o[gr][0][nt], a0, pb[nt][0], pb[nt][1]);
+            mma16816(o[gr][1][nt], a1, pb[nt][0], pb[nt][1]);
+          }
+        }
+      }
+    }
+  }
 
   // ---- join the warps: sums over the lanes' keys, one reference maximum, outputs added in warp order
 #pragma unroll
@@ -563,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
       for (int k = 0; k < 8; k += 4)
         *reinterpret_cast<float4*>(a.part_o + part * D + d0 + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
       if (d0 == 0) a.part_ml[part] = ml;
-    } else {
+    } else if (!TREE || r < nodes * a.G) {         // (rows behind a tree's nodes are left as they were)
       const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
       *reinterpret_cast<uint4*>(a.out + un.q_at(a, a.os, r) + d0) =
           make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
@@ -746,11 +846,11 @@ __global__ void __launch_bounds__(kFinThreads, 4) i4_finish_kernel(const I4AttnA
   }
 }
 
-template <int D, int NT, bool ROW>
+template <int D, int NT, bool ROW, bool TREE = false>
 cudaError_t launch_one(const I4AttnArgs& a, cudaStream_t stream) {
   // the plain scores' kernel is one of its own: with the branches of the others in its loop it takes 3-4 % longer
   const bool mods = a.mods.softcap > 0.f || a.mods.slopes || a.mods.window || a.mods.prefix_len;
-  auto kernel = mods ? i4_attn_kernel<D, NT, ROW, true> : i4_attn_kernel<D, NT, ROW, false>;
+  auto kernel = mods ? i4_attn_kernel<D, NT, ROW, true, TREE> : i4_attn_kernel<D, NT, ROW, false, TREE>;
   const int bytes = static_cast<int>(sizeof(Smem<D, NT, ROW>));
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
@@ -778,6 +878,23 @@ cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream) {
   const dim3 grid(a.merge_blocks + mass_blocks, std::min(a.U, 65535), (a.U + 65534) / 65535);
   const size_t bytes = a.add_mass ? static_cast<size_t>(a.n_q) * a.G * sizeof(float) : 0;
   return launch_after(a.d == 128 ? i4_finish_kernel<128> : i4_finish_kernel<64>, grid, kFinThreads, bytes, stream, a);
+}
+
+cudaError_t launch_i4_tree(const I4AttnArgs& a, cudaStream_t stream) {
+  const bool row = a.rows.quant_mode == KVC_QUANT_ROW_FP16;
+  const int R = a.n_q * a.G;
+  auto go = [&](auto d, auto r) -> cudaError_t {
+    constexpr int D = decltype(d)::value;
+    constexpr bool ROW = decltype(r)::value;
+    if (R <= 8) return launch_one<D, 1, ROW, true>(a, stream);
+    if constexpr (D == 64)
+      if (R > 16) return launch_one<D, 4, ROW, true>(a, stream);
+    return launch_one<D, 2, ROW, true>(a, stream);
+  };
+  using D128 = std::integral_constant<int, 128>;
+  using D64 = std::integral_constant<int, 64>;
+  if (a.d == 128) return row ? go(D128{}, std::true_type{}) : go(D128{}, std::false_type{});
+  return row ? go(D64{}, std::true_type{}) : go(D64{}, std::false_type{});
 }
 
 }  // namespace kvc

@@ -501,6 +501,7 @@ kvc_status check_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n) {
 }
 
 struct TreePlan {
+  bool few = false;
   int32_t block_rows = 0, n_blocks = 0, splits = 1;
   size_t ws_ml = 0, ws_total = 0;
 };
@@ -546,7 +547,17 @@ kvc_status plan_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n, TreePl
   p->n_blocks = static_cast<int32_t>((rows + p->block_rows - 1) / p->block_rows);
   const int64_t items = U * p->n_blocks;
   if (items > (1 << 28)) return KVC_ERR_UNSUPPORTED;
-  p->splits = tree_splits(info.sms, items, tiles, rows > 128, 8.0 * U * rows * s->head_dim);
+  // Up to 16 query rows (32 at d = 64) the warps of kvc_i4_attn do less for a key than a tile of 128 rows costs.  Measured
+  // (tile of 128 rows / those): 8 units of 131,072 rows x 4 query rows 75 us / 42, x 16 76 / 64, x 32 77 / 116; 8 units of
+  // 2,304 x 4 12.1 / 7.5, x 16 12.4 / 9.2; 64 units of 4,096 at d = 64, x 16 28 / 14, x 32 28 / 19, x 64 28 / 34.
+  p->few = rows <= (s->head_dim == 64 ? 32 : 16);
+  if (p->few) {
+    I4AttnPlan f;
+    if ((st = plan_i4_attn(s, r, n, 0, &f)) != KVC_OK) return st;
+    p->splits = f.splits;
+  } else {
+    p->splits = tree_splits(info.sms, items, tiles, rows > 128, 8.0 * U * rows * s->head_dim);
+  }
   if (p->splits > 1) {
     const size_t parts = static_cast<size_t>(U) * rows * p->splits;
     p->ws_ml = (parts * sizeof(float2) + 255) / 256 * 256;
@@ -1309,6 +1320,7 @@ kvc_status kvc_i4_tree_attn(const kvc_shape* shape, const kvc_i4_rows* rows, con
   a.lse = row_lse;
   a.unit_status = unit_status;
   a.stall_unit = g_score_stall_unit.load(std::memory_order_relaxed);   // failure test hook (-1: none)
+  a.few = p.few;
   a.block_rows = p.block_rows;
   a.n_blocks = p.n_blocks;
   a.splits = p.splits;

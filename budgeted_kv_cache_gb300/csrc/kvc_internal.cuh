@@ -284,6 +284,16 @@ struct I4ReadArgs {
   __nv_bfloat16* v;
 };
 
+// A tree of drafted tokens whose nodes are the queries (parent == NULL: none).
+struct TreeNodes {
+  const int32_t* parent;       // [B][n_q]
+  const int32_t* n_nodes;      // optional [B]
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  kvc_strides news;
+  int32_t* unit_status;        // optional [U]
+};
+
 struct I4AttnArgs {
   int32_t U, L, Hkv, B, G, d, n_q;
   float scale;
@@ -302,6 +312,7 @@ struct I4AttnArgs {
   float* part_o;               // splits > 1: [U][n_q G][splits][d]
   float2* part_ml;             // splits > 1 or add_mass: [U][n_q G][splits]
   float* logits;               // add_mass: [U][capacity][logit_stride], base 2
+  TreeNodes tree;
 };
 
 constexpr int kMaxSplits = 128;      // blocks that share a unit's keys in the 4-bit attention
@@ -322,6 +333,7 @@ struct TreeArgs {
   float* lse;                  // optional [B][L][H_q][n]
   int32_t* unit_status;        // optional [U]
   int32_t stall_unit;          // test hook (-1 = none): this unit's wait for its first key tile never completes
+  bool few;                    // few query rows: the kernel of kvc_i4_attn
   int32_t block_rows;          // packed rows per item: 128 or 256
   int32_t n_blocks;            // items per unit
   int32_t splits;              // blocks that share an item's keys
@@ -417,6 +429,7 @@ cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& map_q, const C
 cudaError_t launch_i4_append(const I4AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_read(const I4ReadArgs& a, cudaStream_t stream);
 cudaError_t launch_i4_attn(const I4AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_i4_tree(const I4AttnArgs& a, cudaStream_t stream);     // partial outputs are not joined
 cudaError_t launch_i4_evict(const I4EvictArgs& a, cudaStream_t stream);
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t stream);

@@ -1046,7 +1046,25 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
   auto go_row = [&](auto d) -> cudaError_t {
     return a.rows.quant_mode == KVC_QUANT_ROW_FP16 ? go_mods(d, std::true_type{}) : go_mods(d, std::false_type{});
   };
-  const cudaError_t e = a.d == 128 ? go_row(std::integral_constant<int, 128>{}) : go_row(std::integral_constant<int, 64>{});
+  cudaError_t e;
+  if (a.few) {
+    I4AttnArgs f = {};
+    f.U = a.U, f.L = a.L, f.Hkv = a.Hkv, f.B = a.B, f.G = a.G, f.d = a.d, f.n_q = a.n;
+    f.scale = a.scale;
+    f.rows = a.rows;
+    f.qs = a.qs, f.os = a.os;
+    f.q = a.q;
+    f.mods = a.mods;
+    f.out = a.out;
+    f.lse = a.lse;
+    f.splits = a.splits;
+    f.part_o = a.part_o;
+    f.part_ml = a.part_ml;
+    f.tree = {a.parent, a.n_nodes, a.k_new, a.v_new, a.news, a.unit_status};
+    e = launch_i4_tree(f, stream);
+  } else {
+    e = a.d == 128 ? go_row(std::integral_constant<int, 128>{}) : go_row(std::integral_constant<int, 64>{});
+  }
   if (e != cudaSuccess || a.splits == 1) return e;
   const int64_t rows = static_cast<int64_t>(a.U) * a.n * a.G;
   auto join = [&](auto kernel, int per_block) {
