@@ -193,11 +193,12 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4) tree_mass_kernel(co
         float sum[4];                              // of keys g, g + 8, g + 16, g + 24
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
+          // without modifiers the sums begin at -lse: y is the weight's exponent
           float y[NT][4];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[nt][c] = 0.f;
+            for (int c = 0; c < 4; ++c) y[nt][c] = ROW || MODS ? 0.f : -lse[nt][c & 1];
           const int k0 = sub * 16 + g, k1 = k0 + 8;
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
@@ -211,15 +212,17 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4) tree_mass_kernel(co
               if constexpr (ROW) {
                 mma16816(y[nt], lo, qf[nt][gr][0], qf[nt][gr][1]);
                 mma16816(y[nt], hi, qf[nt][gr][2], qf[nt][gr][3]);
-                if (gr == NG - 1) y[nt][0] *= f0, y[nt][1] *= f0, y[nt][2] *= f1, y[nt][3] *= f1;
+                if (gr == NG - 1) {
+                  const uint64_t begin = MODS ? 0 : pair(-lse[nt][0], -lse[nt][1]);
+                  unpair(fma2(pair(y[nt][0], y[nt][1]), pair(f0, f0), begin), &y[nt][0], &y[nt][1]);
+                  unpair(fma2(pair(y[nt][2], y[nt][3]), pair(f1, f1), begin), &y[nt][2], &y[nt][3]);
+                }
               } else {
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
                 mma16816(acc, lo, qf[nt][gr][0], qf[nt][gr][1]);
                 mma16816(acc, hi, qf[nt][gr][2], qf[nt][gr][3]);
-                y[nt][0] = fmaf(acc[0], f0, y[nt][0]);
-                y[nt][1] = fmaf(acc[1], f0, y[nt][1]);
-                y[nt][2] = fmaf(acc[2], f1, y[nt][2]);
-                y[nt][3] = fmaf(acc[3], f1, y[nt][3]);
+                unpair(fma2(pair(acc[0], acc[1]), pair(f0, f0), pair(y[nt][0], y[nt][1])), &y[nt][0], &y[nt][1]);
+                unpair(fma2(pair(acc[2], acc[3]), pair(f1, f1), pair(y[nt][2], y[nt][3])), &y[nt][2], &y[nt][3]);
               }
             }
           }
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4) tree_mass_kernel(co
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) big = fmaxf(big, fabsf(y[nt][c]));
+                for (int c = 0; c < 4; c += 2) big = fmax3(big, fabsf(y[nt][c]), fabsf(y[nt][c + 1]));
               if (__all_sync(kFull, big * inv_cap <= kTanhRange)) {
                 const uint64_t z2 = pair(inv_cap, inv_cap);
 #pragma unroll
@@ -265,11 +268,21 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4) tree_mass_kernel(co
                   if (p_q[nt][c & 1] - pk[c >> 1] >= a.mods.window && pk[c >> 1] >= prefix) y[nt][c] = -INFINITY;
             }
           }
-          sum[2 * sub] = sum[2 * sub + 1] = 0.f;
+          uint64_t all[2] = {0, 0};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sum[2 * sub + (c >> 1)] += ex2_approx(y[nt][c] - lse[nt][c & 1]);
+            for (int k = 0; k < 2; ++k) {
+              float w0 = y[nt][2 * k], w1 = y[nt][2 * k + 1];
+              if (MODS) unpair(add2(pair(w0, w1), pair(-lse[nt][0], -lse[nt][1])), &w0, &w1);
+              all[k] = add2(all[k], pair(ex2_approx(w0), ex2_approx(w1)));
+            }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float w0, w1;
+            unpair(all[k], &w0, &w1);
+            sum[2 * sub + k] = w0 + w1;
+          }
         }
         // over the query rows of the four lanes; lane (g, t) then keeps that of key 8 t + g
 #pragma unroll
