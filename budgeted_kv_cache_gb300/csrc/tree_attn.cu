@@ -35,9 +35,9 @@
 // walk up.  With a window, tiles that no row sees are not read: the warps that
 // turn rows into operands decide, and say so to the others tile by tile.
 //
-// Warp roles (20 warps): 0-3 and 4-7 softmax of stream 0 and 1 (128 registers),
-// 8-11 make the keys' operands and 12-15 the values' (88; a quarter of every tile
-// each), 16 tensor memory and MMA issuer (48): 2 x 128 + 2 x 88 + 48 = 5 x 96, what
+// Warp roles (20 warps): 0-3 and 4-7 softmax of stream 0 and 1 (152 registers),
+// 8-11 make the keys' operands and 12-15 the values' (64; a quarter of every tile
+// each), 16 tensor memory and MMA issuer (48): 2 x 152 + 2 x 64 + 48 = 5 x 96, what
 // the block was launched with.  Every wait is bounded; one that gives up raises a
 // shared abort flag, the unit is marked KVC_UNIT_TIMEOUT and the block ends.
 #include <algorithm>
@@ -926,11 +926,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
     // (a.stall_unit: a test makes the MMA warp wait for key tiles that never come)
     if (warp == kMmaWarp) issue<D>(t, s, sq, sk, sv, tmem, share, t.u == a.stall_unit);
   } else if (warp >= kKeyWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     const bool v = warp >= kValueWarp;
     make_operands<D, ROW, MODS>(a, t, s, v ? sv : sk, raw + (warp - kKeyWarp) * C::kRaw, v);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     softmax<D, ROW, MODS>(a, t, s, sq, tmem, share);
   }
   tc_fence_before();
