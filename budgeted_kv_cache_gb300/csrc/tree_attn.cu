@@ -130,6 +130,9 @@ __device__ __forceinline__ Item make_item(const TreeArgs& a, int id) {
   return t;
 }
 
+// Distance back to a position that lies at or before p (up to 2^32 - 1: positions are any 32-bit integers).
+__device__ __forceinline__ uint32_t behind(int p, int before) { return static_cast<uint32_t>(p) - static_cast<uint32_t>(before); }
+
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(max(-126, min(127, e)) + 127) << 23); }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -265,7 +268,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
         const int j = at * kKeys + k * 32 + lane;
         if (j < t.count) {
           const int p = a.rows.pos[base + j];
-          seen |= t.next - p < a.mods.window || p < t.prefix;
+          seen |= behind(t.next, p) < static_cast<uint32_t>(a.mods.window) || p < t.prefix;
         }
       }
       if (__any_sync(kFull, seen)) {
@@ -314,7 +317,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
       if (MODS) {
         if (tree && j < t.nodes) p = t.next + s.depth[j];
         s.pos[slot][first + lane] = p;
-        s.behind[slot][first + lane] = static_cast<float>(t.next - p);
+        s.behind[slot][first + lane] = tree ? -static_cast<float>(p - t.next) : static_cast<float>(behind(t.next, p));
         const int low = __reduce_min_sync(kFull, j < (tree ? t.nodes : t.count) ? p : INT32_MAX);
         if (lane == 0) s.p_min[slot][quarter] = low;
       }
@@ -663,11 +666,11 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int p = c == 0 ? low.x : low.y;          // what lies furthest back
-            if (__all_sync(kFull, p == INT32_MAX || p_q - p < a.mods.window)) continue;
+            if (__all_sync(kFull, p == INT32_MAX || behind(p_q, p) < static_cast<uint32_t>(a.mods.window))) continue;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const int k = s.pos[slot][b * 64 + c * 32 + e];
-              if (p_q - k >= a.mods.window && k >= t.prefix) y[c][e] = -INFINITY;
+              if (behind(p_q, k) >= static_cast<uint32_t>(a.mods.window) && k >= t.prefix) y[c][e] = -INFINITY;
             }
           }
         }

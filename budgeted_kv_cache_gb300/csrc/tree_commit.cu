@@ -30,6 +30,9 @@ constexpr int kStages = 4;
 constexpr int kRowThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Distance back to a position that lies before p (up to 2^32 - 1: positions are any 32-bit integers).
+__device__ __forceinline__ uint32_t behind(int p, int before) { return static_cast<uint32_t>(p) - static_cast<uint32_t>(before); }
+
 // A unit's path: its nodes, and whether they and their rows are fit to be committed (else n = 0).
 struct Path {
   int u, b, l, g, n, count, status;
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4) tree_mass_kernel(co
   };
   // seen by the path's first node (and so by any), or in the prefix
   auto seen_by_any = [&](int i, int32_t p) {
-    return __any_sync(kFull, i < t1 && i * kTile + lane < un.count && (next - p < a.mods.window || p < prefix)) != 0;
+    return __any_sync(kFull, i < t1 && i * kTile + lane < un.count && (behind(next, p) < static_cast<uint32_t>(a.mods.window) || p < prefix)) != 0;
   };
   const bool capped = MODS && a.mods.softcap > 0.f, biased = MODS && a.mods.slopes;
   const float pre = capped ? a.scale : a.scale * kLog2e;
@@ -258,14 +261,14 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4) tree_mass_kernel(co
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                  y[nt][c] = fmaf(-slope[nt][c & 1], fabsf(static_cast<float>(p_q[nt][c & 1] - pk[c >> 1])), y[nt][c]);
+                  y[nt][c] = fmaf(-slope[nt][c & 1], static_cast<float>(behind(p_q[nt][c & 1], pk[c >> 1])), y[nt][c]);
             }
             if (windowed) {
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                  if (p_q[nt][c & 1] - pk[c >> 1] >= a.mods.window && pk[c >> 1] >= prefix) y[nt][c] = -INFINITY;
+                  if (behind(p_q[nt][c & 1], pk[c >> 1]) >= static_cast<uint32_t>(a.mods.window) && pk[c >> 1] >= prefix) y[nt][c] = -INFINITY;
             }
           }
           uint64_t all[2] = {0, 0};
@@ -311,7 +314,10 @@ __global__ void __launch_bounds__(kRowThreads) tree_rows_commit_kernel(const Tre
   if (!a.q) wait_for_previous_kernel();
   const Path un(a, blockIdx.x);
   if (un.status != KVC_UNIT_OK && threadIdx.x == 0 && a.unit_status) a.unit_status[un.u] = un.status;
-  if (un.n == 0) return;
+  if (un.n == 0) {
+    if (a.q) wait_for_previous_kernel();           // whoever comes behind this kernel comes behind that one too
+    return;
+  }
   const int next = a.rows.next_pos[un.u];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int piece = threadIdx.x % LPR, sub = threadIdx.x / LPR;
@@ -367,9 +373,9 @@ __global__ void __launch_bounds__(kRowThreads) tree_rows_commit_kernel(const Tre
       if (lane == 0) a.rows.mass[row0 + j] = sum;
     }
   }
+  if (a.q) wait_for_previous_kernel();
   __syncthreads();
   if (threadIdx.x == 0) {
-    if (a.q) wait_for_previous_kernel();
     a.rows.count[un.u] = un.count + un.n;
     a.rows.next_pos[un.u] = next + un.n;
   }

@@ -761,8 +761,8 @@ kvc_status kvc_i4_evict(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t
  *   out[h][i] = sum_j softmax_j(x_hij) v_j,  row_lse[h][i] = ln sum_j exp(x_hij).
  *
  * rows     as for kvc_i4_attn (mass is not touched: see kvc_i4_tree_commit);
- *          positions of the rows in use lie below next_pos[u], and
- *          next_pos[u] + n below 2^31.
+ *          positions of the rows in use lie below next_pos[u] (any 32-bit
+ *          integers), and next_pos[u] + n below 2^31.
  * q, out   bf16 [B][L][H_q][n][d], strides as in kvc_strides; 1 <= n <=
  *          KVC_TREE_MAX_NODES.
  * k_new, v_new  bf16 [B][L][H_kv][n][d] (keys rotated at the nodes' positions),

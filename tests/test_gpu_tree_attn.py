@@ -78,7 +78,7 @@ class Problem:
     def check(self, sizes=None, scale=None, status=55, **mods):
         torch.cuda.synchronize()
         G = self.G
-        slopes, prefix = mods.pop("slopes", None), mods.pop("prefix", [0] * self.B)
+        slopes, prefix = mods.pop("slopes", None), mods.pop("prefix", [-2 ** 40] * self.B)
         for b in range(self.B):
             m = self.n if sizes is None else max(0, min(self.n, sizes[b]))
             for l in range(self.L):
@@ -111,7 +111,7 @@ def test_lengths(counts, mode):
 
 
 @pytest.mark.parametrize("mode", [G32, ROW], ids=["g32", "row"])
-@pytest.mark.parametrize("n,window", [(9, 0), (40, 0), (40, 500), (9, 500)])
+@pytest.mark.parametrize("n,window", [(9, 0), (40, 0), (40, 500), (9, 500), (4, 0), (2, 500), (8, 500)])
 def test_units_that_fill_the_gpu(n, window, mode):
     """Every block walks many tiles: one row tile's two streams take them in turn, two row tiles share them."""
     p = Problem(B=20, G=4, H=8, d=64, n=n, counts=[1500 - 61 * b for b in range(20)], mode=mode, seed=9)
@@ -133,9 +133,10 @@ def test_strides():
     Problem(B=3, L=2, G=3, H=2, n=21, counts=(140, 5, 333), by_token=True).call().check()
 
 
-def test_padded_trees():
-    p = Problem(B=5, G=4, H=2, n=33, counts=(150, 20, 129, 0, 7))
-    sizes = [33, 0, 1, 17, 999]
+@pytest.mark.parametrize("G,n,d", [(4, 33, 128), (1, 16, 128), (2, 16, 64), (4, 4, 64)])
+def test_padded_trees(G, n, d):
+    p = Problem(B=5, G=G, H=2, n=n, d=d, counts=(150, 20, 129, 0, 7))
+    sizes = [n, 0, 1, n // 2, 999]
     for b, m in enumerate(sizes):                              # what is no node may hold any bits
         p.q[b, :, :, m:] = float("nan")
         p.k[b, :, :, m:] = float("nan")
@@ -151,9 +152,11 @@ MODS = [dict(softcap=20.0), dict(softcap=1.0), dict(slopes=True), dict(window=1)
 
 @pytest.mark.parametrize("mods", MODS, ids=lambda m: "-".join(f"{k}{v}" for k, v in m.items()))
 @pytest.mark.parametrize("mode", [G32, ROW], ids=["g32", "row"])
-def test_modifiers(mods, mode):
-    p = Problem(B=2, G=4, H=2, d=64, n=20, counts=(700, 129), mode=mode, kind="random", seed=3)
-    slopes = torch.tensor([2.0 ** -(h + 1) for h in range(8)], device="cuda") if mods.get("slopes") else None
+@pytest.mark.parametrize("G,n,d", [(4, 20, 64), (4, 2, 128), (1, 15, 128), (2, 13, 64)])
+def test_modifiers(mods, mode, G, n, d):
+    """Over the tiles of 128 query rows, and over few rows."""
+    p = Problem(B=2, G=G, H=2, d=d, n=n, counts=(700, 129), mode=mode, kind="random", seed=3)
+    slopes = torch.tensor([2.0 ** -(h + 1) for h in range(2 * G)], device="cuda") if mods.get("slopes") else None
     prefix = [90, 3] if mods.get("prefix") else None
     m = kvc.ScoreMods(mods.get("softcap", 0.0), slopes, mods.get("window", 0), None if prefix is None else i32(prefix))
     p.call(mods=m).check(softcap=mods.get("softcap", 0.0), slopes=slopes, window=mods.get("window", 0), prefix=prefix or [0, 0])
@@ -172,6 +175,23 @@ def test_rows_in_any_order():
         for t in (p.rows.k, p.rows.v, p.rows.k_scale, p.rows.v_scale, p.rows.pos):
             t[u, :1000] = t[u, :1000][order]
     p.call(mods=kvc.ScoreMods(window=300)).check(window=300)
+
+
+@pytest.mark.parametrize("G,n", [(1, 9), (4, 20)])
+@pytest.mark.parametrize("nxt", [2 ** 31 - 30, 0, -2 ** 31 + 2000])
+def test_positions_over_all_of_int32(G, n, nxt):
+    """Distances past 31 bits: far rows are outside a window, and slopes of 2^-30 still tell them apart."""
+    p = Problem(B=1, G=G, H=2, n=n, counts=(700,), seed=6)
+    pos = torch.randint(-2 ** 31, nxt, (2, 700), generator=gen(3), device="cuda")
+    pos[:, :300] = nxt - 1 - torch.arange(300, device="cuda")
+    pos[:, 300] = -2 ** 31
+    p.rows.pos[:, :700] = pos.to(torch.int32)
+    p.rows.next_pos.fill_(nxt)
+    p.call(mods=kvc.ScoreMods(window=250)).check(window=250)
+    slopes = torch.full((2 * G,), 2.0 ** -30, device="cuda")
+    p.call(mods=kvc.ScoreMods(slopes=slopes)).check(slopes=slopes)
+    slopes = torch.full((2 * G,), 0.5, device="cuda")
+    p.call(mods=kvc.ScoreMods(slopes=slopes, window=2 ** 31 - 1)).check(slopes=slopes, window=2 ** 31 - 1)
 
 
 def test_scale_and_missing_outputs():
@@ -208,8 +228,9 @@ def test_groups_of_zeros_beside_small_values():
     p.call().check()
 
 
-def test_parents_that_are_no_earlier_node():
-    p = Problem(B=3, L=1, G=2, H=2, n=12, counts=(50, 60, 70))
+@pytest.mark.parametrize("G", [1, 2])
+def test_parents_that_are_no_earlier_node(G):
+    p = Problem(B=3, L=1, G=G, H=2, n=12, counts=(50, 60, 70))
     for i, bad in ((3, 3), (5, 8), (7, -2), (9, 2 ** 31 - 1), (10, -2 ** 31)):
         p.parent[1, i] = bad
         p.parents[1][i] = -1
@@ -228,8 +249,9 @@ def test_counts_outside_the_capacity_are_limited():
     p.check()
 
 
-def test_capture_streams_and_repeats():
-    p = Problem(B=2, G=4, H=2, n=17, counts=(3000, 1200))
+@pytest.mark.parametrize("G", [4, 1])
+def test_capture_streams_and_repeats(G):
+    p = Problem(B=2, G=G, H=2, n=17, counts=(3000, 1200))
     p.call()
     torch.cuda.synchronize()
     first, lse = p.out.clone(), p.lse.clone()

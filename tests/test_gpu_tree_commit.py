@@ -59,7 +59,7 @@ class Commit(Problem):
     def commit(self, with_mass=True, scale=0.0, mods=None, **about):
         r = self.rows
         self.want, full = {}, 1 / math.sqrt(self.d) if not scale else scale
-        slopes, prefix = about.get("slopes"), about.get("prefix", [0] * self.B)
+        slopes, prefix = about.get("slopes"), about.get("prefix", [-2 ** 40] * self.B)
         for b in range(self.B):
             for l in range(self.L):
                 for h in range(self.H):
@@ -171,6 +171,29 @@ def test_without_queries_and_without_mass():
     for name in ("k", "pos", "count", "next_pos"):
         assert torch.equal(getattr(q.rows, name), getattr(p.rows, name))
     assert len(before) == 8
+
+
+@pytest.mark.parametrize("nxt", [2 ** 31 - 30, 0, -2 ** 31 + 2000])
+def test_positions_over_all_of_int32(nxt):
+    for about in (dict(window=250), dict(slopes=torch.full((8,), 2.0 ** -30, device="cuda"))):
+        p = Commit(steps=4, B=1, G=4, H=2, n=20, counts=(700,), spare=4, kind="chain", seed=6)
+        pos = torch.randint(-2 ** 31, nxt, (2, 700), generator=gen(3), device="cuda")
+        pos[:, :300] = nxt - 1 - torch.arange(300, device="cuda")
+        pos[:, 300] = -2 ** 31
+        p.rows.pos[:, :700] = pos.to(torch.int32)
+        p.rows.next_pos.fill_(nxt)
+        p.commit(mods=kvc.ScoreMods(0.0, about.get("slopes"), about.get("window", 0)), **about).check_commit()
+
+
+def test_nothing_accepted_then_more():
+    """A step that accepts nothing, with calls in front of and behind it in the stream."""
+    p = Commit(steps=3, sizes=[0, 0], B=2, G=4, H=2, n=9, counts=(500, 300), spare=8)
+    p.commit().check_commit()
+    for _ in range(4):
+        p.again()
+        kvc.kvc_i4_append(p.shape, p.rows, p.k[:, :, :, :1], p.v[:, :, :, :1])
+    torch.cuda.synchronize()
+    assert p.rows.count.tolist() == [504, 504, 304, 304]
 
 
 def test_scale():

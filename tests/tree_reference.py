@@ -38,7 +38,7 @@ def trees(kind, n, seed=0):
     return [int(r.randint(max(-1, i - 9), i)) if i else -1 for i in range(n)]
 
 
-def heads_of(rows, u, q, k_new, v_new, parent, scale, softcap=0.0, slopes=None, window=0, prefix=0):
+def heads_of(rows, u, q, k_new, v_new, parent, scale, softcap=0.0, slopes=None, window=0, prefix=-2 ** 40):
     """One unit: q [G][n][d], k_new, v_new [n][d] (64 bits, nodes only): what attend gives for each head, and the values."""
     G, n, d = q.shape
     count, nxt = int(rows.count[u]), int(rows.next_pos[u])
