@@ -105,10 +105,21 @@ struct Smem {
   float2 ml[NT * 8];                               // of the block
 };
 
+// Two weights of adjacent query rows as bf16 operands; with FINE also what the rounding left of them (then off by 2^-18).
+template <bool FINE>
+__device__ __forceinline__ void weights(float x, float y, uint32_t* w, uint32_t* rest) {
+  const uint32_t hi = pack_bf16x2(x, y);
+  *w = transpose8x8(hi);
+  if constexpr (FINE) *rest = transpose8x8(pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u)));
+}
+
 // MODS: some change of the scores (cap, slopes, window, prefix) is asked for.
 // TREE: the queries are the nodes of a drafted tree (a.tree, at most 32 query
 // rows): at next_pos + depth, over the cached rows and over the tree's own bf16
-// rows, which the last warp of the last split takes behind its tiles.
+// rows, which the last warp of the last split takes behind its tiles.  Weights
+// go in as two bf16 operands, so that they are no coarser than where more query
+// rows take fp16 ones (8 units of 131,072 rows, 4 query rows: 42 us with one
+// operand, 48 with two; fp16 would need the values' sizes tile by tile).
 template <int D, int NT, bool ROW, bool MODS, bool TREE>
 __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn_kernel(const I4AttnArgs a) {
   constexpr int NG = D / 32;                       // scale groups
@@ -483,14 +494,14 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
       float f0[NG], f1[NG];
       scale_f(1, k0, f0);
       scale_f(1, k1, f1);
-      uint32_t pb[NT][2];
+      uint32_t pb[NT][2], rest[NT][2];
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         if (!ROW || gr == 0) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            pb[nt][0] = transpose8x8(pack_bf16x2(y[sub][nt][0] * f0[gr], y[sub][nt][1] * f0[gr]));
-            pb[nt][1] = transpose8x8(pack_bf16x2(y[sub][nt][2] * f1[gr], y[sub][nt][3] * f1[gr]));
+            weights<TREE>(y[sub][nt][0] * f0[gr], y[sub][nt][1] * f0[gr], &pb[nt][0], &rest[nt][0]);
+            weights<TREE>(y[sub][nt][2] * f1[gr], y[sub][nt][3] * f1[gr], &pb[nt][1], &rest[nt][1]);
           }
         }
         uint32_t w[4];                             // rows 2t, 2t + 1, 2t + 8, 2t + 9; word g & 3 of the chunk
@@ -506,6 +517,10 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
         for (int nt = 0; nt < NT; ++nt) {
           mma16816(o[gr][0][nt], a0, pb[nt][0], pb[nt][1]);
           mma16816(o[gr][1][nt], a1, pb[nt][0], pb[nt][1]);
+          if constexpr (TREE) {
+            mma16816(o[gr][0][nt], a0, rest[nt][0], rest[nt][1]);
+            mma16816(o[gr][1][nt], a1, rest[nt][0], rest[nt][1]);
+          }
         }
       }
     }
@@ -558,11 +573,11 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
       take(y);
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
-        uint32_t pb[NT][2];
+        uint32_t pb[NT][2], rest[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          pb[nt][0] = transpose8x8(pack_bf16x2(y[sub][nt][0], y[sub][nt][1]));
-          pb[nt][1] = transpose8x8(pack_bf16x2(y[sub][nt][2], y[sub][nt][3]));
+          weights<TREE>(y[sub][nt][0], y[sub][nt][1], &pb[nt][0], &rest[nt][0]);
+          weights<TREE>(y[sub][nt][2], y[sub][nt][3], &pb[nt][1], &rest[nt][1]);
         }
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
@@ -582,6 +597,8 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
           for (int nt = 0; nt < NT; ++nt) {
             mma16816(o[gr][0][nt], a0, pb[nt][0], pb[nt][1]);
             mma16816(o[gr][1][nt], a1, pb[nt][0], pb[nt][1]);
+            mma16816(o[gr][0][nt], a0, rest[nt][0], rest[nt][1]);
+            mma16816(o[gr][1][nt], a1, rest[nt][0], rest[nt][1]);
           }
         }
       }

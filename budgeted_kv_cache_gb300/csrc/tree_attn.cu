@@ -14,8 +14,9 @@
 // keys, 2^-ev for values; it is taken back in fp32: 2^ek goes into the softmax
 // scale, 2^ev into the running maximum).  Elements more than 2^24 below the
 // largest of their 32 rows lose bits to the format's end.  A scale per row in fp16 has 11
-// bits itself: there the operands are the plain codes, and the scales multiply
-// the scores and the weights in fp32.  Queries are scaled to fp16 per row alike;
+// bits itself: there the operands are the plain codes (beside which the tree's
+// values are kept below 2^3, and lose bits from 2^20 below the largest on), and
+// the scales multiply the scores and the weights in fp32.  Queries are scaled to fp16 per row alike;
 // they, and the tree's rows, come in 8 bits.
 //   S = Q K^T      tcgen05, both operands in shared memory, S in tensor memory
 //   softmax        128 threads, one row each, in base 2; the weights are rounded
@@ -392,7 +393,9 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
 #pragma unroll 4
       for (int c = 0; c < BP; ++c) top = max(top, max_bits(*piece(to, first + lane, c)));
       top = __reduce_max_sync(kFull, top);
-      const int e = top ? max(exponent_of(top) - 13, kLeast) : v ? kNoValues : 0;        // the largest element below 2^14
+      // the largest element below 2^14, as a group's code times its scale; below 2^3, as a plain code, with a scale per
+      // row: what the weights are multiplied by is of one size in all tiles, so that none is smaller than it has to be
+      const int e = top ? max(exponent_of(top) - (v && ROW ? 2 : 13), kLeast) : v ? kNoValues : 0;
       publish(e, Scales{}, 0);
       const float by = pow2(-e);
 #pragma unroll 2

@@ -776,7 +776,8 @@ kvc_status kvc_i4_evict(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t
  * unit_status  optional int32 [U], only errors are written (KVC_UNIT_TIMEOUT if
  *          a device wait gave up: its rows are then undefined).
  * Keys and values are used as they are stored (code * scale), but for those
- * more than 2^24 below the largest of their 32 rows, or below 2^-100; fp32
+ * more than 2^24 (the tree's values beside a scale per row: 2^20) below the
+ * largest of their 32 rows, or below 2^-100, which lose bits; fp32
  * scores, statistics and accumulation; the weights of the value product are
  * rounded to fp16 (off by 2^-11 of a weight, and by 2^-25 of the row's largest
  * product of a weight and a value); bf16 output.
@@ -816,11 +817,12 @@ kvc_status kvc_i4_tree_attn(const kvc_shape* shape, const kvc_i4_rows* rows, con
  *          checked).  1 <= max_path <= n, KVC_TREE_MAX_PATH at most.
  * path_len int32 [B], limited to [0, max_path]; 0 leaves a sequence as it was.
  * q, row_lse, mods, softmax_scale  as given to kvc_i4_tree_attn, and its
- *          row_lse; q NULL: no mass is added, the new rows start with 0.
- *          With q, rows->mass is required.
+ *          row_lse (of -inf: no weight); q NULL: no mass is added, the new rows
+ *          start with 0.  With q, rows->mass is required.
  * k_out, v_out  optional (both or none) bf16 [B][L][H_kv][max_path][d], strides
  *          as in kvc_strides: the new rows as the cache holds them (code *
- *          scale, rounded once), for a bf16 store of recent rows beside it.
+ *          scale, rounded once), for a bf16 store of recent rows beside it;
+ *          they overlap neither each other nor k_new and v_new.
  *          Rows at or past path_len[b] are left as they were.
  * unit_status  optional int32 [U], only errors are written: KVC_UNIT_FULL if
  *          the rows do not fit, KVC_UNIT_BAD_INDEX if a node of the path is

@@ -1,7 +1,7 @@
 """Trees of drafted tokens over a 4-bit cache in 64 bits, and how far a kernel may be from them: the bounds of
-attn_reference (a weight's rounding counted at bf16's half step, the coarsest one), and one more of the output.
+attn_reference, but for a weight's rounding, which is fp16's half step at most, and one more of the output.
 
-A weight is held in 16 bits or more, relative to the largest product of a weight and its tile's largest value:
+A weight is held in fp16 or finer, relative to the largest product of a weight and its tile's largest value:
 P'' = 2^(y + e - M) with M within the maximum of y + e, 2^e the size of the tile's values.  Below 2^-14 fp16 has
 steps of 2^-24 (below 2^-126 fp32 has none), so P'' is off by at most 2^-25 there, and the output by 2^-25 of a
 product 2^(M - L) V' <= max_j w_j max|v|, L the row's log-sum-exp: at most n 2^-25 max|v| over n keys."""
@@ -61,7 +61,7 @@ def tree_attention(rows, u, q, k_new, v_new, parent, scale, **mods):
     """out, lse and their bounds, [G][n]."""
     got, v = heads_of(rows, u, q, k_new, v_new, parent, scale, **mods)
     got = [torch.stack([x[i] for x in got]) for i in range(5)]
-    got[3] = got[3] + v.shape[0] * 2.0 ** -25 * v.abs().max()
+    got[3] = got[3] + v.shape[0] * 2.0 ** -25 * v.abs().max() - (2.0 ** -8 - 2.0 ** -11) * (got[2] @ v.abs())
     return got
 
 
