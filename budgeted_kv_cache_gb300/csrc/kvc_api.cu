@@ -548,8 +548,9 @@ kvc_status plan_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n, TreePl
   const int64_t items = U * p->n_blocks;
   if (items > (1 << 28)) return KVC_ERR_UNSUPPORTED;
   // Up to 16 query rows (32 at d = 64) the warps of kvc_i4_attn do less for a key than a tile of 128 rows costs.  Measured
-  // (tile of 128 rows / those): 8 units of 131,072 rows x 4 query rows 75 us / 42, x 16 76 / 64, x 32 77 / 116; 8 units of
-  // 2,304 x 4 12.1 / 7.5, x 16 12.4 / 9.2; 64 units of 4,096 at d = 64, x 16 28 / 14, x 32 28 / 19, x 64 28 / 34.
+  // (tile of 128 rows / those): 8 units of 131,072 rows x 4 query rows 75 us / 48, x 16 76 / 81 (85 / 64 with a scale per
+  // row), x 32 77 / 116; 64 units of 32,768 x 4 157 / 85, x 16 159 / 139; 8 units of 2,304 x 4 12.1 / 7.8, x 16 12.4 /
+  // 10.1; 64 units of 4,096 at d = 64, x 16 28 / 15, x 32 28 / 25, x 64 28 / 34.
   p->few = rows <= (s->head_dim == 64 ? 32 : 16);
   if (p->few) {
     I4AttnPlan f;
@@ -1347,6 +1348,7 @@ kvc_status kvc_i4_tree_commit(const kvc_shape* shape, const kvc_i4_rows* rows, c
   if (max_path < 1 || max_path > n) return KVC_ERR_INVALID_ARG;
   if (max_path > KVC_TREE_MAX_PATH) return KVC_ERR_UNSUPPORTED;
   if (!k_new || !v_new || !path || !path_len || (k_out == nullptr) != (v_out == nullptr)) return KVC_ERR_INVALID_ARG;
+  if (k_out && (k_out == k_new || k_out == v_new || v_out == k_new || v_out == v_new || k_out == v_out)) return KVC_ERR_INVALID_ARG;
   if (q && (!row_lse || !rows->mass)) return KVC_ERR_INVALID_ARG;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(q, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
     return KVC_ERR_INVALID_ARG;

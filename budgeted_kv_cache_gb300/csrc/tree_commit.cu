@@ -59,8 +59,10 @@ struct Path {
   __device__ __forceinline__ int64_t q_at(const TreeCommitArgs& a, int i, int h) const {
     return b * a.qs.batch + l * a.qs.layer + static_cast<int64_t>(g * a.G + h) * a.qs.head + node[i] * a.qs.token;
   }
+  // base 2; infinity, which makes every weight 0, for a row that saw nothing
   __device__ __forceinline__ float lse2(const TreeCommitArgs& a, int i, int h) const {
-    return a.row_lse[((static_cast<int64_t>(b) * a.L + l) * (a.Hkv * a.G) + g * a.G + h) * a.n + node[i]] * kLog2e;
+    const float x = a.row_lse[((static_cast<int64_t>(b) * a.L + l) * (a.Hkv * a.G) + g * a.G + h) * a.n + node[i]];
+    return x == -INFINITY ? INFINITY : x * kLog2e;
   }
   __device__ __forceinline__ int64_t new_at(const TreeCommitArgs& a, const kvc_strides& s, int row) const {
     return b * s.batch + l * s.layer + g * s.head + row * s.token;

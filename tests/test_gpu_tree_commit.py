@@ -185,6 +185,26 @@ def test_positions_over_all_of_int32(nxt):
         p.commit(mods=kvc.ScoreMods(0.0, about.get("slopes"), about.get("window", 0)), **about).check_commit()
 
 
+@pytest.mark.parametrize("G,steps,window", [(1, 3, 0), (4, 4, 0), (4, 3, 200)])
+def test_statistics_of_rows_that_saw_nothing(G, steps, window):
+    """Such a row has no weights, whatever its scores: the second node's rows are those."""
+    p = Commit(steps=steps, B=1, G=G, H=2, n=9, counts=(150,), spare=steps, kind="chain")
+    mods = kvc.ScoreMods(window=window) if window else None
+    p.commit(mods=mods, window=window)
+    kept = p.rows.mass.clone()
+    p.lse[:, :, :, p.paths[0][1]] = -math.inf
+    for x, x0 in zip(fields(p.rows), p.before):
+        x.copy_(x0)
+    p.again()
+    torch.cuda.synchronize()
+    used = slice(0, 150 + steps)
+    now = p.rows.mass[:, used]
+    assert bool(torch.isfinite(now).all()) and bool((now <= kept[:, used]).all())
+    # less by the weights of G rows
+    lost = (kept[:, used] - now).double().sum(1)
+    assert bool(((lost - G).abs() < 1e-3 * G).all())
+
+
 def test_nothing_accepted_then_more():
     """A step that accepts nothing, with calls in front of and behind it in the stream."""
     p = Commit(steps=3, sizes=[0, 0], B=2, G=4, H=2, n=9, counts=(500, 300), spare=8)

@@ -66,8 +66,8 @@ def test_attention(lib):
     assert lib.kvc_i4_tree_attn_workspace_bytes(shape(), rows(), kvc.TREE_MAX_NODES + 1) == 0
 
 
-def commit(lib, sh=None, r=None, k=A, v=A, ks=None, n=8, path=A, size=A, steps=4, q=A, qs=None, lse=A, mods=None, ko=A, vo=A,
-           os=None):
+def commit(lib, sh=None, r=None, k=A, v=A, ks=None, n=8, path=A, size=A, steps=4, q=A, qs=None, lse=A, mods=None, ko=A + 4096,
+           vo=A + 8192, os=None):
     return lib.kvc_i4_tree_commit(sh or shape(), r or rows(), k, v, ks, n, path, size, steps, q, qs, lse,
                                   ctypes.byref(mods) if mods else None, 0.0, ko, vo, os, None, None)
 
@@ -87,6 +87,8 @@ def test_commit(lib):
         assert commit(lib, **{bad: None}) == INVALID
     for bad in ("k", "v", "q", "ko", "vo"):
         assert commit(lib, **{bad: A + 8}) == INVALID
+    assert commit(lib, ko=A) == INVALID and commit(lib, vo=A) == INVALID and commit(lib, ko=A + 4096, vo=A + 4096) == INVALID
+    assert commit(lib, v=A + 4096) == INVALID and commit(lib) not in (INVALID, UNSUPPORTED)
     assert commit(lib, r=rows(mass=None)) == INVALID             # weights with nowhere to go
     for bad in ("ks", "qs", "os"):
         assert commit(lib, **{bad: st(800, 0, 801, 64)}) == INVALID
