@@ -41,6 +41,20 @@
 // each), 16 tensor memory and MMA issuer (48): 2 x 152 + 2 x 64 + 48 = 5 x 96, what
 // the block was launched with.  Every wait is bounded; one that gives up raises a
 // shared abort flag, the unit is marked KVC_UNIT_TIMEOUT and the block ends.
+//
+// Up to 16 query rows (32 at d = 64) kvc_i4_attn's warps take over (launch_tree).
+//
+// Measured, replayed from a graph (d = 128, 32 heads over 8, a scale per 32
+// elements): 64 nodes, 64 units of 20K to 32K rows 263 us = 47 % of the measured
+// tensor rate; 32 nodes, 8 units of 100K to 131K rows 80 us = 1.9 TB/s; 13 nodes,
+// 8 units of 2,304 rows 13 us, two kernels' latencies.  With a scale per row,
+// d = 64, cap, slopes and a window of 4,096, up to 37 nodes and 9,001 rows: 26 us.
+// No unit is full: the chain scores - maximum - weights - product of 64 keys
+// bounds it (a scheduler issues in 55 % of its cycles, tensor pipe 46 %, ALU 34 %,
+// exponentials 23 %; without the exponentials 9 %, without turning codes into
+// operands 8 % less time).  64 keys a step, so that a stream's next scores are in
+// the making meanwhile.  Each operand warp turns its own 32 rows of every tile:
+// with a named barrier that joined four of them at every tile 503 us, not 310.
 #include <algorithm>
 #include <type_traits>
 

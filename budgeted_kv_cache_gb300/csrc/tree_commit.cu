@@ -10,6 +10,11 @@
 // bf16, in the 16-row operand, the key scales applied to the groups' partial
 // sums in fp32.  More than 32 query rows take another pass over the codes each.
 //
+// Measured, replayed (d = 128, the path of 4 to 7 nodes of 4 heads): 8 units of
+// 2,304 rows 6.3 us, 576 of them 50 us = 2.2 TB/s, 64 units of 20K to 32K rows, 5
+// nodes of 3 heads, capped, a scale per row, 54 us = 2.5 TB/s.  What is left is
+// latency: three warps a scheduler, which issues in 47 to 56 % of its cycles.
+//
 // Rows.  One block per unit, launched with the mass (only the counters, which
 // the other kernel reads, wait for it): d / 8 lanes a row, as kvc_i4_append.  A row's own mass is
 // the weight that it got from the path behind it: few products, a lane each.
