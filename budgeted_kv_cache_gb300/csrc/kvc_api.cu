@@ -502,6 +502,7 @@ kvc_status check_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n) {
 
 struct TreePlan {
   bool few = false;
+  bool longest_first = false;
   int32_t block_rows = 0, n_blocks = 0, splits = 1;
   size_t ws_ml = 0, ws_total = 0;
 };
@@ -558,6 +559,8 @@ kvc_status plan_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n, TreePl
     p->splits = f.splits;
   } else {
     p->splits = tree_splits(info.sms, items, tiles, rows > 128, 8.0 * U * rows * s->head_dim);
+    // With more blocks than SMs the longest go first, and short ones fill the end
+    p->longest_first = items * p->splits > info.sms && U <= kTreeRanked;
   }
   if (p->splits > 1) {
     const size_t parts = static_cast<size_t>(U) * rows * p->splits;
@@ -1325,12 +1328,13 @@ kvc_status kvc_i4_tree_attn(const kvc_shape* shape, const kvc_i4_rows* rows, con
   a.block_rows = p.block_rows;
   a.n_blocks = p.n_blocks;
   a.splits = p.splits;
+  a.longest_first = p.longest_first;
   if (p.splits > 1) {
     a.part_ml = static_cast<float2*>(workspace);
     a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.ws_ml);
   }
   a.by_splits = FastDiv::of(a.splits);
-  a.by_units = FastDiv::of(a.U);
+  a.by_blocks = FastDiv::of(a.n_blocks);
   a.by_heads = FastDiv::of(a.Hkv);
   a.by_layers = FastDiv::of(a.L);
   a.by_group = FastDiv::of(a.G);

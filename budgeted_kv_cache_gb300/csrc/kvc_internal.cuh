@@ -318,6 +318,7 @@ struct I4AttnArgs {
 constexpr int kMaxSplits = 128;      // blocks that share a unit's keys in the 4-bit attention
 
 // A tree of drafted tokens over a 4-bit cache.
+constexpr int kTreeRanked = 256;                 // units that blocks put in order
 struct TreeArgs {
   int32_t U, L, Hkv, B, G, d, n;
   float scale;
@@ -337,9 +338,10 @@ struct TreeArgs {
   int32_t block_rows;          // packed rows per item: 128 or 256
   int32_t n_blocks;            // items per unit
   int32_t splits;              // blocks that share an item's keys
+  bool longest_first;          // blocks take the units by their rows in use
   float* part_o;               // splits > 1: [U][n G][splits][d] unnormalised outputs
   float2* part_ml;             // [U][n G][splits] (log2-domain maximum, sum)
-  FastDiv by_splits, by_units, by_heads, by_layers, by_group, by_rows;   // divisors splits, U, Hkv, L, G, n G
+  FastDiv by_splits, by_blocks, by_heads, by_layers, by_group, by_rows;   // divisors splits, n_blocks, Hkv, L, G, n G
 };
 
 // The accepted path of such a tree.

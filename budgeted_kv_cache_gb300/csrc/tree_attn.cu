@@ -45,8 +45,8 @@
 // Up to 16 query rows (32 at d = 64) kvc_i4_attn's warps take over (launch_tree).
 //
 // Measured, replayed from a graph (d = 128, 32 heads over 8, a scale per 32
-// elements): 64 nodes, 64 units of 20K to 32K rows 263 us = 47 % of the measured
-// tensor rate; 32 nodes, 8 units of 100K to 131K rows 80 us = 1.9 TB/s; 13 nodes,
+// elements): 64 nodes, 64 units of 20K to 32K rows 245 us = 50 % of the measured
+// tensor rate (263 without the longest units' blocks first); 32 nodes, 8 units of 100K to 131K rows 80 us = 1.9 TB/s; 13 nodes,
 // 8 units of 2,304 rows 13 us, two kernels' latencies.  With a scale per row,
 // d = 64, cap, slopes and a window of 4,096, up to 37 nodes and 9,001 rows: 26 us.
 // No unit is full: the chain scores - maximum - weights - product of 64 keys
@@ -94,6 +94,7 @@ struct Bars {
   alignas(16) float k_by[kSlots][4];
   alignas(16) float2 v_by[kSlots][4];
   int16_t parent[KVC_TREE_MAX_NODES], depth[KVC_TREE_MAX_NODES];      // of the nodes that the item's rows see
+  int32_t counts[kTreeRanked], unit;   // rows in use of every unit; the one that this block takes
   float2 ml[2][kTileRows];     // of each stream's rows
   int8_t q_exp[128];           // queries are rows times 2^-q_exp (one row tile)
   // with modifiers: smallest position of 32 rows; positions, and how far they lie behind the first nodes
@@ -120,10 +121,23 @@ struct Item {
   int nodes;                   // of the tree, as far as this item's rows see
 };
 
-__device__ __forceinline__ Item make_item(const TreeArgs& a, int id) {
+// Block `id` of the grid: the splits of an item, the items of a unit and the units follow each other.  All threads call.
+__device__ __forceinline__ Item make_item(const TreeArgs& a, int id, Bars& s) {
   Item t;
-  uint32_t split, u, g, l;
-  const int qb = static_cast<int>(a.by_units.divmod(a.by_splits.divmod(id, &split), &u));
+  uint32_t split, qb, g, l, u = a.by_blocks.divmod(a.by_splits.divmod(id, &split), &qb);
+  if (a.longest_first) {
+    // the unit that u others precede
+    const int i = threadIdx.x;
+    const int own = i < a.U ? clamp_count(a.rows.count[i], a.rows.capacity) : 0;
+    if (i < a.U) s.counts[i] = own;
+    __syncthreads();
+    uint32_t rank = 0;
+#pragma unroll 8
+    for (int v = 0; v < a.U; ++v) rank += s.counts[v] > own || (s.counts[v] == own && v < i);
+    if (i < a.U && rank == u) s.unit = i;
+    __syncthreads();
+    u = s.unit;
+  }
   t.split = static_cast<int>(split);
   t.u = static_cast<int>(u);
   t.b = static_cast<int>(a.by_layers.divmod(a.by_heads.divmod(u, &g), &l));
@@ -133,7 +147,7 @@ __device__ __forceinline__ Item make_item(const TreeArgs& a, int id) {
   t.next = a.rows.next_pos[t.u];
   t.prefix = a.mods.prefix_len ? a.mods.prefix_len[t.b] : INT32_MIN;
   const int n = a.n_nodes ? clamp_count(a.n_nodes[t.b], a.n) : a.n;
-  t.row0 = qb * a.block_rows;
+  t.row0 = static_cast<int>(qb) * a.block_rows;
   t.rows = max(0, min(a.block_rows, n * a.G - t.row0));
   t.nodes = t.rows > 0 ? static_cast<int>(a.by_group.div(t.row0 + t.rows - 1)) + 1 : 0;
   t.cached = (t.count + kKeys - 1) / kKeys;
@@ -915,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
   }
   wait_for_previous_kernel();
   let_next_kernel_start();
-  const Item t = make_item(a, blockIdx.x);
+  const Item t = make_item(a, blockIdx.x, s);
   bool bad = false;
   for (int i = threadIdx.x; i < t.nodes; i += kThreads) {
     const int p = a.parent[static_cast<int64_t>(t.b) * a.n + i];
