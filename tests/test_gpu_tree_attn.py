@@ -124,6 +124,11 @@ def test_groups(G, n):
     Problem(B=1, L=2, G=G, H=3, d=64, n=n, counts=(200,), seed=G).call().check()
 
 
+def test_blocks_in_the_order_of_their_lengths():
+    """More blocks than SMs, several row tiles a unit, equal and empty units among them."""
+    Problem(B=13, G=4, H=4, d=64, n=150, counts=[700 * (b % 5) for b in range(13)], seed=5).call().check()
+
+
 @pytest.mark.parametrize("n,kind", [(256, "random"), (300, "chain"), (1024, "random"), (1024, "chain")])
 def test_large_trees(n, kind):
     Problem(G=2, H=1, n=n, counts=(700,), kind=kind, d=64).call().check()
@@ -175,6 +180,13 @@ def test_rows_in_any_order():
         for t in (p.rows.k, p.rows.v, p.rows.k_scale, p.rows.v_scale, p.rows.pos):
             t[u, :1000] = t[u, :1000][order]
     p.call(mods=kvc.ScoreMods(window=300)).check(window=300)
+
+
+def test_blocks_in_the_order_of_their_lengths():
+    """More blocks than SMs, several row tiles a unit, equal and empty units among them."""
+    counts = [700 * (b % 5) for b in range(13)]
+    p = Problem(B=13, G=4, H=4, d=64, n=150, counts=counts, seed=5)
+    p.call().check()
 
 
 @pytest.mark.parametrize("G,n", [(1, 9), (4, 20)])
