@@ -1323,7 +1323,8 @@ kvc_status kvc_i4_tree_attn(const kvc_shape* shape, const kvc_i4_rows* rows, con
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = row_lse;
   a.unit_status = unit_status;
-  a.stall_unit = g_score_stall_unit.load(std::memory_order_relaxed);   // failure test hook (-1: none)
+  a.stall_unit = g_score_stall_unit.load(std::memory_order_relaxed);   // test hooks (-1: none)
+  a.late_unit = g_select_stall_unit.load(std::memory_order_relaxed);
   a.few = p.few;
   a.block_rows = p.block_rows;
   a.n_blocks = p.n_blocks;

@@ -334,6 +334,7 @@ struct TreeArgs {
   float* lse;                  // optional [B][L][H_q][n]
   int32_t* unit_status;        // optional [U]
   int32_t stall_unit;          // test hook (-1 = none): this unit's wait for its first key tile never completes
+  int32_t late_unit;           // test hook (-1 = none): this unit's value tiles come 20 us late
   bool few;                    // few query rows: the kernel of kvc_i4_attn
   int32_t block_rows;          // packed rows per item: 128 or 256
   int32_t n_blocks;            // items per unit

@@ -336,6 +336,9 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
         if (lane == 0) s.v_by[slot][quarter] = make_float2(static_cast<float>(e), pow2(-e));
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.efull[st]));
+        // (a test makes a unit's values late: the softmax is done with the tile by then)
+        if (SELDOM(t.u == a.late_unit))
+          for (int i = 0; i < 20; ++i) __nanosleep(1000);
         return;
       }
       if (lane == 0) {
@@ -515,12 +518,13 @@ __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8
     live0 = next0;
     live1 = next1;
   }
-  // the streams' next scores are none (after an abort they find that by themselves)
-  if (ok && elected) {
-    mbar_arrive(smem_u32(&s.sfull[0][0]));
-    mbar_arrive(smem_u32(&s.sfull[1][0]));
+  // The streams' next scores are none (after an abort they find that by themselves), told by the tensor core once every
+  // product above is done: whoever learns of the end may read the outputs.  A wait for odone could not tell the last
+  // product from the last but one of the same parity, and the values of both halves may be late.
+  if (ok) {
+    commit(smem_u32(&s.sfull[0][0]), elected);
+    commit(smem_u32(&s.sfull[1][0]), elected);
   }
-  __syncwarp();
   // all MMAs issued above complete before tensor memory is freed
   commit(smem_u32(&s.done), elected);
   drain(smem_u32(&s.done), 0);
@@ -799,9 +803,8 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
           sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
   };
   float m2 = m;
-  if (share && valid) write_stats(m2, l);        // while the last product of this stream runs
-  if (!fail && n > 0 && SELDOM(!wait_for(&s.odone[h], 1, abort_flag))) fail = true;         // the last of 2 n products
-  tc_fence_after();
+  if (share && valid) write_stats(m2, l);
+  tc_fence_after();                              // the end is told behind the last product
   // One row tile: both streams hold an output for the same rows, in the same lanes of tensor memory.  They exchange
   // (m, l), and each joins and writes one half of the columns.
   int n_other = 0;

@@ -988,6 +988,9 @@ kvc_status kvc_commit_flags(int32_t batch, int64_t n_tokens, int32_t n_pages,
  *                       for 16 bytes more than its copy brings, so after
  *                       the bounded wait (2 s, then 2 s more for the copy)
  *                       it reports KVC_UNIT_TIMEOUT and keeps nothing.
+ *                       kvc_i4_tree_attn (more query rows than the few that
+ *                       kvc_i4_attn's kernel takes): each value tile of this
+ *                       unit comes 20 us late; its results are the same.
  * NULL restores every default.  Values out of range return
  * KVC_ERR_INVALID_ARG and change nothing.  A call affects calls issued
  * after it from any host thread; it does not synchronise with them.
