@@ -22,8 +22,10 @@
 //   softmax        128 threads, one row each, in base 2; the weights are rounded
 //                  to fp16 (2^-11 of a weight, and 2^-25 of the largest product
 //                  of weight and value) and stored over S in tensor memory; the
-//                  row's sum is that of the unrounded weights.  The accumulator
-//                  is rescaled only when the maximum grew by more than 2^8
+//                  row's sum is that of the unrounded weights (formed anew, key by
+//                  key, where the values' sizes leave no common reference for it and
+//                  the outputs: kSpread).  The accumulator is rescaled only when
+//                  the maximum grew by more than 2^8
 //   O += P V       tcgen05, P from tensor memory, V as an MN-major operand
 // The order of d inside a product is free: the eight codes of a word lie as
 // pairs (0,4), (1,5), (2,6), (3,7), and the queries, the tree's rows and the
@@ -78,16 +80,35 @@ constexpr int kSlots = 4;                        // tiles whose description is h
 constexpr int kAhead = 4;                        // tiles prefetched to L2 behind the one on its way
 constexpr int kEnd = INT32_MIN;
 constexpr int kLeast = -100;                     // least exponent: rows below 2^-90 lose bits, and 2^-ev stays in range
-constexpr int kNoValues = -40;                   // exponent of 32 rows whose values are all zero: below any that matter
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;                     // log2 growth of the maximum that forces a rescale
+// The row sum shares the outputs' reference m, the maximum of y + ev.  A weight 2^(y + ev - m) is lost below 2^-126: with the
+// values' exponents no further apart than kSpread that is less than 2^-34 of the sum (m <= max y + max ev).  From +-kSizes on
+// the sum itself would leave fp32's range (2^31 weights beside exponents of -kSizes do not).
+constexpr int kSpread = 92, kSizes = 85;
+constexpr int kFar = 40;                         // exponents from which on a block's reference is brought back to the scores'
+// Exponents of 32 rows that hold nothing but zeros (below any that matters), and of 32 places without rows (no further than
+// kSpread from any others; nothing is seen there).
+constexpr int kNoValues = -kSizes, kNoRows = kSpread + kLeast;
+
+// What an item covers.
+struct Item {
+  int u, b, l, g, split;
+  int row0, rows;              // first packed row, packed rows of the item (<= 256)
+  int count, next, prefix;     // cached rows, position of the first nodes, visible prefix
+  int cached;                  // tiles of cached rows
+  int i0, i1, step;            // of those and the tree's this split takes i0, i0 + step, .. below i1
+  int nodes;                   // of the tree, as far as this item's rows see
+};
 
 struct Bars {
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-  uint64_t efull[kStages], sfull[2][2], pfull[2][2], odone[2], qfull[2], done;      // [stream][half of a tile's keys]
+  uint64_t efull[kStages], sfull[2][2], pfull[2][2], odone[2], qfull[2], done, sizes;      // [stream][half of a tile's keys]
   uint32_t tmem;
   int abort_flag;
+  int ev_min, ev_max;          // of the values' exponents (once `sizes` is complete)
+  Item item;                   // (for sum_alone)
   int tiles[2];                // of each stream
   int j0[2 * kSlots];          // a tile's first slot, or -1 - its first node; kEnd: no more tiles (for either stream)
   // operands are keys times 2^-ek and values times 2^-ev, per 32 rows: 2^ek; ev and 2^-ev
@@ -103,6 +124,12 @@ struct Bars {
   alignas(16) float ks[kSlots][kKeys], vs[kSlots][kKeys];    // scale per row: of keys; of values times 2^-ev
 };
 
+// Sums that two streams form again exchange them, and their outputs' references, where the first queries lay.
+struct Alone {
+  float2 ml[2][kTileRows];
+  float m[2][kTileRows];
+};
+
 template <int D>
 struct Cfg {
   static constexpr int kTile = D / 64 * kChunkBytes;         // a Q, K or V tile
@@ -110,16 +137,6 @@ struct Cfg {
   static constexpr int kSmem = (2 + 2 * kStages) * kTile + 8 * kRaw + 1024 /* alignment */ + sizeof(Bars);
 };
 static_assert(Cfg<128>::kSmem <= 232448, "shared memory of a block");
-
-// What an item covers.
-struct Item {
-  int u, b, l, g, split;
-  int row0, rows;              // first packed row, packed rows of the item (<= 256)
-  int count, next, prefix;     // cached rows, position of the first nodes, visible prefix
-  int cached;                  // tiles of cached rows
-  int i0, i1, step;            // of those and the tree's this split takes i0, i0 + step, .. below i1
-  int nodes;                   // of the tree, as far as this item's rows see
-};
 
 // Block `id` of the grid: the splits of an item, the items of a unit and the units follow each other.  All threads call.
 __device__ __forceinline__ Item make_item(const TreeArgs& a, int id, Bars& s) {
@@ -379,7 +396,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
       if (!windowed) prefetch(cur + 1 + kAhead);
       cur = next();
       if (cur >= 0 && cur < t.cached) load(cur);
-      int e = v ? kNoValues : 0;                 // rows times 2^-e:
+      int e = !v ? 0 : j0 + first < t.count ? kNoValues : kNoRows;             // rows times 2^-e:
       if (v || !ROW) {
         top = __reduce_max_sync(kFull, top);
         if (top && !ROW) e = max(exponent_of(top) - 10, kLeast);               // the largest scale below 2^11
@@ -426,7 +443,7 @@ __device__ __forceinline__ void make_operands(const TreeArgs& a, const Item& t, 
       top = __reduce_max_sync(kFull, top);
       // the largest element below 2^14, as a group's code times its scale; below 2^3, as a plain code, with a scale per
       // row: what the weights are multiplied by is of one size in all tiles, so that none is smaller than it has to be
-      const int e = top ? max(exponent_of(top) - (v && ROW ? 2 : 13), kLeast) : v ? kNoValues : 0;
+      const int e = top ? max(exponent_of(top) - (v && ROW ? 2 : 13), kLeast) : !v ? 0 : j0 + first < t.nodes ? kNoValues : kNoRows;
       publish(e, Scales{}, 0);
       const float by = pow2(-e);
 #pragma unroll 2
@@ -481,6 +498,7 @@ __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8
     commit(smem_u32(&s.sfull[h][b]), elected);
     if (b == 1 && (!share || h == 1)) commit(smem_u32(&s.kempty[st]), elected);
   };
+  float ev_min = INFINITY, ev_max = -INFINITY;   // of the values' exponents: the issuer has the time to look after them
   auto values = [&](int j, int h, int b) -> bool {
     const int n = tile_of(j, h);
     const uint32_t st = n & 1;
@@ -493,7 +511,12 @@ __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8
     for (int ks = 0; ks < kKeys / 32; ++ks)
       mma_ts(tmem + kOCol + h * 128, tmem + h * 128 + b * 64 + ks * 8, vd + ((ks * 16 * 128) >> 4), idesc_o, ks > 0 ? 1u : more, elected);
     commit(smem_u32(&s.odone[h]), elected);
-    if (b == 1 && (!share || h == 1)) commit(smem_u32(&s.vempty[st]), elected);
+    if (b == 1 && (!share || h == 1)) {
+      commit(smem_u32(&s.vempty[st]), elected);
+      const float ev = *const_cast<volatile float*>(&s.v_by[n & (kSlots - 1)][threadIdx.x & 3].x);
+      ev_min = fminf(ev_min, ev);
+      ev_max = fmaxf(ev_max, ev);
+    }
     return true;
   };
   bool live0 = has(0, 0), live1 = false;
@@ -521,6 +544,17 @@ __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8
   // The streams' next scores are none (after an abort they find that by themselves), told by the tensor core once every
   // product above is done: whoever learns of the end may read the outputs.  A wait for odone could not tell the last
   // product from the last but one of the same parity, and the values of both halves may be late.
+  for (int k = 1; k < 4; k <<= 1) {
+    ev_min = fminf(ev_min, __shfl_xor_sync(kFull, ev_min, k));
+    ev_max = fmaxf(ev_max, __shfl_xor_sync(kFull, ev_max, k));
+  }
+  if (elected) {
+    const bool any = ev_max > -INFINITY;
+    s.ev_min = any ? static_cast<int>(ev_min) : 0;
+    s.ev_max = any ? static_cast<int>(ev_max) : 0;
+    mbar_arrive(smem_u32(&s.sizes));
+  }
+  __syncwarp();
   if (ok) {
     commit(smem_u32(&s.sfull[0][0]), elected);
     commit(smem_u32(&s.sfull[1][0]), elected);
@@ -531,6 +565,77 @@ __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8
 }
 
 // ---------------------------------------------------------------- softmax
+
+// The sum of a row's 2^y (and its reference) over every `parts`-th tile of the item, a key after the other on the CUDA cores:
+// where the sizes of values differ so much that weights relative to the outputs' reference cannot hold it.  Slow (64 units of
+// 20K to 32K rows x 256 query rows 24 ms, not 226 us), for values that no model has; code for them in the loop of the tiles
+// cost everyone 1 to 5 %, not taken.
+template <int D, bool ROW, bool MODS>
+__device__ __noinline__ float2 sum_alone(const TreeArgs& a, const Bars& s, int node, int head, int part, int parts) {
+  const Item& t = s.item;
+  const int64_t base = static_cast<int64_t>(t.u) * a.rows.capacity;
+  const uint4* const q = reinterpret_cast<const uint4*>(a.q + t.b * a.qs.batch + t.l * a.qs.layer + static_cast<int64_t>(head) * a.qs.head +
+                                                        static_cast<int64_t>(node) * a.qs.token);
+  auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
+  auto hi = [](uint32_t x) { return __uint_as_float(x & 0xffff0000u); };
+  const float cap = MODS ? a.mods.softcap : 0.f, slope = MODS && a.mods.slopes ? a.mods.slopes[head] * kLog2e : 0.f;
+  const int p_q = t.next + (MODS && (a.mods.slopes || a.mods.window) ? s.depth[node] : 0);
+  float m = -INFINITY, l = 0.f;
+  auto add = [&](float x, int p) {
+    const uint32_t dist = behind(p_q, p);
+    if (MODS && a.mods.window && dist >= static_cast<uint32_t>(a.mods.window) && p >= t.prefix) return;
+    x *= a.scale;
+    x = cap > 0.f ? capped_base2(x, x * fminf(1.f / cap, 1e30f), cap) : x * kLog2e;
+    if (MODS && a.mods.slopes) x = fmaf(-slope, static_cast<float>(dist), x);
+    if (x - m > kGrow) {                         // also from -inf
+      l *= m == -INFINITY ? 0.f : ex2_approx(m - x);
+      m = x;
+    }
+    l += ex2_approx(x - m);
+  };
+  int n = 0;
+#pragma unroll 1
+  for (int at = t.i0; at < t.i1; at += t.step, ++n) {
+    if (n % parts != part) continue;
+    if (at < t.cached) {
+#pragma unroll 1
+      for (int j = at * kKeys; j < min(t.count, (at + 1) * kKeys); ++j) {
+        const uint32_t* codes = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.rows.k) + (base + j) * (D / 2));
+        const uint16_t* scales = static_cast<const uint16_t*>(a.rows.k_scale) + (base + j) * (ROW ? 1 : D / 32);
+        float x = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 w = q[c];
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w}, code = codes[c];
+          const uint16_t f = scales[ROW ? 0 : c / 4];
+          float y = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y = fmaf(e & 1 ? hi(v[e / 2]) : lo(v[e / 2]), static_cast<float>(static_cast<int32_t>(code << (28 - 4 * e)) >> 28), y);
+          x = fmaf(y, ROW ? __half2float(__ushort_as_half(f)) : __uint_as_float(static_cast<uint32_t>(f) << 16), x);
+        }
+        add(x, MODS ? a.rows.pos[base + j] : 0);
+      }
+    } else {
+      const int j0 = ((t.nodes + kKeys - 1) / kKeys - 1 - (at - t.cached)) * kKeys;
+      for (int j = node; j >= j0; j = s.parent[j]) {
+        if (j >= j0 + kKeys) continue;
+        const uint4* k = reinterpret_cast<const uint4*>(a.k_new + t.b * a.news.batch + t.l * a.news.layer + t.g * a.news.head + j * a.news.token);
+        float x = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 w = k[c], y = q[c];
+          x = fmaf(lo(y.x), lo(w.x), fmaf(hi(y.x), hi(w.x), x));
+          x = fmaf(lo(y.y), lo(w.y), fmaf(hi(y.y), hi(w.y), x));
+          x = fmaf(lo(y.z), lo(w.z), fmaf(hi(y.z), hi(w.z), x));
+          x = fmaf(lo(y.w), lo(w.w), fmaf(hi(y.w), hi(w.w), x));
+        }
+        add(x, MODS && (a.mods.slopes || a.mods.window) ? t.next + s.depth[j] : t.next);
+      }
+    }
+  }
+  return make_float2(m, l);
+}
 
 template <int D, bool ROW, bool MODS>
 __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& s, uint8_t* sq, uint32_t tmem, bool share) {
@@ -737,9 +842,10 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
       if (SELDOM(__any_sync(kFull, grow))) {
         float by = 1.f;
         if (grow) {
-          by = m == -INFINITY ? 0.f : ex2_approx(m - top);
+          const float half = m == -INFINITY ? 0.f : ex2_approx(0.5f * (m - top));
+          by = half * half;
+          l = l * half * half;                   // (l may be so large that more of it is left than of `by`)
           m = top;
-          l *= by;
         }
         if (n + b > 0) {
           if (SELDOM(!wait_for(&s.odone[h], (b ^ 1) & 1, abort_flag))) {       // the product of the 64 keys before
@@ -802,13 +908,35 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
       a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n + node] =
           sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
   };
-  float m2 = m;
-  if (share && valid) write_stats(m2, l);
+  float m2 = m, f0 = 1.f, f1 = 0.f;              // the sum's reference; outputs to it, from this stream and the other
+  // Where values are far from 1 the sum's reference is brought near the largest score (splits are joined by it): by their
+  // exponent, or, where they lie far apart, by a sum formed anew (true).  All tiles' exponents are known by now.
+  if (!fail && SELDOM(!wait_for(&s.sizes, 0, abort_flag))) fail = true;
+  auto far = [&](int* by) -> bool {
+    const int lo = *const_cast<volatile int*>(&s.ev_min), hi = *const_cast<volatile int*>(&s.ev_max);
+    *by = abs(hi) > kFar ? hi : 0;
+    if (hi - lo <= kSpread && hi <= kSizes && (lo >= -kSizes || t.i1 - t.i0 <= 4096)) return false;
+    s.item = t;                                  // (the same from all)
+    __syncwarp();
+    return true;
+  };
+  int ev;
+  if (share && !fail && warp_valid) {
+    if (SELDOM(far(&ev))) {
+      const float2 own = sum_alone<D, ROW, MODS>(a, s, node, head, 0, 1);
+      m2 = own.x, l = own.y;
+      f0 = m == -INFINITY ? 0.f : ex2_approx(m - m2);
+    } else if (SELDOM(ev)) {
+      m2 = m - static_cast<float>(ev);
+      f0 = pow2(ev);
+      l *= f0;
+    }
+    if (valid) write_stats(m2, l);
+  }
   tc_fence_after();                              // the end is told behind the last product
   // One row tile: both streams hold an output for the same rows, in the same lanes of tensor memory.  They exchange
   // (m, l), and each joins and writes one half of the columns.
   int n_other = 0;
-  float f0 = 1.f, f1 = 0.f;
   if (!share) {
     s.ml[h][r] = make_float2(m2, l);
     if (r == 0) s.tiles[h] = n;
@@ -823,6 +951,23 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
     // the same order of the sum on both sides
     l = h == 0 ? fmaf(l, f0, o.y * f1) : fmaf(o.y, f1, l * f0);
     m2 = mm;
+    if (SELDOM(!fail && far(&ev))) {             // in both streams alike: half of the sum from each
+      Alone& x = *reinterpret_cast<Alone*>(sq);
+      x.m[h][r] = m;
+      x.ml[h][r] = warp_valid ? sum_alone<D, ROW, MODS>(a, s, node, head, h, 2) : make_float2(-INFINITY, 0.f);
+      named_bar_or(1, 256, false);
+      const float2 p = x.ml[0][r], q = x.ml[1][r];
+      const float m_other = x.m[h ^ 1][r];
+      m2 = fmaxf(p.x, q.x);
+      l = (p.x == -INFINITY ? p.y : p.y * ex2_approx(p.x - m2)) + (q.x == -INFINITY ? q.y : q.y * ex2_approx(q.x - m2));
+      f0 = m == -INFINITY ? 0.f : ex2_approx(m - m2);
+      f1 = m_other == -INFINITY ? 0.f : ex2_approx(m_other - m2);
+      named_bar_or(1, 256, false);               // before outputs are staged there
+    } else if (SELDOM(!fail && ev)) {
+      const float by = pow2(ev);
+      m2 -= static_cast<float>(ev);
+      l *= by, f0 *= by, f1 *= by;
+    }
     if (valid && h == 0) write_stats(m2, l);
   }
   if (!fail && warp_valid) {
@@ -896,7 +1041,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
 }
 
 template <int D, bool ROW, bool MODS>
-__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -923,6 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a) {
       mbar_init(smem_u32(&s.qfull[i]), 4);
     }
     mbar_init(smem_u32(&s.done), 1);
+    mbar_init(smem_u32(&s.sizes), 1);
     s.abort_flag = 0;
     fence_barrier_init();
   }

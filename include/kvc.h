@@ -780,8 +780,11 @@ kvc_status kvc_i4_evict(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t
  * largest of their 32 rows, or below 2^-100, which lose bits; fp32
  * scores, statistics and accumulation; the weights of the value product are
  * rounded to fp16 (off by 2^-11 of a weight, and by 2^-25 of the row's largest
- * product of a weight and a value); bf16 output.
+ * product of a weight and a value, where 32 cached rows of nothing but zeros
+ * count as values of 2^-71); bf16 output.
  * Rows in use hold finite scales, values below 2^119 / capacity in magnitude.
+ * Sizes of values do not touch the statistics; where they differ by more than
+ * about 2^80, or pass 2^80, the call takes many times as long.
  * workspace >= kvc_i4_tree_attn_workspace_bytes(...), 256-byte aligned,
  *          contents need not be initialised (may be 0 bytes: then NULL is
  *          accepted).
