@@ -665,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
     float sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      if (s.m[w][c] != -INFINITY) sum = fmaf(s.l[w][c], ex2_approx(s.m[w][c] - mm), sum);
+      // (a sum of NaN has no maximum)
+      if (s.m[w][c] != -INFINITY || (TREE && isnan(s.l[w][c]))) sum = fmaf(s.l[w][c], ex2_approx(s.m[w][c] - mm), sum);
     s.ml[c] = make_float2(mm, sum);
   }
   __syncthreads();
@@ -686,7 +687,9 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, NT, ROW>::kBlocks)) i4_attn
           make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
                      pack_bf16x2(x[4] * inv, x[5] * inv), pack_bf16x2(x[6] * inv, x[7] * inv));
       if (d0 == 0) {
-        if (a.lse) a.lse[un.lse_at(a, r)] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
+        // (of a tree's row of NaN: NaN)
+        const bool none = TREE ? ml.y == 0.f : !(ml.y > 0.f);
+        if (a.lse) a.lse[un.lse_at(a, r)] = none ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
         if (a.part_ml) a.part_ml[static_cast<int64_t>(un.u) * un.R + r] = ml;
       }
     }

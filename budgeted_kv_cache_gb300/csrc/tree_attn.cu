@@ -220,6 +220,9 @@ __device__ __forceinline__ int exponent_of(uint32_t bits) { return static_cast<i
 // code that is not there yet costs more than what it skips.
 #define SELDOM(x) (__builtin_expect(static_cast<bool>(x), 0))
 
+// Natural logarithm of 2^top times the sum: -inf for a row that saw nothing, NaN for one whose scores are no numbers.
+__device__ __forceinline__ float row_statistic(float top, float sum) { return sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2; }
+
 // warp_wait, its first test in line.
 __device__ __forceinline__ bool wait_for(const uint64_t* bar, uint32_t parity, volatile int* abort) {
   const uint32_t at = smem_u32(bar);
@@ -905,8 +908,7 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
     if (part)
       a.part_ml[prow * a.splits + t.split] = make_float2(top, sum);
     else if (a.lse)
-      a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n + node] =
-          sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+      a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n + node] = row_statistic(top, sum);
   };
   float m2 = m, f0 = 1.f, f1 = 0.f;              // the sum's reference; outputs to it, from this stream and the other
   // Where values are far from 1 the sum's reference is brought near the largest score (splits are joined by it): by their
@@ -1207,8 +1209,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
 #pragma unroll
   for (int c = 0; c < D / 32; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(x[c] * inv, x[c + 1] * inv);
   if (lane == 0 && a.lse)
-    a.lse[((static_cast<int64_t>(b) * a.L + l) * (a.Hkv * a.G) + head) * a.n + node] =
-        sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    a.lse[((static_cast<int64_t>(b) * a.L + l) * (a.Hkv * a.G) + head) * a.n + node] = row_statistic(top, sum);
 }
 
 }  // namespace

@@ -772,7 +772,8 @@ kvc_status kvc_i4_evict(const kvc_shape* shape, const kvc_i4_rows* rows, int32_t
  *          units of its sequence KVC_UNIT_BAD_INDEX in unit_status.
  * n_nodes  optional int32 [B], limited to [0, n] (NULL: n).  Rows of out and
  *          row_lse at or past n_nodes[b] are left as they were.
- * row_lse  optional fp32 [B][L][H_q][n], dense.
+ * row_lse  optional fp32 [B][L][H_q][n], dense; NaN (as its outputs) for a row
+ *          whose scores are not finite.
  * unit_status  optional int32 [U], only errors are written (KVC_UNIT_TIMEOUT if
  *          a device wait gave up: its rows are then undefined).
  * Keys and values are used as they are stored (code * scale), but for those
