@@ -28,7 +28,7 @@ def _nvcc() -> str:
 
 
 def _deps() -> list:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
     return files + [os.path.join(INCLUDE, "kvc.h"), os.path.abspath(__file__)]
 
 

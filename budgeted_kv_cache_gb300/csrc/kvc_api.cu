@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "kvc_internal.cuh"
+#include "rope_turns.h"
 
 using namespace kvc;
 
@@ -568,44 +569,6 @@ kvc_status plan_tree(const kvc_shape* s, const kvc_i4_rows* r, int32_t n, TreePl
     p->ws_total = p->ws_ml + parts * s->head_dim * sizeof(float);
   }
   return KVC_OK;
-}
-
-// Turns per position of every pair, in 2^-64 (whole turns dropped), and the tables' magnitude; false: not a valid scaling.
-bool rope_turns(int rotary_dim, double base, const kvc_rope_scaling* s, uint64_t* turns, float* magnitude) {
-  constexpr double kTau = 6.283185307179586;
-  if (!(base >= 1.0) || isinf(base)) return false;
-  const int kind = s ? s->kind : KVC_ROPE_SCALE_NONE;
-  *magnitude = s && s->magnitude != 0.f ? s->magnitude : 1.f;
-  if (!isfinite(*magnitude) || kind < KVC_ROPE_SCALE_NONE || kind > KVC_ROPE_SCALE_DIMS) return false;
-  double factor = 1.0, first = 0.0, last = 0.0;
-  if (kind != KVC_ROPE_SCALE_NONE) {
-    factor = s->factor;
-    if (!(factor > 0.0) || isinf(factor)) return false;
-  }
-  if (kind == KVC_ROPE_SCALE_BASE) {
-    base *= pow(factor, rotary_dim / (rotary_dim - 2.0));
-    if (!(base >= 1.0) || isinf(base)) return false;
-  }
-  if (kind == KVC_ROPE_SCALE_TURNS || kind == KVC_ROPE_SCALE_DIMS) {
-    if (!(s->original_len > 0.0) || isinf(s->original_len) || !(s->low >= 0.0) || !(s->high > s->low) || isinf(s->high)) return false;
-    if (kind == KVC_ROPE_SCALE_DIMS) {
-      if (!(s->low > 0.0) || !(base > 1.0)) return false;
-      auto at = [&](double n) { return rotary_dim * log(s->original_len / (n * kTau)) / (2.0 * log(base)); };
-      first = fmax(floor(at(s->high)), 0.0);
-      last = fmin(ceil(at(s->low)), rotary_dim - 1.0);
-    }
-  }
-  for (int i = 0; i < rotary_dim / 2; ++i) {
-    double theta = pow(base, -2.0 * i / rotary_dim), keep = 0.0;
-    if (kind == KVC_ROPE_SCALE_NONE || kind == KVC_ROPE_SCALE_BASE) keep = 1.0;
-    if (kind == KVC_ROPE_SCALE_TURNS) keep = (s->original_len * theta / kTau - s->low) / (s->high - s->low);
-    if (kind == KVC_ROPE_SCALE_DIMS) keep = 1.0 - (i - first) / fmax(last - first, 0.001);
-    keep = fmin(fmax(keep, 0.0), 1.0);
-    theta *= keep + (1.0 - keep) / factor;
-    const double t = fmod(theta / kTau, 1.0) * 0x1p64;
-    turns[i] = t < 0x1p64 ? static_cast<uint64_t>(t) : 0;
-  }
-  return true;
 }
 
 }  // namespace

@@ -2,10 +2,10 @@
 // queries and keys by them.
 //
 // Tables: cos and sin of p theta_i for every position p.  Angles are counted in
-// turns as 64-bit fractions (theta_i / 2 pi 2^64), so p theta_i is one integer
-// product whose overflow drops the whole turns: exact for any p, where a product
-// in fp32 is off by whole radians at a million positions and fp64 runs at a
-// sixtieth of the fp32 rate here.  What is left of the nearest quarter turn (at
+// turns as 64-bit fractions (theta_i / 2 pi 2^64, see rope_turns.h), so p theta_i is
+// one integer product whose overflow drops the whole turns: off by 2^-30 of angle
+// at position 2^31 - 1, where a product in fp32 is off by whole radians at a million
+// positions and fp64 runs at a sixtieth of the fp32 rate here.  What is left of the nearest quarter turn (at
 // most an eighth of a turn) goes through two polynomials in its square, fitted
 // at Chebyshev points (within 1e-7 of sin and cos after their fp32 roundings).
 // Written once, 8 bytes a (position, pair).
