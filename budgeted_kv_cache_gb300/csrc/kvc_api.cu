@@ -1318,6 +1318,8 @@ kvc_status kvc_i4_tree_commit(const kvc_shape* shape, const kvc_i4_rows* rows, c
   if (!k_new || !v_new || !path || !path_len || (k_out == nullptr) != (v_out == nullptr)) return KVC_ERR_INVALID_ARG;
   if (k_out && (k_out == k_new || k_out == v_new || v_out == k_new || v_out == v_new || k_out == v_out)) return KVC_ERR_INVALID_ARG;
   if (q && (!row_lse || !rows->mass)) return KVC_ERR_INVALID_ARG;
+  // the rows are put out beside the mass, which reads these
+  if (q && k_out && (k_out == q || v_out == q || k_out == row_lse || v_out == row_lse)) return KVC_ERR_INVALID_ARG;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(q, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
     return KVC_ERR_INVALID_ARG;
   TreeCommitArgs a = {};

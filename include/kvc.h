@@ -826,7 +826,8 @@ kvc_status kvc_i4_tree_attn(const kvc_shape* shape, const kvc_i4_rows* rows, con
  * k_out, v_out  optional (both or none) bf16 [B][L][H_kv][max_path][d], strides
  *          as in kvc_strides: the new rows as the cache holds them (code *
  *          scale, rounded once), for a bf16 store of recent rows beside it;
- *          they overlap neither each other nor k_new and v_new.
+ *          they overlap neither each other nor k_new, v_new, q and row_lse,
+ *          which are still read while they are written.
  *          Rows at or past path_len[b] are left as they were.
  * unit_status  optional int32 [U], only errors are written: KVC_UNIT_FULL if
  *          the rows do not fit, KVC_UNIT_BAD_INDEX if a node of the path is
