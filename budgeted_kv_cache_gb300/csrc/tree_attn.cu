@@ -845,9 +845,13 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
       if (SELDOM(__any_sync(kFull, grow))) {
         float by = 1.f;
         if (grow) {
-          const float half = m == -INFINITY ? 0.f : ex2_approx(0.5f * (m - top));
-          by = half * half;
-          l = l * half * half;                   // (l may be so large that more of it is left than of `by`)
+          by = m == -INFINITY ? 0.f : ex2_approx(m - top);
+          if (SELDOM(m - top < -100.f)) {        // (l may be so large that more of it is left than of `by`)
+            const float half = ex2_approx(0.5f * (m - top));
+            l = l * half * half;
+          } else {
+            l *= by;
+          }
           m = top;
         }
         if (n + b > 0) {
