@@ -116,18 +116,13 @@ struct Bars {
   alignas(16) float2 v_by[kSlots][4];
   int16_t parent[KVC_TREE_MAX_NODES], depth[KVC_TREE_MAX_NODES];      // of the nodes that the item's rows see
   int32_t counts[kTreeRanked], unit;   // rows in use of every unit; the one that this block takes
-  float2 ml[2][kTileRows];     // of each stream's rows
+  float2 ml[2][kTileRows];     // of each stream's rows: reference of the sum, and the sum
+  float m[2][kTileRows];       // reference of the outputs
   int8_t q_exp[128];           // queries are rows times 2^-q_exp (one row tile)
   // with modifiers: smallest position of 32 rows; positions, and how far they lie behind the first nodes
   alignas(16) int32_t p_min[kSlots][4], pos[kSlots][kKeys];
   alignas(16) float behind[kSlots][kKeys];
   alignas(16) float ks[kSlots][kKeys], vs[kSlots][kKeys];    // scale per row: of keys; of values times 2^-ev
-};
-
-// Sums that two streams form again exchange them, and their outputs' references, where the first queries lay.
-struct Alone {
-  float2 ml[2][kTileRows];
-  float m[2][kTileRows];
 };
 
 template <int D>
@@ -547,6 +542,11 @@ __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8
   // The streams' next scores are none (after an abort they find that by themselves), told by the tensor core once every
   // product above is done: whoever learns of the end may read the outputs.  A wait for odone could not tell the last
   // product from the last but one of the same parity, and the values of both halves may be late.
+  if (ok) {
+    commit(smem_u32(&s.sfull[0][0]), elected);
+    commit(smem_u32(&s.sfull[1][0]), elected);
+  }
+  // (and the values' exponents, while those products run)
   for (int k = 1; k < 4; k <<= 1) {
     ev_min = fminf(ev_min, __shfl_xor_sync(kFull, ev_min, k));
     ev_max = fmaxf(ev_max, __shfl_xor_sync(kFull, ev_max, k));
@@ -558,10 +558,6 @@ __device__ __forceinline__ void issue(const Item& t, Bars& s, uint8_t* sq, uint8
     mbar_arrive(smem_u32(&s.sizes));
   }
   __syncwarp();
-  if (ok) {
-    commit(smem_u32(&s.sfull[0][0]), elected);
-    commit(smem_u32(&s.sfull[1][0]), elected);
-  }
   // all MMAs issued above complete before tensor memory is freed
   commit(smem_u32(&s.done), elected);
   drain(smem_u32(&s.done), 0);
@@ -914,66 +910,49 @@ __device__ __forceinline__ void softmax(const TreeArgs& a, const Item& t, Bars& 
     else if (a.lse)
       a.lse[((static_cast<int64_t>(t.b) * a.L + t.l) * (a.Hkv * a.G) + head) * a.n + node] = row_statistic(top, sum);
   };
-  float m2 = m, f0 = 1.f, f1 = 0.f;              // the sum's reference; outputs to it, from this stream and the other
-  // Where values are far from 1 the sum's reference is brought near the largest score (splits are joined by it): by their
-  // exponent, or, where they lie far apart, by a sum formed anew (true).  All tiles' exponents are known by now.
+  // Where values are far from 1 the sum's reference m2 is brought near the largest score (splits are joined by it): by their
+  // exponent, or, where they lie far apart, by a sum formed anew.
+  float m2 = m;
   if (!fail && SELDOM(!wait_for(&s.sizes, 0, abort_flag))) fail = true;
-  auto far = [&](int* by) -> bool {
+  if (!fail && warp_valid) {
     const int lo = *const_cast<volatile int*>(&s.ev_min), hi = *const_cast<volatile int*>(&s.ev_max);
-    *by = abs(hi) > kFar ? hi : 0;
-    if (hi - lo <= kSpread && hi <= kSizes && (lo >= -kSizes || t.i1 - t.i0 <= 4096)) return false;
-    s.item = t;                                  // (the same from all)
-    __syncwarp();
-    return true;
-  };
-  int ev;
-  if (share && !fail && warp_valid) {
-    if (SELDOM(far(&ev))) {
-      const float2 own = sum_alone<D, ROW, MODS>(a, s, node, head, 0, 1);
-      m2 = own.x, l = own.y;
-      f0 = m == -INFINITY ? 0.f : ex2_approx(m - m2);
-    } else if (SELDOM(ev)) {
-      m2 = m - static_cast<float>(ev);
-      f0 = pow2(ev);
-      l *= f0;
+    if (SELDOM(abs(hi) > kFar || hi - lo > kSpread || lo < -kSizes)) {
+      if (hi - lo > kSpread || hi > kSizes || (lo < -kSizes && t.i1 - t.i0 > 4096)) {
+        s.item = t;                              // (the same from all)
+        __syncwarp();
+        const float2 own = sum_alone<D, ROW, MODS>(a, s, node, head, share ? 0 : h, share ? 1 : 2);
+        m2 = own.x, l = own.y;
+      } else {
+        m2 -= static_cast<float>(hi);
+        l *= pow2(hi);
+      }
     }
-    if (valid) write_stats(m2, l);
+    if (share && valid) write_stats(m2, l);
   }
   tc_fence_after();                              // the end is told behind the last product
   // One row tile: both streams hold an output for the same rows, in the same lanes of tensor memory.  They exchange
-  // (m, l), and each joins and writes one half of the columns.
+  // (m, l) and their outputs' references, and each joins and writes one half of the columns.
   int n_other = 0;
+  // factors of the outputs, those of this stream and of the other
+  auto factor = [](float m, float to) { return m == -INFINITY ? 0.f : ex2_approx(m - to); };
+  float f0 = m2 == m ? 1.f : factor(m, m2), f1 = 0.f;
   if (!share) {
     s.ml[h][r] = make_float2(m2, l);
+    s.m[h][r] = m;
     if (r == 0) s.tiles[h] = n;
     tc_fence_before();
     fail = named_bar_or(1, 256, fail);                       // both streams' products are done
     tc_fence_after();
     n_other = uniform(s.tiles[h ^ 1]);
     const float2 o = s.ml[h ^ 1][r];
-    const float mm = fmaxf(m2, o.x);
-    f0 = m2 == -INFINITY ? 0.f : ex2_approx(m2 - mm);
-    f1 = o.x == -INFINITY ? 0.f : ex2_approx(o.x - mm);
+    const float m_other = s.m[h ^ 1][r], mm = fmaxf(m2, o.x);
+    f0 = factor(m2, mm);
+    f1 = factor(o.x, mm);
     // the same order of the sum on both sides
     l = h == 0 ? fmaf(l, f0, o.y * f1) : fmaf(o.y, f1, l * f0);
+    if (SELDOM(m2 != m)) f0 = factor(m, mm);
+    if (SELDOM(o.x != m_other)) f1 = factor(m_other, mm);
     m2 = mm;
-    if (SELDOM(!fail && far(&ev))) {             // in both streams alike: half of the sum from each
-      Alone& x = *reinterpret_cast<Alone*>(sq);
-      x.m[h][r] = m;
-      x.ml[h][r] = warp_valid ? sum_alone<D, ROW, MODS>(a, s, node, head, h, 2) : make_float2(-INFINITY, 0.f);
-      named_bar_or(1, 256, false);
-      const float2 p = x.ml[0][r], q = x.ml[1][r];
-      const float m_other = x.m[h ^ 1][r];
-      m2 = fmaxf(p.x, q.x);
-      l = (p.x == -INFINITY ? p.y : p.y * ex2_approx(p.x - m2)) + (q.x == -INFINITY ? q.y : q.y * ex2_approx(q.x - m2));
-      f0 = m == -INFINITY ? 0.f : ex2_approx(m - m2);
-      f1 = m_other == -INFINITY ? 0.f : ex2_approx(m_other - m2);
-      named_bar_or(1, 256, false);               // before outputs are staged there
-    } else if (SELDOM(!fail && ev)) {
-      const float by = pow2(ev);
-      m2 -= static_cast<float>(ev);
-      l *= by, f0 *= by, f1 *= by;
-    }
     if (valid && h == 0) write_stats(m2, l);
   }
   if (!fail && warp_valid) {
