@@ -48,7 +48,7 @@
 //
 // Measured, replayed from a graph (d = 128, 32 heads over 8, a scale per 32
 // elements): 64 nodes, 64 units of 20K to 32K rows 245 us = 50 % of the measured
-// tensor rate (263 without the longest units' blocks first); 32 nodes, 8 units of 100K to 131K rows 80 us = 1.9 TB/s; 13 nodes,
+// tensor rate (263 without the longest units' blocks first); 32 nodes, 8 units of 131,072 rows 81 us = 1.9 TB/s; 13 nodes,
 // 8 units of 2,304 rows 13 us, two kernels' latencies.  With a scale per row,
 // d = 64, cap, slopes and a window of 4,096, up to 37 nodes and 9,001 rows: 26 us.
 // No unit is full: the chain scores - maximum - weights - product of 64 keys
